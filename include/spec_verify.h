@@ -388,6 +388,125 @@ spec_status_t spec_d3d_select(const int32_t* num_accepted, const int32_t* out_to
                               const int32_t* branch_block, int B, int k, int NB, int blk,
                               int32_t* hit, int32_t* next_block, int32_t* hits, void* stream);
 
+/*
+ * Training the drafter on what verification has read: the loss of a linear
+ * vocabulary head with its gradients, the gradient of the mixture
+ * distillation loss, and the clip of gradients by their global norm.  As
+ * everywhere, the calls are asynchronous on `stream`, allocate nothing and can
+ * be captured into a graph.  Host-detectable errors return before anything is
+ * enqueued; among them is an output that shares memory with an input or
+ * another output (SPEC_ERR_INVALID_ARG).
+ */
+
+#define SPEC_MAX_TOKENS (1 << 18) /* tokens per linear cross-entropy call */
+#define SPEC_MAX_WIDTH (1 << 15)  /* width of a hidden state */
+
+/*
+ * Softmax cross entropy of a linear vocabulary head, without keeping the
+ * logits (the hard-label term of AdaFlash Section 3.1 from hidden states; the
+ * gradients' per-token weights carry DFlash's decay with the position in the
+ * block):
+ *   z_iv  = sum_d hidden[i][d] weight[v][d]
+ *   lse_i = log sum_v exp z_iv
+ *   nll_i = lse_i - z_{i, labels[i]}
+ *
+ *   hidden  [N, D] bfloat16, row-major contiguous, 16-byte aligned
+ *   weight  [V, D] bfloat16, row-major contiguous, 16-byte aligned
+ *   dtype          SPEC_BF16; SPEC_F32 is SPEC_ERR_UNSUPPORTED
+ *   labels  [N]    int32: in [0, V), or negative for a token without a label
+ *                  (nll 0, no gradient; its lse is computed all the same)
+ *   N, V, D        1 <= N <= SPEC_MAX_TOKENS, 1 <= V <= SPEC_MAX_V,
+ *                  8 <= D <= SPEC_MAX_WIDTH, D a multiple of 8
+ *                  (below 1: SPEC_ERR_INVALID_ARG, else SPEC_ERR_UNSUPPORTED)
+ *   nll     [N]    float out
+ *   lse     [N]    float out
+ *   workspace      >= spec_linear_ce_workspace_bytes(N, V, D) bytes (0 for
+ *                  unsupported sizes), 256-byte aligned; not shared by calls
+ *                  that may overlap; needs no initialisation
+ *
+ * Products and sums are in single precision.  A label >= V makes its token's
+ * nll NaN (no gradient) and records SPEC_ERR_BAD_INPUT, readable with
+ * spec_verify_device_status() on `workspace`.  A hidden state or weight that
+ * is not finite makes the results it enters NaN, as the formula does.
+ */
+size_t spec_linear_ce_workspace_bytes(int N, int V, int D);
+spec_status_t spec_linear_ce(const void* hidden, const void* weight, spec_dtype_t dtype,
+                             const int32_t* labels, int N, int V, int D, float* nll, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of sum_i grad_nll[i] nll_i:
+ *   dZ_iv    = grad_nll[i] (exp(z_iv - lse[i]) - [v == labels[i]])
+ *   d_hidden = dZ weight      [N, D] bfloat16 out, 16-byte aligned
+ *   d_weight = dZ^T hidden    [V, D] bfloat16 out, 16-byte aligned
+ *
+ *   lse       [N]  float: from spec_linear_ce on the same inputs
+ *   grad_nll  [N]  float: not read for tokens without a label
+ *   d_hidden, d_weight  either may be NULL (a frozen head, a frozen drafter),
+ *                  not both
+ *   workspace      >= spec_linear_ce_grad_workspace_bytes(N, V, D) bytes
+ * The logits are formed again, a piece of the vocabulary at a time.  dZ is
+ * rounded to bfloat16 before the two products, whose sums are in single
+ * precision.  The hidden states of tokens without a label enter d_weight with
+ * weight 0 and have to be finite.  Everything else is as for spec_linear_ce.
+ */
+size_t spec_linear_ce_grad_workspace_bytes(int N, int V, int D);
+spec_status_t spec_linear_ce_grad(const void* hidden, const void* weight, spec_dtype_t dtype,
+                                  const int32_t* labels, const float* lse, const float* grad_nll,
+                                  int N, int V, int D, void* d_hidden, void* d_weight,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of sum_b grad_loss[b] loss[b] with respect to the draft logits,
+ * loss[b] being spec_opd_stats's mixture loss (AdaFlash Section 3.1).  With
+ * p, q, x_star as there, t_v = log q_v - log p_v, u_v = t_v + 1 where
+ * q_v t_v < delta and 0 elsewhere (the clip holds those entries constant):
+ *   d_draft[b][i][j] = grad_loss[b] / L_b * [ alpha (q_j - [j == x_star])
+ *                      + (1 - alpha) q_j (u_j - sum_v q_v u_v) ],   i < L_b
+ *
+ * target_logits, draft_logits, dtype, lengths, delta, alpha: as for
+ * spec_opd_stats (device memory).  grad_loss [B] float.  d_draft [B, k, V]
+ * (dtype) out: positions i >= L_b get 0; an invalid L_b makes the request's
+ * gradient NaN, a row without finite mass its position's.  Needs no workspace.
+ */
+spec_status_t spec_opd_grad(const void* target_logits, const void* draft_logits,
+                            spec_dtype_t dtype, const int32_t* lengths, const float* grad_loss,
+                            int B, int k, int V, float delta, float alpha, void* d_draft,
+                            void* stream);
+
+/*
+ * Global norm of `count` gradient tensors, norm[0] = sqrt(sum x^2) over all
+ * entries of all tensors, and the tensors scaled to a largest norm:
+ *   out_t = grad_t * min(1, max_norm / norm)
+ *
+ *   grads   [count]  device pointers, each to contiguous entries, aligned to
+ *                    the entry (16-byte alignment is faster)
+ *   outs    [count]  device pointers of the results, or NULL: in place.
+ *                    outs[t] may be grads[t]; else no output may share memory
+ *                    with any other tensor (the same tensor twice in place is
+ *                    SPEC_ERR_INVALID_ARG)
+ *   sizes   [count]  entries, 0 allowed (the pointers may then be NULL)
+ *   dtypes  [count]  SPEC_F32 or SPEC_BF16 (as int)
+ *   max_norm         finite, > 0
+ *   norm    [1]      float out (device)
+ *   workspace        >= spec_grad_norm_workspace_bytes(count) bytes, 256-byte
+ *                    aligned (0 for a count below 1 or above 2^20)
+ * grads, outs, sizes and dtypes are host arrays, read before the call returns.
+ * The sums hold entries from the smallest to the largest of their type without
+ * overflow; a sum above the largest float gives norm = +inf, and the tensors
+ * are scaled all the same.  Where an entry is infinite or NaN the norm is, and
+ * every tensor keeps its values.  The order of additions depends on the sizes
+ * and alignments alone: the same tensors give the same bits.
+ */
+size_t spec_grad_norm_workspace_bytes(int count);
+spec_status_t spec_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes,
+                             int count, float* norm, void* workspace, size_t workspace_bytes,
+                             void* stream);
+spec_status_t spec_clip_grad_norm(const void* const* grads, void* const* outs,
+                                  const long long* sizes, const int* dtypes, int count,
+                                  float max_norm, float* norm, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* spec_status_string(spec_status_t status);
 
@@ -410,6 +529,8 @@ int spec_abi_version(void);
  *    4 sweep: partial slot         10 OPD: logit row, argmax element
  *    5 sweep: completion counter   11 OPD: output element
  *    6 sweep: decided position     12 D3D: branch slot
+ *   13 OPD gradient: logit row     14 linear cross entropy: label, dZ or gradient element
+ *   15 gradient norm: tensor of a unit
  */
 
 /* 1 if the loaded library is the range-checking build, else 0. */

@@ -19,6 +19,13 @@ The functions keep the C names:
 ``spec_opd_stats(...)``              OPD supervision statistics (hard label, reverse KL, clipped)
 ``spec_verify_opd(...)``             verification and OPD statistics in one pass over the rows
 ``spec_d3d_select(...)``             D3D branch selection: reuse a prepared successor block
+``spec_linear_ce(...)``              cross entropy of a linear vocabulary head, without the logits
+``spec_linear_ce_grad(...)``         its gradients (hidden states and weight)
+``LinearCe(...)``                    both bound to fixed buffers
+``spec_opd_grad(...)``               gradient of the OPD mixture loss (draft logits)
+``spec_grad_norm(...)``              global norm of many gradient tensors
+``spec_clip_grad_norm(...)``         the same, and the tensors scaled to a largest norm
+``GradClipper(...)``                 the clip bound to fixed tensors
 ``spec_status_string(code)``
 ``spec_debug_build()``, ``spec_debug_checks()``  the range-checking build (SPEC_VERIFY_DEBUG=1)
 """
@@ -53,7 +60,10 @@ EXPORTS = ("spec_verify_workspace_bytes", "spec_verify", "spec_verify_ex", "spec
            "spec_verify_packed", "spec_verify_report",
            "spec_verify_device_status", "spec_row_stats_workspace_bytes", "spec_row_stats",
            "spec_status_string", "spec_abi_version", "spec_verify_static", "spec_opd_stats",
-           "spec_verify_opd", "spec_d3d_select", "spec_debug_build", "spec_debug_checks")
+           "spec_verify_opd", "spec_d3d_select", "spec_linear_ce_workspace_bytes",
+           "spec_linear_ce", "spec_linear_ce_grad_workspace_bytes", "spec_linear_ce_grad",
+           "spec_opd_grad", "spec_grad_norm_workspace_bytes", "spec_grad_norm",
+           "spec_clip_grad_norm", "spec_debug_build", "spec_debug_checks")
 SPEC_STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -133,6 +143,22 @@ def lib() -> ctypes.CDLL:
     L.spec_d3d_select.argtypes = [i32p, i32p, i32p, i32p, i32p, ci, ci, ci, ci, i32p, i32p, i32p,
                                   vp]
     L.spec_d3d_select.restype = ci
+    for name in ("spec_linear_ce_workspace_bytes", "spec_linear_ce_grad_workspace_bytes"):
+        getattr(L, name).argtypes = [ci, ci, ci]
+        getattr(L, name).restype = csz
+    L.spec_linear_ce.argtypes = [vp, vp, ci, i32p, ci, ci, ci, f32p, f32p, vp, csz, vp]
+    L.spec_linear_ce.restype = ci
+    L.spec_linear_ce_grad.argtypes = [vp, vp, ci, i32p, f32p, f32p, ci, ci, ci, vp, vp, vp, csz, vp]
+    L.spec_linear_ce_grad.restype = ci
+    L.spec_opd_grad.argtypes = [vp, vp, ci, i32p, f32p, ci, ci, ci, ctypes.c_float, ctypes.c_float,
+                                vp, vp]
+    L.spec_opd_grad.restype = ci
+    L.spec_grad_norm_workspace_bytes.argtypes = [ci]
+    L.spec_grad_norm_workspace_bytes.restype = csz
+    L.spec_grad_norm.argtypes = [vp, vp, vp, ci, f32p, vp, csz, vp]
+    L.spec_grad_norm.restype = ci
+    L.spec_clip_grad_norm.argtypes = [vp, vp, vp, vp, ci, ctypes.c_float, f32p, vp, csz, vp]
+    L.spec_clip_grad_norm.restype = ci
     L.spec_status_string.argtypes = [ci]
     L.spec_status_string.restype = ctypes.c_char_p
     L.spec_abi_version.argtypes = []
@@ -602,6 +628,223 @@ def spec_d3d_select(num_accepted, out_tokens, branch_pos, branch_tok, branch_blo
                                  next_block.data_ptr(), hits.data_ptr(), _stream_ptr(stream)),
            "spec_d3d_select")
     return hit, next_block, hits
+
+
+def _stream_on(stream, device) -> int:
+    """The given stream, or the current one of the tensors' own device."""
+    return _stream_ptr(_torch().cuda.current_stream(device) if stream is None else stream)
+
+
+def _need_cuda(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
+
+
+def _need_workspace(ws, name, nbytes, device):
+    torch = _torch()
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if ws.device != device:
+        raise ValueError(f"{name} is on {ws.device}, expected {device}")
+    if not ws.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return ws
+
+
+class LinearCe:
+    """Cross entropy of a linear vocabulary head and its gradients, bound to fixed buffers.
+
+    ``hidden`` [N, D] and ``weight`` [V, D] bfloat16, ``labels`` int32 [N]
+    (negative: no label), ``grad_nll`` float32 [N] (the loss's derivative by
+    each token's nll; needed for ``grad``).  Like ``Verifier``, the object
+    checks its buffers once and keeps the C calls' arguments; the buffers'
+    contents may change between calls, the tensors must stay alive.
+
+    ``loss()`` fills and returns (nll, lse), ``grad()`` (d_hidden, d_weight)
+    from the lse of the last ``loss()``.  ``need_hidden`` / ``need_weight``
+    False leaves that gradient out (None).  Both calls share one workspace:
+    enqueue them on one stream.
+    """
+
+    def __init__(self, hidden, weight, labels, grad_nll=None, *, nll=None, lse=None, d_hidden=None,
+                 d_weight=None, need_hidden: bool = True, need_weight: bool = True, workspace=None,
+                 stream=None):
+        torch = _torch()
+        N, D = hidden.shape
+        V = weight.shape[0]
+        dev = hidden.device
+        _need_cuda(hidden, "hidden")
+        dt = _dtype_code(hidden)
+        _need(hidden, "hidden", hidden.dtype, (N, D), dev)
+        _need(weight, "weight", hidden.dtype, (V, D), dev)
+        _need(labels, "labels", torch.int32, (N,), dev)
+        if nll is None:
+            nll = torch.empty(N, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(N, dtype=torch.float32, device=dev)
+        _need(nll, "nll", torch.float32, (N,), dev)
+        _need(lse, "lse", torch.float32, (N,), dev)
+        n = int(lib().spec_linear_ce_workspace_bytes(N, V, D))
+        if grad_nll is not None:
+            _need(grad_nll, "grad_nll", torch.float32, (N,), dev)
+            n = max(n, int(lib().spec_linear_ce_grad_workspace_bytes(N, V, D)))
+            if not (need_hidden or need_weight):
+                raise ValueError("grad_nll is given, but neither gradient is wanted")
+            if need_hidden and d_hidden is None:
+                d_hidden = torch.empty_like(hidden)
+            if need_weight and d_weight is None:
+                d_weight = torch.empty_like(weight)
+            if need_hidden:
+                _need(d_hidden, "d_hidden", hidden.dtype, (N, D), dev)
+            if need_weight:
+                _need(d_weight, "d_weight", hidden.dtype, (V, D), dev)
+        # Unsupported sizes (n == 0) reach the library, which says so.
+        ws = _need_workspace(workspace, "workspace", max(n, 256), dev)
+        self._keep = (hidden, weight, labels, grad_nll, ws)
+        self.workspace, self.nll, self.lse = ws, nll, lse
+        self.d_hidden = d_hidden if grad_nll is not None and need_hidden else None
+        self.d_weight = d_weight if grad_nll is not None and need_weight else None
+        st = _stream_on(stream, dev)
+        wsb = ws.numel() * ws.element_size()
+        self._loss = lib().spec_linear_ce
+        self._loss_args = (hidden.data_ptr(), weight.data_ptr(), dt, labels.data_ptr(), N, V, D,
+                           nll.data_ptr(), lse.data_ptr(), ws.data_ptr(), wsb, st)
+        self._grad = lib().spec_linear_ce_grad
+        self._grad_args = None if grad_nll is None else (
+            hidden.data_ptr(), weight.data_ptr(), dt, labels.data_ptr(), lse.data_ptr(),
+            grad_nll.data_ptr(), N, V, D,
+            None if self.d_hidden is None else d_hidden.data_ptr(),
+            None if self.d_weight is None else d_weight.data_ptr(), ws.data_ptr(), wsb, st)
+
+    def loss(self):
+        """Enqueue the loss; returns (nll, lse)."""
+        _check(self._loss(*self._loss_args), "spec_linear_ce")
+        return self.nll, self.lse
+
+    def grad(self):
+        """Enqueue the gradients; returns (d_hidden, d_weight)."""
+        if self._grad_args is None:
+            raise ValueError("LinearCe was made without grad_nll")
+        _check(self._grad(*self._grad_args), "spec_linear_ce_grad")
+        return self.d_hidden, self.d_weight
+
+
+def spec_linear_ce(hidden, weight, labels, *, nll=None, lse=None, workspace=None, stream=None):
+    """Token losses of a linear vocabulary head, without keeping the logits.
+
+    hidden [N, D], weight [V, D] bfloat16 (D a multiple of 8), labels int32
+    [N] (negative: no label, nll 0).  Returns (nll, lse), float32 [N]:
+    lse_i = logsumexp_v(hidden_i . weight_v), nll_i = lse_i - hidden_i .
+    weight_{labels_i}.
+    """
+    return LinearCe(hidden, weight, labels, nll=nll, lse=lse, workspace=workspace,
+                    stream=stream).loss()
+
+
+def spec_linear_ce_grad(hidden, weight, labels, lse, grad_nll, *, d_hidden=None, d_weight=None,
+                        need_hidden: bool = True, need_weight: bool = True, workspace=None,
+                        stream=None):
+    """Gradients of sum_i grad_nll_i nll_i: (d_hidden [N, D], d_weight [V, D]), bfloat16.
+
+    ``lse`` is ``spec_linear_ce``'s on the same inputs; ``grad_nll`` float32 [N].
+    ``need_hidden`` / ``need_weight`` False leaves that gradient out (None).
+    """
+    return LinearCe(hidden, weight, labels, grad_nll, lse=lse, d_hidden=d_hidden,
+                    d_weight=d_weight, need_hidden=need_hidden, need_weight=need_weight,
+                    workspace=workspace, stream=stream).grad()
+
+
+def spec_opd_grad(target_logits, draft_logits, lengths, grad_loss, *, delta: float = 0.01,
+                  alpha: float = 0.8, d_draft=None, stream=None):
+    """Gradient of sum_b grad_loss_b loss_b with respect to the draft logits.
+
+    loss is ``spec_opd_stats``'s mixture loss; target [B, k+1, V], draft [B, k, V]
+    (float32 or bfloat16), lengths int32 [B], grad_loss float32 [B].  Returns
+    ``d_draft`` [B, k, V] of the logits' dtype, 0 past each request's length.
+    """
+    torch = _torch()
+    B, k1, V = target_logits.shape
+    k = k1 - 1
+    dev = lengths.device
+    dt = _dtype_code(target_logits)
+    # Host-resident logits reach the library, which refuses them.
+    _need_logits(target_logits, "target_logits", target_logits.dtype, (B, k + 1, V), dev)
+    _need_logits(draft_logits, "draft_logits", target_logits.dtype, (B, k, V), dev)
+    _need_cuda(lengths, "lengths")
+    _need(lengths, "lengths", torch.int32, (B,), dev)
+    _need(grad_loss, "grad_loss", torch.float32, (B,), dev)
+    if d_draft is None:
+        d_draft = torch.empty((B, k, V), dtype=target_logits.dtype, device=dev)
+    _need(d_draft, "d_draft", target_logits.dtype, (B, k, V), dev)
+    _check(lib().spec_opd_grad(target_logits.data_ptr(), draft_logits.data_ptr(), dt,
+                               lengths.data_ptr(), grad_loss.data_ptr(), B, k, V, float(delta),
+                               float(alpha), d_draft.data_ptr(), _stream_on(stream, dev)),
+           "spec_opd_grad")
+    return d_draft
+
+
+class GradClipper:
+    """``spec_clip_grad_norm`` bound to one fixed set of gradient tensors.
+
+    ``grads``: contiguous float32 / bfloat16 tensors of one device, any shapes;
+    ``out``: tensors of the same shapes and types for the results, or None to
+    scale in place; ``max_norm`` None only takes the norm.  Calling the object
+    enqueues the clip and returns ``norm`` (float32 [1], on the device).
+    """
+
+    def __init__(self, grads, max_norm, *, out=None, norm=None, workspace=None, stream=None):
+        torch = _torch()
+        grads = list(grads)
+        if not grads:
+            raise ValueError("grads is empty")
+        out = None if out is None else list(out)
+        if out is not None and (max_norm is None or len(out) != len(grads)):
+            raise ValueError("out has one tensor for each of grads, and needs a max_norm")
+        dev = grads[0].device
+        _need_cuda(grads[0], "grads[0]")
+        for i, g in enumerate(grads):
+            _need(g, f"grads[{i}]", g.dtype, g.shape, dev)
+            if out is not None:
+                _need(out[i], f"out[{i}]", g.dtype, g.shape, dev)
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=dev)
+        _need(norm, "norm", torch.float32, (1,), dev)
+        m = len(grads)
+        n = int(lib().spec_grad_norm_workspace_bytes(m))
+        ws = _need_workspace(workspace, "workspace", max(n, 256), dev)
+        self._keep = (grads, out, ws)
+        self.norm, self.workspace = norm, ws
+        ptrs = (ctypes.c_void_p * m)(*[g.data_ptr() or None for g in grads])
+        outs = None if out is None else (ctypes.c_void_p * m)(*[t.data_ptr() or None for t in out])
+        sizes = (ctypes.c_longlong * m)(*[g.numel() for g in grads])
+        codes = (ctypes.c_int * m)(*[_dtype_code(g) for g in grads])
+        tail = (norm.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                _stream_on(stream, dev))
+        if max_norm is None:
+            self._fn, self._name = lib().spec_grad_norm, "spec_grad_norm"
+            self._args = (ptrs, sizes, codes, m) + tail
+        else:
+            self._fn, self._name = lib().spec_clip_grad_norm, "spec_clip_grad_norm"
+            self._args = (ptrs, outs, sizes, codes, m, float(max_norm)) + tail
+
+    def __call__(self):
+        """Enqueue on the bound stream; returns the norm before clipping."""
+        _check(self._fn(*self._args), self._name)
+        return self.norm
+
+
+def spec_grad_norm(grads, *, norm=None, workspace=None, stream=None):
+    """Global norm sqrt(sum x^2) over all entries of ``grads`` (float32 [1], on the device)."""
+    return GradClipper(grads, None, norm=norm, workspace=workspace, stream=stream)()
+
+
+def spec_clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stream=None):
+    """Scale ``grads`` by min(1, max_norm / norm), in place or into ``out``; returns the norm.
+
+    A norm that is infinite or NaN (because an entry is) leaves every value as it is.
+    """
+    return GradClipper(grads, max_norm, out=out, norm=norm, workspace=workspace,
+                       stream=stream)()
 
 
 def to_device(inputs, device="cuda"):

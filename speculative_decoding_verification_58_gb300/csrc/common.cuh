@@ -769,6 +769,9 @@ enum SpecDebugSite {
   kSiteOpdRow = 10,       // OPD statistics: logit row < rows of its buffer
   kSiteOpdOut = 11,       // OPD statistics: output element < B k
   kSiteD3d = 12,          // D3D selection: branch slot < branches
+  kSiteOpdGradRow = 13,   // OPD gradient: logit row < rows of the draft buffer
+  kSiteLinearCe = 14,     // linear cross entropy: logit column, label or gradient element
+  kSiteNormUnit = 15,     // gradient norm: tensor of a unit < tensors
 };
 
 __device__ int g_debug_failures;  // checks that failed since the last reset

@@ -9,11 +9,15 @@
 
 #include <algorithm>
 #include <mutex>
+#include <vector>
 
 #include "common.cuh"
 #include "d3d.cuh"
 #include "final.cuh"
+#include "grad_norm.cuh"
+#include "linear_ce.cuh"
 #include "opd.cuh"
+#include "opd_grad.cuh"
 #include "plan.cuh"
 #include "sweep.cuh"
 
@@ -1025,3 +1029,5 @@ extern "C" spec_status_t spec_verify_static(const void* target_logits, const voi
                                 temperature, B, k, V, out_tokens, num_accepted, scratch, s, 0u, 1,
                                 nullptr, nullptr, nullptr, 0, 0, direct);
 }
+
+#include "train_api.cuh"

@@ -1,0 +1,381 @@
+// C entry points of the drafter-training operators: argument checks and launches.
+#pragma once
+
+namespace specv {
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na != 0 && nb != 0 && x < y + nb && y < x + na;
+}
+
+// ---------------------------------------------------------------------------
+// Linear cross entropy.
+// ---------------------------------------------------------------------------
+
+inline bool ce_sizes_ok(int N, int V, int D) {
+  return N <= kCeMaxTokens && V <= SPEC_MAX_V && D <= kCeMaxWidth && D % 8 == 0;
+}
+
+template <CeMode M>
+cudaError_t launch_ce_gemm(const CeParams& p, cudaStream_t stream) {
+  const int rows = M == kCeDw ? p.nv : p.N;
+  const int cols = M == kCeLoss ? p.V : M == kCeDz ? p.nv : p.D;
+  return launch(ce_gemm_kernel<M>, dim3((cols + 63) / 64, (rows + 63) / 64), dim3(256), 0, stream,
+                false, p);
+}
+
+inline CeParams ce_params(const void* hidden, const void* weight, const int32_t* labels, int N,
+                          int V, int D, const CeLayout& lay, unsigned char* ws) {
+  CeParams p = {};
+  p.h = static_cast<const uint16_t*>(hidden);
+  p.w = static_cast<const uint16_t*>(weight);
+  p.labels = labels;
+  p.N = N;
+  p.V = V;
+  p.D = D;
+  p.tiles = lay.tiles;
+  p.partials = reinterpret_cast<float2*>(ws + lay.partials);
+  p.z_label = reinterpret_cast<float*>(ws + lay.z_label);
+  p.dz = reinterpret_cast<uint16_t*>(ws + lay.dz);
+  p.piece = lay.piece;
+  p.dh_acc = reinterpret_cast<float*>(ws + lay.dh_acc);
+  return p;
+}
+
+inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32_t* labels, int N,
+                             int V, int D, float* nll, float* lse, unsigned char* ws,
+                             cudaStream_t s) {
+  NvtxRange r("spec_linear_ce");
+  const CeLayout lay = ce_layout(N, V, D, false);
+  const CeParams p = ce_params(hidden, weight, labels, N, V, D, lay, ws);
+  if (launch(ce_check_kernel, dim3(1), dim3(256), 0, s, false, reinterpret_cast<WsHeader*>(ws),
+             labels, N, V) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (launch_ce_gemm<kCeLoss>(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (launch(ce_finish_kernel, dim3((N + 7) / 8), dim3(256), 0, s, false, p, nll, lse) !=
+      cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return SPEC_OK;
+}
+
+inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32_t* labels,
+                             const float* lse, const float* grad_nll, int N, int V, int D,
+                             void* d_hidden, void* d_weight, unsigned char* ws, cudaStream_t s) {
+  NvtxRange r("spec_linear_ce_grad");
+  const CeLayout lay = ce_layout(N, V, D, true);
+  CeParams p = ce_params(hidden, weight, labels, N, V, D, lay, ws);
+  p.lse = lse;
+  p.g = grad_nll;
+  p.dw = static_cast<uint16_t*>(d_weight);
+  if (launch(ce_check_kernel, dim3(1), dim3(256), 0, s, false, reinterpret_cast<WsHeader*>(ws),
+             labels, N, V) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  for (int v0 = 0; v0 < V; v0 += lay.piece) {
+    p.v0 = v0;
+    p.nv = std::min(lay.piece, V - v0);
+    p.first = v0 == 0;
+    if (launch_ce_gemm<kCeDz>(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    if (d_hidden != nullptr && launch_ce_gemm<kCeDh>(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    if (d_weight != nullptr && launch_ce_gemm<kCeDw>(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  }
+  if (d_hidden != nullptr) {
+    const long long n = (long long)N * D;
+    if (launch(ce_round_kernel, dim3((unsigned)std::min<long long>((n + 255) / 256, 2048)),
+               dim3(256), 0, s, false, (const float*)p.dh_acc, static_cast<uint16_t*>(d_hidden),
+               n) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+  }
+  return SPEC_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Mixture-loss gradient.
+// ---------------------------------------------------------------------------
+
+// CTAs per position: one per 4096 entries of a row, up to the cluster limit.
+inline int opd_grad_cluster(int V) {
+  int cs = 1;
+  while (cs < kOgMaxCluster && (long long)cs * 4096 < V) cs *= 2;
+  return cs;
+}
+
+template <typename TIn>
+spec_status_t opd_grad_typed(OpdGradParams p, cudaStream_t stream) {
+  NvtxRange r("spec_opd_grad");
+  const int cs = opd_grad_cluster(p.V);
+  p.slice = (((p.V + cs - 1) / cs) + 7) & ~7;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)p.B * p.k * cs));
+  cfg.blockDim = dim3(kOgThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, opd_grad_kernel<TIn>, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping.
+// ---------------------------------------------------------------------------
+
+constexpr int kNormMaxTensors = 1 << 20;
+constexpr int kNormMaxCtas = 1024;  // partials a launch may leave, whatever the device
+
+inline size_t grad_norm_ws(int count) {
+  const size_t launches = ((size_t)count + kNormTensors - 1) / kNormTensors;
+  return align256(launches * kNormMaxCtas * sizeof(NormPartial));
+}
+
+inline spec_status_t norm_run(const void* const* grads, void* const* outs, const long long* sizes,
+                              const int* dtypes, int count, float max_norm, float* norm,
+                              void* workspace, cudaStream_t s, bool clip) {
+  NvtxRange r(clip ? "spec_clip_grad_norm" : "spec_grad_norm");
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != cudaSuccess) return SPEC_ERR_CUDA;
+  NormPartial* partials = static_cast<NormPartial*>(workspace);
+  int parts = 0;
+  NormBatch batch;
+  const int most = std::min(kNormMaxCtas, d->sms * kNormCtasPerSm);
+  for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
+    int t = 0;
+    do {  // batches of tensors that are not empty; the norm of nothing is 0
+      batch.count = 0;
+      long long units = 0;
+      for (; t < count && batch.count < kNormTensors; ++t) {
+        if (sizes[t] == 0) continue;
+        const int c = batch.count;
+        const int es = dtypes[t] == SPEC_BF16 ? 2 : 4;
+        void* out = clip ? (outs != nullptr ? outs[t] : const_cast<void*>(grads[t])) : nullptr;
+        const long long u = norm_units(grads[t], out, sizes[t], es);
+        batch.in[c] = grads[t];
+        batch.out[c] = out;
+        batch.n[c] = sizes[t];
+        batch.bf16[c] = es == 2;
+        batch.first_unit[c] = (int)units;
+        units += u;
+        batch.first_unit[++batch.count] = (int)units;
+      }
+      if (batch.count == 0) batch.first_unit[0] = 0;
+      const int grid = (int)std::max<long long>(1, std::min<long long>(units, most));
+      if (pass == 0) {
+        if (launch(grad_norm_kernel, dim3(grid), dim3(kNormThreads), 0, s, true, batch,
+                   partials + parts) != cudaSuccess)
+          return SPEC_ERR_CUDA;
+        parts += grid;
+      } else if (launch(clip_kernel, dim3(grid), dim3(kNormThreads), 0, s, true, batch,
+                        (const NormPartial*)partials, parts, max_norm, norm) != cudaSuccess) {
+        return SPEC_ERR_CUDA;
+      }
+    } while (t < count);
+  }
+  if (!clip && launch(grad_norm_finish_kernel, dim3(1), dim3(32), 0, s, true,
+                      (const NormPartial*)partials, parts, norm) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return SPEC_OK;
+}
+
+// The byte ranges of a clip's tensors: no output may share a byte with another
+// tensor's input or output (its own input, exactly, is the in-place form).
+inline bool norm_ranges_ok(const void* const* grads, void* const* outs, const long long* sizes,
+                           const int* dtypes, int count) {
+  struct Range {
+    uintptr_t a, b;
+    int t;
+    bool out;
+  };
+  std::vector<Range> rs;
+  rs.reserve(2 * (size_t)count);
+  for (int t = 0; t < count; ++t) {
+    if (sizes[t] == 0) continue;
+    const size_t bytes = (size_t)sizes[t] * (dtypes[t] == SPEC_BF16 ? 2 : 4);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(grads[t]);
+    const uintptr_t o = outs != nullptr ? reinterpret_cast<uintptr_t>(outs[t]) : a;
+    rs.push_back({o, o + bytes, t, true});
+    if (o != a) rs.push_back({a, a + bytes, t, false});
+  }
+  std::sort(rs.begin(), rs.end(), [](const Range& x, const Range& y) { return x.a < y.a; });
+  // Inputs may share bytes among themselves; an output with nothing.
+  uintptr_t end_any = 0, end_out = 0;
+  for (const Range& r : rs) {
+    if (r.a < (r.out ? end_any : end_out)) return false;
+    end_any = std::max(end_any, r.b);
+    if (r.out) end_out = std::max(end_out, r.b);
+  }
+  return true;
+}
+
+inline spec_status_t norm_entry(const void* const* grads, void* const* outs,
+                                const long long* sizes, const int* dtypes, int count,
+                                float max_norm, float* norm, void* workspace,
+                                size_t workspace_bytes, void* stream, bool clip) {
+  if (count < 1 || !grads || !sizes || !dtypes || !norm || !aligned(norm, 4))
+    return SPEC_ERR_INVALID_ARG;
+  if (count > kNormMaxTensors) return SPEC_ERR_UNSUPPORTED;
+  if (clip && !(max_norm > 0.0f && max_norm <= FLT_MAX)) return SPEC_ERR_INVALID_ARG;
+  long long units = 0;
+  for (int t = 0; t < count; ++t) {
+    if (dtypes[t] != SPEC_F32 && dtypes[t] != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+    if (sizes[t] < 0) return SPEC_ERR_INVALID_ARG;
+    if (sizes[t] > (1LL << 40)) return SPEC_ERR_UNSUPPORTED;
+    const size_t es = dtypes[t] == SPEC_F32 ? 4 : 2;
+    if (sizes[t] > 0 && (!grads[t] || !aligned(grads[t], es))) return SPEC_ERR_INVALID_ARG;
+    if (sizes[t] > 0 && outs != nullptr && (!outs[t] || !aligned(outs[t], es)))
+      return SPEC_ERR_INVALID_ARG;
+    units += norm_units(grads[t], outs != nullptr ? outs[t] : nullptr, sizes[t], (int)es);
+    if (sizes[t] > 0 && overlap(norm, 4, grads[t], (size_t)sizes[t] * es))
+      return SPEC_ERR_INVALID_ARG;
+    if (sizes[t] > 0 && outs != nullptr && overlap(norm, 4, outs[t], (size_t)sizes[t] * es))
+      return SPEC_ERR_INVALID_ARG;
+  }
+  if (units > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+  try {  // the check sorts ranges in host memory it allocates
+    if (clip && !norm_ranges_ok(grads, outs, sizes, dtypes, count)) return SPEC_ERR_INVALID_ARG;
+  } catch (...) {
+    return SPEC_ERR_INTERNAL;
+  }
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < grad_norm_ws(count))
+    return SPEC_ERR_WORKSPACE;
+  DeviceOf on_device(norm);
+  if (!on_device.ok()) return SPEC_ERR_CUDA;
+  return norm_run(grads, outs, sizes, dtypes, count, max_norm, norm, workspace,
+                  static_cast<cudaStream_t>(stream), clip);
+}
+
+}  // namespace specv
+
+extern "C" {
+
+size_t spec_linear_ce_workspace_bytes(int N, int V, int D) {
+  if (N < 1 || V < 1 || D < 1 || !ce_sizes_ok(N, V, D)) return 0;
+  return ce_layout(N, V, D, false).total;
+}
+
+size_t spec_linear_ce_grad_workspace_bytes(int N, int V, int D) {
+  if (N < 1 || V < 1 || D < 1 || !ce_sizes_ok(N, V, D)) return 0;
+  return ce_layout(N, V, D, true).total;
+}
+
+spec_status_t spec_linear_ce(const void* hidden, const void* weight, spec_dtype_t dtype,
+                             const int32_t* labels, int N, int V, int D, float* nll, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (N < 1 || V < 1 || D < 1) return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_BF16 || !ce_sizes_ok(N, V, D)) return SPEC_ERR_UNSUPPORTED;
+  if (!hidden || !weight || !labels || !nll || !lse) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(labels, 4) || !aligned(nll, 4) ||
+      !aligned(lse, 4))
+    return SPEC_ERR_INVALID_ARG;
+  const size_t n4 = (size_t)N * 4, nh = (size_t)N * D * 2, nw = (size_t)V * D * 2;
+  for (const void* o : {(const void*)nll, (const void*)lse})
+    if (overlap(o, n4, hidden, nh) || overlap(o, n4, weight, nw) || overlap(o, n4, labels, n4))
+      return SPEC_ERR_INVALID_ARG;
+  if (overlap(nll, n4, lse, n4)) return SPEC_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < spec_linear_ce_workspace_bytes(N, V, D))
+    return SPEC_ERR_WORKSPACE;
+  DeviceOf on_device(weight);
+  if (!on_device.ok()) return SPEC_ERR_CUDA;
+  return ce_loss(hidden, weight, labels, N, V, D, nll, lse, static_cast<unsigned char*>(workspace),
+                 static_cast<cudaStream_t>(stream));
+}
+
+spec_status_t spec_linear_ce_grad(const void* hidden, const void* weight, spec_dtype_t dtype,
+                                  const int32_t* labels, const float* lse, const float* grad_nll,
+                                  int N, int V, int D, void* d_hidden, void* d_weight,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (N < 1 || V < 1 || D < 1) return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_BF16 || !ce_sizes_ok(N, V, D)) return SPEC_ERR_UNSUPPORTED;
+  if (!hidden || !weight || !labels || !lse || !grad_nll || (!d_hidden && !d_weight))
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(labels, 4) || !aligned(lse, 4) ||
+      !aligned(grad_nll, 4) || !aligned(d_hidden, 16) || !aligned(d_weight, 16))
+    return SPEC_ERR_INVALID_ARG;
+  const size_t n4 = (size_t)N * 4, nh = (size_t)N * D * 2, nw = (size_t)V * D * 2;
+  const void* outs[2] = {d_hidden, d_weight};
+  const size_t out_bytes[2] = {d_hidden ? nh : 0, d_weight ? nw : 0};
+  for (int o = 0; o < 2; ++o)
+    if (overlap(outs[o], out_bytes[o], hidden, nh) || overlap(outs[o], out_bytes[o], weight, nw) ||
+        overlap(outs[o], out_bytes[o], labels, n4) || overlap(outs[o], out_bytes[o], lse, n4) ||
+        overlap(outs[o], out_bytes[o], grad_nll, n4))
+      return SPEC_ERR_INVALID_ARG;
+  if (overlap(d_hidden, out_bytes[0], d_weight, out_bytes[1])) return SPEC_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < spec_linear_ce_grad_workspace_bytes(N, V, D))
+    return SPEC_ERR_WORKSPACE;
+  DeviceOf on_device(weight);
+  if (!on_device.ok()) return SPEC_ERR_CUDA;
+  return ce_grad(hidden, weight, labels, lse, grad_nll, N, V, D, d_hidden, d_weight,
+                 static_cast<unsigned char*>(workspace), static_cast<cudaStream_t>(stream));
+}
+
+spec_status_t spec_opd_grad(const void* target_logits, const void* draft_logits,
+                            spec_dtype_t dtype, const int32_t* lengths, const float* grad_loss,
+                            int B, int k, int V, float delta, float alpha, void* d_draft,
+                            void* stream) {
+  if (B < 1 || k < 1 || V < 1) return SPEC_ERR_INVALID_ARG;
+  if (!sizes_ok(B, k, V)) return SPEC_ERR_UNSUPPORTED;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (!(delta > 0.0f && delta <= FLT_MAX) || !(alpha >= 0.0f && alpha <= 1.0f))
+    return SPEC_ERR_INVALID_ARG;
+  if (!target_logits || !draft_logits || !lengths || !grad_loss || !d_draft)
+    return SPEC_ERR_INVALID_ARG;
+  const size_t es = dtype == SPEC_F32 ? 4 : 2;
+  if (!aligned(target_logits, es) || !aligned(draft_logits, es) || !aligned(lengths, 4) ||
+      !aligned(grad_loss, 4) || !aligned(d_draft, es))
+    return SPEC_ERR_INVALID_ARG;
+  const size_t nd = (size_t)B * k * V * es, nt = (size_t)B * (k + 1) * V * es;
+  if (overlap(d_draft, nd, draft_logits, nd) || overlap(d_draft, nd, target_logits, nt) ||
+      overlap(d_draft, nd, lengths, (size_t)B * 4) || overlap(d_draft, nd, grad_loss, (size_t)B * 4))
+    return SPEC_ERR_INVALID_ARG;
+  {
+    bool direct = false;
+    const void* t = target_logits;
+    const void* d = draft_logits;
+    if (!resolve_logits(&t, &d, &direct) || direct) return SPEC_ERR_INVALID_ARG;
+  }
+  DeviceOf on_device(target_logits);
+  if (!on_device.ok()) return SPEC_ERR_CUDA;
+  OpdGradParams p = {};
+  p.target = target_logits;
+  p.draft = draft_logits;
+  p.lengths = lengths;
+  p.grad_loss = grad_loss;
+  p.out = d_draft;
+  p.B = B;
+  p.k = k;
+  p.V = V;
+  p.vec_ok = aligned(target_logits, 16) && aligned(draft_logits, 16) && aligned(d_draft, 16) &&
+             ((size_t)V * es) % 16 == 0;
+  p.delta = delta;
+  p.alpha = alpha;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == SPEC_F32 ? opd_grad_typed<float>(p, s) : opd_grad_typed<uint16_t>(p, s);
+}
+
+size_t spec_grad_norm_workspace_bytes(int count) {
+  if (count < 1 || count > kNormMaxTensors) return 0;
+  return grad_norm_ws(count);
+}
+
+spec_status_t spec_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes,
+                             int count, float* norm, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  return norm_entry(grads, nullptr, sizes, dtypes, count, 0.0f, norm, workspace, workspace_bytes,
+                    stream, false);
+}
+
+spec_status_t spec_clip_grad_norm(const void* const* grads, void* const* outs,
+                                  const long long* sizes, const int* dtypes, int count,
+                                  float max_norm, float* norm, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return norm_entry(grads, outs, sizes, dtypes, count, max_norm, norm, workspace, workspace_bytes,
+                    stream, true);
+}
+
+}  // extern "C"

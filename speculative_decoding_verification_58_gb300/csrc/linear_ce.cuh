@@ -14,24 +14,37 @@
 #pragma once
 
 #include "grad_norm.cuh"
+#include "tcgen05.cuh"
 
 namespace specv {
 
-constexpr int kCeTileV = 64;       // vocabulary entries per (max, sum) pair
-constexpr int kCePiece = 8192;     // vocabulary entries per piece of the gradients
-constexpr int kCeMaxTokens = 1 << 18;
-constexpr int kCeMaxWidth = 1 << 15;
+constexpr int kCeTileV = 256;      // vocabulary entries per (max, sum) pair
+constexpr int kCePieceBytes = 48 << 20;  // most bytes of a piece's dZ
+constexpr int kCeMaxTokens = SPEC_MAX_TOKENS;
+constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
 
 struct CeLayout {
-  size_t header, partials, z_label, dz, dh_acc, total;
-  int tiles;     // vocabulary tiles
-  int piece;     // vocabulary entries per piece (a multiple of kCeTileV)
+  size_t partials, z_label, dz, dh_acc, total;
+  int tiles;  // vocabulary tiles
+  int piece;   // vocabulary entries per piece (a multiple of kCeTileV)
+  int splits;  // slices of a piece whose parts of dH are summed apart
+  bool direct;  // dH comes out of one tile whole: no sums to keep
 };
+
+// Slices of the piece's entries that dH = dZ W is summed over: one unless the
+// output has too few 128 x 256 tiles for the SMs (two for each of 152 are aimed
+// at), and no shorter than 16 steps of 64 entries.
+inline int ce_splits(int N, int D, int piece) {
+  const long long tiles = (long long)((N + 127) / 128) * ((D + 255) / 256);
+  const long long want = (304 + tiles - 1) / tiles, most = piece / (16 * 64);
+  return (int)std::max<long long>(1, std::min(want, most));
+}
 
 inline CeLayout ce_layout(int N, int V, int D, bool grad) {
   CeLayout l = {};
   l.tiles = (V + kCeTileV - 1) / kCeTileV;
-  l.piece = (int)std::min<long long>(kCePiece, (long long)l.tiles * kCeTileV);
+  const long long fit = kCePieceBytes / 2 / N / kCeTileV;  // tiles whose dZ fits
+  l.piece = (int)std::max<long long>(1, std::min<long long>(l.tiles, fit)) * kCeTileV;
   size_t o = align256(sizeof(WsHeader));
   if (!grad) {
     l.partials = o;
@@ -41,174 +54,462 @@ inline CeLayout ce_layout(int N, int V, int D, bool grad) {
   } else {
     l.dz = o;
     o = align256(o + (size_t)N * l.piece * 2);
+    l.splits = ce_splits(N, D, l.piece);
+    l.direct = l.splits == 1 && l.piece >= V;
     l.dh_acc = o;
-    o = align256(o + (size_t)N * D * sizeof(float));
+    if (!l.direct) o = align256(o + (size_t)l.splits * N * D * sizeof(float));
   }
   l.total = o;
   return l;
 }
 
 struct CeParams {
-  const uint16_t* h;       // [N, D]
-  const uint16_t* w;       // [V, D]
   const int32_t* labels;   // [N]
   const float* lse;        // [N] (gradients)
   const float* g;          // [N] (gradients)
   int N, V, D, tiles;
-  float2* partials;        // [N, tiles]
+  float2* partials;        // [tiles, N]: (max log2 e, sum 2^(z log2 e - max log2 e))
   float* z_label;          // [N]
   uint16_t* dz;            // [N, piece]
   int piece, v0, nv;       // piece: buffer width, first entry, entries
-  float* dh_acc;           // [N, D]
+  float* dh_acc;           // [splits, N, D]
+  uint16_t* dh;            // [N, D], where it comes out of one tile whole (else null)
   uint16_t* dw;            // [V, D]
   int first;               // first piece: dh_acc is set, not added to
+  int splits, split_iters;  // slices of the piece in dH, 64-entry steps of a slice
+  int dh_units, dw_units;  // units of the two products (0: not wanted)
+  int check;               // CTA 0 checks the labels and writes the header
+  WsHeader* header;
 };
 
-enum CeMode { kCeLoss, kCeDz, kCeDh, kCeDw };
+// ---------------------------------------------------------------------------
+// The products.  A persistent kernel, one CTA per SM, on tiles of 128 x 256: a
+// warp that issues the TMA loads into a ring of four 64-deep stages, a warp that
+// issues the tcgen05.mma, and four warps that take finished tiles out of
+// tensor memory, where two accumulators of 256 columns alternate, so that one
+// tile's epilogue runs under the next one's products.
+//   loss   z  = H W^T          both operands K-major
+//   dz     z  = H W^T          the piece's columns
+//   grads  dH = dZ W           A K-major, B MN-major  (K: the piece's entries)
+//          dW = dZ^T H         A and B MN-major       (K: the tokens)
+// ---------------------------------------------------------------------------
+enum CeMode { kCeLoss, kCeDz, kCeGrads };
 
-// C[m][n] = sum_k A[m][k] B[n][k] on 64 x 64 tiles, one 4 x 4 block per thread.
-template <CeMode M>
-__global__ void __launch_bounds__(256) ce_gemm_kernel(CeParams p) {
-  constexpr int BM = 64, BN = 64, BK = 16;
-  __shared__ float sa[BK][BM + 4], sb[BK][BN + 4];
-  const int rows = M == kCeDw ? p.nv : p.N;
-  const int cols = M == kCeLoss ? p.V : M == kCeDz ? p.nv : p.D;
-  const int K = M == kCeDh ? p.nv : M == kCeDw ? p.N : p.D;
-  const int m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += BK) {
-    for (int l = threadIdx.x; l < BM * BK; l += 256) {
-      const int kk = (M == kCeDw) ? l / BM : l % BK, mm = (M == kCeDw) ? l % BM : l / BK;
-      const int m = m0 + mm, k = k0 + kk;
-      float x = 0.0f;
-      if (m < rows && k < K) {
-        if (M == kCeLoss || M == kCeDz) x = bf16_to_f32(p.h[(size_t)m * p.D + k]);
-        if (M == kCeDh) x = bf16_to_f32(p.dz[(size_t)m * p.piece + k]);
-        if (M == kCeDw) x = bf16_to_f32(p.dz[(size_t)k * p.piece + m]);
-      }
-      sa[kk][mm] = x;
-    }
-    for (int l = threadIdx.x; l < BN * BK; l += 256) {
-      const bool kfast = M == kCeLoss || M == kCeDz;
-      const int kk = kfast ? l % BK : l / BN, nn = kfast ? l / BK : l % BN;
-      const int n = n0 + nn, k = k0 + kk;
-      float x = 0.0f;
-      if (n < cols && k < K) {
-        if (kfast) x = bf16_to_f32(p.w[(size_t)(p.v0 + n) * p.D + k]);
-        if (M == kCeDh) x = bf16_to_f32(p.w[(size_t)(p.v0 + k) * p.D + n]);
-        if (M == kCeDw) x = bf16_to_f32(p.h[(size_t)k * p.D + n]);
-      }
-      sb[kk][nn] = x;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < BK; ++kk) {
-      float a[4], b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = sa[kk][ty * 4 + j];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = sb[kk][tx + 16 * j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
+constexpr int kMmM = 128, kMmN = 256, kMmK = 64, kMmStages = 4;
+constexpr int kMmABytes = kMmM * kMmK * 2, kMmBBytes = kMmN * kMmK * 2;
+constexpr int kMmStageBytes = kMmABytes + kMmBBytes;
+constexpr int kMmThreads = 192;
+constexpr int kMmProducer = 0, kMmIssuer = 1, kMmEpilogue = 2;  // first warps of the roles
+constexpr int kMmSmem = kMmStages * kMmStageBytes + 1024;       // + alignment
+
+struct CeMaps {
+  CUtensorMap h_k, w_k;            // boxes of 64 x 128 / 64 x 256: rows of hidden, of weight
+  CUtensorMap dz_k;                // 64 x 128: rows of dZ
+  CUtensorMap h_mn, w_mn, dz_mn;   // 64 x 64
+};
+
+struct CeBars {
+  uint64_t full[kMmStages], empty[kMmStages], tfull[2], tempty[2];
+  uint32_t tmem;
+  int abort_flag;
+  int bad;  // labels outside the vocabulary
+};
+
+struct CeTile {
+  int kind;  // 0: z, 1: dH, 2: dW
+  int m0, n0;
+  int k0, iters;  // first entry of the sum, steps of kMmK
+  int slice;      // dH: which of the sums kept apart
+};
+
+// Units of dH and dW over the CTAs.  A unit of dH costs split_iters steps, one of
+// dW as many as the tokens need, each some more for its epilogue.  The units of dH
+// go round, so that the first `more` CTAs have one more of them; dW's are dealt to
+// bring every CTA up to the same level, and those that are left go round.
+// Returns the index of CTA c's i-th unit, dH's first; -1: no more.
+constexpr int kCeEpilogueSteps = 6;  // an epilogue's time, in steps
+__host__ __device__ inline long long ce_unit(int dh_units, int dw_units, int dh_iters, int dw_iters,
+                                             int G, int c, int i) {
+  const int h = dh_units / G, more = dh_units % G, less = G - more;
+  const int mine = h + (c < more ? 1 : 0);
+  if (i < mine) return (long long)i * G + c;
+  int j = i - mine;
+  const long long ch = dh_iters + kCeEpilogueSteps, cw = dw_iters + kCeEpilogueSteps;
+  const long long level = ((long long)dh_units * ch + (long long)dw_units * cw) / G;
+  // dW units that fit under the level: w1 for each of the first `more` CTAs, w0
+  // for each of the others.
+  long long w0 = level > h * ch ? (level - h * ch) / cw : 0;
+  if (w0 > dw_units / less) w0 = dw_units / less;
+  long long w1 = more > 0 && level > (h + 1) * ch ? (level - (h + 1) * ch) / cw : 0;
+  if (more > 0 && w1 > (dw_units - w0 * less) / more) w1 = (dw_units - w0 * less) / more;
+  if (c >= more) {
+    if (j < w0) return dh_units + (long long)j * less + (c - more);
+    j -= (int)w0;
+  } else {
+    if (j < w1) return dh_units + w0 * less + (long long)j * more + c;
+    j -= (int)w1;
   }
+  const long long idx = w0 * less + w1 * more + (long long)j * G + (G - 1 - c);
+  return idx < dw_units ? dh_units + idx : -1;
+}
+
+// This CTA's tiles: which is the i-th (kind -1: no more).
+template <CeMode M>
+__device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
+  CeTile t;
+  t.kind = -1;
+  t.k0 = t.slice = 0;
+  if (M != kCeGrads) {
+    // Token blocks fastest: a vocabulary tile is read once from memory, and by
+    // the other token blocks from L2.
+    const int cols = M == kCeLoss ? p.V : p.nv;
+    const int mb = (p.N + kMmM - 1) / kMmM, nb = (cols + kMmN - 1) / kMmN;
+    const long long idx = (long long)i * gridDim.x + blockIdx.x;
+    if (idx >= (long long)mb * nb) return t;
+    t.kind = 0;
+    t.m0 = (int)(idx % mb) * kMmM;
+    t.n0 = (int)(idx / mb) * kMmN;
+    t.iters = (p.D + kMmK - 1) / kMmK;
+  } else {
+    const int dw_iters = (p.N + kMmK - 1) / kMmK;
+    const long long idx = ce_unit(p.dh_units, p.dw_units, p.split_iters, dw_iters, gridDim.x,
+                                  blockIdx.x, i);
+    if (idx < 0) return t;
+    const int nb = (p.D + kMmN - 1) / kMmN;
+    const bool dh = idx < p.dh_units;
+    int j = (int)(dh ? idx : idx - p.dh_units);
+    t.kind = dh ? 1 : 2;
+    if (dh) {
+      t.slice = j % p.splits;
+      j /= p.splits;
+      t.k0 = t.slice * p.split_iters * kMmK;
+      const int left = (p.nv - t.k0 + kMmK - 1) / kMmK;
+      t.iters = min(p.split_iters, max(left, 0));
+    } else {
+      t.iters = dw_iters;
+    }
+    t.m0 = j / nb * kMmM;
+    t.n0 = j % nb * kMmN;
+  }
+  return t;
+}
+
+// Epilogue of one thread: row `m` of the tile, 256 columns of tensor memory.
+__device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, uint32_t addr,
+                                            int m) {
+  const bool live = m < p.N;
+  const int y = live ? __ldg(&p.labels[m]) : -1;
+  const int cols = min(kMmN, p.V - t.n0);
+  // Below every logit: a tile of -inf keeps a finite maximum and a sum of 0.
+  float ms = -FLT_MAX / 2, s = 0.0f;
+  for (int c0 = 0; c0 < cols; c0 += 32) {
+    float x[32];
+    tmem_load32(addr + c0, x);
+    if (c0 + 32 > cols) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + ty * 4 + i;
-    if (M == kCeLoss) {
-      // The 16 threads of a row: one (max, sum) pair of the tile.
-      float mx = -INFINITY;
+      for (int c = 0; c < 32; ++c)
+        if (c0 + c >= cols) x[c] = -INFINITY;
+    }
+    const int rel = y - t.n0 - c0;
+    if (__any_sync(0xffffffffu, rel >= 0 && rel < 32)) {
+      float z = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n0 + tx + 16 * j < cols) mx = fmaxf(mx, acc[i][j]);
-      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      float s = 0.0f;
+      for (int c = 0; c < 32; ++c)
+        if (c == rel) z = x[c];
+      if (rel >= 0 && rel < 32) p.z_label[SPEC_CHECKED(m, p.N, kSiteLinearCe)] = z;
+    }
+    float mx = x[0];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n0 + tx + 16 * j < cols) s += ex2((acc[i][j] - mx) * kLog2e);
-      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (m < rows) {
-        if (tx == 0) p.partials[(size_t)m * p.tiles + blockIdx.x] = make_float2(mx, s);
-        const int y = p.labels[m];
+    for (int c = 1; c < 32; ++c) mx = fmaxf(mx, x[c]);
+    const float nms = fmaxf(ms, __fmul_rn(mx, kLog2e));
+    float2 a[2] = {make_float2(__fmul_rn(s, ex2(__fsub_rn(ms, nms))), 0.0f),
+                   make_float2(0.0f, 0.0f)};
+    const float2 l2 = make_float2(kLog2e, kLog2e), mm = make_float2(-nms, -nms);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n0 + tx + 16 * j == y) p.z_label[m] = acc[i][j];
+    for (int c = 0; c < 32; c += 2)
+      a[(c >> 1) & 1] =
+          f32x2_add(a[(c >> 1) & 1], ex2x2(f32x2_fma(make_float2(x[c], x[c + 1]), l2, mm)));
+    const float2 r = f32x2_add(a[0], a[1]);
+    s = __fadd_rn(r.x, r.y);
+    ms = nms;
+  }
+  if (live) p.partials[(size_t)(t.n0 / kMmN) * p.N + m] = make_float2(ms, s);
+}
+
+__device__ __forceinline__ void ce_dz_row(const CeParams& p, const CeTile& t, uint32_t addr,
+                                          int m) {
+  const bool live = m < p.N;
+  int y = live ? __ldg(&p.labels[m]) : -1;
+  const bool has = y >= 0 && y < p.V;
+  const float g = has ? __ldg(&p.g[m]) : 0.0f;
+  const float l2 = has ? __fmul_rn(__ldg(&p.lse[m]), kLog2e) : 0.0f;
+  y -= p.v0 + t.n0;
+  const int cols = min(kMmN, p.nv - t.n0);
+  uint16_t* out = p.dz + (size_t)SPEC_CHECKED(live ? m : 0, p.N, kSiteLinearCe) * p.piece + t.n0;
+  // The buffer's rows hold whole tiles: columns past the piece are written too.
+  for (int c0 = 0; c0 < cols; c0 += 32) {
+    float x[32];
+    tmem_load32(addr + c0, x);
+    if (!live) continue;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      float d = ex2(fmaf(x[c], kLog2e, -l2));
+      if (c0 + c == y) d = __fsub_rn(d, 1.0f);
+      x[c] = has ? __fmul_rn(d, g) : 0.0f;
+    }
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) *reinterpret_cast<uint4*>(out + c0 + c) = pack_vec<uint16_t>(x + c);
+  }
+}
+
+__device__ __forceinline__ void ce_grad_row(const CeParams& p, const CeTile& t, uint32_t addr,
+                                            int m) {
+  const bool dh = t.kind == 1;
+  const bool live = m < (dh ? p.N : p.nv);
+  const int cols = min(kMmN, p.D - t.n0);  // a multiple of 8
+  const size_t row = dh ? (size_t)SPEC_CHECKED(live ? m : 0, p.N, kSiteLinearCe)
+                        : (size_t)SPEC_CHECKED(live ? p.v0 + m : 0, p.V, kSiteLinearCe);
+  float* acc = p.dh_acc + (size_t)t.slice * p.N * p.D;
+  uint16_t* out = dh ? p.dh : p.dw;
+  for (int c0 = 0; c0 < cols; c0 += 32) {
+    float x[32];
+    if (t.iters > 0) {
+      tmem_load32(addr + c0, x);
+    } else {  // a slice past the end of a short last piece
+#pragma unroll
+      for (int c = 0; c < 32; ++c) x[c] = 0.0f;
+    }
+    if (!live) continue;
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+      if (c0 + c >= cols) break;
+      const size_t at = row * p.D + t.n0 + c0 + c;
+      if (out != nullptr) {
+        *reinterpret_cast<uint4*>(out + at) = pack_vec<uint16_t>(x + c);
+      } else {
+        float4* o = reinterpret_cast<float4*>(acc + at);
+        float4 a = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+        float4 b = make_float4(x[c + 4], x[c + 5], x[c + 6], x[c + 7]);
+        if (!p.first) {
+          const float4 u = o[0], v = o[1];
+          a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+          b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
+        }
+        o[0] = a;
+        o[1] = b;
       }
-    } else if (m < rows) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx + 16 * j;
-        if (n >= cols) continue;
-        if (M == kCeDz) {
-          const int y = p.labels[m];
-          float d = 0.0f;
-          if (y >= 0 && y < p.V) {
-            d = ex2((acc[i][j] - p.lse[m]) * kLog2e);
-            if (p.v0 + n == y) d -= 1.0f;
-            d *= p.g[m];
+    }
+  }
+}
+
+// Header of the workspace, and labels outside the vocabulary: the epilogue warps
+// of one CTA (its other warps go on).
+__device__ __forceinline__ void ce_check(const CeParams& p, int* bad) {
+  const int th = threadIdx.x - kMmEpilogue * 32, n = kMmThreads - kMmEpilogue * 32;
+  int mine = 0;
+#pragma unroll 4
+  for (int i = th; i < p.N; i += n) mine += __ldg(&p.labels[i]) >= p.V ? 1 : 0;
+  if (mine) atomicAdd(bad, mine);
+  asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
+  if (th == 0) {
+    p.header->status = *bad ? SPEC_ERR_BAD_INPUT : SPEC_OK;
+    p.header->bad_requests = *bad;
+    p.header->first_bad = INT32_MAX;
+  }
+}
+
+template <CeMode M>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    ce_mma_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CeParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ CeBars bars;
+  const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMmStages; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&bars.tfull[a], 1);
+      mbar_init(&bars.tempty[a], 4);
+    }
+    bars.abort_flag = 0;
+    bars.bad = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmIssuer) tmem_alloc(&bars.tmem, 512);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = bars.tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+  bool ok = true;
+  int loads = 0;  // stages the producer has filled
+
+  if (warp == kMmProducer) {
+    if (lane == 0) {
+      // The previous kernel's stores (dZ) before this one's asynchronous reads.
+      asm volatile("fence.proxy.async;" ::: "memory");
+      for (int i = 0; ok; ++i) {
+        const CeTile t = ce_tile<M>(p, i);
+        if (t.kind < 0) break;
+        for (int k = 0; k < t.iters; ++k, ++loads) {
+          const int s = loads % kMmStages, round = loads / kMmStages;
+          if (round > 0 && !mbar_wait_bounded(&bars.empty[s], (round - 1) & 1, &bars.abort_flag)) {
+            ok = false;
+            break;
           }
-          p.dz[(size_t)m * p.piece + n] = (uint16_t)pack_bf16(d, 0.0f);
-        } else if (M == kCeDh) {
-          float* at = p.dh_acc + (size_t)m * p.D + n;
-          *at = p.first ? acc[i][j] : *at + acc[i][j];
-        } else {
-          p.dw[(size_t)(p.v0 + m) * p.D + n] = (uint16_t)pack_bf16(acc[i][j], 0.0f);
+          const uint32_t a = ring + s * kMmStageBytes, b = a + kMmABytes;
+          mbar_arrive_expect_tx(&bars.full[s], kMmStageBytes);
+          const int k0 = t.k0 + k * kMmK;
+          if (M != kCeGrads) {
+            tma_load(a, &maps.h_k, k0, t.m0, &bars.full[s]);
+            tma_load(b, &maps.w_k, k0, (M == kCeDz ? p.v0 : 0) + t.n0, &bars.full[s]);
+          } else {
+            if (t.kind == 1) {
+              tma_load(a, &maps.dz_k, k0, t.m0, &bars.full[s]);
+            } else {
+              for (int c = 0; c < kMmM / 64; ++c)
+                tma_load(a + c * 8192, &maps.dz_mn, t.m0 + c * 64, k0, &bars.full[s]);
+            }
+            for (int c = 0; c < kMmN / 64; ++c)
+              tma_load(b + c * 8192, t.kind == 1 ? &maps.w_mn : &maps.h_mn, t.n0 + c * 64,
+                       (t.kind == 1 ? p.v0 : 0) + k0, &bars.full[s]);
+          }
         }
       }
+      // The products' last arrivals on `empty` come before the CTA ends.
+      for (int l = max(0, loads - kMmStages); ok && l < loads; ++l)
+        ok = mbar_wait_bounded(&bars.empty[l % kMmStages], (l / kMmStages) & 1, &bars.abort_flag);
+    }
+  } else if (warp == kMmIssuer) {
+    if (lane == 0) {
+      int it = 0;
+      for (int i = 0; ok; ++i) {
+        const CeTile t = ce_tile<M>(p, i);
+        if (t.kind < 0) break;
+        const int acc = i & 1;
+        if (i >= 2 && !mbar_wait_bounded(&bars.tempty[acc], ((i >> 1) - 1) & 1, &bars.abort_flag)) {
+          ok = false;
+          break;
+        }
+        tmem_fence_after();
+        const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
+        const uint32_t idesc = mma_idesc(kMmM, kMmN, a_mn, b_mn);
+        const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
+        for (int k = 0; k < t.iters; ++k, ++it) {
+          const int s = it % kMmStages;
+          if (!mbar_wait_bounded(&bars.full[s], (it / kMmStages) & 1, &bars.abort_flag)) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint32_t a = ring + s * kMmStageBytes, b = a + kMmABytes;
+#pragma unroll
+          for (int j = 0; j < kMmK / 16; ++j)
+            mma_f16(tmem + acc * kMmN, mma_desc(a + j * a_step, 8192, 1024),
+                    mma_desc(b + j * b_step, 8192, 1024), idesc, k > 0 || j > 0);
+          mma_commit(&bars.empty[s]);
+        }
+        if (!ok) break;
+        mma_commit(&bars.tfull[acc]);  // also where there was nothing to sum
+      }
+    }
+  } else {
+    if (p.check && blockIdx.x == 0) ce_check(p, &bars.bad);
+    const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
+    for (int i = 0;; ++i) {
+      const CeTile t = ce_tile<M>(p, i);
+      if (t.kind < 0) break;
+      const int acc = i & 1;
+      if (!mbar_wait_bounded(&bars.tfull[acc], (i >> 1) & 1, &bars.abort_flag)) ok = false;
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tmem_fence_after();
+      const uint32_t addr = tmem + acc * kMmN + ((uint32_t)(quarter * 32) << 16);
+      const int m = t.m0 + quarter * 32 + lane;
+      if (M == kCeLoss) ce_loss_row(p, t, addr, m);
+      else if (M == kCeDz) ce_dz_row(p, t, addr, m);
+      else ce_grad_row(p, t, addr, m);
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.tempty[acc]);
     }
   }
-}
-
-// Header of the workspace, and labels outside the vocabulary.
-__global__ void ce_check_kernel(WsHeader* h, const int32_t* labels, int N, int V) {
-  __shared__ int bad;
-  if (threadIdx.x == 0) bad = 0;
+  if (!ok) {
+    *(volatile int*)&bars.abort_flag = 1;
+    if (lane == 0) record_status(p.header, SPEC_ERR_TIMEOUT);
+    // Loads still on their way have to land before the CTA ends.
+    if (warp == kMmProducer && lane == 0) {
+      int never = 0;
+      for (int l = max(0, loads - kMmStages); l < loads; ++l)
+        mbar_wait_bounded(&bars.full[l % kMmStages], (l / kMmStages) & 1, &never);
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
   __syncthreads();
-  int mine = 0;
-  for (int i = threadIdx.x; i < N; i += blockDim.x) mine += labels[i] >= V ? 1 : 0;
-  if (mine) atomicAdd(&bad, mine);
+  tmem_fence_after();
+  if (warp == kMmIssuer) tmem_free(tmem, 512);
+}
+
+// Tokens' tiles into lse and nll: 32 tokens a CTA, 32 threads each over the tiles.
+__global__ void __launch_bounds__(1024) ce_finish_kernel(CeParams p, float* nll, float* lse) {
+  pdl_wait();
+  __shared__ float sm[32][33];
+  const int tok = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + tok;
+  const float2* part = p.partials + i;
+  float m = -FLT_MAX / 2;
+  if (i < p.N)
+    for (int t = grp; t < p.tiles; t += 32) m = fmaxf(m, part[(size_t)t * p.N].x);
+  sm[grp][tok] = m;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    h->status = bad ? SPEC_ERR_BAD_INPUT : SPEC_OK;
-    h->bad_requests = bad;
-    h->first_bad = INT32_MAX;
-  }
+  float top = sm[0][tok];
+#pragma unroll 8
+  for (int k = 1; k < 32; ++k) top = fmaxf(top, sm[k][tok]);
+  __syncthreads();
+  float s = 0.0f;
+  if (i < p.N)
+    for (int t = grp; t < p.tiles; t += 32) {
+      const float2 q = part[(size_t)t * p.N];
+      s = fmaf(q.y, ex2(__fsub_rn(q.x, top)), s);
+    }
+  sm[grp][tok] = s;
+  __syncthreads();
+  if (grp != 0 || i >= p.N) return;
+  s = 0.0f;
+#pragma unroll 8
+  for (int k = 0; k < 32; ++k) s = __fadd_rn(s, sm[k][tok]);
+  const float nan = __int_as_float(0x7fc00000);
+  // lse = ln 2 (max log2 e + log2 sum): the sum is relative to the scaled
+  // maximum as it was rounded.  A sum that is not positive and finite (an
+  // infinity or NaN among the inputs) gives NaN.
+  const float l = s > 0.0f && s <= FLT_MAX ? __fmul_rn(__fadd_rn(top, log2f(s)), kLn2f) : nan;
+  const int y = p.labels[i];
+  lse[i] = l;
+  nll[i] = y < 0 ? 0.0f : y < p.V ? __fsub_rn(l, p.z_label[i]) : nan;
 }
 
-// One warp per token: its tiles' pairs into lse and nll.
-__global__ void ce_finish_kernel(CeParams p, float* nll, float* lse) {
-  const int i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (i >= p.N) return;
-  const float2* part = p.partials + (size_t)i * p.tiles;
-  float m = -INFINITY;
-  bool nan = false;
-  for (int t = lane; t < p.tiles; t += 32) m = fmaxf(m, part[t].x);
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  FF s = {0.0f, 0.0f};
-  for (int t = lane; t < p.tiles; t += 32) {
-    const float e = __fmul_rn(part[t].y, ex2((part[t].x - m) * kLog2e));
-    if (!(e <= FLT_MAX)) nan = true;
-    else s = ff_add_f(s, e);
+// dH from its parts: the slices are added in order and rounded once.
+__global__ void __launch_bounds__(256)
+    ce_round_kernel(const float* acc, uint16_t* out, long long n, int splits) {
+  pdl_wait();
+  for (long long i = (blockIdx.x * 256LL + threadIdx.x) * 8; i < n; i += gridDim.x * 2048LL) {
+    float x[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4* a = reinterpret_cast<const float4*>(acc + s * n + i);
+      const float4 u = a[0], v = a[1];
+      x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+      x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+    }
+    *reinterpret_cast<uint4*>(out + i) = pack_vec<uint16_t>(x);
   }
-  s = warp_sum_ff(s);
-  nan = __any_sync(0xffffffffu, nan);
-  if (lane == 0) {
-    const float l = nan ? __int_as_float(0x7fc00000) : m + logf(ff_to_float(s));
-    const int y = p.labels[i];
-    lse[i] = l;
-    nll[i] = y < 0 ? 0.0f : y < p.V ? l - p.z_label[i] : __int_as_float(0x7fc00000);
-  }
-}
-
-__global__ void ce_round_kernel(const float* acc, uint16_t* out, long long n) {
-  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n;
-       i += (long long)gridDim.x * blockDim.x)
-    out[i] = (uint16_t)pack_bf16(acc[i], 0.0f);
 }
 
 }  // namespace specv

@@ -118,6 +118,7 @@ struct DeviceInfo {
   int sweep_blocks_per_sm[2][2] = {{0, 0}, {0, 0}};  // [dtype][verify]
   size_t final_smem_optin = 0;
   bool opd_ready = false;
+  bool ce_ready = false;
   int opd_clusters[2][4] = {};  // [dtype][cluster size - 1]: co-resident OPD clusters
 };
 

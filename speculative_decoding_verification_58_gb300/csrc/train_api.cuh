@@ -17,19 +17,63 @@ inline bool ce_sizes_ok(int N, int V, int D) {
   return N <= kCeMaxTokens && V <= SPEC_MAX_V && D <= kCeMaxWidth && D % 8 == 0;
 }
 
-template <CeMode M>
-cudaError_t launch_ce_gemm(const CeParams& p, cudaStream_t stream) {
-  const int rows = M == kCeDw ? p.nv : p.N;
-  const int cols = M == kCeLoss ? p.V : M == kCeDz ? p.nv : p.D;
-  return launch(ce_gemm_kernel<M>, dim3((cols + 63) / 64, (rows + 63) / 64), dim3(256), 0, stream,
-                false, p);
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
 }
 
-inline CeParams ce_params(const void* hidden, const void* weight, const int32_t* labels, int N,
-                          int V, int D, const CeLayout& lay, unsigned char* ws) {
+// Tensor map of a row-major bf16 matrix [rows, cols], rows `ld` entries apart,
+// read in boxes of box_rows x 64 with the 128-byte swizzle; what lies outside
+// the matrix reads as 0.
+inline bool ce_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld,
+                   int box_rows) {
+  EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t one[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline cudaError_t ce_prepare(DeviceInfo* d) {
+  std::lock_guard<std::mutex> lock(g_dev_mu);
+  if (d->ce_ready) return cudaSuccess;
+  cudaError_t e;
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeLoss>, attr, kMmSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeDz>, attr, kMmSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads>, attr, kMmSmem)) != cudaSuccess) return e;
+  d->ce_ready = true;
+  return cudaSuccess;
+}
+
+template <CeMode M>
+cudaError_t launch_ce(const DeviceInfo* d, const CeMaps& maps, const CeParams& p, long long tiles,
+                      cudaStream_t stream) {
+  const unsigned grid = (unsigned)std::max<long long>(1, std::min<long long>(tiles, d->sms));
+  return launch(ce_mma_kernel<M>, dim3(grid), dim3(kMmThreads), kMmSmem, stream, true, maps, p);
+}
+
+inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLayout& lay,
+                          unsigned char* ws) {
   CeParams p = {};
-  p.h = static_cast<const uint16_t*>(hidden);
-  p.w = static_cast<const uint16_t*>(weight);
   p.labels = labels;
   p.N = N;
   p.V = V;
@@ -40,21 +84,28 @@ inline CeParams ce_params(const void* hidden, const void* weight, const int32_t*
   p.dz = reinterpret_cast<uint16_t*>(ws + lay.dz);
   p.piece = lay.piece;
   p.dh_acc = reinterpret_cast<float*>(ws + lay.dh_acc);
+  p.header = reinterpret_cast<WsHeader*>(ws);
   return p;
 }
+
+inline long long blocks_of(long long n, int b) { return (n + b - 1) / b; }
 
 inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32_t* labels, int N,
                              int V, int D, float* nll, float* lse, unsigned char* ws,
                              cudaStream_t s) {
   NvtxRange r("spec_linear_ce");
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != cudaSuccess || ce_prepare(d) != cudaSuccess) return SPEC_ERR_CUDA;
   const CeLayout lay = ce_layout(N, V, D, false);
-  const CeParams p = ce_params(hidden, weight, labels, N, V, D, lay, ws);
-  if (launch(ce_check_kernel, dim3(1), dim3(256), 0, s, false, reinterpret_cast<WsHeader*>(ws),
-             labels, N, V) != cudaSuccess)
+  CeParams p = ce_params(labels, N, V, D, lay, ws);
+  p.check = 1;
+  CeMaps maps = {};
+  if (!ce_map(&maps.h_k, hidden, N, D, D, kMmM) || !ce_map(&maps.w_k, weight, V, D, D, kMmN))
     return SPEC_ERR_CUDA;
-  if (launch_ce_gemm<kCeLoss>(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
-  if (launch(ce_finish_kernel, dim3((N + 7) / 8), dim3(256), 0, s, false, p, nll, lse) !=
-      cudaSuccess)
+  if (launch_ce<kCeLoss>(d, maps, p, blocks_of(N, kMmM) * lay.tiles, s) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (launch(ce_finish_kernel, dim3((unsigned)blocks_of(N, 32)), dim3(1024), 0, s, true, p, nll,
+             lse) != cudaSuccess)
     return SPEC_ERR_CUDA;
   return SPEC_OK;
 }
@@ -63,27 +114,41 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
                              const float* lse, const float* grad_nll, int N, int V, int D,
                              void* d_hidden, void* d_weight, unsigned char* ws, cudaStream_t s) {
   NvtxRange r("spec_linear_ce_grad");
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != cudaSuccess || ce_prepare(d) != cudaSuccess) return SPEC_ERR_CUDA;
   const CeLayout lay = ce_layout(N, V, D, true);
-  CeParams p = ce_params(hidden, weight, labels, N, V, D, lay, ws);
+  CeParams p = ce_params(labels, N, V, D, lay, ws);
   p.lse = lse;
   p.g = grad_nll;
   p.dw = static_cast<uint16_t*>(d_weight);
-  if (launch(ce_check_kernel, dim3(1), dim3(256), 0, s, false, reinterpret_cast<WsHeader*>(ws),
-             labels, N, V) != cudaSuccess)
+  p.dh = lay.direct ? static_cast<uint16_t*>(d_hidden) : nullptr;
+  p.splits = lay.splits;
+  CeMaps maps = {};
+  if (!ce_map(&maps.h_k, hidden, N, D, D, kMmM) || !ce_map(&maps.w_k, weight, V, D, D, kMmN) ||
+      !ce_map(&maps.h_mn, hidden, N, D, D, 64) || !ce_map(&maps.w_mn, weight, V, D, D, 64))
     return SPEC_ERR_CUDA;
+  const long long mb = blocks_of(N, kMmM), db = blocks_of(D, kMmN);
   for (int v0 = 0; v0 < V; v0 += lay.piece) {
     p.v0 = v0;
     p.nv = std::min(lay.piece, V - v0);
     p.first = v0 == 0;
-    if (launch_ce_gemm<kCeDz>(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
-    if (d_hidden != nullptr && launch_ce_gemm<kCeDh>(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
-    if (d_weight != nullptr && launch_ce_gemm<kCeDw>(p, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    p.check = p.first;
+    p.split_iters = (int)blocks_of(blocks_of(p.nv, kMmK), p.splits);
+    p.dh_units = d_hidden != nullptr ? (int)(mb * db * p.splits) : 0;
+    p.dw_units = d_weight != nullptr ? (int)(blocks_of(p.nv, kMmM) * db) : 0;
+    if (!ce_map(&maps.dz_k, p.dz, N, p.nv, lay.piece, kMmM) ||
+        !ce_map(&maps.dz_mn, p.dz, N, p.nv, lay.piece, 64))
+      return SPEC_ERR_CUDA;
+    if (launch_ce<kCeDz>(d, maps, p, mb * blocks_of(p.nv, kMmN), s) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    if (launch_ce<kCeGrads>(d, maps, p, (long long)p.dh_units + p.dw_units, s) != cudaSuccess)
+      return SPEC_ERR_CUDA;
   }
-  if (d_hidden != nullptr) {
+  if (d_hidden != nullptr && !lay.direct) {
     const long long n = (long long)N * D;
-    if (launch(ce_round_kernel, dim3((unsigned)std::min<long long>((n + 255) / 256, 2048)),
-               dim3(256), 0, s, false, (const float*)p.dh_acc, static_cast<uint16_t*>(d_hidden),
-               n) != cudaSuccess)
+    if (launch(ce_round_kernel, dim3((unsigned)std::min<long long>(blocks_of(n, 2048), 1216)),
+               dim3(256), 0, s, true, (const float*)p.dh_acc, static_cast<uint16_t*>(d_hidden), n,
+               p.splits) != cudaSuccess)
       return SPEC_ERR_CUDA;
   }
   return SPEC_OK;

@@ -70,11 +70,9 @@ struct CeParams {
   int N, V, D, tiles;
   float2* partials;        // [tiles, N]: (max log2 e, sum 2^(z log2 e - max log2 e))
   float* z_label;          // [N]
-  uint16_t* dz;            // [N, piece]
   int piece, v0, nv;       // piece: buffer width, first entry, entries
   float* dh_acc;           // [splits, N, D]
-  uint16_t* dh;            // [N, D], where it comes out of one tile whole (else null)
-  uint16_t* dw;            // [V, D]
+  int dh_direct;           // dH comes out of one tile whole
   int first;               // first piece: dh_acc is set, not added to
   int splits, split_iters;  // slices of the piece in dH, 64-entry steps of a slice
   int dh_units, dw_units;  // units of the two products (0: not wanted)
@@ -100,12 +98,16 @@ constexpr int kMmABytes = kMmM * kMmK * 2, kMmBBytes = kMmN * kMmK * 2;
 constexpr int kMmStageBytes = kMmABytes + kMmBBytes;
 constexpr int kMmThreads = 192;
 constexpr int kMmProducer = 0, kMmIssuer = 1, kMmEpilogue = 2;  // first warps of the roles
-constexpr int kMmSmem = kMmStages * kMmStageBytes + 1024;       // + alignment
+// Results leave through two boxes of 32 rows x 128 bytes for each epilogue warp.
+constexpr int kMmBoxBytes = 32 * 128, kMmOutBytes = 4 * 2 * kMmBoxBytes;
+constexpr int kMmSmem = kMmStages * kMmStageBytes + kMmOutBytes + 1024;  // + alignment
 
 struct CeMaps {
   CUtensorMap h_k, w_k;            // boxes of 64 x 128 / 64 x 256: rows of hidden, of weight
   CUtensorMap dz_k;                // 64 x 128: rows of dZ
   CUtensorMap h_mn, w_mn, dz_mn;   // 64 x 64
+  CUtensorMap dz_out, dh_out, dw_out;  // 64 x 32: stores of bf16 results
+  CUtensorMap acc;                     // 32 x 32 x 1: sums of dH, [splits, N, D] floats
 };
 
 struct CeBars {
@@ -236,69 +238,102 @@ __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, 
   if (live) p.partials[(size_t)(t.n0 / kMmN) * p.N + m] = make_float2(ms, s);
 }
 
-__device__ __forceinline__ void ce_dz_row(const CeParams& p, const CeTile& t, uint32_t addr,
-                                          int m) {
-  const bool live = m < p.N;
-  int y = live ? __ldg(&p.labels[m]) : -1;
+// A warp's results go through shared memory: a box of 32 rows x 128 bytes, its
+// 16-byte pieces swizzled as the tensor map has them (no two lanes of a store meet in a
+// bank), then one TMA store.  Rows written by the lanes themselves, 16 bytes at a
+// time, were half sectors each and took as long as the products (2 x 230 us of
+// 1236 for 512 tokens, V = 151936, D = 2048).  Two boxes alternate.
+struct CeOut {
+  uint32_t base;  // the warp's two boxes
+  int n;          // boxes stored so far
+};
+
+__device__ __forceinline__ uint32_t ce_box_begin(const CeOut& o) {
+  if ((threadIdx.x & 31) == 0) bulk_wait_read<1>();
+  __syncwarp();
+  return o.base + (o.n & 1) * kMmBoxBytes;
+}
+
+// The lane's 16-byte piece `q` of its row.
+__device__ __forceinline__ void ce_box_put(uint32_t box, int q, uint4 v) {
+  const uint32_t lane = threadIdx.x & 31;
+  st_shared16(box + lane * 128 + ((q ^ (lane & 7)) << 4), v);
+}
+
+__device__ __forceinline__ void ce_box_ready() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
+__device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps, const CeTile& t,
+                                           uint32_t addr, int row0, CeOut& o) {
+  const int lane = threadIdx.x & 31, m = t.m0 + row0 + lane;
+  int y = m < p.N ? __ldg(&p.labels[m]) : -1;
   const bool has = y >= 0 && y < p.V;
   const float g = has ? __ldg(&p.g[m]) : 0.0f;
   const float l2 = has ? __fmul_rn(__ldg(&p.lse[m]), kLog2e) : 0.0f;
   y -= p.v0 + t.n0;
   const int cols = min(kMmN, p.nv - t.n0);
-  uint16_t* out = p.dz + (size_t)SPEC_CHECKED(live ? m : 0, p.N, kSiteLinearCe) * p.piece + t.n0;
-  // The buffer's rows hold whole tiles: columns past the piece are written too.
-  for (int c0 = 0; c0 < cols; c0 += 32) {
-    float x[32];
-    tmem_load32(addr + c0, x);
-    if (!live) continue;
+  for (int c0 = 0; c0 < cols; c0 += 64) {
+    const uint32_t box = ce_box_begin(o);
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      float d = ex2(fmaf(x[c], kLog2e, -l2));
-      if (c0 + c == y) d = __fsub_rn(d, 1.0f);
-      x[c] = has ? __fmul_rn(d, g) : 0.0f;
+    for (int h = 0; h < 2; ++h) {
+      float x[32];
+      tmem_load32(addr + c0 + h * 32, x);
+      const int rel = y - c0 - h * 32;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        float d = ex2(fmaf(x[c], kLog2e, -l2));
+        if (c == rel) d = __fsub_rn(d, 1.0f);
+        x[c] = has ? __fmul_rn(d, g) : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) ce_box_put(box, h * 4 + q, pack_vec<uint16_t>(x + q * 8));
     }
-#pragma unroll
-    for (int c = 0; c < 32; c += 8) *reinterpret_cast<uint4*>(out + c0 + c) = pack_vec<uint16_t>(x + c);
+    ce_box_ready();
+    if (lane == 0 && t.m0 + row0 < p.N) {
+      tma_store(&maps.dz_out, box, t.n0 + c0, t.m0 + row0);
+      bulk_commit();
+    }
+    ++o.n;
   }
 }
 
-__device__ __forceinline__ void ce_grad_row(const CeParams& p, const CeTile& t, uint32_t addr,
-                                            int m) {
+// dH and dW: bf16 where the tile is the whole sum, else dH's sums in single
+// precision, set by the first piece and added to by the others.
+__device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& maps,
+                                             const CeTile& t, uint32_t addr, int row0, CeOut& o) {
+  const int lane = threadIdx.x & 31;
   const bool dh = t.kind == 1;
-  const bool live = m < (dh ? p.N : p.nv);
-  const int cols = min(kMmN, p.D - t.n0);  // a multiple of 8
-  const size_t row = dh ? (size_t)SPEC_CHECKED(live ? m : 0, p.N, kSiteLinearCe)
-                        : (size_t)SPEC_CHECKED(live ? p.v0 + m : 0, p.V, kSiteLinearCe);
-  float* acc = p.dh_acc + (size_t)t.slice * p.N * p.D;
-  uint16_t* out = dh ? p.dh : p.dw;
-  for (int c0 = 0; c0 < cols; c0 += 32) {
-    float x[32];
-    if (t.iters > 0) {
-      tmem_load32(addr + c0, x);
-    } else {  // a slice past the end of a short last piece
+  const int rows = dh ? p.N : p.nv, r0 = t.m0 + row0;
+  const int cols = min(kMmN, p.D - t.n0);
+  const bool sums = dh && !p.dh_direct;
+  const int step = sums ? 32 : 64;
+  for (int c0 = 0; c0 < cols; c0 += step) {
+    const uint32_t box = ce_box_begin(o);
+    for (int h = 0; h < step; h += 32) {
+      float x[32];
+      tmem_load32(addr + c0 + h, x);
+      if (t.iters == 0) {  // a slice past the end of a short last piece
 #pragma unroll
-      for (int c = 0; c < 32; ++c) x[c] = 0.0f;
-    }
-    if (!live) continue;
+        for (int c = 0; c < 32; ++c) x[c] = 0.0f;
+      }
+      if (sums) {
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-      if (c0 + c >= cols) break;
-      const size_t at = row * p.D + t.n0 + c0 + c;
-      if (out != nullptr) {
-        *reinterpret_cast<uint4*>(out + at) = pack_vec<uint16_t>(x + c);
+        for (int q = 0; q < 8; ++q) ce_box_put(box, q, pack_vec<float>(x + q * 4));
       } else {
-        float4* o = reinterpret_cast<float4*>(acc + at);
-        float4 a = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
-        float4 b = make_float4(x[c + 4], x[c + 5], x[c + 6], x[c + 7]);
-        if (!p.first) {
-          const float4 u = o[0], v = o[1];
-          a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
-          b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
-        }
-        o[0] = a;
-        o[1] = b;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ce_box_put(box, h / 8 + q, pack_vec<uint16_t>(x + q * 8));
       }
     }
+    ce_box_ready();
+    if (lane == 0 && r0 < rows) {
+      if (!sums) tma_store(dh ? &maps.dh_out : &maps.dw_out, box, t.n0 + c0, (dh ? 0 : p.v0) + r0);
+      else if (p.first) tma_store3(&maps.acc, box, t.n0 + c0, r0, t.slice);
+      else tma_add3(&maps.acc, box, t.n0 + c0, r0, t.slice);
+      bulk_commit();
+    }
+    ++o.n;
   }
 }
 
@@ -420,6 +455,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   } else {
     if (p.check && blockIdx.x == 0) ce_check(p, &bars.bad);
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
+    CeOut out = {ring + kMmStages * kMmStageBytes + quarter * 2 * kMmBoxBytes, 0};
     for (int i = 0;; ++i) {
       const CeTile t = ce_tile<M>(p, i);
       if (t.kind < 0) break;
@@ -431,14 +467,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       }
       tmem_fence_after();
       const uint32_t addr = tmem + acc * kMmN + ((uint32_t)(quarter * 32) << 16);
-      const int m = t.m0 + quarter * 32 + lane;
-      if (M == kCeLoss) ce_loss_row(p, t, addr, m);
-      else if (M == kCeDz) ce_dz_row(p, t, addr, m);
-      else ce_grad_row(p, t, addr, m);
+      if (M == kCeLoss) ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane);
+      else if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, out);
+      else ce_grad_tile(p, maps, t, addr, quarter * 32, out);
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.tempty[acc]);
     }
+    if (M != kCeLoss && lane == 0) bulk_wait_all();
   }
   if (!ok) {
     *(volatile int*)&bars.abort_flag = 1;

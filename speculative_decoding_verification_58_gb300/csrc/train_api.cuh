@@ -36,9 +36,9 @@ inline EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Tensor map of a row-major bf16 matrix [rows, cols], rows `ld` entries apart,
-// read in boxes of box_rows x 64 with the 128-byte swizzle; what lies outside
-// the matrix reads as 0.
+// Tensor map of a row-major bf16 matrix [rows, cols], rows `ld` entries apart, in
+// boxes of box_rows x 64 with the 128-byte swizzle.  What lies outside the matrix
+// reads as 0 and is not written.
 inline bool ce_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld,
                    int box_rows) {
   EncodeTiled fn = encode_tiled();
@@ -49,6 +49,19 @@ inline bool ce_map(CUtensorMap* m, const void* base, long long rows, long long c
   const cuuint32_t one[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor map of floats [slices, rows, cols] in boxes of 1 x 32 x 32.
+inline bool ce_map3(CUtensorMap* m, void* base, long long slices, long long rows, long long cols) {
+  EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)slices};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)(cols * rows) * 4};
+  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -81,7 +94,6 @@ inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLa
   p.tiles = lay.tiles;
   p.partials = reinterpret_cast<float2*>(ws + lay.partials);
   p.z_label = reinterpret_cast<float*>(ws + lay.z_label);
-  p.dz = reinterpret_cast<uint16_t*>(ws + lay.dz);
   p.piece = lay.piece;
   p.dh_acc = reinterpret_cast<float*>(ws + lay.dh_acc);
   p.header = reinterpret_cast<WsHeader*>(ws);
@@ -120,12 +132,16 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
   CeParams p = ce_params(labels, N, V, D, lay, ws);
   p.lse = lse;
   p.g = grad_nll;
-  p.dw = static_cast<uint16_t*>(d_weight);
-  p.dh = lay.direct ? static_cast<uint16_t*>(d_hidden) : nullptr;
+  p.dh_direct = lay.direct;
+  void* dz = ws + lay.dz;
   p.splits = lay.splits;
   CeMaps maps = {};
   if (!ce_map(&maps.h_k, hidden, N, D, D, kMmM) || !ce_map(&maps.w_k, weight, V, D, D, kMmN) ||
       !ce_map(&maps.h_mn, hidden, N, D, D, 64) || !ce_map(&maps.w_mn, weight, V, D, D, 64))
+    return SPEC_ERR_CUDA;
+  if (d_weight != nullptr && !ce_map(&maps.dw_out, d_weight, V, D, D, 32)) return SPEC_ERR_CUDA;
+  if (d_hidden != nullptr && !(lay.direct ? ce_map(&maps.dh_out, d_hidden, N, D, D, 32)
+                                          : ce_map3(&maps.acc, p.dh_acc, lay.splits, N, D)))
     return SPEC_ERR_CUDA;
   const long long mb = blocks_of(N, kMmM), db = blocks_of(D, kMmN);
   for (int v0 = 0; v0 < V; v0 += lay.piece) {
@@ -136,8 +152,11 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
     p.split_iters = (int)blocks_of(blocks_of(p.nv, kMmK), p.splits);
     p.dh_units = d_hidden != nullptr ? (int)(mb * db * p.splits) : 0;
     p.dw_units = d_weight != nullptr ? (int)(blocks_of(p.nv, kMmM) * db) : 0;
-    if (!ce_map(&maps.dz_k, p.dz, N, p.nv, lay.piece, kMmM) ||
-        !ce_map(&maps.dz_mn, p.dz, N, p.nv, lay.piece, 64))
+    // dZ's own extent: what its last tile has past the vocabulary is not written,
+    // and reads as 0.
+    if (!ce_map(&maps.dz_k, dz, N, p.nv, lay.piece, kMmM) ||
+        !ce_map(&maps.dz_mn, dz, N, p.nv, lay.piece, 64) ||
+        !ce_map(&maps.dz_out, dz, N, p.nv, lay.piece, 32))
       return SPEC_ERR_CUDA;
     if (launch_ce<kCeDz>(d, maps, p, mb * blocks_of(p.nv, kMmN), s) != cudaSuccess)
       return SPEC_ERR_CUDA;

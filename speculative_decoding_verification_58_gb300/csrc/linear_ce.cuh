@@ -31,20 +31,56 @@ struct CeLayout {
   bool direct;  // dH comes out of one tile whole: no sums to keep
 };
 
-// Slices of the piece's entries that dH = dZ W is summed over: one unless the
-// output has too few 128 x 256 tiles for the SMs (two for each of 152 are aimed
-// at), and no shorter than 16 steps of 64 entries.
+constexpr int kCePairs = 76;  // CTA pairs the sizes below are chosen for (152 SMs)
+
+inline long long ce_waves(long long tiles) { return (tiles + kCePairs - 1) / kCePairs; }
+
+// Vocabulary tiles per piece of the gradients: of those whose dZ fits, the number
+// that needs the fewest rounds of 76 tiles in all, a round's tenth counted for each
+// piece's launches (2048 tokens, V = 151936: 38 tiles, 16 pieces of 4 full rounds; the
+// most that fit, 48, would be 13 pieces of 5.05 rounds, done in 6).
+inline int ce_piece_tiles(int N, int tiles) {
+  const long long mb = (N + 255) / 256;
+  const int most = (int)std::max<long long>(
+      1, std::min<long long>(tiles, kCePieceBytes / 2 / N / kCeTileV));
+  int best = most;
+  long long cost = -1;
+  for (int n = most; n >= std::max(1, most / 2); --n) {
+    const int pieces = (tiles + n - 1) / n, last = tiles - (pieces - 1) * n;
+    const long long c =
+        10 * ((pieces - 1) * ce_waves(mb * n) + ce_waves(mb * last)) + pieces;
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = n;
+    }
+  }
+  return best;
+}
+
+// Slices of the piece's entries that dH = dZ W is summed over: the fewest that
+// fill nine tenths of the pairs' rounds with 256 x 256 tiles of dH, or else those
+// that fill them best; none shorter than 16 steps of 64 entries.  The same whether
+// dW is wanted too (its units would even out less), so that dH is.
 inline int ce_splits(int N, int D, int piece) {
-  const long long tiles = (long long)((N + 127) / 128) * ((D + 255) / 256);
-  const long long want = (304 + tiles - 1) / tiles, most = piece / (16 * 64);
-  return (int)std::max<long long>(1, std::min(want, most));
+  const long long tiles = (long long)((N + 255) / 256) * ((D + 255) / 256);
+  const int most = (int)std::max<long long>(
+      1, std::min<long long>((4 * kCePairs + tiles - 1) / tiles, piece / (16 * 64)));
+  int best = 1;
+  double fill = 0.0;
+  for (int n = 1; n <= most && fill < 0.9; ++n) {
+    const double f = (double)(tiles * n) / (double)(ce_waves(tiles * n) * kCePairs);
+    if (f > fill + 0.02) {
+      fill = f;
+      best = n;
+    }
+  }
+  return best;
 }
 
 inline CeLayout ce_layout(int N, int V, int D, bool grad) {
   CeLayout l = {};
   l.tiles = (V + kCeTileV - 1) / kCeTileV;
-  const long long fit = kCePieceBytes / 2 / N / kCeTileV;  // tiles whose dZ fits
-  l.piece = (int)std::max<long long>(1, std::min<long long>(l.tiles, fit)) * kCeTileV;
+  l.piece = grad ? ce_piece_tiles(N, l.tiles) * kCeTileV : 0;
   size_t o = align256(sizeof(WsHeader));
   if (!grad) {
     l.partials = o;
@@ -81,11 +117,16 @@ struct CeParams {
 };
 
 // ---------------------------------------------------------------------------
-// The products.  A persistent kernel, one CTA per SM, on tiles of 128 x 256: a
-// warp that issues the TMA loads into a ring of four 64-deep stages, a warp that
-// issues the tcgen05.mma, and four warps that take finished tiles out of
-// tensor memory, where two accumulators of 256 columns alternate, so that one
-// tile's epilogue runs under the next one's products.
+// The products.  A persistent kernel of CTA pairs, one CTA per SM, on tiles of
+// 256 x 256 (rows 0..127 of a tile are the first CTA's): in each CTA a warp that
+// issues the TMA loads into a ring of six 64-deep stages and four warps that take
+// finished tiles out of tensor memory, in the first a warp that issues the
+// tcgen05.mma for both.  Two accumulators of 256 columns alternate, so that one
+// tile's epilogue runs under the next one's products.  A pair's CTAs each load one
+// half of either operand, 32 KB for the products of a stage; single CTAs on
+// 128 x 256 tiles need 48 KB for as many, which the L2 did not deliver where
+// operands are MN-major (dW of 2048 tokens at 58 % of the tensor cores' cycles;
+// without the loads of one operand they ran at full rate).
 //   loss   z  = H W^T          both operands K-major
 //   dz     z  = H W^T          the piece's columns
 //   grads  dH = dZ W           A K-major, B MN-major  (K: the piece's entries)
@@ -93,9 +134,10 @@ struct CeParams {
 // ---------------------------------------------------------------------------
 enum CeMode { kCeLoss, kCeDz, kCeGrads };
 
-constexpr int kMmM = 128, kMmN = 256, kMmK = 64, kMmStages = 4;
-constexpr int kMmABytes = kMmM * kMmK * 2, kMmBBytes = kMmN * kMmK * 2;
-constexpr int kMmStageBytes = kMmABytes + kMmBBytes;
+constexpr int kMmM = 256, kMmN = 256, kMmK = 64, kMmStages = 6;
+constexpr int kMmHalf = 128;  // rows of A, of B and of the result in each CTA
+constexpr int kMmABytes = kMmHalf * kMmK * 2, kMmBBytes = kMmHalf * kMmK * 2;
+constexpr int kMmStageBytes = kMmABytes + kMmBBytes;  // each CTA's
 constexpr int kMmThreads = 192;
 constexpr int kMmProducer = 0, kMmIssuer = 1, kMmEpilogue = 2;  // first warps of the roles
 // Results leave through two boxes of 32 rows x 128 bytes for each epilogue warp.
@@ -103,8 +145,7 @@ constexpr int kMmBoxBytes = 32 * 128, kMmOutBytes = 4 * 2 * kMmBoxBytes;
 constexpr int kMmSmem = kMmStages * kMmStageBytes + kMmOutBytes + 1024;  // + alignment
 
 struct CeMaps {
-  CUtensorMap h_k, w_k;            // boxes of 64 x 128 / 64 x 256: rows of hidden, of weight
-  CUtensorMap dz_k;                // 64 x 128: rows of dZ
+  CUtensorMap h_k, w_k, dz_k;      // boxes of 64 x 128: rows of hidden, weight, dZ
   CUtensorMap h_mn, w_mn, dz_mn;   // 64 x 64
   CUtensorMap dz_out, dh_out, dw_out;  // 64 x 32: stores of bf16 results
   CUtensorMap acc;                     // 32 x 32 x 1: sums of dH, [splits, N, D] floats
@@ -124,11 +165,11 @@ struct CeTile {
   int slice;      // dH: which of the sums kept apart
 };
 
-// Units of dH and dW over the CTAs.  A unit of dH costs split_iters steps, one of
+// Units of dH and dW over the pairs.  A unit of dH costs split_iters steps, one of
 // dW as many as the tokens need, each some more for its epilogue.  The units of dH
-// go round, so that the first `more` CTAs have one more of them; dW's are dealt to
-// bring every CTA up to the same level, and those that are left go round.
-// Returns the index of CTA c's i-th unit, dH's first; -1: no more.
+// go round, so that the first `more` pairs have one more of them; dW's are dealt to
+// bring every pair up to the same level, and those that are left go round.
+// Returns the index of pair c's i-th unit, dH's first; -1: no more.
 constexpr int kCeEpilogueSteps = 6;  // an epilogue's time, in steps
 __host__ __device__ inline long long ce_unit(int dh_units, int dw_units, int dh_iters, int dw_iters,
                                              int G, int c, int i) {
@@ -138,7 +179,7 @@ __host__ __device__ inline long long ce_unit(int dh_units, int dw_units, int dh_
   int j = i - mine;
   const long long ch = dh_iters + kCeEpilogueSteps, cw = dw_iters + kCeEpilogueSteps;
   const long long level = ((long long)dh_units * ch + (long long)dw_units * cw) / G;
-  // dW units that fit under the level: w1 for each of the first `more` CTAs, w0
+  // dW units that fit under the level: w1 for each of the first `more` pairs, w0
   // for each of the others.
   long long w0 = level > h * ch ? (level - h * ch) / cw : 0;
   if (w0 > dw_units / less) w0 = dw_units / less;
@@ -155,7 +196,7 @@ __host__ __device__ inline long long ce_unit(int dh_units, int dw_units, int dh_
   return idx < dw_units ? dh_units + idx : -1;
 }
 
-// This CTA's tiles: which is the i-th (kind -1: no more).
+// This pair's tiles: which is the i-th (kind -1: no more).
 template <CeMode M>
 __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
   CeTile t;
@@ -166,7 +207,7 @@ __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
     // the other token blocks from L2.
     const int cols = M == kCeLoss ? p.V : p.nv;
     const int mb = (p.N + kMmM - 1) / kMmM, nb = (cols + kMmN - 1) / kMmN;
-    const long long idx = (long long)i * gridDim.x + blockIdx.x;
+    const long long idx = (long long)i * (gridDim.x >> 1) + (blockIdx.x >> 1);
     if (idx >= (long long)mb * nb) return t;
     t.kind = 0;
     t.m0 = (int)(idx % mb) * kMmM;
@@ -174,8 +215,8 @@ __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
     t.iters = (p.D + kMmK - 1) / kMmK;
   } else {
     const int dw_iters = (p.N + kMmK - 1) / kMmK;
-    const long long idx = ce_unit(p.dh_units, p.dw_units, p.split_iters, dw_iters, gridDim.x,
-                                  blockIdx.x, i);
+    const long long idx = ce_unit(p.dh_units, p.dw_units, p.split_iters, dw_iters, gridDim.x >> 1,
+                                  blockIdx.x >> 1, i);
     if (idx < 0) return t;
     const int nb = (p.D + kMmN - 1) / kMmN;
     const bool dh = idx < p.dh_units;
@@ -354,12 +395,13 @@ __device__ __forceinline__ void ce_check(const CeParams& p, int* bad) {
 }
 
 template <CeMode M>
-__global__ void __launch_bounds__(kMmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     ce_mma_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CeParams p) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ CeBars bars;
   const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMmStages; ++s) {
       mbar_init(&bars.full[s], 1);
@@ -367,7 +409,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bars.tfull[a], 1);
-      mbar_init(&bars.tempty[a], 4);
+      mbar_init(&bars.tempty[a], 8);  // the epilogue warps of both CTAs
     }
     bars.abort_flag = 0;
     bars.bad = 0;
@@ -375,7 +417,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   }
   if (warp == kMmIssuer) tmem_alloc(&bars.tmem, 512);
   tmem_fence_before();
-  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there
   tmem_fence_after();
   const uint32_t tmem = bars.tmem;
   pdl_wait();
@@ -390,6 +432,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       for (int i = 0; ok; ++i) {
         const CeTile t = ce_tile<M>(p, i);
         if (t.kind < 0) break;
+        const int am = t.m0 + rank * kMmHalf, bn = t.n0 + rank * kMmHalf;
         for (int k = 0; k < t.iters; ++k, ++loads) {
           const int s = loads % kMmStages, round = loads / kMmStages;
           if (round > 0 && !mbar_wait_bounded(&bars.empty[s], (round - 1) & 1, &bars.abort_flag)) {
@@ -397,21 +440,23 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             break;
           }
           const uint32_t a = ring + s * kMmStageBytes, b = a + kMmABytes;
-          mbar_arrive_expect_tx(&bars.full[s], kMmStageBytes);
+          // Both CTAs' loads complete on the first one's barrier.
+          const uint32_t bar = dsmem_map(&bars.full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * kMmStageBytes);
           const int k0 = t.k0 + k * kMmK;
           if (M != kCeGrads) {
-            tma_load(a, &maps.h_k, k0, t.m0, &bars.full[s]);
-            tma_load(b, &maps.w_k, k0, (M == kCeDz ? p.v0 : 0) + t.n0, &bars.full[s]);
+            tma_load(a, &maps.h_k, k0, am, bar);
+            tma_load(b, &maps.w_k, k0, (M == kCeDz ? p.v0 : 0) + bn, bar);
           } else {
             if (t.kind == 1) {
-              tma_load(a, &maps.dz_k, k0, t.m0, &bars.full[s]);
+              tma_load(a, &maps.dz_k, k0, am, bar);
             } else {
-              for (int c = 0; c < kMmM / 64; ++c)
-                tma_load(a + c * 8192, &maps.dz_mn, t.m0 + c * 64, k0, &bars.full[s]);
+              for (int c = 0; c < kMmHalf; c += 64)
+                tma_load(a + c * 128, &maps.dz_mn, am + c, k0, bar);
             }
-            for (int c = 0; c < kMmN / 64; ++c)
-              tma_load(b + c * 8192, t.kind == 1 ? &maps.w_mn : &maps.h_mn, t.n0 + c * 64,
-                       (t.kind == 1 ? p.v0 : 0) + k0, &bars.full[s]);
+            for (int c = 0; c < kMmHalf; c += 64)
+              tma_load(b + c * 128, t.kind == 1 ? &maps.w_mn : &maps.h_mn, bn + c,
+                       (t.kind == 1 ? p.v0 : 0) + k0, bar);
           }
         }
       }
@@ -420,13 +465,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         ok = mbar_wait_bounded(&bars.empty[l % kMmStages], (l / kMmStages) & 1, &bars.abort_flag);
     }
   } else if (warp == kMmIssuer) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       int it = 0;
       for (int i = 0; ok; ++i) {
         const CeTile t = ce_tile<M>(p, i);
         if (t.kind < 0) break;
         const int acc = i & 1;
-        if (i >= 2 && !mbar_wait_bounded(&bars.tempty[acc], ((i >> 1) - 1) & 1, &bars.abort_flag)) {
+        if (i >= 2 &&
+            !mbar_wait_cluster_bounded(&bars.tempty[acc], ((i >> 1) - 1) & 1, &bars.abort_flag)) {
           ok = false;
           break;
         }
@@ -436,7 +482,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
         for (int k = 0; k < t.iters; ++k, ++it) {
           const int s = it % kMmStages;
-          if (!mbar_wait_bounded(&bars.full[s], (it / kMmStages) & 1, &bars.abort_flag)) {
+          if (!mbar_wait_cluster_bounded(&bars.full[s], (it / kMmStages) & 1, &bars.abort_flag)) {
             ok = false;
             break;
           }
@@ -457,10 +503,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
     CeOut out = {ring + kMmStages * kMmStageBytes + quarter * 2 * kMmBoxBytes, 0};
     for (int i = 0;; ++i) {
-      const CeTile t = ce_tile<M>(p, i);
+      CeTile t = ce_tile<M>(p, i);
       if (t.kind < 0) break;
+      t.m0 += rank * kMmHalf;
       const int acc = i & 1;
-      if (!mbar_wait_bounded(&bars.tfull[acc], (i >> 1) & 1, &bars.abort_flag)) ok = false;
+      if (!mbar_wait_cluster_bounded(&bars.tfull[acc], (i >> 1) & 1, &bars.abort_flag)) ok = false;
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -472,15 +519,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       else ce_grad_tile(p, maps, t, addr, quarter * 32, out);
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.tempty[acc]);
+      if (lane == 0) mbar_arrive_remote(dsmem_map(&bars.tempty[acc], 0));
     }
     if (M != kCeLoss && lane == 0) bulk_wait_all();
   }
   if (!ok) {
     *(volatile int*)&bars.abort_flag = 1;
     if (lane == 0) record_status(p.header, SPEC_ERR_TIMEOUT);
-    // Loads still on their way have to land before the CTA ends.
-    if (warp == kMmProducer && lane == 0) {
+    // Loads still on their way have to land before the CTAs end.
+    if (warp == kMmProducer && lane == 0 && rank == 0) {
       int never = 0;
       for (int l = max(0, loads - kMmStages); l < loads; ++l)
         mbar_wait_bounded(&bars.full[l % kMmStages], (l / kMmStages) & 1, &never);
@@ -488,7 +535,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   }
   __syncwarp();
   tmem_fence_before();
-  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still reach its barriers
   tmem_fence_after();
   if (warp == kMmIssuer) tmem_free(tmem, 512);
 }

@@ -89,11 +89,6 @@ struct OgSmem {
   float2 part_c[kOgMaxCluster];
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
 // Eight entries from e of a row, as floats; entries past the part's end are -inf.
 template <typename TIn>
 __device__ __forceinline__ void og_load(const TIn* row, int e, int n, bool vec, float* x) {

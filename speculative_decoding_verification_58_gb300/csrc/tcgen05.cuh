@@ -1,10 +1,13 @@
 // Inline-PTX wrappers for the fifth-generation tensor cores: tensor memory,
-// tcgen05.mma on bfloat16 operands in shared memory, and tiled TMA loads.
+// tcgen05.mma on bfloat16 operands in shared memory, and tiled TMA copies.  All
+// for a pair of CTAs (a cluster of two): an M = 256 product whose rows 0..127 of A
+// and of the result are CTA 0's and 128..255 CTA 1's, each holding one half of
+// B's rows; one thread of CTA 0 issues for both.
 #pragma once
 
 #include <cuda.h>
 
-#include "common.cuh"
+#include "opd.cuh"
 
 namespace specv {
 
@@ -28,30 +31,31 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
                                         bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
 
-// Arrive on `bar` once every tcgen05.mma this thread has issued is done.
+// Arrive on `bar` of both CTAs once every tcgen05.mma this thread has issued is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"((uint16_t)3)
       : "memory");
 }
 
-// Whole-warp allocation of tensor memory columns (a power of two >= 32); the
-// address goes to *out in shared memory.
+// Whole-warp allocation of tensor memory columns (a power of two >= 32) in both CTAs,
+// called by a warp of each; the address goes to *out in shared memory.
 __device__ __forceinline__ void tmem_alloc(uint32_t* out, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_addr(out)),
                "r"(cols)
                : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
                : "memory");
 }
 
@@ -82,13 +86,14 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&x)[32]) {
   for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(r[c]);
 }
 
-// Tiled TMA load of one box; x (innermost coordinate) a multiple of 8 entries.
+// Tiled TMA load of one box into this CTA's shared memory; x (innermost coordinate)
+// a multiple of 8 entries.  `bar` is a cluster address: it may lie in the other CTA.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                         uint64_t* bar) {
+                                         uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 

@@ -80,8 +80,9 @@ inline cudaError_t ce_prepare(DeviceInfo* d) {
 template <CeMode M>
 cudaError_t launch_ce(const DeviceInfo* d, const CeMaps& maps, const CeParams& p, long long tiles,
                       cudaStream_t stream) {
-  const unsigned grid = (unsigned)std::max<long long>(1, std::min<long long>(tiles, d->sms));
-  return launch(ce_mma_kernel<M>, dim3(grid), dim3(kMmThreads), kMmSmem, stream, true, maps, p);
+  const long long pairs = std::max<long long>(1, std::min<long long>(tiles, d->sms / 2));
+  return launch(ce_mma_kernel<M>, dim3((unsigned)(2 * pairs)), dim3(kMmThreads), kMmSmem, stream,
+                true, maps, p);
 }
 
 inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLayout& lay,
@@ -112,7 +113,8 @@ inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32
   CeParams p = ce_params(labels, N, V, D, lay, ws);
   p.check = 1;
   CeMaps maps = {};
-  if (!ce_map(&maps.h_k, hidden, N, D, D, kMmM) || !ce_map(&maps.w_k, weight, V, D, D, kMmN))
+  if (!ce_map(&maps.h_k, hidden, N, D, D, kMmHalf) ||
+      !ce_map(&maps.w_k, weight, V, D, D, kMmHalf))
     return SPEC_ERR_CUDA;
   if (launch_ce<kCeLoss>(d, maps, p, blocks_of(N, kMmM) * lay.tiles, s) != cudaSuccess)
     return SPEC_ERR_CUDA;
@@ -132,16 +134,17 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
   CeParams p = ce_params(labels, N, V, D, lay, ws);
   p.lse = lse;
   p.g = grad_nll;
+  p.splits = lay.splits;
   p.dh_direct = lay.direct;
   void* dz = ws + lay.dz;
-  p.splits = lay.splits;
   CeMaps maps = {};
-  if (!ce_map(&maps.h_k, hidden, N, D, D, kMmM) || !ce_map(&maps.w_k, weight, V, D, D, kMmN) ||
+  if (!ce_map(&maps.h_k, hidden, N, D, D, kMmHalf) ||
+      !ce_map(&maps.w_k, weight, V, D, D, kMmHalf) ||
       !ce_map(&maps.h_mn, hidden, N, D, D, 64) || !ce_map(&maps.w_mn, weight, V, D, D, 64))
     return SPEC_ERR_CUDA;
   if (d_weight != nullptr && !ce_map(&maps.dw_out, d_weight, V, D, D, 32)) return SPEC_ERR_CUDA;
   if (d_hidden != nullptr && !(lay.direct ? ce_map(&maps.dh_out, d_hidden, N, D, D, 32)
-                                          : ce_map3(&maps.acc, p.dh_acc, lay.splits, N, D)))
+                                          : ce_map3(&maps.acc, p.dh_acc, p.splits, N, D)))
     return SPEC_ERR_CUDA;
   const long long mb = blocks_of(N, kMmM), db = blocks_of(D, kMmN);
   for (int v0 = 0; v0 < V; v0 += lay.piece) {
@@ -154,7 +157,7 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
     p.dw_units = d_weight != nullptr ? (int)(blocks_of(p.nv, kMmM) * db) : 0;
     // dZ's own extent: what its last tile has past the vocabulary is not written,
     // and reads as 0.
-    if (!ce_map(&maps.dz_k, dz, N, p.nv, lay.piece, kMmM) ||
+    if (!ce_map(&maps.dz_k, dz, N, p.nv, lay.piece, kMmHalf) ||
         !ce_map(&maps.dz_mn, dz, N, p.nv, lay.piece, 64) ||
         !ce_map(&maps.dz_out, dz, N, p.nv, lay.piece, 32))
       return SPEC_ERR_CUDA;

@@ -119,6 +119,7 @@ struct DeviceInfo {
   size_t final_smem_optin = 0;
   bool opd_ready = false;
   bool ce_ready = false;
+  bool opd_grad_ready = false;
   int opd_clusters[2][4] = {};  // [dtype][cluster size - 1]: co-resident OPD clusters
 };
 

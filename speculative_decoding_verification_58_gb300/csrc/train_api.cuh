@@ -180,30 +180,63 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
 // Mixture-loss gradient.
 // ---------------------------------------------------------------------------
 
-// CTAs per position: one per 4096 entries of a row, up to the cluster limit.
-inline int opd_grad_cluster(int V) {
-  int cs = 1;
-  while (cs < kOgMaxCluster && (long long)cs * 4096 < V) cs *= 2;
-  return cs;
+// CTAs per position.  Rows go through shared memory where eight CTAs or fewer can
+// share them at kOgSliceBytes each, so that three fit an SM (a CTA's own
+// variables and what the system keeps are in the difference to a third of 228 KB).
+// Longer ones are read from memory in every pass, one CTA per 4096 entries up to eight
+// (measured: 128 requests of up to 16 rows of 151936 bf16 336 us from shared memory,
+// 453 us without; 32 requests in float, which would leave one CTA per SM, 241 and
+// 193 us; 60 requests of 32000 bf16 41 and 58 us).
+constexpr int kOgSliceBytes = 76000;
+
+inline size_t opd_grad_slice(int V, int cs, size_t es) {
+  const long long wins = V / 8;  // at most: the entries before the first window are less
+  return (size_t)((wins + cs - 1) / cs) * 8 * es * 2 + 16;
+}
+
+inline cudaError_t opd_grad_prepare(DeviceInfo* d) {
+  std::lock_guard<std::mutex> lock(g_dev_mu);
+  if (d->opd_grad_ready) return cudaSuccess;
+  for (const void* k : {(const void*)opd_grad_smem_kernel<float>,
+                        (const void*)opd_grad_smem_kernel<uint16_t>}) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kOgSliceBytes);
+    if (e != cudaSuccess) return e;
+  }
+  d->opd_grad_ready = true;
+  return cudaSuccess;
 }
 
 template <typename TIn>
 spec_status_t opd_grad_typed(OpdGradParams p, cudaStream_t stream) {
   NvtxRange r("spec_opd_grad");
-  const int cs = opd_grad_cluster(p.V);
-  p.slice = (((p.V + cs - 1) / cs) + 7) & ~7;
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != cudaSuccess || opd_grad_prepare(d) != cudaSuccess) return SPEC_ERR_CUDA;
+  int cs = 1;
+  while (cs < kOgMaxCluster && opd_grad_slice(p.V, cs, sizeof(TIn)) > kOgSliceBytes) cs *= 2;
+  const size_t bytes = opd_grad_slice(p.V, cs, sizeof(TIn));
+  const bool smem = p.draft_vec && p.target_vec && bytes <= kOgSliceBytes;
+  if (!smem) {
+    cs = 1;
+    while (cs < kOgMaxCluster && (long long)cs * 4096 < p.V) cs *= 2;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)p.B * p.k * cs));
   cfg.blockDim = dim3(kOgThreads);
+  cfg.dynamicSmemBytes = smem ? bytes : 0;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, opd_grad_kernel<TIn>, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  cfg.numAttrs = 2;
+  const cudaError_t e = smem ? cudaLaunchKernelEx(&cfg, opd_grad_smem_kernel<TIn>, p)
+                             : cudaLaunchKernelEx(&cfg, opd_grad_kernel<TIn>, p);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -437,8 +470,8 @@ spec_status_t spec_opd_grad(const void* target_logits, const void* draft_logits,
   p.B = B;
   p.k = k;
   p.V = V;
-  p.vec_ok = aligned(target_logits, 16) && aligned(draft_logits, 16) && aligned(d_draft, 16) &&
-             ((size_t)V * es) % 16 == 0;
+  p.draft_vec = aligned(draft_logits, 16) && aligned(d_draft, 16);
+  p.target_vec = aligned(target_logits, 16);
   p.delta = delta;
   p.alpha = alpha;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

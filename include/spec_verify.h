@@ -440,7 +440,8 @@ spec_status_t spec_linear_ce(const void* hidden, const void* weight, spec_dtype_
  *   d_hidden = dZ weight      [N, D] bfloat16 out, 16-byte aligned
  *   d_weight = dZ^T hidden    [V, D] bfloat16 out, 16-byte aligned
  *
- *   lse       [N]  float: from spec_linear_ce on the same inputs
+ *   nll, lse  [N]  float: from spec_linear_ce on the same inputs (the label's
+ *                  entry is formed as exp(-nll) - 1)
  *   grad_nll  [N]  float: not read for tokens without a label
  *   d_hidden, d_weight  either may be NULL (a frozen head, a frozen drafter),
  *                  not both
@@ -452,9 +453,10 @@ spec_status_t spec_linear_ce(const void* hidden, const void* weight, spec_dtype_
  */
 size_t spec_linear_ce_grad_workspace_bytes(int N, int V, int D);
 spec_status_t spec_linear_ce_grad(const void* hidden, const void* weight, spec_dtype_t dtype,
-                                  const int32_t* labels, const float* lse, const float* grad_nll,
-                                  int N, int V, int D, void* d_hidden, void* d_weight,
-                                  void* workspace, size_t workspace_bytes, void* stream);
+                                  const int32_t* labels, const float* nll, const float* lse,
+                                  const float* grad_nll, int N, int V, int D, void* d_hidden,
+                                  void* d_weight, void* workspace, size_t workspace_bytes,
+                                  void* stream);
 
 /*
  * Gradient of sum_b grad_loss[b] loss[b] with respect to the draft logits,

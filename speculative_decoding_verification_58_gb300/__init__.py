@@ -148,7 +148,8 @@ def lib() -> ctypes.CDLL:
         getattr(L, name).restype = csz
     L.spec_linear_ce.argtypes = [vp, vp, ci, i32p, ci, ci, ci, f32p, f32p, vp, csz, vp]
     L.spec_linear_ce.restype = ci
-    L.spec_linear_ce_grad.argtypes = [vp, vp, ci, i32p, f32p, f32p, ci, ci, ci, vp, vp, vp, csz, vp]
+    L.spec_linear_ce_grad.argtypes = [vp, vp, ci, i32p, f32p, f32p, f32p, ci, ci, ci, vp, vp, vp,
+                                      csz, vp]
     L.spec_linear_ce_grad.restype = ci
     L.spec_opd_grad.argtypes = [vp, vp, ci, i32p, f32p, ci, ci, ci, ctypes.c_float, ctypes.c_float,
                                 vp, vp]
@@ -661,7 +662,7 @@ class LinearCe:
     contents may change between calls, the tensors must stay alive.
 
     ``loss()`` fills and returns (nll, lse), ``grad()`` (d_hidden, d_weight)
-    from the lse of the last ``loss()``.  ``need_hidden`` / ``need_weight``
+    from the nll and lse of the last ``loss()``.  ``need_hidden`` / ``need_weight``
     False leaves that gradient out (None).  Both calls share one workspace:
     enqueue them on one stream.
     """
@@ -711,8 +712,8 @@ class LinearCe:
                            nll.data_ptr(), lse.data_ptr(), ws.data_ptr(), wsb, st)
         self._grad = lib().spec_linear_ce_grad
         self._grad_args = None if grad_nll is None else (
-            hidden.data_ptr(), weight.data_ptr(), dt, labels.data_ptr(), lse.data_ptr(),
-            grad_nll.data_ptr(), N, V, D,
+            hidden.data_ptr(), weight.data_ptr(), dt, labels.data_ptr(), nll.data_ptr(),
+            lse.data_ptr(), grad_nll.data_ptr(), N, V, D,
             None if self.d_hidden is None else d_hidden.data_ptr(),
             None if self.d_weight is None else d_weight.data_ptr(), ws.data_ptr(), wsb, st)
 
@@ -741,15 +742,15 @@ def spec_linear_ce(hidden, weight, labels, *, nll=None, lse=None, workspace=None
                     stream=stream).loss()
 
 
-def spec_linear_ce_grad(hidden, weight, labels, lse, grad_nll, *, d_hidden=None, d_weight=None,
+def spec_linear_ce_grad(hidden, weight, labels, nll, lse, grad_nll, *, d_hidden=None, d_weight=None,
                         need_hidden: bool = True, need_weight: bool = True, workspace=None,
                         stream=None):
     """Gradients of sum_i grad_nll_i nll_i: (d_hidden [N, D], d_weight [V, D]), bfloat16.
 
-    ``lse`` is ``spec_linear_ce``'s on the same inputs; ``grad_nll`` float32 [N].
+    ``nll`` and ``lse`` are ``spec_linear_ce``'s on the same inputs; ``grad_nll`` float32 [N].
     ``need_hidden`` / ``need_weight`` False leaves that gradient out (None).
     """
-    return LinearCe(hidden, weight, labels, grad_nll, lse=lse, d_hidden=d_hidden,
+    return LinearCe(hidden, weight, labels, grad_nll, nll=nll, lse=lse, d_hidden=d_hidden,
                     d_weight=d_weight, need_hidden=need_hidden, need_weight=need_weight,
                     workspace=workspace, stream=stream).grad()
 

@@ -101,6 +101,7 @@ inline CeLayout ce_layout(int N, int V, int D, bool grad) {
 
 struct CeParams {
   const int32_t* labels;   // [N]
+  const float* nll;        // [N] (gradients)
   const float* lse;        // [N] (gradients)
   const float* g;          // [N] (gradients)
   int N, V, D, tiles;
@@ -237,7 +238,8 @@ __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
   return t;
 }
 
-// Epilogue of one thread: row `m` of the tile, 256 columns of tensor memory.
+// Epilogue of one thread: row `m` of the tile, 256 columns of tensor memory.  The
+// label's logit goes to z_label and is left out of the sums.
 __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, uint32_t addr,
                                             int m) {
   const bool live = m < p.N;
@@ -258,7 +260,10 @@ __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, 
       float z = 0.0f;
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        if (c == rel) z = x[c];
+        if (c == rel) {
+          z = x[c];
+          x[c] = -INFINITY;
+        }
       if (rel >= 0 && rel < 32) p.z_label[SPEC_CHECKED(m, p.N, kSiteLinearCe)] = z;
     }
     float mx = x[0];
@@ -315,6 +320,10 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
   const float l2 = has ? __fmul_rn(__ldg(&p.lse[m]), kLog2e) : 0.0f;
   y -= p.v0 + t.n0;
   const int cols = min(kMmN, p.nv - t.n0);
+  // The label's entry is exp(-nll) - 1: from the loss itself, because for a token that
+  // is well predicted the difference of its logit and lse has few bits left.
+  const float at_label =
+      has && y >= 0 && y < kMmN ? __fmul_rn(expm1f(-__ldg(&p.nll[m])), g) : 0.0f;
   for (int c0 = 0; c0 < cols; c0 += 64) {
     const uint32_t box = ce_box_begin(o);
 #pragma unroll
@@ -324,9 +333,8 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
       const int rel = y - c0 - h * 32;
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
-        float d = ex2(fmaf(x[c], kLog2e, -l2));
-        if (c == rel) d = __fsub_rn(d, 1.0f);
-        x[c] = has ? __fmul_rn(d, g) : 0.0f;
+        const float d = has ? __fmul_rn(ex2(fmaf(x[c], kLog2e, -l2)), g) : 0.0f;
+        x[c] = c == rel && has ? at_label : d;
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) ce_box_put(box, h * 4 + q, pack_vec<uint16_t>(x + q * 8));
@@ -569,13 +577,26 @@ __global__ void __launch_bounds__(1024) ce_finish_kernel(CeParams p, float* nll,
 #pragma unroll 8
   for (int k = 0; k < 32; ++k) s = __fadd_rn(s, sm[k][tok]);
   const float nan = __int_as_float(0x7fc00000);
-  // lse = ln 2 (max log2 e + log2 sum): the sum is relative to the scaled
-  // maximum as it was rounded.  A sum that is not positive and finite (an
-  // infinity or NaN among the inputs) gives NaN.
-  const float l = s > 0.0f && s <= FLT_MAX ? __fmul_rn(__fadd_rn(top, log2f(s)), kLn2f) : nan;
   const int y = p.labels[i];
+  const bool has = y >= 0 && y < p.V;
+  const float z = has ? p.z_label[i] : -INFINITY;
+  // s = sum over the others of 2^(z_v log2 e - top); the label's own term is apart.
+  // `gap` is how far the others' maximum lies above the label, in base 2:
+  //   nll = log(1 + s 2^gap),  lse = log(s 2^top + 2^(z log2 e)).
+  // A token that is well predicted so keeps the relative precision of its small
+  // loss, which the difference of lse and z does not have.
+  const float zl = __fmul_rn(z, kLog2e), gap = fmaf(z, -kLog2e, top), T = fmaxf(top, zl);
+  const float all = __fadd_rn(__fmul_rn(s, ex2(__fsub_rn(top, T))), ex2(__fsub_rn(zl, T)));
+  // A sum that is not positive and finite (an infinity or NaN among the inputs)
+  // gives NaN.
+  const float l = all > 0.0f && all <= FLT_MAX && s >= 0.0f
+                      ? __fmul_rn(__fadd_rn(T, log2f(all)), kLn2f)
+                      : nan;
   lse[i] = l;
-  nll[i] = y < 0 ? 0.0f : y < p.V ? __fsub_rn(l, p.z_label[i]) : nan;
+  if (y < 0) nll[i] = 0.0f;
+  else if (!has || !(l == l)) nll[i] = nan;
+  else if (gap <= 0.0f) nll[i] = log1pf(__fmul_rn(s, ex2(gap)));
+  else nll[i] = __fmul_rn(__fadd_rn(gap, log2f(__fadd_rn(s, ex2(-gap)))), kLn2f);
 }
 
 // dH from its parts: the slices are added in order and rounded once.

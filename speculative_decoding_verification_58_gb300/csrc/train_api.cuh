@@ -125,13 +125,14 @@ inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32
 }
 
 inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32_t* labels,
-                             const float* lse, const float* grad_nll, int N, int V, int D,
-                             void* d_hidden, void* d_weight, unsigned char* ws, cudaStream_t s) {
+                             const float* nll, const float* lse, const float* grad_nll, int N,
+                             int V, int D, void* d_hidden, void* d_weight, unsigned char* ws, cudaStream_t s) {
   NvtxRange r("spec_linear_ce_grad");
   DeviceInfo* d = nullptr;
   if (device_info(&d) != cudaSuccess || ce_prepare(d) != cudaSuccess) return SPEC_ERR_CUDA;
   const CeLayout lay = ce_layout(N, V, D, true);
   CeParams p = ce_params(labels, N, V, D, lay, ws);
+  p.nll = nll;
   p.lse = lse;
   p.g = grad_nll;
   p.splits = lay.splits;
@@ -405,16 +406,17 @@ spec_status_t spec_linear_ce(const void* hidden, const void* weight, spec_dtype_
 }
 
 spec_status_t spec_linear_ce_grad(const void* hidden, const void* weight, spec_dtype_t dtype,
-                                  const int32_t* labels, const float* lse, const float* grad_nll,
-                                  int N, int V, int D, void* d_hidden, void* d_weight,
+                                  const int32_t* labels, const float* nll, const float* lse,
+                                  const float* grad_nll, int N, int V, int D, void* d_hidden,
+                                  void* d_weight,
                                   void* workspace, size_t workspace_bytes, void* stream) {
   if (N < 1 || V < 1 || D < 1) return SPEC_ERR_INVALID_ARG;
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
   if (dtype != SPEC_BF16 || !ce_sizes_ok(N, V, D)) return SPEC_ERR_UNSUPPORTED;
-  if (!hidden || !weight || !labels || !lse || !grad_nll || (!d_hidden && !d_weight))
+  if (!hidden || !weight || !labels || !nll || !lse || !grad_nll || (!d_hidden && !d_weight))
     return SPEC_ERR_INVALID_ARG;
-  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(labels, 4) || !aligned(lse, 4) ||
-      !aligned(grad_nll, 4) || !aligned(d_hidden, 16) || !aligned(d_weight, 16))
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(labels, 4) || !aligned(nll, 4) ||
+      !aligned(lse, 4) || !aligned(grad_nll, 4) || !aligned(d_hidden, 16) || !aligned(d_weight, 16))
     return SPEC_ERR_INVALID_ARG;
   const size_t n4 = (size_t)N * 4, nh = (size_t)N * D * 2, nw = (size_t)V * D * 2;
   const void* outs[2] = {d_hidden, d_weight};
@@ -422,6 +424,7 @@ spec_status_t spec_linear_ce_grad(const void* hidden, const void* weight, spec_d
   for (int o = 0; o < 2; ++o)
     if (overlap(outs[o], out_bytes[o], hidden, nh) || overlap(outs[o], out_bytes[o], weight, nw) ||
         overlap(outs[o], out_bytes[o], labels, n4) || overlap(outs[o], out_bytes[o], lse, n4) ||
+        overlap(outs[o], out_bytes[o], nll, n4) ||
         overlap(outs[o], out_bytes[o], grad_nll, n4))
       return SPEC_ERR_INVALID_ARG;
   if (overlap(d_hidden, out_bytes[0], d_weight, out_bytes[1])) return SPEC_ERR_INVALID_ARG;
@@ -430,7 +433,7 @@ spec_status_t spec_linear_ce_grad(const void* hidden, const void* weight, spec_d
     return SPEC_ERR_WORKSPACE;
   DeviceOf on_device(weight);
   if (!on_device.ok()) return SPEC_ERR_CUDA;
-  return ce_grad(hidden, weight, labels, lse, grad_nll, N, V, D, d_hidden, d_weight,
+  return ce_grad(hidden, weight, labels, nll, lse, grad_nll, N, V, D, d_hidden, d_weight,
                  static_cast<unsigned char*>(workspace), static_cast<cudaStream_t>(stream));
 }
 

@@ -103,11 +103,11 @@ def test_full_vocabulary(N, V, D):
 def test_one_gradient_alone_is_the_same():
     h, w, y, g = inputs(150, 9000, 128, seed=3)
     ce = sv.LinearCe(h, w, y, g)
-    _, lse = ce.loss()
+    nll, lse = ce.loss()
     dh, dw = ce.grad()
-    dh1, none = sv.spec_linear_ce_grad(h, w, y, lse, g, need_weight=False)
+    dh1, none = sv.spec_linear_ce_grad(h, w, y, nll, lse, g, need_weight=False)
     assert none is None and torch.equal(dh, dh1)
-    none, dw1 = sv.spec_linear_ce_grad(h, w, y, lse, g, need_hidden=False)
+    none, dw1 = sv.spec_linear_ce_grad(h, w, y, nll, lse, g, need_hidden=False)
     assert none is None and torch.equal(dw, dw1)
 
 
@@ -145,6 +145,27 @@ def test_peaked_and_extreme_logits():
     dh, dw = ce.grad()
     check_loss(h, w, y, nll, lse)
     check_grad(h, w, y, g, dh, dw)
+
+
+def test_well_predicted_tokens():
+    # Every label's probability is within 1e-2 .. 1e-7 of 1: the loss and the
+    # gradient keep their relative precision up to that of the logits themselves.
+    h, w, y, g = inputs(64, 500, 64, seed=10)
+    y = torch.arange(64, device="cuda", dtype=torch.int32)
+    lean = torch.linspace(3.5, 6.5, 64, device="cuda")[:, None]
+    h = (0.1 * h.float() + lean * w[:64].float()).to(torch.bfloat16)
+    ce = sv.LinearCe(h, w, y, g)
+    nll, lse = ce.loss()
+    dh, dw = ce.grad()
+    check_loss(h, w, y, nll, lse)
+    check_grad(h, w, y, g, dh, dw)
+    rn, _ = ref.ce(h, w, y)
+    # log(1 + sum exp(z_v - z_y)): the logits' errors and those of the exponentials
+    # and sums (2^-18, above) are relative in it.
+    assert torch.all((nll.double() - rn).abs() <= (2.1 * z_error(h, w) + 2.0 ** -18) * rn)
+    rh, rw, dz, _ = ref.ce_grad(h, w, y, g)
+    tol = (2.0 ** -7 + 4 * z_error(h, w) + 2.0 ** -16) * (dz.abs() @ w.double().abs())
+    assert torch.all((dh.double() - rh).abs() <= tol)
 
 
 def test_not_finite_hidden_state_spoils_its_own_row_only():
@@ -268,9 +289,9 @@ def test_refusals():
     assert e.value.code == sv.SPEC_ERR_WORKSPACE
     nll, lse = sv.spec_linear_ce(h, w, y)
     with pytest.raises(sv.SpecVerifyError) as e:
-        sv.spec_linear_ce_grad(h, w, y, lse, g, d_hidden=h)  # the output is an input
+        sv.spec_linear_ce_grad(h, w, y, nll, lse, g, d_hidden=h)  # the output is an input
     assert e.value.code == sv.SPEC_ERR_INVALID_ARG
     with pytest.raises(ValueError):
-        sv.spec_linear_ce_grad(h, w, y, lse, g, need_hidden=False, need_weight=False)
+        sv.spec_linear_ce_grad(h, w, y, nll, lse, g, need_hidden=False, need_weight=False)
     with pytest.raises(ValueError):
         sv.LinearCe(h, w, y).grad()

@@ -41,12 +41,12 @@ def test_linear_ce_host_checks(lib):
     for kw in (dict(ws=None), dict(ws=6 * A + 16), dict(n=16)):
         assert loss(**kw) == wsp, kw
 
-    def grad(h=A, w=2 * A, dt=1, y=3 * A, lse=4 * A, g=5 * A, N=4, V=32, D=16, dh=7 * A, dw=8 * A,
+    def grad(h=A, w=2 * A, dt=1, y=3 * A, nll=9 * A, lse=4 * A, g=5 * A, N=4, V=32, D=16, dh=7 * A, dw=8 * A,
              ws=6 * A, n=1 << 20):
-        return lib.spec_linear_ce_grad(h, w, dt, y, lse, g, N, V, D, dh, dw, ws, n, None)
+        return lib.spec_linear_ce_grad(h, w, dt, y, nll, lse, g, N, V, D, dh, dw, ws, n, None)
 
-    for kw in (dict(N=0), dict(g=None), dict(lse=None), dict(dh=None, dw=None), dict(dh=A),
-               dict(dw=2 * A), dict(dh=8 * A), dict(dw=8 * A + 2), dict(dt=-1), dict(dw=4 * A)):
+    for kw in (dict(N=0), dict(g=None), dict(lse=None), dict(nll=None), dict(dh=None, dw=None), dict(dh=A),
+               dict(dw=2 * A), dict(dh=8 * A), dict(dw=8 * A + 2), dict(dt=-1), dict(dw=4 * A), dict(dh=9 * A)):
         assert grad(**kw) == bad, kw
     assert grad(dt=0) == uns and grad(D=20) == uns
     assert grad(n=100) == wsp

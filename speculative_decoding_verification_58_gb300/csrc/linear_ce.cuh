@@ -9,8 +9,11 @@
 // pair per row.  The gradients form them again, a piece of the vocabulary at a
 // time: the piece's dZ is written in bfloat16 to a scratch buffer that stays in
 // L2, and both products read it from there.  dZ is rounded to bfloat16 (relative
-// 2^-9) because the matrix units take both operands in one type, and the
-// gradients come out in bfloat16 anyway; every sum is in single precision.
+// 2^-8) because the matrix units take both operands in one type, and the
+// gradients come out in bfloat16 anyway; every sum is in single precision.  The
+// label's entry, which is the largest of most rows and would pass its own rounding
+// on to a whole row of dW and dH, is made good: what the rounding took from it is
+// kept per token and added to both in single precision.
 #pragma once
 
 #include "grad_norm.cuh"
@@ -24,7 +27,7 @@ constexpr int kCeMaxTokens = SPEC_MAX_TOKENS;
 constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
 
 struct CeLayout {
-  size_t partials, z_label, dz, dh_acc, total;
+  size_t partials, z_label, resid, in_tile, dz, dh_acc, total;
   int tiles;  // vocabulary tiles
   int piece;   // vocabulary entries per piece (a multiple of kCeTileV)
   int splits;  // slices of a piece whose parts of dH are summed apart
@@ -88,6 +91,10 @@ inline CeLayout ce_layout(int N, int V, int D, bool grad) {
     l.z_label = o;
     o = align256(o + (size_t)N * sizeof(float));
   } else {
+    l.resid = o;
+    o = align256(o + (size_t)N * sizeof(float));
+    l.in_tile = o;
+    o = align256(o + (size_t)(l.piece / kCeTileV) * ((N + 31) / 32) * sizeof(uint32_t));
     l.dz = o;
     o = align256(o + (size_t)N * l.piece * 2);
     l.splits = ce_splits(N, D, l.piece);
@@ -108,6 +115,10 @@ struct CeParams {
   float2* partials;        // [tiles, N]: (max log2 e, sum 2^(z log2 e - max log2 e))
   float* z_label;          // [N]
   int piece, v0, nv;       // piece: buffer width, first entry, entries
+  const uint16_t* h;       // [N, D]
+  const uint16_t* w;       // [V, D]
+  float* resid;            // [N]: the label's entry of dZ less its bf16 rounding
+  uint32_t* in_tile;       // [piece's tiles, N / 32]: tokens whose label is in the tile
   float* dh_acc;           // [splits, N, D]
   int dh_direct;           // dH comes out of one tile whole
   int first;               // first piece: dh_acc is set, not added to
@@ -324,6 +335,12 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
   // is well predicted the difference of its logit and lse has few bits left.
   const float at_label =
       has && y >= 0 && y < kMmN ? __fmul_rn(expm1f(-__ldg(&p.nll[m])), g) : 0.0f;
+  const bool here = has && y >= 0 && y < kMmN;
+  const uint32_t tokens = __ballot_sync(0xffffffffu, here);
+  if (lane == 0 && m < p.N)
+    p.in_tile[(size_t)(t.n0 / kMmN) * ((p.N + 31) / 32) + m / 32] = tokens;
+  if (here)
+    p.resid[m] = __fsub_rn(at_label, __uint_as_float(pack_bf16(at_label, 0.0f) << 16));
   for (int c0 = 0; c0 < cols; c0 += 64) {
     const uint32_t box = ce_box_begin(o);
 #pragma unroll
@@ -348,10 +365,82 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
   }
 }
 
+// 32 entries of a row of hidden or weight, of which `n` (a multiple of 8) exist.
+struct CeRow {
+  uint4 v[4];
+};
+__device__ __forceinline__ CeRow ce_row(const uint16_t* src, int n) {
+  CeRow r;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    r.v[q] = q * 8 < n ? __ldg(reinterpret_cast<const uint4*>(src) + q) : make_uint4(0, 0, 0, 0);
+  return r;
+}
+__device__ __forceinline__ void ce_add_row(float (&x)[32], const CeRow& row, float r) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float a[8];
+    ElemTraits<uint16_t>::unpack(row.v[q], a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[q * 8 + e] = fmaf(r, a[e], x[q * 8 + e]);
+  }
+}
+
+// The tokens whose label is this lane's entry, r0 + lane of the piece: f(token) for
+// each, in order.
+template <typename F>
+__device__ __forceinline__ void ce_tokens_of(const CeParams& p, int r0, F&& f) {
+  const int lane = threadIdx.x & 31, words = (p.N + 31) / 32;
+  const uint32_t* in_tile = p.in_tile + (size_t)(r0 / kMmN) * words;
+  for (int base = 0; base < words; base += 32) {
+    const uint32_t mine = base + lane < words ? __ldg(in_tile + base + lane) : 0;
+    for (uint32_t some = __ballot_sync(0xffffffffu, mine != 0); some != 0; some &= some - 1) {
+      const int src = __ffs(some) - 1, i = (base + src) * 32 + lane;
+      const uint32_t word = __shfl_sync(0xffffffffu, mine, src);
+      const int rel = (word >> lane) & 1 ? __ldg(&p.labels[i]) - p.v0 - r0 : -1;
+      for (uint32_t m = __ballot_sync(0xffffffffu, rel >= 0 && rel < 32); m != 0; m &= m - 1) {
+        const int j = __ffs(m) - 1;
+        if (__shfl_sync(0xffffffffu, rel, j) == lane) f((base + src) * 32 + j);
+      }
+    }
+  }
+}
+
+// Whose rounding residual a lane's row takes: of dH the row's own token, of dW the
+// tokens with this label.  `src`: where the row to add starts.
+struct CeFix {
+  int tok, toks;  // the first token, how many
+  bool several;   // some lane of the warp has more than one
+  const uint16_t* src;
+  float r;
+};
+__device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int row0) {
+  const int lane = threadIdx.x & 31, r0 = t.m0 + row0;
+  CeFix f = {-1, 0, false, nullptr, 0.0f};
+  if (t.kind == 1) {
+    // (Sums of several slices or pieces get theirs at the end.)
+    const int y = p.dh_direct && r0 + lane < p.N ? __ldg(&p.labels[r0 + lane]) : -1;
+    if (y >= 0 && y < p.V) {
+      f.tok = r0 + lane;
+      f.toks = 1;
+      f.src = p.w + (size_t)y * p.D;
+    }
+  } else if (r0 < p.nv) {
+    ce_tokens_of(p, r0, [&](int i) {
+      if (f.toks++ == 0) f.tok = i;
+    });
+    if (f.toks > 0) f.src = p.h + (size_t)SPEC_CHECKED(f.tok, p.N, kSiteLinearCe) * p.D;
+  }
+  if (f.toks > 0) f.r = p.resid[f.tok];
+  f.several = __any_sync(0xffffffffu, f.toks > 1);
+  return f;
+}
+
 // dH and dW: bf16 where the tile is the whole sum, else dH's sums in single
 // precision, set by the first piece and added to by the others.
 __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& maps,
-                                             const CeTile& t, uint32_t addr, int row0, CeOut& o) {
+                                             const CeTile& t, uint32_t addr, int row0, CeOut& o,
+                                             const CeFix& fix) {
   const int lane = threadIdx.x & 31;
   const bool dh = t.kind == 1;
   const int rows = dh ? p.N : p.nv, r0 = t.m0 + row0;
@@ -361,11 +450,22 @@ __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& ma
   for (int c0 = 0; c0 < cols; c0 += step) {
     const uint32_t box = ce_box_begin(o);
     for (int h = 0; h < step; h += 32) {
+      const int at = t.n0 + c0 + h;
+      CeRow row;
+      if (fix.toks > 0) row = ce_row(fix.src + at, p.D - at);
       float x[32];
       tmem_load32(addr + c0 + h, x);
       if (t.iters == 0) {  // a slice past the end of a short last piece
 #pragma unroll
         for (int c = 0; c < 32; ++c) x[c] = 0.0f;
+      }
+      if (fix.toks > 0) ce_add_row(x, row, fix.r);
+      if (fix.several) {
+        int nth = 0;
+        ce_tokens_of(p, r0, [&](int i) {
+          if (nth++ > 0)
+            ce_add_row(x, ce_row(p.h + (size_t)i * p.D + at, p.D - at), p.resid[i]);
+        });
       }
       if (sums) {
 #pragma unroll
@@ -514,6 +614,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       CeTile t = ce_tile<M>(p, i);
       if (t.kind < 0) break;
       t.m0 += rank * kMmHalf;
+      CeFix fix;
+      if (M == kCeGrads) fix = ce_fix(p, t, quarter * 32);
       const int acc = i & 1;
       if (!mbar_wait_cluster_bounded(&bars.tfull[acc], (i >> 1) & 1, &bars.abort_flag)) ok = false;
       if (!__all_sync(0xffffffffu, ok)) {
@@ -524,7 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       const uint32_t addr = tmem + acc * kMmN + ((uint32_t)(quarter * 32) << 16);
       if (M == kCeLoss) ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane);
       else if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, out);
-      else ce_grad_tile(p, maps, t, addr, quarter * 32, out);
+      else ce_grad_tile(p, maps, t, addr, quarter * 32, out, fix);
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(dsmem_map(&bars.tempty[acc], 0));
@@ -599,18 +701,30 @@ __global__ void __launch_bounds__(1024) ce_finish_kernel(CeParams p, float* nll,
   else nll[i] = __fmul_rn(__fadd_rn(gap, log2f(__fadd_rn(s, ex2(-gap)))), kLn2f);
 }
 
-// dH from its parts: the slices are added in order and rounded once.
+// dH from its parts: the slices are added in order, then what rounding took from
+// the label's entry, and rounded once.
 __global__ void __launch_bounds__(256)
-    ce_round_kernel(const float* acc, uint16_t* out, long long n, int splits) {
+    ce_round_kernel(const __grid_constant__ CeParams p, uint16_t* out) {
   pdl_wait();
+  const long long n = (long long)p.N * p.D;
   for (long long i = (blockIdx.x * 256LL + threadIdx.x) * 8; i < n; i += gridDim.x * 2048LL) {
     float x[8] = {};
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float4* a = reinterpret_cast<const float4*>(acc + s * n + i);
+    for (int s = 0; s < p.splits; ++s) {
+      const float4* a = reinterpret_cast<const float4*>(p.dh_acc + s * n + i);
       const float4 u = a[0], v = a[1];
       x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
       x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+    }
+    const int row = (int)(i / p.D), col = (int)(i - (long long)row * p.D);
+    const int y = __ldg(&p.labels[row]);
+    if (y >= 0 && y < p.V) {
+      float a[8];
+      ElemTraits<uint16_t>::unpack(
+          __ldg(reinterpret_cast<const uint4*>(p.w + (size_t)y * p.D + col)), a);
+      const float r = p.resid[row];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(r, a[e], x[e]);
     }
     *reinterpret_cast<uint4*>(out + i) = pack_vec<uint16_t>(x);
   }

@@ -97,6 +97,8 @@ inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLa
   p.z_label = reinterpret_cast<float*>(ws + lay.z_label);
   p.piece = lay.piece;
   p.dh_acc = reinterpret_cast<float*>(ws + lay.dh_acc);
+  p.resid = reinterpret_cast<float*>(ws + lay.resid);
+  p.in_tile = reinterpret_cast<uint32_t*>(ws + lay.in_tile);
   p.header = reinterpret_cast<WsHeader*>(ws);
   return p;
 }
@@ -132,6 +134,8 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
   if (device_info(&d) != cudaSuccess || ce_prepare(d) != cudaSuccess) return SPEC_ERR_CUDA;
   const CeLayout lay = ce_layout(N, V, D, true);
   CeParams p = ce_params(labels, N, V, D, lay, ws);
+  p.h = static_cast<const uint16_t*>(hidden);
+  p.w = static_cast<const uint16_t*>(weight);
   p.nll = nll;
   p.lse = lse;
   p.g = grad_nll;
@@ -170,8 +174,7 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
   if (d_hidden != nullptr && !lay.direct) {
     const long long n = (long long)N * D;
     if (launch(ce_round_kernel, dim3((unsigned)std::min<long long>(blocks_of(n, 2048), 1216)),
-               dim3(256), 0, s, true, (const float*)p.dh_acc, static_cast<uint16_t*>(d_hidden), n,
-               p.splits) != cudaSuccess)
+               dim3(256), 0, s, true, p, static_cast<uint16_t*>(d_hidden)) != cudaSuccess)
       return SPEC_ERR_CUDA;
   }
   return SPEC_OK;

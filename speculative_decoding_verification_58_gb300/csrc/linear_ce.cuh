@@ -21,7 +21,8 @@
 
 namespace specv {
 
-constexpr int kCeTileV = 256;      // vocabulary entries per (max, sum) pair
+constexpr int kCeTileV = 256;      // vocabulary entries per tile of the products
+constexpr int kCePartV = 128;      // and per (max, sum) pair
 constexpr int kCePieceBytes = 48 << 20;  // most bytes of a piece's dZ
 constexpr int kCeMaxTokens = SPEC_MAX_TOKENS;
 constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
@@ -29,6 +30,7 @@ constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
 struct CeLayout {
   size_t partials, z_label, resid, in_tile, dz, dh_acc, total;
   int tiles;  // vocabulary tiles
+  int parts;  // (max, sum) pairs of a token
   int piece;   // vocabulary entries per piece (a multiple of kCeTileV)
   int splits;  // slices of a piece whose parts of dH are summed apart
   bool direct;  // dH comes out of one tile whole: no sums to keep
@@ -83,11 +85,12 @@ inline int ce_splits(int N, int D, int piece) {
 inline CeLayout ce_layout(int N, int V, int D, bool grad) {
   CeLayout l = {};
   l.tiles = (V + kCeTileV - 1) / kCeTileV;
+  l.parts = (V + kCePartV - 1) / kCePartV;
   l.piece = grad ? ce_piece_tiles(N, l.tiles) * kCeTileV : 0;
   size_t o = align256(sizeof(WsHeader));
   if (!grad) {
     l.partials = o;
-    o = align256(o + (size_t)N * l.tiles * sizeof(float2));
+    o = align256(o + (size_t)N * l.parts * sizeof(float2));
     l.z_label = o;
     o = align256(o + (size_t)N * sizeof(float));
   } else {
@@ -111,8 +114,8 @@ struct CeParams {
   const float* nll;        // [N] (gradients)
   const float* lse;        // [N] (gradients)
   const float* g;          // [N] (gradients)
-  int N, V, D, tiles;
-  float2* partials;        // [tiles, N]: (max log2 e, sum 2^(z log2 e - max log2 e))
+  int N, V, D, parts;
+  float2* partials;        // [parts, N]: (max log2 e, sum 2^(z log2 e - max log2 e))
   float* z_label;          // [N]
   int piece, v0, nv;       // piece: buffer width, first entry, entries
   const uint16_t* h;       // [N, D]
@@ -131,8 +134,8 @@ struct CeParams {
 // ---------------------------------------------------------------------------
 // The products.  A persistent kernel of CTA pairs, one CTA per SM, on tiles of
 // 256 x 256 (rows 0..127 of a tile are the first CTA's): in each CTA a warp that
-// issues the TMA loads into a ring of six 64-deep stages and four warps that take
-// finished tiles out of tensor memory, in the first a warp that issues the
+// issues the TMA loads into a ring of six 64-deep stages and eight warps that take
+// finished tiles out of tensor memory (half a row each thread), in the first a warp that issues the
 // tcgen05.mma for both.  Two accumulators of 256 columns alternate, so that one
 // tile's epilogue runs under the next one's products.  A pair's CTAs each load one
 // half of either operand, 32 KB for the products of a stage; single CTAs on
@@ -150,10 +153,10 @@ constexpr int kMmM = 256, kMmN = 256, kMmK = 64, kMmStages = 6;
 constexpr int kMmHalf = 128;  // rows of A, of B and of the result in each CTA
 constexpr int kMmABytes = kMmHalf * kMmK * 2, kMmBBytes = kMmHalf * kMmK * 2;
 constexpr int kMmStageBytes = kMmABytes + kMmBBytes;  // each CTA's
-constexpr int kMmThreads = 192;
+constexpr int kMmThreads = 320;
 constexpr int kMmProducer = 0, kMmIssuer = 1, kMmEpilogue = 2;  // first warps of the roles
-// Results leave through two boxes of 32 rows x 128 bytes for each epilogue warp.
-constexpr int kMmBoxBytes = 32 * 128, kMmOutBytes = 4 * 2 * kMmBoxBytes;
+// Results leave through a box of 32 rows x 128 bytes for each epilogue warp.
+constexpr int kMmBoxBytes = 32 * 128, kMmOutBytes = 8 * kMmBoxBytes;
 constexpr int kMmSmem = kMmStages * kMmStageBytes + kMmOutBytes + 1024;  // + alignment
 
 struct CeMaps {
@@ -249,16 +252,16 @@ __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
   return t;
 }
 
-// Epilogue of one thread: row `m` of the tile, 256 columns of tensor memory.  The
-// label's logit goes to z_label and is left out of the sums.
+// Epilogue of one thread: row `m` of the tile, one half of its columns in tensor memory.
+// The label's logit goes to z_label and is left out of the sums.
 __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, uint32_t addr,
-                                            int m) {
+                                            int m, int half) {
   const bool live = m < p.N;
   const int y = live ? __ldg(&p.labels[m]) : -1;
-  const int cols = min(kMmN, p.V - t.n0);
+  const int from = half * kCePartV, cols = min(from + kCePartV, p.V - t.n0);
   // Below every logit: a tile of -inf keeps a finite maximum and a sum of 0.
   float ms = -FLT_MAX / 2, s = 0.0f;
-  for (int c0 = 0; c0 < cols; c0 += 32) {
+  for (int c0 = from; c0 < cols; c0 += 32) {
     float x[32];
     tmem_load32(addr + c0, x);
     if (c0 + 32 > cols) {
@@ -292,23 +295,18 @@ __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, 
     s = __fadd_rn(r.x, r.y);
     ms = nms;
   }
-  if (live) p.partials[(size_t)(t.n0 / kMmN) * p.N + m] = make_float2(ms, s);
+  if (live && from < cols)
+    p.partials[(size_t)(t.n0 / kCePartV + half) * p.N + m] = make_float2(ms, s);
 }
 
 // A warp's results go through shared memory: a box of 32 rows x 128 bytes, its
 // 16-byte pieces swizzled as the tensor map has them (no two lanes of a store meet in a
 // bank), then one TMA store.  Rows written by the lanes themselves, 16 bytes at a
 // time, were half sectors each and took as long as the products (2 x 230 us of
-// 1236 for 512 tokens, V = 151936, D = 2048).  Two boxes alternate.
-struct CeOut {
-  uint32_t base;  // the warp's two boxes
-  int n;          // boxes stored so far
-};
-
-__device__ __forceinline__ uint32_t ce_box_begin(const CeOut& o) {
-  if ((threadIdx.x & 31) == 0) bulk_wait_read<1>();
+// 1236 for 512 tokens, V = 151936, D = 2048).
+__device__ __forceinline__ void ce_box_begin() {
+  if ((threadIdx.x & 31) == 0) bulk_wait_read<0>();
   __syncwarp();
-  return o.base + (o.n & 1) * kMmBoxBytes;
 }
 
 // The lane's 16-byte piece `q` of its row.
@@ -323,26 +321,26 @@ __device__ __forceinline__ void ce_box_ready() {
 }
 
 __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps, const CeTile& t,
-                                           uint32_t addr, int row0, CeOut& o) {
+                                           uint32_t addr, int row0, int half, uint32_t box) {
   const int lane = threadIdx.x & 31, m = t.m0 + row0 + lane;
   int y = m < p.N ? __ldg(&p.labels[m]) : -1;
   const bool has = y >= 0 && y < p.V;
   const float g = has ? __ldg(&p.g[m]) : 0.0f;
   const float l2 = has ? __fmul_rn(__ldg(&p.lse[m]), kLog2e) : 0.0f;
   y -= p.v0 + t.n0;
-  const int cols = min(kMmN, p.nv - t.n0);
+  const int from = half * 128, cols = min(from + 128, p.nv - t.n0);
   // The label's entry is exp(-nll) - 1: from the loss itself, because for a token that
   // is well predicted the difference of its logit and lse has few bits left.
   const float at_label =
       has && y >= 0 && y < kMmN ? __fmul_rn(expm1f(-__ldg(&p.nll[m])), g) : 0.0f;
-  const bool here = has && y >= 0 && y < kMmN;
+  const bool here = has && y >= 0 && y < kMmN && half == 0;  // one of the two warps
   const uint32_t tokens = __ballot_sync(0xffffffffu, here);
-  if (lane == 0 && m < p.N)
+  if (lane == 0 && half == 0 && m < p.N)
     p.in_tile[(size_t)(t.n0 / kMmN) * ((p.N + 31) / 32) + m / 32] = tokens;
   if (here)
     p.resid[m] = __fsub_rn(at_label, __uint_as_float(pack_bf16(at_label, 0.0f) << 16));
-  for (int c0 = 0; c0 < cols; c0 += 64) {
-    const uint32_t box = ce_box_begin(o);
+  for (int c0 = from; c0 < cols; c0 += 64) {
+    ce_box_begin();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float x[32];
@@ -361,7 +359,6 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
       tma_store(&maps.dz_out, box, t.n0 + c0, t.m0 + row0);
       bulk_commit();
     }
-    ++o.n;
   }
 }
 
@@ -439,16 +436,16 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
 // dH and dW: bf16 where the tile is the whole sum, else dH's sums in single
 // precision, set by the first piece and added to by the others.
 __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& maps,
-                                             const CeTile& t, uint32_t addr, int row0, CeOut& o,
-                                             const CeFix& fix) {
+                                             const CeTile& t, uint32_t addr, int row0, int half,
+                                             uint32_t box, const CeFix& fix) {
   const int lane = threadIdx.x & 31;
   const bool dh = t.kind == 1;
   const int rows = dh ? p.N : p.nv, r0 = t.m0 + row0;
-  const int cols = min(kMmN, p.D - t.n0);
+  const int from = half * 128, cols = min(from + 128, p.D - t.n0);
   const bool sums = dh && !p.dh_direct;
   const int step = sums ? 32 : 64;
-  for (int c0 = 0; c0 < cols; c0 += step) {
-    const uint32_t box = ce_box_begin(o);
+  for (int c0 = from; c0 < cols; c0 += step) {
+    ce_box_begin();
     for (int h = 0; h < step; h += 32) {
       const int at = t.n0 + c0 + h;
       CeRow row;
@@ -482,7 +479,6 @@ __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& ma
       else tma_add3(&maps.acc, box, t.n0 + c0, r0, t.slice);
       bulk_commit();
     }
-    ++o.n;
   }
 }
 
@@ -517,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bars.tfull[a], 1);
-      mbar_init(&bars.tempty[a], 8);  // the epilogue warps of both CTAs
+      mbar_init(&bars.tempty[a], 16);  // the epilogue warps of both CTAs
     }
     bars.abort_flag = 0;
     bars.bad = 0;
@@ -609,7 +605,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   } else {
     if (p.check && blockIdx.x == 0) ce_check(p, &bars.bad);
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
-    CeOut out = {ring + kMmStages * kMmStageBytes + quarter * 2 * kMmBoxBytes, 0};
+    const int half = (warp - kMmEpilogue) >> 2;
+    const uint32_t box = ring + kMmStages * kMmStageBytes + (warp - kMmEpilogue) * kMmBoxBytes;
     for (int i = 0;; ++i) {
       CeTile t = ce_tile<M>(p, i);
       if (t.kind < 0) break;
@@ -624,9 +621,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       }
       tmem_fence_after();
       const uint32_t addr = tmem + acc * kMmN + ((uint32_t)(quarter * 32) << 16);
-      if (M == kCeLoss) ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane);
-      else if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, out);
-      else ce_grad_tile(p, maps, t, addr, quarter * 32, out, fix);
+      if (M == kCeLoss) ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half);
+      else if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, half, box);
+      else ce_grad_tile(p, maps, t, addr, quarter * 32, half, box, fix);
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(dsmem_map(&bars.tempty[acc], 0));
@@ -650,34 +647,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   if (warp == kMmIssuer) tmem_free(tmem, 512);
 }
 
-// Tokens' tiles into lse and nll: 32 tokens a CTA, 32 threads each over the tiles.
-__global__ void __launch_bounds__(1024) ce_finish_kernel(CeParams p, float* nll, float* lse) {
+// Tokens' pairs into lse and nll: `tokens` (a power of two up to 32) a CTA, the
+// other threads over each one's pairs, eight loads at a time.
+constexpr int kCeFinishThreads = 1024;
+__global__ void __launch_bounds__(kCeFinishThreads)
+    ce_finish_kernel(const __grid_constant__ CeParams p, int tokens, float* nll, float* lse) {
   pdl_wait();
-  __shared__ float sm[32][33];
-  const int tok = threadIdx.x & 31, grp = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + tok;
+  pdl_launch_dependents();
+  __shared__ float sm[kCeFinishThreads];
+  const int tid = threadIdx.x, tok = tid & (tokens - 1), groups = kCeFinishThreads / tokens;
+  const int i = blockIdx.x * tokens + tok;
   const float2* part = p.partials + i;
-  float m = -FLT_MAX / 2;
-  if (i < p.N)
-    for (int t = grp; t < p.tiles; t += 32) m = fmaxf(m, part[(size_t)t * p.N].x);
-  sm[grp][tok] = m;
-  __syncthreads();
-  float top = sm[0][tok];
-#pragma unroll 8
-  for (int k = 1; k < 32; ++k) top = fmaxf(top, sm[k][tok]);
-  __syncthreads();
-  float s = 0.0f;
-  if (i < p.N)
-    for (int t = grp; t < p.tiles; t += 32) {
-      const float2 q = part[(size_t)t * p.N];
-      s = fmaf(q.y, ex2(__fsub_rn(q.x, top)), s);
+  const float none = -FLT_MAX / 2;
+  float m = none, s = 0.0f;
+  if (i < p.N) {
+    for (int t = tid / tokens; t < p.parts; t += 8 * groups) {
+      float2 q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        q[j] = t + j * groups < p.parts ? part[(size_t)(t + j * groups) * p.N]
+                                        : make_float2(none, 0.0f);
+      float n = m;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) n = fmaxf(n, q[j].x);
+      s = __fmul_rn(s, ex2(__fsub_rn(m, n)));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fmaf(q[j].y, ex2(__fsub_rn(q[j].x, n)), s);
+      m = n;
     }
-  sm[grp][tok] = s;
+  }
+  // The CTA's maximum of each token, then its sum, by halves.
+  sm[tid] = m;
+  for (int o = kCeFinishThreads / 2; o >= tokens; o >>= 1) {
+    __syncthreads();
+    if (tid < o) sm[tid] = fmaxf(sm[tid], sm[tid + o]);
+  }
   __syncthreads();
-  if (grp != 0 || i >= p.N) return;
-  s = 0.0f;
-#pragma unroll 8
-  for (int k = 0; k < 32; ++k) s = __fadd_rn(s, sm[k][tok]);
+  const float top = sm[tok];
+  __syncthreads();
+  sm[tid] = __fmul_rn(s, ex2(__fsub_rn(m, top)));
+  for (int o = kCeFinishThreads / 2; o >= tokens; o >>= 1) {
+    __syncthreads();
+    if (tid < o) sm[tid] = __fadd_rn(sm[tid], sm[tid + o]);
+  }
+  if (tid >= tokens || i >= p.N) return;
+  s = sm[tid];
   const float nan = __int_as_float(0x7fc00000);
   const int y = p.labels[i];
   const bool has = y >= 0 && y < p.V;

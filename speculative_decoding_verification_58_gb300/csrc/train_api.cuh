@@ -92,7 +92,7 @@ inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLa
   p.N = N;
   p.V = V;
   p.D = D;
-  p.tiles = lay.tiles;
+  p.parts = lay.parts;
   p.partials = reinterpret_cast<float2*>(ws + lay.partials);
   p.z_label = reinterpret_cast<float*>(ws + lay.z_label);
   p.piece = lay.piece;
@@ -120,8 +120,10 @@ inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32
     return SPEC_ERR_CUDA;
   if (launch_ce<kCeLoss>(d, maps, p, blocks_of(N, kMmM) * lay.tiles, s) != cudaSuccess)
     return SPEC_ERR_CUDA;
-  if (launch(ce_finish_kernel, dim3((unsigned)blocks_of(N, 32)), dim3(1024), 0, s, true, p, nll,
-             lse) != cudaSuccess)
+  int tokens = 1;
+  while (tokens < 32 && tokens < N) tokens *= 2;
+  if (launch(ce_finish_kernel, dim3((unsigned)blocks_of(N, tokens)), dim3(kCeFinishThreads), 0, s,
+             true, p, tokens, nll, lse) != cudaSuccess)
     return SPEC_ERR_CUDA;
   return SPEC_OK;
 }

@@ -23,7 +23,7 @@ namespace specv {
 
 constexpr int kCeTileV = 256;      // vocabulary entries per tile of the products
 constexpr int kCePartV = 128;      // and per (max, sum) pair
-constexpr int kCePieceBytes = 48 << 20;  // most bytes of a piece's dZ
+constexpr int kCePieceBytes = 160 << 20;  // most bytes of a piece's dZ
 constexpr int kCeMaxTokens = SPEC_MAX_TOKENS;
 constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
 
@@ -127,6 +127,7 @@ struct CeParams {
   int first;               // first piece: dh_acc is set, not added to
   int splits, split_iters;  // slices of the piece in dH, 64-entry steps of a slice
   int dh_units, dw_units;  // units of the two products (0: not wanted)
+  int a_rows;              // rows of A in a box (fewer than 128 where there are fewer tokens)
   int check;               // CTA 0 checks the labels and writes the header
   WsHeader* header;
 };
@@ -155,8 +156,9 @@ constexpr int kMmABytes = kMmHalf * kMmK * 2, kMmBBytes = kMmHalf * kMmK * 2;
 constexpr int kMmStageBytes = kMmABytes + kMmBBytes;  // each CTA's
 constexpr int kMmThreads = 320;
 constexpr int kMmProducer = 0, kMmIssuer = 1, kMmEpilogue = 2;  // first warps of the roles
-// Results leave through a box of 32 rows x 128 bytes for each epilogue warp.
-constexpr int kMmBoxBytes = 32 * 128, kMmOutBytes = 8 * kMmBoxBytes;
+// Results leave through kMmBoxes boxes of 32 rows x 128 bytes for each epilogue warp.
+constexpr int kMmBoxes = 1;
+constexpr int kMmBoxBytes = 32 * 128, kMmOutBytes = 8 * kMmBoxes * kMmBoxBytes;
 constexpr int kMmSmem = kMmStages * kMmStageBytes + kMmOutBytes + 1024;  // + alignment
 
 struct CeMaps {
@@ -304,9 +306,15 @@ __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, 
 // bank), then one TMA store.  Rows written by the lanes themselves, 16 bytes at a
 // time, were half sectors each and took as long as the products (2 x 230 us of
 // 1236 for 512 tokens, V = 151936, D = 2048).
-__device__ __forceinline__ void ce_box_begin() {
-  if ((threadIdx.x & 31) == 0) bulk_wait_read<0>();
+struct CeOut {
+  uint32_t base;  // the warp's boxes
+  int n;          // boxes stored so far
+};
+
+__device__ __forceinline__ uint32_t ce_box_begin(CeOut& o) {
+  if ((threadIdx.x & 31) == 0) bulk_wait_read<kMmBoxes - 1>();
   __syncwarp();
+  return o.base + (o.n++ % kMmBoxes) * kMmBoxBytes;
 }
 
 // The lane's 16-byte piece `q` of its row.
@@ -321,7 +329,7 @@ __device__ __forceinline__ void ce_box_ready() {
 }
 
 __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps, const CeTile& t,
-                                           uint32_t addr, int row0, int half, uint32_t box) {
+                                           uint32_t addr, int row0, int half, CeOut& o) {
   const int lane = threadIdx.x & 31, m = t.m0 + row0 + lane;
   int y = m < p.N ? __ldg(&p.labels[m]) : -1;
   const bool has = y >= 0 && y < p.V;
@@ -340,7 +348,7 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
   if (here)
     p.resid[m] = __fsub_rn(at_label, __uint_as_float(pack_bf16(at_label, 0.0f) << 16));
   for (int c0 = from; c0 < cols; c0 += 64) {
-    ce_box_begin();
+    const uint32_t box = ce_box_begin(o);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float x[32];
@@ -437,7 +445,7 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
 // precision, set by the first piece and added to by the others.
 __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& maps,
                                              const CeTile& t, uint32_t addr, int row0, int half,
-                                             uint32_t box, const CeFix& fix) {
+                                             CeOut& o, const CeFix& fix) {
   const int lane = threadIdx.x & 31;
   const bool dh = t.kind == 1;
   const int rows = dh ? p.N : p.nv, r0 = t.m0 + row0;
@@ -445,7 +453,7 @@ __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& ma
   const bool sums = dh && !p.dh_direct;
   const int step = sums ? 32 : 64;
   for (int c0 = from; c0 < cols; c0 += step) {
-    ce_box_begin();
+    const uint32_t box = ce_box_begin(o);
     for (int h = 0; h < step; h += 32) {
       const int at = t.n0 + c0 + h;
       CeRow row;
@@ -546,14 +554,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           const uint32_t a = ring + s * kMmStageBytes, b = a + kMmABytes;
           // Both CTAs' loads complete on the first one's barrier.
           const uint32_t bar = dsmem_map(&bars.full[s], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * kMmStageBytes);
+          // Rows of A past the last token are not loaded where the tile is the only
+          // one: what is left there reaches rows of the result that nobody reads.
+          const bool a_mn = t.kind == 2, all_a = a_mn || p.a_rows == kMmHalf;
+          if (rank == 0)
+            mbar_arrive_expect_tx(&bars.full[s], 2 * kMmBBytes + (all_a ? 2 * kMmABytes
+                                                                        : p.a_rows * kMmK * 2));
           const int k0 = t.k0 + k * kMmK;
           if (M != kCeGrads) {
-            tma_load(a, &maps.h_k, k0, am, bar);
+            if (all_a || rank == 0) tma_load(a, &maps.h_k, k0, am, bar);
             tma_load(b, &maps.w_k, k0, (M == kCeDz ? p.v0 : 0) + bn, bar);
           } else {
-            if (t.kind == 1) {
-              tma_load(a, &maps.dz_k, k0, am, bar);
+            if (!a_mn) {
+              if (all_a || rank == 0) tma_load(a, &maps.dz_k, k0, am, bar);
             } else {
               for (int c = 0; c < kMmHalf; c += 64)
                 tma_load(a + c * 128, &maps.dz_mn, am + c, k0, bar);
@@ -606,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     if (p.check && blockIdx.x == 0) ce_check(p, &bars.bad);
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
     const int half = (warp - kMmEpilogue) >> 2;
-    const uint32_t box = ring + kMmStages * kMmStageBytes + (warp - kMmEpilogue) * kMmBoxBytes;
+    CeOut out = {ring + kMmStages * kMmStageBytes + (warp - kMmEpilogue) * kMmBoxes * kMmBoxBytes, 0};
     for (int i = 0;; ++i) {
       CeTile t = ce_tile<M>(p, i);
       if (t.kind < 0) break;
@@ -622,8 +635,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       tmem_fence_after();
       const uint32_t addr = tmem + acc * kMmN + ((uint32_t)(quarter * 32) << 16);
       if (M == kCeLoss) ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half);
-      else if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, half, box);
-      else ce_grad_tile(p, maps, t, addr, quarter * 32, half, box, fix);
+      else if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);
+      else ce_grad_tile(p, maps, t, addr, quarter * 32, half, out, fix);
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(dsmem_map(&bars.tempty[acc], 0));

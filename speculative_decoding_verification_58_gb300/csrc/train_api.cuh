@@ -93,6 +93,7 @@ inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLa
   p.V = V;
   p.D = D;
   p.parts = lay.parts;
+  p.a_rows = N < kMmHalf ? (N + 7) / 8 * 8 : kMmHalf;
   p.partials = reinterpret_cast<float2*>(ws + lay.partials);
   p.z_label = reinterpret_cast<float*>(ws + lay.z_label);
   p.piece = lay.piece;
@@ -115,7 +116,7 @@ inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32
   CeParams p = ce_params(labels, N, V, D, lay, ws);
   p.check = 1;
   CeMaps maps = {};
-  if (!ce_map(&maps.h_k, hidden, N, D, D, kMmHalf) ||
+  if (!ce_map(&maps.h_k, hidden, N, D, D, p.a_rows) ||
       !ce_map(&maps.w_k, weight, V, D, D, kMmHalf))
     return SPEC_ERR_CUDA;
   if (launch_ce<kCeLoss>(d, maps, p, blocks_of(N, kMmM) * lay.tiles, s) != cudaSuccess)
@@ -145,7 +146,7 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
   p.dh_direct = lay.direct;
   void* dz = ws + lay.dz;
   CeMaps maps = {};
-  if (!ce_map(&maps.h_k, hidden, N, D, D, kMmHalf) ||
+  if (!ce_map(&maps.h_k, hidden, N, D, D, p.a_rows) ||
       !ce_map(&maps.w_k, weight, V, D, D, kMmHalf) ||
       !ce_map(&maps.h_mn, hidden, N, D, D, 64) || !ce_map(&maps.w_mn, weight, V, D, D, 64))
     return SPEC_ERR_CUDA;
@@ -164,7 +165,7 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
     p.dw_units = d_weight != nullptr ? (int)(blocks_of(p.nv, kMmM) * db) : 0;
     // dZ's own extent: what its last tile has past the vocabulary is not written,
     // and reads as 0.
-    if (!ce_map(&maps.dz_k, dz, N, p.nv, lay.piece, kMmHalf) ||
+    if (!ce_map(&maps.dz_k, dz, N, p.nv, lay.piece, p.a_rows) ||
         !ce_map(&maps.dz_mn, dz, N, p.nv, lay.piece, 64) ||
         !ce_map(&maps.dz_out, dz, N, p.nv, lay.piece, 32))
       return SPEC_ERR_CUDA;

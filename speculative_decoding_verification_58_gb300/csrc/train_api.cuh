@@ -258,52 +258,79 @@ inline size_t grad_norm_ws(int count) {
   return align256(launches * kNormMaxCtas * sizeof(NormPartial));
 }
 
-inline spec_status_t norm_run(const void* const* grads, void* const* outs, const long long* sizes,
-                              const int* dtypes, int count, float max_norm, float* norm,
-                              void* workspace, cudaStream_t s, bool clip) {
-  NvtxRange r(clip ? "spec_clip_grad_norm" : "spec_grad_norm");
-  DeviceInfo* d = nullptr;
-  if (device_info(&d) != cudaSuccess) return SPEC_ERR_CUDA;
-  NormPartial* partials = static_cast<NormPartial*>(workspace);
+// Tensors from t on that are not empty, up to a launch's number: their descriptors.
+// Returns how many units they have.
+template <int kN>
+int norm_fill(NormBatch<kN>& batch, const void* const* grads, void* const* outs,
+              const long long* sizes, const int* dtypes, int count, bool clip, int& t) {
+  batch.count = 0;
+  int units = 0;
+  batch.first_unit[0] = 0;
+  for (; t < count && batch.count < kN; ++t) {
+    if (sizes[t] == 0) continue;
+    const int c = batch.count;
+    const int es = dtypes[t] == SPEC_BF16 ? 2 : 4;
+    void* out = clip ? (outs != nullptr ? outs[t] : const_cast<void*>(grads[t])) : nullptr;
+    batch.in[c] = grads[t];
+    batch.out[c] = out;
+    batch.n[c] = sizes[t];
+    batch.bf16[c] = es == 2;
+    units += (int)norm_units(grads[t], out, sizes[t], es);
+    batch.first_unit[++batch.count] = units;
+  }
+  return units;
+}
+
+template <int kN>
+spec_status_t norm_launches(const void* const* grads, void* const* outs, const long long* sizes,
+                            const int* dtypes, int count, float max_norm, float* norm,
+                            NormPartial* partials, cudaStream_t s, bool clip, int most) {
+  NormBatch<kN> batch;
   int parts = 0;
-  NormBatch batch;
-  const int most = std::min(kNormMaxCtas, d->sms * kNormCtasPerSm);
   for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
     int t = 0;
-    do {  // batches of tensors that are not empty; the norm of nothing is 0
-      batch.count = 0;
-      long long units = 0;
-      for (; t < count && batch.count < kNormTensors; ++t) {
-        if (sizes[t] == 0) continue;
-        const int c = batch.count;
-        const int es = dtypes[t] == SPEC_BF16 ? 2 : 4;
-        void* out = clip ? (outs != nullptr ? outs[t] : const_cast<void*>(grads[t])) : nullptr;
-        const long long u = norm_units(grads[t], out, sizes[t], es);
-        batch.in[c] = grads[t];
-        batch.out[c] = out;
-        batch.n[c] = sizes[t];
-        batch.bf16[c] = es == 2;
-        batch.first_unit[c] = (int)units;
-        units += u;
-        batch.first_unit[++batch.count] = (int)units;
-      }
-      if (batch.count == 0) batch.first_unit[0] = 0;
-      const int grid = (int)std::max<long long>(1, std::min<long long>(units, most));
+    do {  // (the norm of nothing is 0)
+      const int units = norm_fill(batch, grads, outs, sizes, dtypes, count, clip, t);
+      const int grid = std::max(1, std::min(units, most));
       if (pass == 0) {
-        if (launch(grad_norm_kernel, dim3(grid), dim3(kNormThreads), 0, s, true, batch,
+        if (launch(grad_norm_kernel<kN>, dim3(grid), dim3(kNormThreads), 0, s, true, batch,
                    partials + parts) != cudaSuccess)
           return SPEC_ERR_CUDA;
         parts += grid;
-      } else if (launch(clip_kernel, dim3(grid), dim3(kNormThreads), 0, s, true, batch,
+      } else if (launch(clip_kernel<kN>, dim3(grid), dim3(kNormThreads), 0, s, true, batch,
                         (const NormPartial*)partials, parts, max_norm, norm) != cudaSuccess) {
         return SPEC_ERR_CUDA;
       }
     } while (t < count);
   }
-  if (!clip && launch(grad_norm_finish_kernel, dim3(1), dim3(32), 0, s, true,
+  if (!clip && launch(grad_norm_finish_kernel, dim3(1), dim3(kNormThreads), 0, s, true,
                       (const NormPartial*)partials, parts, norm) != cudaSuccess)
     return SPEC_ERR_CUDA;
   return SPEC_OK;
+}
+
+inline spec_status_t norm_run(const void* const* grads, void* const* outs, const long long* sizes,
+                              const int* dtypes, int count, long long units, float max_norm,
+                              float* norm, void* workspace, cudaStream_t s, bool clip) {
+  NvtxRange r(clip ? "spec_clip_grad_norm" : "spec_grad_norm");
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != cudaSuccess) return SPEC_ERR_CUDA;
+  NormPartial* partials = static_cast<NormPartial*>(workspace);
+  const int most = std::min(kNormMaxCtas, d->sms * kNormCtasPerSm);
+  if (count <= kNormFewTensors && units <= kNormFewUnits) {
+    NormBatch<kNormFewTensors> batch;
+    int t = 0;
+    norm_fill(batch, grads, outs, sizes, dtypes, count, clip, t);
+    return launch(clip_few_kernel, dim3(kNormCluster), dim3(kNormThreads), 0, s, true, batch,
+                  max_norm, clip, norm) == cudaSuccess
+               ? SPEC_OK
+               : SPEC_ERR_CUDA;
+  }
+  if (count <= kNormFewTensors)
+    return norm_launches<kNormFewTensors>(grads, outs, sizes, dtypes, count, max_norm, norm,
+                                          partials, s, clip, most);
+  return norm_launches<kNormTensors>(grads, outs, sizes, dtypes, count, max_norm, norm, partials, s,
+                                     clip, most);
 }
 
 // The byte ranges of a clip's tensors: no output may share a byte with another
@@ -369,7 +396,7 @@ inline spec_status_t norm_entry(const void* const* grads, void* const* outs,
     return SPEC_ERR_WORKSPACE;
   DeviceOf on_device(norm);
   if (!on_device.ok()) return SPEC_ERR_CUDA;
-  return norm_run(grads, outs, sizes, dtypes, count, max_norm, norm, workspace,
+  return norm_run(grads, outs, sizes, dtypes, count, units, max_norm, norm, workspace,
                   static_cast<cudaStream_t>(stream), clip);
 }
 

@@ -633,7 +633,10 @@ def spec_d3d_select(num_accepted, out_tokens, branch_pos, branch_tok, branch_blo
 
 def _stream_on(stream, device) -> int:
     """The given stream, or the current one of the tensors' own device."""
-    return _stream_ptr(_torch().cuda.current_stream(device) if stream is None else stream)
+    if stream is None:
+        # The handle alone: making a torch.cuda.Stream costs as much as the C call.
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
+    return _stream_ptr(stream)
 
 
 def _need_cuda(t, name):

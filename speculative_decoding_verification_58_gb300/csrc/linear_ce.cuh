@@ -528,6 +528,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     fence_mbar_init();
   }
   if (warp == kMmIssuer) tmem_alloc(&bars.tmem, 512);
+  if (warp == kMmProducer && lane < 6) {  // the maps this kernel loads from
+    const CUtensorMap* m = lane == 0   ? &maps.h_k
+                           : lane == 1 ? &maps.w_k
+                           : lane == 2 ? &maps.dz_k
+                           : lane == 3 ? &maps.h_mn
+                           : lane == 4 ? &maps.w_mn
+                                       : &maps.dz_mn;
+    if (M == kCeGrads ? lane >= 2 : lane < 2) tma_prefetch_map(m);
+  }
   tmem_fence_before();
   cluster_sync();  // both CTAs' barriers are there
   tmem_fence_after();
@@ -641,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(dsmem_map(&bars.tempty[acc], 0));
     }
-    if (M != kCeLoss && lane == 0) bulk_wait_all();
+    if (M != kCeLoss && lane == 0) bulk_wait_read<0>();
   }
   if (!ok) {
     *(volatile int*)&bars.abort_flag = 1;

@@ -391,53 +391,71 @@ __device__ __forceinline__ void ce_add_row(float (&x)[32], const CeRow& row, flo
   }
 }
 
-// The tokens whose label is this lane's entry, r0 + lane of the piece: f(token) for
-// each, in order.
-template <typename F>
-__device__ __forceinline__ void ce_tokens_of(const CeParams& p, int r0, F&& f) {
-  const int lane = threadIdx.x & 31, words = (p.N + 31) / 32;
-  const uint32_t* in_tile = p.in_tile + (size_t)(r0 / kMmN) * words;
-  for (int base = 0; base < words; base += 32) {
-    const uint32_t mine = base + lane < words ? __ldg(in_tile + base + lane) : 0;
-    for (uint32_t some = __ballot_sync(0xffffffffu, mine != 0); some != 0; some &= some - 1) {
-      const int src = __ffs(some) - 1, i = (base + src) * 32 + lane;
-      const uint32_t word = __shfl_sync(0xffffffffu, mine, src);
-      const int rel = (word >> lane) & 1 ? __ldg(&p.labels[i]) - p.v0 - r0 : -1;
-      for (uint32_t m = __ballot_sync(0xffffffffu, rel >= 0 && rel < 32); m != 0; m &= m - 1) {
-        const int j = __ffs(m) - 1;
-        if (__shfl_sync(0xffffffffu, rel, j) == lane) f((base + src) * 32 + j);
-      }
-    }
-  }
-}
-
 // Whose rounding residual a lane's row takes: of dH the row's own token, of dW the
-// tokens with this label.  `src`: where the row to add starts.
+// first kCeFixes tokens with this label (in order; a row with more of them is a sum
+// in which their roundings, independent of one another, are no more than those of the
+// tokens that follow).  `src`: where the row to add starts.
+constexpr int kCeFixes = 4;
 struct CeFix {
-  int tok, toks;  // the first token, how many
-  bool several;   // some lane of the warp has more than one
-  const uint16_t* src;
-  float r;
+  int toks;
+  const uint16_t* src[kCeFixes];
+  float r[kCeFixes];
 };
 __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int row0) {
   const int lane = threadIdx.x & 31, r0 = t.m0 + row0;
-  CeFix f = {-1, 0, false, nullptr, 0.0f};
+  CeFix f;
+  f.toks = 0;
   if (t.kind == 1) {
     // (Sums of several slices or pieces get theirs at the end.)
     const int y = p.dh_direct && r0 + lane < p.N ? __ldg(&p.labels[r0 + lane]) : -1;
     if (y >= 0 && y < p.V) {
-      f.tok = r0 + lane;
       f.toks = 1;
-      f.src = p.w + (size_t)y * p.D;
+      f.src[0] = p.w + (size_t)y * p.D;
+      f.r[0] = p.resid[r0 + lane];
     }
-  } else if (r0 < p.nv) {
-    ce_tokens_of(p, r0, [&](int i) {
-      if (f.toks++ == 0) f.tok = i;
-    });
-    if (f.toks > 0) f.src = p.h + (size_t)SPEC_CHECKED(f.tok, p.N, kSiteLinearCe) * p.D;
+    return f;
   }
-  if (f.toks > 0) f.r = p.resid[f.tok];
-  f.several = __any_sync(0xffffffffu, f.toks > 1);
+  if (r0 >= p.nv) return f;
+  int tok[kCeFixes];
+#pragma unroll
+  for (int k = 0; k < kCeFixes; ++k) tok[k] = 0;
+  const int words = (p.N + 31) / 32;
+  const uint32_t* in_tile = p.in_tile + (size_t)(r0 / kMmN) * words;
+  for (int base = 0; base < words; base += 32) {
+    const uint32_t mine = base + lane < words ? __ldg(in_tile + base + lane) : 0;
+    uint32_t some = __ballot_sync(0xffffffffu, mine != 0);
+    while (some != 0) {
+      // Up to four words with tokens at a time: their labels' loads go together.
+      int first[4], rel[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        first[k] = some != 0 ? __ffs(some) - 1 : -1;
+        some &= some - 1;
+        const uint32_t word = __shfl_sync(0xffffffffu, mine, first[k] < 0 ? 0 : first[k]);
+        const bool bit = first[k] >= 0 && ((word >> lane) & 1);
+        rel[k] = bit ? __ldg(&p.labels[(base + first[k]) * 32 + lane]) - p.v0 - r0 : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t m = __ballot_sync(0xffffffffu, rel[k] >= 0 && rel[k] < 32);
+        for (; m != 0; m &= m - 1) {
+          const int j = __ffs(m) - 1;
+          if (__shfl_sync(0xffffffffu, rel[k], j) == lane) {
+#pragma unroll
+            for (int q = 0; q < kCeFixes; ++q)
+              if (f.toks == q) tok[q] = (base + first[k]) * 32 + j;
+            f.toks = min(f.toks + 1, kCeFixes);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kCeFixes; ++q)
+    if (q < f.toks) {
+      f.src[q] = p.h + (size_t)SPEC_CHECKED(tok[q], p.N, kSiteLinearCe) * p.D;
+      f.r[q] = p.resid[tok[q]];
+    }
   return f;
 }
 
@@ -457,21 +475,17 @@ __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& ma
     for (int h = 0; h < step; h += 32) {
       const int at = t.n0 + c0 + h;
       CeRow row;
-      if (fix.toks > 0) row = ce_row(fix.src + at, p.D - at);
+      if (fix.toks > 0) row = ce_row(fix.src[0] + at, p.D - at);
       float x[32];
       tmem_load32(addr + c0 + h, x);
       if (t.iters == 0) {  // a slice past the end of a short last piece
 #pragma unroll
         for (int c = 0; c < 32; ++c) x[c] = 0.0f;
       }
-      if (fix.toks > 0) ce_add_row(x, row, fix.r);
-      if (fix.several) {
-        int nth = 0;
-        ce_tokens_of(p, r0, [&](int i) {
-          if (nth++ > 0)
-            ce_add_row(x, ce_row(p.h + (size_t)i * p.D + at, p.D - at), p.resid[i]);
-        });
-      }
+      if (fix.toks > 0) ce_add_row(x, row, fix.r[0]);
+#pragma unroll
+      for (int q = 1; q < kCeFixes; ++q)
+        if (q < fix.toks) ce_add_row(x, ce_row(fix.src[q] + at, p.D - at), fix.r[q]);
       if (sums) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) ce_box_put(box, q, pack_vec<float>(x + q * 4));
@@ -737,33 +751,45 @@ __global__ void __launch_bounds__(kCeFinishThreads)
   else nll[i] = __fmul_rn(__fadd_rn(gap, log2f(__fadd_rn(s, ex2(-gap)))), kLn2f);
 }
 
-// dH from its parts: the slices are added in order, then what rounding took from
-// the label's entry, and rounded once.
+// dH from its parts: the slices are added in a fixed order, then what rounding took
+// from the label's entry, and rounded once.  A CTA does 32 groups of eight entries, eight
+// threads over the slices of each.
 __global__ void __launch_bounds__(256)
     ce_round_kernel(const __grid_constant__ CeParams p, uint16_t* out) {
   pdl_wait();
+  pdl_launch_dependents();
+  __shared__ float part[8][32][9];
   const long long n = (long long)p.N * p.D;
-  for (long long i = (blockIdx.x * 256LL + threadIdx.x) * 8; i < n; i += gridDim.x * 2048LL) {
-    float x[8] = {};
+  const int g = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const long long i = (blockIdx.x * 32LL + g) * 8;
+  float x[8] = {};
+  if (i < n) {
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
+    for (int s = sl; s < p.splits; s += 8) {
       const float4* a = reinterpret_cast<const float4*>(p.dh_acc + s * n + i);
       const float4 u = a[0], v = a[1];
       x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
       x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
     }
-    const int row = (int)(i / p.D), col = (int)(i - (long long)row * p.D);
-    const int y = __ldg(&p.labels[row]);
-    if (y >= 0 && y < p.V) {
-      float a[8];
-      ElemTraits<uint16_t>::unpack(
-          __ldg(reinterpret_cast<const uint4*>(p.w + (size_t)y * p.D + col)), a);
-      const float r = p.resid[row];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(r, a[e], x[e]);
-    }
-    *reinterpret_cast<uint4*>(out + i) = pack_vec<uint16_t>(x);
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) part[sl][g][e] = x[e];
+  __syncthreads();
+  if (sl != 0 || i >= n) return;
+  for (int k = 1; k < min(8, p.splits); ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += part[k][g][e];
+  const int row = (int)(i / p.D), col = (int)(i - (long long)row * p.D);
+  const int y = __ldg(&p.labels[row]);
+  if (y >= 0 && y < p.V) {
+    float a[8];
+    ElemTraits<uint16_t>::unpack(
+        __ldg(reinterpret_cast<const uint4*>(p.w + (size_t)y * p.D + col)), a);
+    const float r = p.resid[row];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = fmaf(r, a[e], x[e]);
+  }
+  *reinterpret_cast<uint4*>(out + i) = pack_vec<uint16_t>(x);
 }
 
 }  // namespace specv

@@ -176,8 +176,7 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
   }
   if (d_hidden != nullptr && !lay.direct) {
     const long long n = (long long)N * D;
-    if (launch(ce_round_kernel, dim3((unsigned)std::min<long long>(blocks_of(n, 2048), 1216)),
-               dim3(256), 0, s, true, p, static_cast<uint16_t*>(d_hidden)) != cudaSuccess)
+    if (launch(ce_round_kernel, dim3((unsigned)blocks_of(n, 256)), dim3(256), 0, s, true, p, static_cast<uint16_t*>(d_hidden)) != cudaSuccess)
       return SPEC_ERR_CUDA;
   }
   return SPEC_OK;

@@ -28,7 +28,7 @@ constexpr int kCeMaxTokens = SPEC_MAX_TOKENS;
 constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
 
 struct CeLayout {
-  size_t partials, z_label, resid, in_tile, dz, dh_acc, total;
+  size_t partials, z_label, resid, in_rows, dz, dh_acc, total;
   int tiles;  // vocabulary tiles
   int parts;  // (max, sum) pairs of a token
   int piece;   // vocabulary entries per piece (a multiple of kCeTileV)
@@ -96,8 +96,8 @@ inline CeLayout ce_layout(int N, int V, int D, bool grad) {
   } else {
     l.resid = o;
     o = align256(o + (size_t)N * sizeof(float));
-    l.in_tile = o;
-    o = align256(o + (size_t)(l.piece / kCeTileV) * ((N + 31) / 32) * sizeof(uint32_t));
+    l.in_rows = o;
+    o = align256(o + (size_t)(l.piece / 32) * ((N + 31) / 32) * sizeof(uint32_t));
     l.dz = o;
     o = align256(o + (size_t)N * l.piece * 2);
     l.splits = ce_splits(N, D, l.piece);
@@ -107,6 +107,46 @@ inline CeLayout ce_layout(int N, int V, int D, bool grad) {
   }
   l.total = o;
   return l;
+}
+
+// Units of dH and dW over the pairs.  A unit of dH costs split_iters steps, one of
+// dW as many as the tokens need, each some more for its epilogue.  The units of dH
+// go round, so that the first `more` pairs have one more of them; dW's are dealt to
+// bring every pair up to the same level (w1 to each of the first `more` pairs, w0 to
+// each of the others), and those that are left go round.  Worked out on the host.
+struct CeDeal {
+  int h, more;  // dH units of every pair, pairs with one more
+  int w0, w1;   // dW units under the level
+};
+constexpr int kCeEpilogueSteps = 6;  // an epilogue's time, in steps
+inline CeDeal ce_deal(int dh_units, int dw_units, int dh_iters, int dw_iters, int G) {
+  CeDeal d;
+  d.h = dh_units / G;
+  d.more = dh_units % G;
+  const int less = G - d.more;
+  const long long ch = dh_iters + kCeEpilogueSteps, cw = dw_iters + kCeEpilogueSteps;
+  const long long level = ((long long)dh_units * ch + (long long)dw_units * cw) / G;
+  const long long w0 = level > d.h * ch ? (level - d.h * ch) / cw : 0;
+  d.w0 = (int)std::min<long long>(w0, dw_units / less);
+  const long long w1 = d.more > 0 && level > (d.h + 1) * ch ? (level - (d.h + 1) * ch) / cw : 0;
+  d.w1 = d.more > 0
+             ? (int)std::min<long long>(w1, (dw_units - (long long)d.w0 * less) / d.more)
+             : 0;
+  return d;
+}
+// Pair c's i-th unit, dH's first, then dh_units + dW's; -1: no more.
+__host__ __device__ inline int ce_unit(const CeDeal& d, int dh_units, int dw_units, int G, int c,
+                                       int i) {
+  const bool first = c < d.more;
+  const int mine = d.h + (first ? 1 : 0), less = G - d.more;
+  if (i < mine) return i * G + c;
+  int j = i - mine;
+  const int w = first ? d.w1 : d.w0;
+  if (j < w) return dh_units + (first ? d.w0 * less + j * d.more + c : j * less + (c - d.more));
+  j -= w;
+  const long long idx = (long long)d.w0 * less + (long long)d.w1 * d.more + (long long)j * G +
+                        (G - 1 - c);
+  return idx < dw_units ? dh_units + (int)idx : -1;
 }
 
 struct CeParams {
@@ -121,12 +161,14 @@ struct CeParams {
   const uint16_t* h;       // [N, D]
   const uint16_t* w;       // [V, D]
   float* resid;            // [N]: the label's entry of dZ less its bf16 rounding
-  uint32_t* in_tile;       // [piece's tiles, N / 32]: tokens whose label is in the tile
+  uint32_t* in_rows;       // [piece / 32, N / 32]: tokens whose label is one of 32 entries
   float* dh_acc;           // [splits, N, D]
   int dh_direct;           // dH comes out of one tile whole
   int first;               // first piece: dh_acc is set, not added to
   int splits, split_iters;  // slices of the piece in dH, 64-entry steps of a slice
+  int z_tiles, m_blocks;   // tiles of z, of which so many are one vocabulary tile's
   int dh_units, dw_units;  // units of the two products (0: not wanted)
+  CeDeal deal;             // and how the pairs share them
   int a_rows;              // rows of A in a box (fewer than 128 where there are fewer tokens)
   int check;               // CTA 0 checks the labels and writes the header
   WsHeader* header;
@@ -182,74 +224,41 @@ struct CeTile {
   int slice;      // dH: which of the sums kept apart
 };
 
-// Units of dH and dW over the pairs.  A unit of dH costs split_iters steps, one of
-// dW as many as the tokens need, each some more for its epilogue.  The units of dH
-// go round, so that the first `more` pairs have one more of them; dW's are dealt to
-// bring every pair up to the same level, and those that are left go round.
-// Returns the index of pair c's i-th unit, dH's first; -1: no more.
-constexpr int kCeEpilogueSteps = 6;  // an epilogue's time, in steps
-__host__ __device__ inline long long ce_unit(int dh_units, int dw_units, int dh_iters, int dw_iters,
-                                             int G, int c, int i) {
-  const int h = dh_units / G, more = dh_units % G, less = G - more;
-  const int mine = h + (c < more ? 1 : 0);
-  if (i < mine) return (long long)i * G + c;
-  int j = i - mine;
-  const long long ch = dh_iters + kCeEpilogueSteps, cw = dw_iters + kCeEpilogueSteps;
-  const long long level = ((long long)dh_units * ch + (long long)dw_units * cw) / G;
-  // dW units that fit under the level: w1 for each of the first `more` pairs, w0
-  // for each of the others.
-  long long w0 = level > h * ch ? (level - h * ch) / cw : 0;
-  if (w0 > dw_units / less) w0 = dw_units / less;
-  long long w1 = more > 0 && level > (h + 1) * ch ? (level - (h + 1) * ch) / cw : 0;
-  if (more > 0 && w1 > (dw_units - w0 * less) / more) w1 = (dw_units - w0 * less) / more;
-  if (c >= more) {
-    if (j < w0) return dh_units + (long long)j * less + (c - more);
-    j -= (int)w0;
-  } else {
-    if (j < w1) return dh_units + w0 * less + (long long)j * more + c;
-    j -= (int)w1;
-  }
-  const long long idx = w0 * less + w1 * more + (long long)j * G + (G - 1 - c);
-  return idx < dw_units ? dh_units + idx : -1;
-}
-
 // This pair's tiles: which is the i-th (kind -1: no more).
 template <CeMode M>
 __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
   CeTile t;
   t.kind = -1;
   t.k0 = t.slice = 0;
+  const int G = gridDim.x >> 1, c = blockIdx.x >> 1;
   if (M != kCeGrads) {
     // Token blocks fastest: a vocabulary tile is read once from memory, and by
     // the other token blocks from L2.
-    const int cols = M == kCeLoss ? p.V : p.nv;
-    const int mb = (p.N + kMmM - 1) / kMmM, nb = (cols + kMmN - 1) / kMmN;
-    const long long idx = (long long)i * (gridDim.x >> 1) + (blockIdx.x >> 1);
-    if (idx >= (long long)mb * nb) return t;
+    const long long at = (long long)i * G + c;
+    if (at >= p.z_tiles) return t;
+    const uint32_t idx = (uint32_t)at, mb = (uint32_t)p.m_blocks;
     t.kind = 0;
     t.m0 = (int)(idx % mb) * kMmM;
     t.n0 = (int)(idx / mb) * kMmN;
     t.iters = (p.D + kMmK - 1) / kMmK;
   } else {
-    const int dw_iters = (p.N + kMmK - 1) / kMmK;
-    const long long idx = ce_unit(p.dh_units, p.dw_units, p.split_iters, dw_iters, gridDim.x >> 1,
-                                  blockIdx.x >> 1, i);
+    const int idx = ce_unit(p.deal, p.dh_units, p.dw_units, G, c, i);
     if (idx < 0) return t;
-    const int nb = (p.D + kMmN - 1) / kMmN;
-    const bool dh = idx < p.dh_units;
-    int j = (int)(dh ? idx : idx - p.dh_units);
-    t.kind = dh ? 1 : 2;
-    if (dh) {
-      t.slice = j % p.splits;
-      j /= p.splits;
+    const uint32_t nb = (uint32_t)(p.D + kMmN - 1) / kMmN;
+    uint32_t j = (uint32_t)idx;
+    if (idx < p.dh_units) {
+      t.kind = 1;
+      t.slice = (int)(j % (uint32_t)p.splits);
+      j /= (uint32_t)p.splits;
       t.k0 = t.slice * p.split_iters * kMmK;
-      const int left = (p.nv - t.k0 + kMmK - 1) / kMmK;
-      t.iters = min(p.split_iters, max(left, 0));
+      t.iters = min(p.split_iters, max((p.nv - t.k0 + kMmK - 1) / kMmK, 0));
     } else {
-      t.iters = dw_iters;
+      t.kind = 2;
+      j -= (uint32_t)p.dh_units;
+      t.iters = (p.N + kMmK - 1) / kMmK;
     }
-    t.m0 = j / nb * kMmM;
-    t.n0 = j % nb * kMmN;
+    t.m0 = (int)(j / nb) * kMmM;
+    t.n0 = (int)(j % nb) * kMmN;
   }
   return t;
 }
@@ -341,11 +350,15 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
   // is well predicted the difference of its logit and lse has few bits left.
   const float at_label =
       has && y >= 0 && y < kMmN ? __fmul_rn(expm1f(-__ldg(&p.nll[m])), g) : 0.0f;
-  const bool here = has && y >= 0 && y < kMmN && half == 0;  // one of the two warps
-  const uint32_t tokens = __ballot_sync(0xffffffffu, here);
-  if (lane == 0 && half == 0 && m < p.N)
-    p.in_tile[(size_t)(t.n0 / kMmN) * ((p.N + 31) / 32) + m / 32] = tokens;
-  if (here)
+  // Which tokens have a label among each 32 entries of this warp's half.
+  const int words = (p.N + 31) / 32;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t tokens = __ballot_sync(0xffffffffu, has && y >> 5 == from / 32 + k);
+    if (lane == k && t.m0 + row0 < p.N)
+      p.in_rows[(size_t)(t.n0 / 32 + from / 32 + k) * words + (t.m0 + row0) / 32] = tokens;
+  }
+  if (has && y >= from && y < from + 128)
     p.resid[m] = __fsub_rn(at_label, __uint_as_float(pack_bf16(at_label, 0.0f) << 16));
   for (int c0 = from; c0 < cols; c0 += 64) {
     const uint32_t box = ce_box_begin(o);
@@ -401,7 +414,16 @@ struct CeFix {
   const uint16_t* src[kCeFixes];
   float r[kCeFixes];
 };
-__device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int row0) {
+// The first 32 words of the map of labels for a warp's 32 entries of dW, one per lane
+// (read a tile ahead).
+__device__ __forceinline__ uint32_t ce_fix_word(const CeParams& p, const CeTile& t, int row0) {
+  const int lane = threadIdx.x & 31, words = (p.N + 31) / 32, r0 = t.m0 + row0;
+  return t.kind == 2 && r0 < p.nv && lane < words ? __ldg(p.in_rows + (size_t)(r0 / 32) * words + lane)
+                                                  : 0;
+}
+
+__device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int row0,
+                                        uint32_t word0) {
   const int lane = threadIdx.x & 31, r0 = t.m0 + row0;
   CeFix f;
   f.toks = 0;
@@ -420,9 +442,11 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
 #pragma unroll
   for (int k = 0; k < kCeFixes; ++k) tok[k] = 0;
   const int words = (p.N + 31) / 32;
-  const uint32_t* in_tile = p.in_tile + (size_t)(r0 / kMmN) * words;
+  const uint32_t* in_rows = p.in_rows + (size_t)(r0 / 32) * words;
   for (int base = 0; base < words; base += 32) {
-    const uint32_t mine = base + lane < words ? __ldg(in_tile + base + lane) : 0;
+    const uint32_t mine = base == 0               ? word0
+                          : base + lane < words ? __ldg(in_rows + base + lane)
+                                                : 0;
     uint32_t some = __ballot_sync(0xffffffffu, mine != 0);
     while (some != 0) {
       // Up to four words with tokens at a time: their labels' loads go together.
@@ -437,7 +461,7 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t m = __ballot_sync(0xffffffffu, rel[k] >= 0 && rel[k] < 32);
+        uint32_t m = __ballot_sync(0xffffffffu, rel[k] >= 0);
         for (; m != 0; m &= m - 1) {
           const int j = __ffs(m) - 1;
           if (__shfl_sync(0xffffffffu, rel[k], j) == lane) {
@@ -643,12 +667,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
     const int half = (warp - kMmEpilogue) >> 2;
     CeOut out = {ring + kMmStages * kMmStageBytes + (warp - kMmEpilogue) * kMmBoxes * kMmBoxBytes, 0};
+    CeTile next = ce_tile<M>(p, 0);
+    next.m0 += rank * kMmHalf;
+    uint32_t word = M == kCeGrads ? ce_fix_word(p, next, quarter * 32) : 0;
     for (int i = 0;; ++i) {
-      CeTile t = ce_tile<M>(p, i);
+      const CeTile t = next;
       if (t.kind < 0) break;
-      t.m0 += rank * kMmHalf;
+      next = ce_tile<M>(p, i + 1);
+      next.m0 += rank * kMmHalf;
       CeFix fix;
-      if (M == kCeGrads) fix = ce_fix(p, t, quarter * 32);
+      if (M == kCeGrads) {
+        fix = ce_fix(p, t, quarter * 32, word);
+        word = ce_fix_word(p, next, quarter * 32);
+      }
       const int acc = i & 1;
       if (!mbar_wait_cluster_bounded(&bars.tfull[acc], (i >> 1) & 1, &bars.abort_flag)) ok = false;
       if (!__all_sync(0xffffffffu, ok)) {

@@ -78,9 +78,13 @@ inline cudaError_t ce_prepare(DeviceInfo* d) {
 }
 
 template <CeMode M>
-cudaError_t launch_ce(const DeviceInfo* d, const CeMaps& maps, const CeParams& p, long long tiles,
+cudaError_t launch_ce(const DeviceInfo* d, const CeMaps& maps, CeParams& p, long long tiles,
                       cudaStream_t stream) {
   const long long pairs = std::max<long long>(1, std::min<long long>(tiles, d->sms / 2));
+  if (M == kCeGrads)
+    p.deal = ce_deal(p.dh_units, p.dw_units, p.split_iters, (p.N + kMmK - 1) / kMmK, (int)pairs);
+  else
+    p.z_tiles = (int)tiles;
   return launch(ce_mma_kernel<M>, dim3((unsigned)(2 * pairs)), dim3(kMmThreads), kMmSmem, stream,
                 true, maps, p);
 }
@@ -93,13 +97,14 @@ inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLa
   p.V = V;
   p.D = D;
   p.parts = lay.parts;
+  p.m_blocks = (N + kMmM - 1) / kMmM;
   p.a_rows = N < kMmHalf ? (N + 7) / 8 * 8 : kMmHalf;
   p.partials = reinterpret_cast<float2*>(ws + lay.partials);
   p.z_label = reinterpret_cast<float*>(ws + lay.z_label);
   p.piece = lay.piece;
   p.dh_acc = reinterpret_cast<float*>(ws + lay.dh_acc);
   p.resid = reinterpret_cast<float*>(ws + lay.resid);
-  p.in_tile = reinterpret_cast<uint32_t*>(ws + lay.in_tile);
+  p.in_rows = reinterpret_cast<uint32_t*>(ws + lay.in_rows);
   p.header = reinterpret_cast<WsHeader*>(ws);
   return p;
 }

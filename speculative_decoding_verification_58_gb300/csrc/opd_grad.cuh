@@ -197,10 +197,11 @@ __device__ __forceinline__ void og_store(TIn* at, bool vec, const OgWin& w) {
   }
 }
 
+// Largest of the lanes' values (NaN is passed over), in one instruction.
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -467,22 +468,27 @@ __device__ __forceinline__ float2 og_clip_part(const OgTerms& k, float2 zt, floa
 // Rows in shared memory.
 // ---------------------------------------------------------------------------
 
-// A thread's sums over its windows; the maxima are the warp's.
+// A thread's sums over its windows, relative to the warp's references mt, md:
+// logits of the first windows, raised only when a logit lies more than kOgAhead
+// above them (a sum then has terms up to e^40, which single precision holds as well as
+// any), so that the rescaling almost never runs.
+constexpr float kOgAhead = 40.0f;
 struct OgSums {
   float mt, md;
   float2 st, sd, a;  // sums of e^(z_t - m_t), e^(z_d - m_d) and of A's terms
   float dmax;        // largest (z_d - m_d) - (z_t - m_t)
-  ArgAcc arg;
+  float best;        // the thread's largest target logit, and the window it is in
+  int best_w;
+  float dtop;        // the thread's largest draft logit
 };
 
-// Raise the warp's maxima to include gt, gd of its lanes (a vote and, seldom, the
-// rescaling of the sums; windows come in index order, so only a strictly larger
-// target maximum moves the argmax).  Returns whether the target's rose.
-__device__ __forceinline__ bool og_raise(OgSums& s, float gt, float gd) {
-  if (!__any_sync(0xffffffffu, gt > s.mt || gd > s.md)) return false;
+// The references to include gt, gd of the warp's lanes.
+__device__ __forceinline__ void og_raise(OgSums& s, float gt, float gd) {
+  if (!__any_sync(0xffffffffu, gt > __fadd_rn(s.mt, kOgAhead) || gd > __fadd_rn(s.md, kOgAhead)))
+    return;
   const float nt = fmaxf(s.mt, warp_max(gt)), nd = fmaxf(s.md, warp_max(gd));
   const float ft = og_exp(s.mt, nt), fd = og_exp(s.md, nd);
-  // A's terms are relative to both maxima: each moves by the difference of the moves.
+  // A's terms are relative to both references: each moves by the difference of the moves.
   const float move = __fsub_rn(__fsub_rn(s.md, nd), __fsub_rn(s.mt, nt));
   if (s.sd.x != 0.0f || s.sd.y != 0.0f) {  // else there is nothing to move
     s.a = f32x2_mul(f32x2_fma(s.sd, dup2(move), s.a), dup2(fd));
@@ -490,22 +496,17 @@ __device__ __forceinline__ bool og_raise(OgSums& s, float gt, float gd) {
   }
   s.st = f32x2_mul(s.st, dup2(ft));
   s.sd = f32x2_mul(s.sd, dup2(fd));
-  const bool rose = nt > s.mt;
   s.mt = nt;
   s.md = nd;
-  return rose;
 }
 
-// A window's terms; `top`: it holds the target's new maximum.
-__device__ __forceinline__ void og_window(OgSums& s, const OgWin& t, const OgWin& d, bool top,
-                                          int e) {
-  if (top) {
-    const float gt = s.mt;
-    s.arg.v = gt;
-#pragma unroll
-    for (int j = 7; j >= 0; --j)
-      if (((j & 1) ? t.x[j >> 1].y : t.x[j >> 1].x) == gt) s.arg.i = e + j;
-  }
+// A window's terms (`gt`, `gd`: its largest logits).
+__device__ __forceinline__ void og_window(OgSums& s, const OgWin& t, const OgWin& d, float gt,
+                                          float gd, int w) {
+  s.dtop = fmaxf(s.dtop, gd);
+  const bool top = gt > s.best;
+  s.best = top ? gt : s.best;
+  s.best_w = top ? w : s.best_w;
   const float2 nt = dup2(-s.mt), nd = dup2(-s.md), l2 = dup2(kLog2e);
   float2 et[4], ed[4], a = dup2(0.0f);
 #pragma unroll
@@ -522,14 +523,16 @@ __device__ __forceinline__ void og_window(OgSums& s, const OgWin& t, const OgWin
   s.a = f32x2_add(s.a, a);
 }
 
-// A position's partial: a warp's, a CTA's, the cluster's.  32 bytes.
+// A position's partial: a warp's, a CTA's, the cluster's.
 struct OgPos {
   float mt, st, md, sd, a, dmax, argv;
   int argi;
+  float dtop;
 };
 
 __device__ __forceinline__ OgPos og_none_pos() {
-  return OgPos{-FLT_MAX, 0.0f, -FLT_MAX, 0.0f, 0.0f, -INFINITY, -INFINITY, INT32_MAX};
+  return OgPos{-FLT_MAX, 0.0f,      -FLT_MAX,  0.0f,      0.0f,
+               -INFINITY, -INFINITY, INT32_MAX, -INFINITY};
 }
 
 // The lanes' partials as one, in every lane.
@@ -546,7 +549,14 @@ __device__ __forceinline__ OgPos og_warp(const OgPos& x) {
   r.dmax = warp_max(any ? __fadd_rn(x.dmax, move) : -INFINITY);
   r.argv = warp_max(x.argv);
   r.argi = __reduce_min_sync(0xffffffffu, x.argv == r.argv ? x.argi : INT32_MAX);
+  r.dtop = warp_max(x.dtop);
   return r;
+}
+
+// e^-x, x >= 0, with the rounding of x log2 e made good.
+__device__ __forceinline__ float og_exp_down(float x) {
+  const float y = __fmul_rn(x, kLog2e), rest = fmaf(x, kLog2e, -y);
+  return __fmul_rn(ex2(-y), fmaf(rest, -kLn2f, 1.0f));
 }
 
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
@@ -574,6 +584,15 @@ __device__ __forceinline__ OgWin og_smem(uint32_t addr, int shift) {
   return og_unpack(r, TIn());
 }
 
+// The largest entry of an aligned window.
+template <typename TIn>
+__device__ __forceinline__ float og_smem_max(uint32_t addr) {
+  uint4 v[8 * sizeof(TIn) / 16];
+#pragma unroll
+  for (int b = 0; b < (int)(8 * sizeof(TIn) / 16); ++b) v[b] = ld_shared16(addr + 16 * b);
+  return batch_max<TIn>(v);
+}
+
 struct OgShared {
   OgPos warp[kOgThreads / 32];
   OgPos part[kOgMaxCluster];
@@ -598,29 +617,45 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
   OgSums s;
   s.mt = s.md = -FLT_MAX;
   s.st = s.sd = s.a = dup2(0.0f);
-  s.dmax = -INFINITY;
-  arg_init(s.arg);
-  int have = 0;  // pieces known to have arrived
+  s.dmax = s.best = s.dtop = -INFINITY;
+  s.best_w = 0;
+  int have = 0, ready = 0;  // pieces known to have arrived, their windows
   bool late = false;
-  for (int r = 0; r < nw; r += kOgThreads) {
-    const int w = r + th;
-    const bool mine = w < nw;
-    while (have < kOgPieces && have * piece <= w)
+  const int whole = nw / kOgThreads * kOgThreads;
+  for (int r = 0; r < whole; r += kOgThreads) {
+    for (; ready < r + kOgThreads && have < kOgPieces; ready += piece)
       late |= !mbar_wait_bounded(&sm.full[have++], 0, &sm.abort_flag);
-    __syncwarp();
-    OgWin t, d;
-    if (mine) {
-      t = og_smem<TIn, kShift>(bt + w * kWin, g.shift);
-      d = og_smem<TIn, false>(bd + w * kWin, 0);
-    }
-    const float gt = mine ? og_win_max(t) : -INFINITY;
-    const bool rose = og_raise(s, gt, mine ? og_win_max(d) : -INFINITY);
-    if (mine) og_window(s, t, d, rose && gt == s.mt, e0 + w * 8);
+    const int w = r + th;
+    const OgWin t = og_smem<TIn, kShift>(bt + w * kWin, g.shift);
+    const OgWin d = og_smem<TIn, false>(bd + w * kWin, 0);
+    const float gt = og_win_max(t), gd = og_win_max(d);
+    og_raise(s, gt, gd);
+    og_window(s, t, d, gt, gd, w);
   }
   // Every piece is waited for before the CTA can end; a copy that never came (a
   // bounded wait that ran out) leaves the position NaN.
   while (have < kOgPieces) late |= !mbar_wait_bounded(&sm.full[have++], 0, &sm.abort_flag);
   __syncwarp();
+  if (whole < nw) {
+    const int w = whole + th;
+    const bool mine = w < nw;
+    OgWin t, d;
+    if (mine) {
+      t = og_smem<TIn, kShift>(bt + w * kWin, g.shift);
+      d = og_smem<TIn, false>(bd + w * kWin, 0);
+    }
+    const float gt = mine ? og_win_max(t) : -INFINITY, gd = mine ? og_win_max(d) : -INFINITY;
+    og_raise(s, gt, gd);
+    if (mine) og_window(s, t, d, gt, gd, w);
+  }
+  // The thread's argmax: its best window's first entry with that value.
+  ArgAcc arg = {s.best, INT32_MAX};
+  if (s.best > -INFINITY) {
+    const OgWin t = og_smem<TIn, kShift>(bt + s.best_w * kWin, g.shift);
+#pragma unroll
+    for (int j = 7; j >= 0; --j)
+      if (((j & 1) ? t.x[j >> 1].y : t.x[j >> 1].x) == s.best) arg.i = e0 + s.best_w * 8 + j;
+  }
   float et = 0.0f, ed = 0.0f;
   if (g.rank == 0 && warp == 0) {
     const bool mine = g.edge >= 0;
@@ -630,7 +665,8 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
     }
     og_raise(s, mine ? et : -INFINITY, mine ? ed : -INFINITY);
     if (mine) {
-      if (et > s.arg.v || (et == s.arg.v && g.edge < s.arg.i)) s.arg = ArgAcc{et, g.edge};
+      if (et > arg.v || (et == arg.v && g.edge < arg.i)) arg = ArgAcc{et, g.edge};
+      s.dtop = fmaxf(s.dtop, ed);
       const float xt = __fsub_rn(et, s.mt), xd = __fsub_rn(ed, s.md);
       const float e = og_exp(ed, s.md), diff = __fsub_rn(xd, xt);
       s.st.x = __fadd_rn(s.st.x, og_exp(et, s.mt));
@@ -640,7 +676,8 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
     }
   }
   OgPos r = {s.mt, __fadd_rn(s.st.x, s.st.y), s.md, __fadd_rn(s.sd.x, s.sd.y),
-             __fadd_rn(s.a.x, s.a.y), s.dmax, s.arg.v, s.arg.i};
+             __fadd_rn(s.a.x, s.a.y), s.dmax, arg.v, arg.i,
+             s.dtop};
   if (late) r.sd = nan;
   r = og_warp(r);
   if (lane == 0) sm.warp[warp] = r;
@@ -650,8 +687,11 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
     r = og_warp(lane < kOgThreads / 32 ? sm.warp[lane] : og_none_pos());
     if (lane < (int)g.cs) {  // to every CTA, this one included
       const uint32_t to = dsmem_map(&sm.part[g.rank], lane);
-      dsmem_st4(to, make_float4(r.mt, r.st, r.md, r.sd));
-      dsmem_st4(to + 16, make_float4(r.a, r.dmax, r.argv, __int_as_float(r.argi)));
+      const float v[9] = {r.mt, r.st,   r.md,   r.sd, r.a,
+                          r.dmax, r.argv, __int_as_float(r.argi), r.dtop};
+#pragma unroll
+      for (int e = 0; e < 9; ++e)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * e), "f"(v[e]) : "memory");
     }
   }
   cluster_sync();
@@ -659,29 +699,33 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
   // A row without finite mass: its position is NaN.
   const bool ok = r.mt <= FLT_MAX && r.md <= FLT_MAX && r.st > 0.0f && r.st <= FLT_MAX &&
                   r.sd > 0.0f && r.sd <= FLT_MAX;
+  // From the references to the rows' maxima, where the large probabilities have
+  // small exponents.
+  const float up_d = __fsub_rn(r.dtop, r.md), up_t = __fsub_rn(r.argv, r.mt);
+  const float shift = __fsub_rn(up_d, up_t);
   OgTerms k;
-  k.md = r.md;
-  k.mt = r.mt;
-  k.l2d = log2f(r.sd);
-  k.cdt = __fmul_rn(__fsub_rn(k.l2d, log2f(r.st)), kLn2f);
+  k.md = r.dtop;
+  k.mt = r.argv;
+  k.l2d = log2f(__fmul_rn(r.sd, og_exp_down(up_d)));
+  k.cdt = __fmul_rn(__fsub_rn(k.l2d, log2f(__fmul_rn(r.st, og_exp_down(up_t)))), kLn2f);
   k.delta = p.delta;
 
   // Pass 2.  `sums`: A holds, and only clipped entries are looked for; q t >= delta
   // with t <= tmax needs z_d - m_d >= least (lowered by more than the roundings).
-  const float tmax = __fsub_rn(r.dmax, k.cdt);
+  const float tmax = __fsub_rn(__fsub_rn(r.dmax, shift), k.cdt);
   const bool sums = ok && fabsf(r.a) <= FLT_MAX && tmax <= FLT_MAX;
   const float least = tmax > 0.0f ? __fadd_rn(__fmul_rn(__fadd_rn(log2f(__fdiv_rn(p.delta, tmax)), k.l2d),
                                                         kLn2f),
                                               -0.01f)
                                   : INFINITY;
-  float C = sums ? __fadd_rn(__fsub_rn(__fdiv_rn(r.a, r.sd), k.cdt), 1.0f) : 0.0f;
+  float C = sums ? __fadd_rn(__fsub_rn(__fsub_rn(__fdiv_rn(r.a, r.sd), shift), k.cdt), 1.0f) : 0.0f;
   // The same in every CTA of the cluster.
   if (ok && !(sums && least > 0.0f)) {
     const float from = sums ? least : -INFINITY;
     float2 c = dup2(0.0f);
     for (int w = th; w < nw; w += kOgThreads) {
+      if (!(__fsub_rn(og_smem_max<TIn>(bd + w * kWin), k.md) >= from)) continue;
       const OgWin d = og_smem<TIn, false>(bd + w * kWin, 0);
-      if (!(__fsub_rn(og_win_max(d), k.md) >= from)) continue;
       const OgWin t = og_smem<TIn, kShift>(bt + w * kWin, g.shift);
 #pragma unroll
       for (int j = 0; j < 4; ++j) c = f32x2_add(c, og_clip_part(k, t.x[j], d.x[j], sums));

@@ -193,6 +193,11 @@ struct CeParams {
 enum CeMode { kCeLoss, kCeDz, kCeGrads };
 
 constexpr int kMmM = 256, kMmN = 256, kMmK = 64, kMmStages = 6;
+// The loss sums a logit in chunks of kMmChunk steps, each from zero in an accumulator of
+// its own, and adds the chunks in registers, rounded to nearest: the tensor cores'
+// sums are cut off towards zero at every step, which over a long row is a bias (loss
+// of 2048 tokens, D = 2048: off by 1.1e-6 of itself in one chunk).
+constexpr int kMmChunk = 16;
 constexpr int kMmHalf = 128;  // rows of A, of B and of the result in each CTA
 constexpr int kMmABytes = kMmHalf * kMmK * 2, kMmBBytes = kMmHalf * kMmK * 2;
 constexpr int kMmStageBytes = kMmABytes + kMmBBytes;  // each CTA's
@@ -266,15 +271,20 @@ __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
 // Epilogue of one thread: row `m` of the tile, one half of its columns in tensor memory.
 // The label's logit goes to z_label and is left out of the sums.
 __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, uint32_t addr,
-                                            int m, int half) {
+                                            int m, int half, const float (&sum)[kCePartV]) {
   const bool live = m < p.N;
   const int y = live ? __ldg(&p.labels[m]) : -1;
   const int from = half * kCePartV, cols = min(from + kCePartV, p.V - t.n0);
   // Below every logit: a tile of -inf keeps a finite maximum and a sum of 0.
   float ms = -FLT_MAX / 2, s = 0.0f;
-  for (int c0 = from; c0 < cols; c0 += 32) {
+#pragma unroll
+  for (int q = 0; q < kCePartV; q += 32) {
+    const int c0 = from + q;
+    if (c0 >= cols) break;
     float x[32];
     tmem_load32(addr + c0, x);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x[c] = __fadd_rn(x[c], sum[q + c]);
     if (c0 + 32 > cols) {
 #pragma unroll
       for (int c = 0; c < 32; ++c)
@@ -630,36 +640,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     }
   } else if (warp == kMmIssuer) {
     if (lane == 0 && rank == 0) {
-      int it = 0;
+      int it = 0, sub = 0;  // stages used, accumulators filled
       for (int i = 0; ok; ++i) {
         const CeTile t = ce_tile<M>(p, i);
         if (t.kind < 0) break;
-        const int acc = i & 1;
-        if (i >= 2 &&
-            !mbar_wait_cluster_bounded(&bars.tempty[acc], ((i >> 1) - 1) & 1, &bars.abort_flag)) {
-          ok = false;
-          break;
-        }
-        tmem_fence_after();
         const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
         const uint32_t idesc = mma_idesc(kMmM, kMmN, a_mn, b_mn);
         const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
-        for (int k = 0; k < t.iters; ++k, ++it) {
-          const int s = it % kMmStages;
-          if (!mbar_wait_cluster_bounded(&bars.full[s], (it / kMmStages) & 1, &bars.abort_flag)) {
+        int k = 0;
+        do {  // (once where there is nothing to sum)
+          const int acc = sub & 1, end = M == kCeLoss ? min(t.iters, k + kMmChunk) : t.iters;
+          if (sub >= 2 &&
+              !mbar_wait_cluster_bounded(&bars.tempty[acc], ((sub >> 1) - 1) & 1, &bars.abort_flag)) {
             ok = false;
             break;
           }
           tmem_fence_after();
-          const uint32_t a = ring + s * kMmStageBytes, b = a + kMmABytes;
+          for (const int first = k; k < end; ++k, ++it) {
+            const int s = it % kMmStages;
+            if (!mbar_wait_cluster_bounded(&bars.full[s], (it / kMmStages) & 1, &bars.abort_flag)) {
+              ok = false;
+              break;
+            }
+            tmem_fence_after();
+            const uint32_t a = ring + s * kMmStageBytes, b = a + kMmABytes;
 #pragma unroll
-          for (int j = 0; j < kMmK / 16; ++j)
-            mma_f16(tmem + acc * kMmN, mma_desc(a + j * a_step, 8192, 1024),
-                    mma_desc(b + j * b_step, 8192, 1024), idesc, k > 0 || j > 0);
-          mma_commit(&bars.empty[s]);
-        }
-        if (!ok) break;
-        mma_commit(&bars.tfull[acc]);  // also where there was nothing to sum
+            for (int j = 0; j < kMmK / 16; ++j)
+              mma_f16(tmem + acc * kMmN, mma_desc(a + j * a_step, 8192, 1024),
+                      mma_desc(b + j * b_step, 8192, 1024), idesc, k > first || j > 0);
+            mma_commit(&bars.empty[s]);
+          }
+          if (!ok) break;
+          mma_commit(&bars.tfull[acc]);
+          ++sub;
+        } while (k < t.iters);
       }
     }
   } else {
@@ -670,6 +684,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     CeTile next = ce_tile<M>(p, 0);
     next.m0 += rank * kMmHalf;
     uint32_t word = M == kCeGrads ? ce_fix_word(p, next, quarter * 32) : 0;
+    int sub = 0;
+    auto filled = [&]() -> uint32_t {  // the next accumulator, once filled
+      const int acc = sub & 1;
+      if (!mbar_wait_cluster_bounded(&bars.tfull[acc], (sub >> 1) & 1, &bars.abort_flag)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      tmem_fence_after();
+      return tmem + acc * kMmN + ((uint32_t)(quarter * 32) << 16);
+    };
+    auto drained = [&]() {
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(dsmem_map(&bars.tempty[sub & 1], 0));
+      ++sub;
+    };
     for (int i = 0;; ++i) {
       const CeTile t = next;
       if (t.kind < 0) break;
@@ -680,20 +708,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         fix = ce_fix(p, t, quarter * 32, word);
         word = ce_fix_word(p, next, quarter * 32);
       }
-      const int acc = i & 1;
-      if (!mbar_wait_cluster_bounded(&bars.tfull[acc], (i >> 1) & 1, &bars.abort_flag)) ok = false;
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+      if constexpr (M == kCeLoss) {
+        float sum[kCePartV];
+#pragma unroll
+        for (int c = 0; c < kCePartV; ++c) sum[c] = 0.0f;
+        for (int k = kMmChunk; k < t.iters && ok; k += kMmChunk) {
+          const uint32_t addr = filled() + half * kCePartV;
+          if (!ok) break;
+#pragma unroll
+          for (int q = 0; q < kCePartV; q += 32) {
+            float x[32];
+            tmem_load32(addr + q, x);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sum[q + c] = __fadd_rn(sum[q + c], x[c]);
+          }
+          drained();
+        }
+        const uint32_t addr = ok ? filled() : 0;
+        if (!ok) break;
+        ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half, sum);
+      } else {
+        const uint32_t addr = filled();
+        if (!ok) break;
+        if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);
+        else ce_grad_tile(p, maps, t, addr, quarter * 32, half, out, fix);
       }
-      tmem_fence_after();
-      const uint32_t addr = tmem + acc * kMmN + ((uint32_t)(quarter * 32) << 16);
-      if (M == kCeLoss) ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half);
-      else if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);
-      else ce_grad_tile(p, maps, t, addr, quarter * 32, half, out, fix);
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(dsmem_map(&bars.tempty[acc], 0));
+      drained();
     }
     if (M != kCeLoss && lane == 0) bulk_wait_read<0>();
   }

@@ -170,12 +170,6 @@ __device__ __forceinline__ void norm_add(NormPartial& p, int cls, float s) {
     if (c == cls) p.s[c] = ff_add_f(p.s[c], s);
 }
 
-__device__ __forceinline__ void norm_merge(NormPartial& p, const NormPartial& q) {
-#pragma unroll
-  for (int c = 0; c < 3; ++c) p.s[c] = ff_add(p.s[c], q.s[c]);
-  p.bad = __fadd_rn(p.bad, q.bad);
-}
-
 __device__ __forceinline__ NormPartial norm_zero() {
   NormPartial p;
 #pragma unroll
@@ -184,9 +178,14 @@ __device__ __forceinline__ NormPartial norm_zero() {
   return p;
 }
 
+// The lanes' sums in every lane; the first `levels` powers of two of the lanes have some.
+template <int levels = 5>
 __device__ __forceinline__ void norm_warp_sum(NormPartial& p) {
+  p.s[0] = group_sum_ff(p.s[0], levels);
+  // Seldom: some entry was very large, very small or not finite.
+  if (!__any_sync(0xffffffffu, p.s[1].hi != 0.0f || p.s[2].hi != 0.0f || p.bad != 0.0f)) return;
 #pragma unroll
-  for (int c = 0; c < 3; ++c) p.s[c] = warp_sum_ff(p.s[c]);
+  for (int c = 1; c < 3; ++c) p.s[c] = group_sum_ff(p.s[c], levels);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
     p.bad = __fadd_rn(p.bad, __shfl_xor_sync(0xffffffffu, p.bad, off));
@@ -248,8 +247,10 @@ __device__ __forceinline__ NormPartial norm_cta_sum(const NormBatch<kN>& b, int 
   norm_warp_sum(p);
   if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = p;
   __syncthreads();
-  if (threadIdx.x == 0)
-    for (int w = 1; w < kNormThreads / 32; ++w) norm_merge(p, warp_sum[w]);
+  if (threadIdx.x < 32) {
+    p = threadIdx.x < kNormThreads / 32 ? warp_sum[threadIdx.x] : norm_zero();
+    norm_warp_sum<3>(p);
+  }
   return p;
 }
 

@@ -73,6 +73,12 @@ inline cudaError_t ce_prepare(DeviceInfo* d) {
   if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeLoss>, attr, kMmSmem)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeDz>, attr, kMmSmem)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads>, attr, kMmSmem)) != cudaSuccess) return e;
+  // The small kernels between the products take the same split of L1, so that no SM has
+  // to be idle to change it.
+  for (const void* k : {(const void*)ce_finish_kernel, (const void*)ce_round_kernel})
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                  cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+      return e;
   d->ce_ready = true;
   return cudaSuccess;
 }

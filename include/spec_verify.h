@@ -393,9 +393,11 @@ spec_status_t spec_d3d_select(const int32_t* num_accepted, const int32_t* out_to
  * vocabulary head with its gradients, the gradient of the mixture
  * distillation loss, and the clip of gradients by their global norm.  As
  * everywhere, the calls are asynchronous on `stream`, allocate nothing and can
- * be captured into a graph.  Host-detectable errors return before anything is
- * enqueued; among them is an output that shares memory with an input or
- * another output (SPEC_ERR_INVALID_ARG).
+ * be captured into a graph (after a first call of each on the device, which
+ * sets its kernels up).  Calls that may overlap on the GPU need workspaces of
+ * their own; a workspace needs no initialisation.  Host-detectable errors return
+ * before anything is enqueued; among them is an output that shares memory with
+ * an input or another output (SPEC_ERR_INVALID_ARG).
  */
 
 #define SPEC_MAX_TOKENS (1 << 18) /* tokens per linear cross-entropy call */

@@ -7,8 +7,8 @@
 //
 // The loss forms the logits tile by tile and keeps of each tile one (max, sum)
 // pair per row.  The gradients form them again, a piece of the vocabulary at a
-// time: the piece's dZ is written in bfloat16 to a scratch buffer that stays in
-// L2, and both products read it from there.  dZ is rounded to bfloat16 (relative
+// time: the piece's dZ is written in bfloat16 to the workspace, and both products read
+// it from there.  dZ is rounded to bfloat16 (relative
 // 2^-8) because the matrix units take both operands in one type, and the
 // gradients come out in bfloat16 anyway; every sum is in single precision.  The
 // label's entry, which is the largest of most rows and would pass its own rounding
@@ -29,8 +29,8 @@ constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
 
 struct CeLayout {
   size_t partials, z_label, resid, in_rows, dz, dh_acc, total;
-  int tiles;  // vocabulary tiles
-  int parts;  // (max, sum) pairs of a token
+  int tiles;   // vocabulary tiles
+  int parts;   // (max, sum) pairs of a token
   int piece;   // vocabulary entries per piece (a multiple of kCeTileV)
   int splits;  // slices of a piece whose parts of dH are summed apart
   bool direct;  // dH comes out of one tile whole: no sums to keep
@@ -42,15 +42,17 @@ inline long long ce_waves(long long tiles) { return (tiles + kCePairs - 1) / kCe
 
 // Vocabulary tiles per piece of the gradients: of those whose dZ fits, the number
 // that needs the fewest rounds of 76 tiles in all, a round's tenth counted for each
-// piece's launches (2048 tokens, V = 151936: 38 tiles, 16 pieces of 4 full rounds; the
-// most that fit, 48, would be 13 pieces of 5.05 rounds, done in 6).
+// piece's launches.  Few large pieces: every piece ends with a round that is not full
+// (512 tokens, V = 151936, D = 2048: gradients in 694 us as one piece, in 766 us as
+// four of 48 MB whose dZ stays in L2; 2048 tokens, D = 4096: 4.60 ms as four pieces,
+// 4.90 ms as sixteen).
 inline int ce_piece_tiles(int N, int tiles) {
   const long long mb = (N + 255) / 256;
   const int most = (int)std::max<long long>(
       1, std::min<long long>(tiles, kCePieceBytes / 2 / N / kCeTileV));
   int best = most;
   long long cost = -1;
-  for (int n = most; n >= std::max(1, most / 2); --n) {
+  for (int n = most; n >= std::max({1, most / 2, most - 256}); --n) {
     const int pieces = (tiles + n - 1) / n, last = tiles - (pieces - 1) * n;
     const long long c =
         10 * ((pieces - 1) * ce_waves(mb * n) + ce_waves(mb * last)) + pieces;
@@ -178,8 +180,8 @@ struct CeParams {
 // The products.  A persistent kernel of CTA pairs, one CTA per SM, on tiles of
 // 256 x 256 (rows 0..127 of a tile are the first CTA's): in each CTA a warp that
 // issues the TMA loads into a ring of six 64-deep stages and eight warps that take
-// finished tiles out of tensor memory (half a row each thread), in the first a warp that issues the
-// tcgen05.mma for both.  Two accumulators of 256 columns alternate, so that one
+// finished tiles out of tensor memory (half a row each thread), in the first a warp
+// that issues the tcgen05.mma for both.  Two accumulators of 256 columns alternate, so that one
 // tile's epilogue runs under the next one's products.  A pair's CTAs each load one
 // half of either operand, 32 KB for the products of a stage; single CTAs on
 // 128 x 256 tiles need 48 KB for as many, which the L2 did not deliver where
@@ -278,7 +280,7 @@ __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
 __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, uint32_t addr,
                                             int m, int half, const float (&sum)[kCePartV]) {
   const bool live = m < p.N;
-  const int y = live ? __ldg(&p.labels[m]) : -1;
+  const int y = max(live ? __ldg(&p.labels[m]) : -1, -1);
   const int from = half * kCePartV, cols = min(from + kCePartV, p.V - t.n0);
   // Below every logit: a tile of -inf keeps a finite maximum and a sum of 0.
   float ms = -FLT_MAX / 2, s = 0.0f;
@@ -359,7 +361,7 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
   const bool has = y >= 0 && y < p.V;
   const float g = has ? __ldg(&p.g[m]) : 0.0f;
   const float l2 = has ? __fmul_rn(__ldg(&p.lse[m]), kLog2e) : 0.0f;
-  y -= p.v0 + t.n0;
+  y = has ? y - p.v0 - t.n0 : -1;
   const int from = half * 128, cols = min(from + 128, p.nv - t.n0);
   // The label's entry is exp(-nll) - 1: from the loss itself, because for a token that
   // is well predicted the difference of its logit and lse has few bits left.
@@ -420,9 +422,10 @@ __device__ __forceinline__ void ce_add_row(float (&x)[32], const CeRow& row, flo
 }
 
 // Whose rounding residual a lane's row takes: of dH the row's own token, of dW the
-// first kCeFixes tokens with this label (in order; a row with more of them is a sum
-// in which their roundings, independent of one another, are no more than those of the
-// tokens that follow).  `src`: where the row to add starts.
+// first kCeFixes tokens with this label, in order.  (What dW needs it for are rows with
+// one token or a few, which would carry one rounding as a whole; the roundings of
+// many are independent of one another, and stay as small in their sum as they are in one
+// term.)  `src`: where the row to add starts.
 constexpr int kCeFixes = 4;
 struct CeFix {
   int toks;

@@ -100,6 +100,51 @@ def test_full_vocabulary(N, V, D):
     check_grad(h, w, y, g, dh, dw)
 
 
+@pytest.mark.parametrize("N,V,D", [
+    (600, 151936, 64),    # two pieces of the vocabulary, slices past the end of the second
+    (1030, 100003, 72),
+    (2300, 40001, 200),   # dH from one slice, two pieces
+])
+def test_several_pieces(N, V, D):
+    h, w, y, g = inputs(N, V, D, seed=8)
+    y[:3] = torch.tensor([0, V - 1, V // 2], dtype=torch.int32)
+    ce = sv.LinearCe(h, w, y, g)
+    nll, lse = ce.loss()
+    dh, dw = ce.grad()
+    check_loss(h, w, y, nll, lse)
+    check_grad(h, w, y, g, dh, dw)
+
+
+@pytest.mark.parametrize("N,V,D", [(3001, 300, 64), (9000, 100, 72), (1500, 1, 64), (4097, 257, 8)])
+def test_many_tokens_of_few_entries(N, V, D):
+    # Every entry is the label of more tokens than are kept for one; the map of labels
+    # is longer than a warp.
+    h, w, y, g = inputs(N, V, D, seed=12)
+    y[N // 2:] = 0
+    ce = sv.LinearCe(h, w, y, g)
+    nll, lse = ce.loss()
+    dh, dw = ce.grad()
+    check_loss(h, w, y, nll, lse)
+    check_grad(h, w, y, g, dh, dw)
+
+
+def test_inputs_inside_larger_buffers():
+    # Rows of larger tensors as inputs; what surrounds them is NaN.
+    N, V, D = 77, 900, 136
+    h, w, y, g = inputs(N, V, D, seed=14)
+    fh = torch.full((N + 40, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fw = torch.full((V + 300, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fy = torch.full((N + 9,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    fg = torch.full((N + 9,), float("nan"), device="cuda")
+    fh[5:5 + N], fw[7:7 + V], fy[3:3 + N], fg[1:1 + N] = h, w, y, g
+    ce = sv.LinearCe(fh[5:5 + N], fw[7:7 + V], fy[3:3 + N], fg[1:1 + N])
+    nll, lse = ce.loss()
+    dh, dw = ce.grad()
+    check_loss(h, w, y, nll, lse)
+    check_grad(h, w, y, g, dh, dw)
+    assert sv.spec_verify_device_status(ce.workspace) == sv.SPEC_OK
+
+
 def test_one_gradient_alone_is_the_same():
     h, w, y, g = inputs(150, 9000, 128, seed=3)
     ce = sv.LinearCe(h, w, y, g)

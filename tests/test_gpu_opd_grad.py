@@ -68,6 +68,33 @@ def test_gradient(recipe, B, k, V, dtype, seed):
     check(t, d, L, g, sv.spec_opd_grad(t, d, L, g))
 
 
+@pytest.mark.parametrize("V", [2, 7, 8, 9, 15, 16, 17, 100, 2047, 2049, 16385])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_small_and_ragged_rows(V, dtype):
+    t, d, L, g = device(synth.make_inputs("zipf_mixed_noise", 3, 5, V, dtype, seed=500 + V))
+    check(t, d, L, g, sv.spec_opd_grad(t, d, L, g))
+
+
+@pytest.mark.parametrize("off", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (3, 3, 3), (0, 5, 5), (2, 0, 4)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [777, 1024])
+def test_buffers_off_16_byte_lines(off, dtype, V):
+    # Contiguous tensors that start anywhere; NaN around the inputs, a mark around the output.
+    t, d, L, g = device(synth.make_inputs("zipf_mixed_noise", 4, 3, V, dtype, seed=510))
+    out = torch.empty_like(d)
+    views, flats = [], []
+    for x, o, fill in ((t, off[0], float("nan")), (d, off[1], float("nan")), (out, off[2], 7.0)):
+        f = torch.full((x.numel() + 16,), fill, dtype=x.dtype, device="cuda")
+        v = f[o:o + x.numel()].view(x.shape)
+        if fill != 7.0:
+            v.copy_(x)
+        views.append(v)
+        flats.append(f)
+    got = sv.spec_opd_grad(views[0], views[1], L, g, d_draft=views[2])
+    check(t, d, L, g, got)
+    assert torch.all(flats[2][:off[2]] == 7) and torch.all(flats[2][off[2] + out.numel():] == 7)
+
+
 @pytest.mark.parametrize("alpha,delta", [(0.0, 0.01), (1.0, 0.01), (0.5, 1e-4), (0.3, 1e9)])
 def test_mixture_and_clip(alpha, delta):
     t, d, L, g = device(synth.make_inputs("zipf_mixed_noise", 6, 5, 3000, "f32", seed=421))

@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kCeFinishThreads)
     ce_finish_kernel(const __grid_constant__ CeParams p, int tokens, float* nll, float* lse) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float sm[kCeFinishThreads];
+  __shared__ float sm[2][kCeFinishThreads / 32][32];
   const int tid = threadIdx.x, tok = tid & (tokens - 1), groups = kCeFinishThreads / tokens;
   const int i = blockIdx.x * tokens + tok;
   const float2* part = p.partials + i;
@@ -791,22 +791,27 @@ __global__ void __launch_bounds__(kCeFinishThreads)
       m = n;
     }
   }
-  // The CTA's maximum of each token, then its sum, by halves.
-  sm[tid] = m;
-  for (int o = kCeFinishThreads / 2; o >= tokens; o >>= 1) {
-    __syncthreads();
-    if (tid < o) sm[tid] = fmaxf(sm[tid], sm[tid + o]);
+  // Each token's maximum and sum: over its lanes in a warp, then over the warps.
+  const int warp = tid >> 5;
+  for (int o = 16; o >= tokens; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const float n = fmaxf(m, m2);
+    s = __fadd_rn(__fmul_rn(s, ex2(__fsub_rn(m, n))), __fmul_rn(s2, ex2(__fsub_rn(m2, n))));
+    m = n;
+  }
+  if ((tid & 31) < tokens) {
+    sm[0][warp][tok] = m;
+    sm[1][warp][tok] = s;
   }
   __syncthreads();
-  const float top = sm[tok];
-  __syncthreads();
-  sm[tid] = __fmul_rn(s, ex2(__fsub_rn(m, top)));
-  for (int o = kCeFinishThreads / 2; o >= tokens; o >>= 1) {
-    __syncthreads();
-    if (tid < o) sm[tid] = __fadd_rn(sm[tid], sm[tid + o]);
-  }
   if (tid >= tokens || i >= p.N) return;
-  s = sm[tid];
+  float top = sm[0][0][tok];
+#pragma unroll
+  for (int w = 1; w < kCeFinishThreads / 32; ++w) top = fmaxf(top, sm[0][w][tok]);
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kCeFinishThreads / 32; ++w)
+    s = fmaf(sm[1][w][tok], ex2(__fsub_rn(sm[0][w][tok], top)), s);
   const float nan = __int_as_float(0x7fc00000);
   const int y = p.labels[i];
   const bool has = y >= 0 && y < p.V;

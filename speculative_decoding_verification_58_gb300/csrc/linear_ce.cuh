@@ -612,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const int am = t.m0 + rank * kMmHalf, bn = t.n0 + rank * kMmHalf;
         for (int k = 0; k < t.iters; ++k, ++loads) {
           const int s = loads % kMmStages, round = loads / kMmStages;
-          if (round > 0 && !mbar_wait_bounded(&bars.empty[s], (round - 1) & 1, &bars.abort_flag)) {
+          if (round > 0 && !mbar_sleep(&bars.empty[s], (round - 1) & 1, &bars.abort_flag)) {
             ok = false;
             break;
           }
@@ -644,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       }
       // The products' last arrivals on `empty` come before the CTA ends.
       for (int l = max(0, loads - kMmStages); ok && l < loads; ++l)
-        ok = mbar_wait_bounded(&bars.empty[l % kMmStages], (l / kMmStages) & 1, &bars.abort_flag);
+        ok = mbar_sleep(&bars.empty[l % kMmStages], (l / kMmStages) & 1, &bars.abort_flag);
     }
   } else if (warp == kMmIssuer) {
     if (lane == 0 && rank == 0) {
@@ -659,14 +659,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         do {  // (once where there is nothing to sum)
           const int acc = sub & 1, end = M == kCeLoss ? min(t.iters, k + kMmChunk) : t.iters;
           if (sub >= 2 &&
-              !mbar_wait_cluster_bounded(&bars.tempty[acc], ((sub >> 1) - 1) & 1, &bars.abort_flag)) {
+              !mbar_sleep(&bars.tempty[acc], ((sub >> 1) - 1) & 1, &bars.abort_flag)) {
             ok = false;
             break;
           }
           tmem_fence_after();
           for (const int first = k; k < end; ++k, ++it) {
             const int s = it % kMmStages;
-            if (!mbar_wait_cluster_bounded(&bars.full[s], (it / kMmStages) & 1, &bars.abort_flag)) {
+            if (!mbar_sleep(&bars.full[s], (it / kMmStages) & 1, &bars.abort_flag)) {
               ok = false;
               break;
             }
@@ -695,7 +695,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     int sub = 0;
     auto filled = [&]() -> uint32_t {  // the next accumulator, once filled
       const int acc = sub & 1;
-      if (!mbar_wait_cluster_bounded(&bars.tfull[acc], (sub >> 1) & 1, &bars.abort_flag)) ok = false;
+      if (!mbar_sleep(&bars.tfull[acc], (sub >> 1) & 1, &bars.abort_flag)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       tmem_fence_after();
       return tmem + acc * kMmN + ((uint32_t)(quarter * 32) << 16);
@@ -752,7 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     if (warp == kMmProducer && lane == 0 && rank == 0) {
       int never = 0;
       for (int l = max(0, loads - kMmStages); l < loads; ++l)
-        mbar_wait_bounded(&bars.full[l % kMmStages], (l / kMmStages) & 1, &never);
+        mbar_sleep(&bars.full[l % kMmStages], (l / kMmStages) & 1, &never);
     }
   }
   __syncwarp();

@@ -624,7 +624,7 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
   const int whole = nw / kOgThreads * kOgThreads;
   for (int r = 0; r < whole; r += kOgThreads) {
     for (; ready < r + kOgThreads && have < kOgPieces; ready += piece)
-      late |= !mbar_wait_bounded(&sm.full[have++], 0, &sm.abort_flag);
+      late |= !mbar_sleep(&sm.full[have++], 0, &sm.abort_flag);
     const int w = r + th;
     const OgWin t = og_smem<TIn, kShift>(bt + w * kWin, g.shift);
     const OgWin d = og_smem<TIn, false>(bd + w * kWin, 0);
@@ -634,7 +634,7 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
   }
   // Every piece is waited for before the CTA can end; a copy that never came (a
   // bounded wait that ran out) leaves the position NaN.
-  while (have < kOgPieces) late |= !mbar_wait_bounded(&sm.full[have++], 0, &sm.abort_flag);
+  while (have < kOgPieces) late |= !mbar_sleep(&sm.full[have++], 0, &sm.abort_flag);
   __syncwarp();
   if (whole < nw) {
     const int w = whole + th;

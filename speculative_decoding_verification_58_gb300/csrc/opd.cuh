@@ -172,6 +172,27 @@ __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_
     }
   }
 }
+// Bounded wait (acquire at cluster scope) of warps that have nothing else to do: the
+// hardware suspends the thread for up to a millisecond a try, so that waiting takes no
+// issue slots and no power from the warps that work (with the hardware's own, short
+// limit the head's loss and gradients over 2048 tokens, D = 4096, took 6.12 ms
+// instead of 5.93).
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort || global_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
 // Per-element pass-2 term q log(q/p) = q (dz - c) with dz = z_d - z_t,
 // c = lse_d - lse_t and q = 2^(z_d log2 e + nl2d), nl2d = -lse_d log2 e.
 // Only infinite logits make it non-finite; then 0 log 0 = 0 (z_d = -inf)

@@ -68,8 +68,8 @@ __device__ __forceinline__ void tmem_fence_after() {
 
 // 32 columns of the warp's 32 lanes: thread = lane, x[c] = column c.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&x)[32]) {
-  uint32_t r[32];
   __syncwarp();  // an aligned instruction: lanes that skipped work rejoin here
+  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -82,6 +82,12 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&x)[32]) {
       : "r"(addr)
       : "memory");
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  // The values are there from here on: none is used earlier.
+#pragma unroll
+  for (int c = 0; c < 32; c += 8)
+    asm volatile(""
+                 : "+r"(r[c]), "+r"(r[c + 1]), "+r"(r[c + 2]), "+r"(r[c + 3]), "+r"(r[c + 4]),
+                   "+r"(r[c + 5]), "+r"(r[c + 6]), "+r"(r[c + 7]));
 #pragma unroll
   for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(r[c]);
 }

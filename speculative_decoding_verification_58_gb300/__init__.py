@@ -32,6 +32,7 @@ The functions keep the C names:
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -639,15 +640,31 @@ def _stream_on(stream, device) -> int:
     return _stream_ptr(stream)
 
 
+def _alloc_on(stream, device):
+    """Context in which a call's own tensors are allocated: on the stream that uses them.
+
+    The caching allocator hands a freed tensor's memory out again in the order of the
+    stream it was allocated on; a workspace of the current stream's, freed when the call
+    returns, could be in other hands while another stream still works in it.
+    """
+    if stream is None:
+        return contextlib.nullcontext()
+    cuda = _torch().cuda
+    if not hasattr(stream, "cuda_stream"):
+        stream = cuda.ExternalStream(int(stream), device=device)
+    return cuda.stream(stream)
+
+
 def _need_cuda(t, name):
     if t.device.type != "cuda":
         raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
 
 
-def _need_workspace(ws, name, nbytes, device):
+def _need_workspace(ws, name, nbytes, device, stream):
     torch = _torch()
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with _alloc_on(stream, device):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if ws.device != device:
         raise ValueError(f"{name} is on {ws.device}, expected {device}")
     if not ws.is_contiguous():
@@ -682,10 +699,11 @@ class LinearCe:
         _need(hidden, "hidden", hidden.dtype, (N, D), dev)
         _need(weight, "weight", hidden.dtype, (V, D), dev)
         _need(labels, "labels", torch.int32, (N,), dev)
-        if nll is None:
-            nll = torch.empty(N, dtype=torch.float32, device=dev)
-        if lse is None:
-            lse = torch.empty(N, dtype=torch.float32, device=dev)
+        with _alloc_on(stream, dev):
+            if nll is None:
+                nll = torch.empty(N, dtype=torch.float32, device=dev)
+            if lse is None:
+                lse = torch.empty(N, dtype=torch.float32, device=dev)
         _need(nll, "nll", torch.float32, (N,), dev)
         _need(lse, "lse", torch.float32, (N,), dev)
         n = int(lib().spec_linear_ce_workspace_bytes(N, V, D))
@@ -694,16 +712,17 @@ class LinearCe:
             n = max(n, int(lib().spec_linear_ce_grad_workspace_bytes(N, V, D)))
             if not (need_hidden or need_weight):
                 raise ValueError("grad_nll is given, but neither gradient is wanted")
-            if need_hidden and d_hidden is None:
-                d_hidden = torch.empty_like(hidden)
-            if need_weight and d_weight is None:
-                d_weight = torch.empty_like(weight)
+            with _alloc_on(stream, dev):
+                if need_hidden and d_hidden is None:
+                    d_hidden = torch.empty_like(hidden)
+                if need_weight and d_weight is None:
+                    d_weight = torch.empty_like(weight)
             if need_hidden:
                 _need(d_hidden, "d_hidden", hidden.dtype, (N, D), dev)
             if need_weight:
                 _need(d_weight, "d_weight", hidden.dtype, (V, D), dev)
         # Unsupported sizes (n == 0) reach the library, which says so.
-        ws = _need_workspace(workspace, "workspace", max(n, 256), dev)
+        ws = _need_workspace(workspace, "workspace", max(n, 256), dev, stream)
         self._keep = (hidden, weight, labels, grad_nll, ws)
         self.workspace, self.nll, self.lse = ws, nll, lse
         self.d_hidden = d_hidden if grad_nll is not None and need_hidden else None
@@ -778,7 +797,8 @@ def spec_opd_grad(target_logits, draft_logits, lengths, grad_loss, *, delta: flo
     _need(lengths, "lengths", torch.int32, (B,), dev)
     _need(grad_loss, "grad_loss", torch.float32, (B,), dev)
     if d_draft is None:
-        d_draft = torch.empty((B, k, V), dtype=target_logits.dtype, device=dev)
+        with _alloc_on(stream, dev):
+            d_draft = torch.empty((B, k, V), dtype=target_logits.dtype, device=dev)
     _need(d_draft, "d_draft", target_logits.dtype, (B, k, V), dev)
     _check(lib().spec_opd_grad(target_logits.data_ptr(), draft_logits.data_ptr(), dt,
                                lengths.data_ptr(), grad_loss.data_ptr(), B, k, V, float(delta),
@@ -811,11 +831,12 @@ class GradClipper:
             if out is not None:
                 _need(out[i], f"out[{i}]", g.dtype, g.shape, dev)
         if norm is None:
-            norm = torch.empty(1, dtype=torch.float32, device=dev)
+            with _alloc_on(stream, dev):
+                norm = torch.empty(1, dtype=torch.float32, device=dev)
         _need(norm, "norm", torch.float32, (1,), dev)
         m = len(grads)
         n = int(lib().spec_grad_norm_workspace_bytes(m))
-        ws = _need_workspace(workspace, "workspace", max(n, 256), dev)
+        ws = _need_workspace(workspace, "workspace", max(n, 256), dev, stream)
         self._keep = (grads, out, ws)
         self.norm, self.workspace = norm, ws
         ptrs = (ctypes.c_void_p * m)(*[g.data_ptr() or None for g in grads])

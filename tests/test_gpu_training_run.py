@@ -162,6 +162,42 @@ def test_two_loops_on_two_streams():
         check(*args[:5], b)
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_calls_given_a_stream_keep_their_memory(handle):
+    """What a call allocates for a stream of its own is not handed out while that stream uses it.
+
+    The stream is held up, the calls are enqueued behind that, and their workspaces'
+    sizes are allocated and filled from the current stream meanwhile.
+    """
+    N, V, D = 64, 1024, 128
+    w, h, draft, target, L, tok, u, T = make(8, 8, V, D, 3)
+    h = h.reshape(N, D)
+    y = torch.arange(N, device="cuda", dtype=torch.int32) * 7 % V
+    g = torch.full((N,), 1.0 / N, device="cuda")
+    gl = torch.full((8,), 0.125, device="cuda")
+
+    def run(stream):
+        nll, lse = sv.spec_linear_ce(h, w, y, stream=stream)
+        dh, dw = sv.spec_linear_ce_grad(h, w, y, nll, lse, g, stream=stream)
+        dz = sv.spec_opd_grad(target, draft, L, gl, stream=stream)
+        return nll, lse, dh, dw, dz, sv.spec_grad_norm([h, w], stream=stream)
+
+    want = run(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+    got = run(s.cuda_stream if handle else s)
+    sizes = [sv.lib().spec_linear_ce_workspace_bytes(N, V, D),
+             sv.lib().spec_linear_ce_grad_workspace_bytes(N, V, D),
+             sv.lib().spec_grad_norm_workspace_bytes(2)]
+    others = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes * 3]
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert all(bool((t == 255).all()) for t in others)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_range_checking_build():
     """The training calls through libspecverify_debug.so: no index leaves its buffer."""
     code = """

@@ -34,8 +34,9 @@
 // Measured: 128 requests of up to 16 rows of 151936 bf16, 310 us (1.28 GB read and
 // written once: 189 us); DRAM at 45 % and issue at 56 % of their peaks: a third of the
 // time lies between the passes (copies, cluster barriers), which three CTAs an SM
-// overlap in part.  16-CTA clusters took 394 to 409 us, resident clusters that copy
-// ahead 359, three passes over L2 453.
+// overlap in part.  192, 224, 288 or 320 threads a CTA took 319 to 327 us (352 and more,
+// 375 and up), 16-CTA clusters 394 to 409, resident clusters that copy ahead 359, three
+// passes over L2 453.
 #pragma once
 
 #include "grad_norm.cuh"

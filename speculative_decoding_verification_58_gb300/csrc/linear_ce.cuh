@@ -286,7 +286,7 @@ __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
 __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, uint32_t addr,
                                             int m, int half, const float (&sum)[kCePartV]) {
   const bool live = m < p.N;
-  const int y = max(live ? __ldg(&p.labels[m]) : -1, -1);
+  const int y = max(live ? p.labels[m] : -1, -1);
   const int from = half * kCePartV, cols = min(from + kCePartV, p.V - t.n0);
   // Below every logit: a tile of -inf keeps a finite maximum and a sum of 0.
   float ms = -FLT_MAX / 2, s = 0.0f;
@@ -363,16 +363,16 @@ __device__ __forceinline__ void ce_box_ready() {
 __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps, const CeTile& t,
                                            uint32_t addr, int row0, int half, CeOut& o) {
   const int lane = threadIdx.x & 31, m = t.m0 + row0 + lane;
-  int y = m < p.N ? __ldg(&p.labels[m]) : -1;
+  int y = m < p.N ? p.labels[m] : -1;
   const bool has = y >= 0 && y < p.V;
-  const float g = has ? __ldg(&p.g[m]) : 0.0f;
-  const float l2 = has ? __fmul_rn(__ldg(&p.lse[m]), kLog2e) : 0.0f;
+  const float g = has ? p.g[m] : 0.0f;
+  const float l2 = has ? __fmul_rn(p.lse[m], kLog2e) : 0.0f;
   y = has ? y - p.v0 - t.n0 : -1;
   const int from = half * 128, cols = min(from + 128, p.nv - t.n0);
   // The label's entry is exp(-nll) - 1: from the loss itself, because for a token that
   // is well predicted the difference of its logit and lse has few bits left.
   const float at_label =
-      has && y >= 0 && y < kMmN ? __fmul_rn(expm1f(-__ldg(&p.nll[m])), g) : 0.0f;
+      has && y >= 0 && y < kMmN ? __fmul_rn(expm1f(-p.nll[m]), g) : 0.0f;
   // Which tokens have a label among each 32 entries of this warp's half.
   const int words = (p.N + 31) / 32;
 #pragma unroll
@@ -414,7 +414,7 @@ __device__ __forceinline__ CeRow ce_row(const uint16_t* src, int n) {
   CeRow r;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    r.v[q] = q * 8 < n ? __ldg(reinterpret_cast<const uint4*>(src) + q) : make_uint4(0, 0, 0, 0);
+    r.v[q] = q * 8 < n ? reinterpret_cast<const uint4*>(src)[q] : make_uint4(0, 0, 0, 0);
   return r;
 }
 __device__ __forceinline__ void ce_add_row(float (&x)[32], const CeRow& row, float r) {
@@ -442,7 +442,7 @@ struct CeFix {
 // (read a tile ahead).
 __device__ __forceinline__ uint32_t ce_fix_word(const CeParams& p, const CeTile& t, int row0) {
   const int lane = threadIdx.x & 31, words = (p.N + 31) / 32, r0 = t.m0 + row0;
-  return t.kind == 2 && r0 < p.nv && lane < words ? __ldg(p.in_rows + (size_t)(r0 / 32) * words + lane)
+  return t.kind == 2 && r0 < p.nv && lane < words ? p.in_rows[(size_t)(r0 / 32) * words + lane]
                                                   : 0;
 }
 
@@ -453,7 +453,7 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
   f.toks = 0;
   if (t.kind == 1) {
     // (Sums of several slices or pieces get theirs at the end.)
-    const int y = p.dh_direct && r0 + lane < p.N ? __ldg(&p.labels[r0 + lane]) : -1;
+    const int y = p.dh_direct && r0 + lane < p.N ? p.labels[r0 + lane] : -1;
     if (y >= 0 && y < p.V) {
       f.toks = 1;
       f.src[0] = p.w + (size_t)y * p.D;
@@ -469,7 +469,7 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
   const uint32_t* in_rows = p.in_rows + (size_t)(r0 / 32) * words;
   for (int base = 0; base < words; base += 32) {
     const uint32_t mine = base == 0               ? word0
-                          : base + lane < words ? __ldg(in_rows + base + lane)
+                          : base + lane < words ? in_rows[base + lane]
                                                 : 0;
     uint32_t some = __ballot_sync(0xffffffffu, mine != 0);
     while (some != 0) {
@@ -481,7 +481,7 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
         some &= some - 1;
         const uint32_t word = __shfl_sync(0xffffffffu, mine, first[k] < 0 ? 0 : first[k]);
         const bool bit = first[k] >= 0 && ((word >> lane) & 1);
-        rel[k] = bit ? __ldg(&p.labels[(base + first[k]) * 32 + lane]) - p.v0 - r0 : -1;
+        rel[k] = bit ? p.labels[(base + first[k]) * 32 + lane] - p.v0 - r0 : -1;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -558,7 +558,7 @@ __device__ __forceinline__ void ce_check(const CeParams& p, int* bad) {
   const int th = threadIdx.x - kMmEpilogue * 32, n = kMmThreads - kMmEpilogue * 32;
   int mine = 0;
 #pragma unroll 4
-  for (int i = th; i < p.N; i += n) mine += __ldg(&p.labels[i]) >= p.V ? 1 : 0;
+  for (int i = th; i < p.N; i += n) mine += p.labels[i] >= p.V ? 1 : 0;
   if (mine) atomicAdd(bad, mine);
   asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
   if (th == 0) {
@@ -870,11 +870,11 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] += part[k][g][e];
   const int row = (int)(i / p.D), col = (int)(i - (long long)row * p.D);
-  const int y = __ldg(&p.labels[row]);
+  const int y = p.labels[row];
   if (y >= 0 && y < p.V) {
     float a[8];
     ElemTraits<uint16_t>::unpack(
-        __ldg(reinterpret_cast<const uint4*>(p.w + (size_t)y * p.D + col)), a);
+        *(reinterpret_cast<const uint4*>(p.w + (size_t)y * p.D + col)), a);
     const float r = p.resid[row];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = fmaf(r, a[e], x[e]);

@@ -171,21 +171,22 @@ __device__ __forceinline__ OgWin og_load(const OgRow& row, int e) {
     uint32_t r[4 * NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      *reinterpret_cast<uint4*>(r + 4 * b) = __ldg(reinterpret_cast<const uint4*>(at) + b);
+      *reinterpret_cast<uint4*>(r + 4 * b) = reinterpret_cast<const uint4*>(at)[b];
     return og_unpack(r, TIn());
   }
   if (row.shift > 0) {
     uint32_t r[4 * NB + 4];
     const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(at) - row.shift);
 #pragma unroll
-    for (int b = 0; b <= NB; ++b) *reinterpret_cast<uint4*>(r + 4 * b) = __ldg(q + b);
+    for (int b = 0; b <= NB; ++b) *reinterpret_cast<uint4*>(r + 4 * b) = q[b];
     og_shift<NB>(r, row.shift);
     return og_unpack(r, TIn());
   }
   OgWin w;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    w.x[j] = make_float2(ElemTraits<TIn>::load(at, 2 * j), ElemTraits<TIn>::load(at, 2 * j + 1));
+    w.x[j] = make_float2(ElemTraits<TIn>::to_float(at[2 * j]),
+                         ElemTraits<TIn>::to_float(at[2 * j + 1]));
   return w;
 }
 
@@ -293,7 +294,7 @@ __device__ __forceinline__ OgPart<TIn> og_part(const OpdGradParams& p) {
     if (th < g.head) g.edge = th;
     else if (tail + th - g.head < p.V) g.edge = tail + th - g.head;
   }
-  g.L = __ldg(&p.lengths[g.b]);
+  g.L = p.lengths[g.b];
   g.active = g.L >= 1 && g.L <= p.k && i < g.L;
   return g;
 }
@@ -348,8 +349,8 @@ __global__ void __launch_bounds__(kOgThreads, 5) opd_grad_kernel(OpdGradParams p
   }
   float et = 0.0f, ed = 0.0f;  // the entry outside the windows
   if (edge >= 0) {
-    et = Tr::load(g.zt, edge);
-    ed = Tr::load(g.zd, edge);
+    et = Tr::to_float(g.zt[edge]);
+    ed = Tr::to_float(g.zd[edge]);
     og_add1(at, et);
     og_add1(ad, ed);
     arg_merge(ag, ArgAcc{et == et ? et : -INFINITY, et > -INFINITY ? edge : INT32_MAX});
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kOgThreads, 5) opd_grad_kernel(OpdGradParams p
 
   // Pass 3: the gradient, q (beta u + base) less alpha at the argmax, all times
   // g / L.
-  const float g0 = ok ? __fdiv_rn(__ldg(&p.grad_loss[g.b]), (float)g.L) : nan;
+  const float g0 = ok ? __fdiv_rn(p.grad_loss[g.b], (float)g.L) : nan;
   const float al = __fmul_rn(p.alpha, g0), be = __fmul_rn(__fsub_rn(1.0f, p.alpha), g0);
   const float base = fmaf(-be, C, al);
   const float2 be2 = dup2(be), base2 = dup2(base);
@@ -667,8 +668,8 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
   if (g.rank == 0 && warp == 0) {
     const bool mine = g.edge >= 0;
     if (mine) {
-      et = Tr::load(g.zt, g.edge);
-      ed = Tr::load(g.zd, g.edge);
+      et = Tr::to_float(g.zt[g.edge]);
+      ed = Tr::to_float(g.zd[g.edge]);
     }
     og_raise(s, mine ? et : -INFINITY, mine ? ed : -INFINITY);
     if (mine) {
@@ -754,7 +755,7 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
 
   // Pass 3: q (beta u + base), less alpha at the argmax, all times g / L.  With
   // f = q t this is beta f + (beta + base) q below the clip, base q above.
-  const float g0 = ok ? __fdiv_rn(__ldg(&p.grad_loss[g.b]), (float)g.L) : nan;
+  const float g0 = ok ? __fdiv_rn(p.grad_loss[g.b], (float)g.L) : nan;
   const float al = __fmul_rn(p.alpha, g0), be = __fmul_rn(__fsub_rn(1.0f, p.alpha), g0);
   const float base = fmaf(-be, C, al);
   const float2 be2 = dup2(be), low2 = dup2(__fadd_rn(be, base));

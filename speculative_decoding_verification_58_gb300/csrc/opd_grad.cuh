@@ -20,8 +20,10 @@
 //      q >= delta / max t, so that most windows are passed over after one look at
 //      the draft's logits, and all of them where no q is that large.
 //   3. The gradient.
-// Infinite logits make A useless (0 x inf); such a position sums q u entry by
-// entry in its second pass.  Rows too long for shared memory, or not on 16-byte
+// What is taken off has to be small, or the difference keeps its roundings alone: where
+// some t_v is above kOgMaxT (a target that masks entries with -1e9, say, which the drafter
+// does not), and where an infinite logit makes A useless (0 x inf), the position
+// sums q u entry by entry in its second pass.  Rows too long for shared memory, or not on 16-byte
 // lines at their buffer's base, are read from memory in every pass (the later
 // ones from L2), by the plain kernel below.
 //
@@ -481,6 +483,10 @@ __device__ __forceinline__ float2 og_clip_part(const OgTerms& k, float2 zt, floa
 // above them (a sum then has terms up to e^40, which single precision holds as well as
 // any), so that the rescaling almost never runs.
 constexpr float kOgAhead = 40.0f;
+// Largest t_v with which the sum over all entries is used.  The clipped entries' part
+// of it is at most (kOgMaxT + 1) sum q, and the sums are good to about 2^-22 of their
+// terms: 2^-17 of C's own size.
+constexpr float kOgMaxT = 32.0f;
 struct OgSums {
   float mt, md;
   float2 st, sd, a;  // sums of e^(z_t - m_t), e^(z_d - m_d) and of A's terms
@@ -718,10 +724,10 @@ __device__ __forceinline__ void og_passes(const OpdGradParams& p, const OgPart<T
   k.cdt = __fmul_rn(__fsub_rn(k.l2d, log2f(__fmul_rn(r.st, og_exp_down(up_t)))), kLn2f);
   k.delta = p.delta;
 
-  // Pass 2.  `sums`: A holds, and only clipped entries are looked for; q t >= delta
+  // Pass 2.  `sums`: A is used, and only clipped entries are looked for; q t >= delta
   // with t <= tmax needs z_d - m_d >= least (lowered by more than the roundings).
   const float tmax = __fsub_rn(__fsub_rn(r.dmax, shift), k.cdt);
-  const bool sums = ok && fabsf(r.a) <= FLT_MAX && tmax <= FLT_MAX;
+  const bool sums = ok && fabsf(r.a) <= FLT_MAX && tmax <= kOgMaxT;
   const float least = tmax > 0.0f ? __fadd_rn(__fmul_rn(__fadd_rn(log2f(__fdiv_rn(p.delta, tmax)), k.l2d),
                                                         kLn2f),
                                               -0.01f)

@@ -15,10 +15,12 @@
 //
 // Range.  x^2 overflows single precision from |x| = 2^64 and vanishes below
 // 2^-75, both inside the range of bfloat16 and float gradients.  A thread sums
-// its share of a unit in single precision; if that sum is not finite it sums
-// the share again with x scaled by 2^-100, if it is tiny (below 2^-100, but
-// some entry is not zero) with x scaled by 2^100.  The three kinds of sums are
-// carried apart, as float-float pairs, and joined in double precision at the end.
+// its share of a unit in single precision; if that sum is above 2^100 (or not
+// finite) it sums the share again with x scaled by 2^-100, if it is tiny (below 2^-100,
+// but some entry is not zero) with x scaled by 2^100.  So shares have room to be added:
+// 2^27 of them in each kind, where a block has at most 2^23 (280 GB over 456 blocks).
+// The three kinds of sums are carried apart, as float-float pairs, and joined in double
+// precision at the end.
 // Infinities and NaN, which a float-float pair cannot carry, go into a plain sum
 // of their own; a norm that is not finite leaves every tensor as it is.
 //
@@ -163,9 +165,10 @@ __device__ __forceinline__ float sum_squares(const uint4 (&v)[kNormVecsPerThread
 }
 
 // Whether a share's plain sum has to be taken again, and with which scale:
-// 0 keep it, 1 scale down, 2 scale up.
+// 0 keep it, 1 scale down (above 2^100, not only where it overflows itself: the shares
+// are added up), 2 scale up.
 __device__ __forceinline__ int norm_class(float s, bool any) {
-  if (!(s <= FLT_MAX)) return 1;
+  if (!(s <= kNormUp)) return 1;
   return (any && s < kNormDown) ? 2 : 0;
 }
 

@@ -450,7 +450,7 @@ spec_status_t spec_linear_ce(const void* hidden, const void* weight, spec_dtype_
  *   workspace      >= spec_linear_ce_grad_workspace_bytes(N, V, D) bytes
  * The logits are formed again, a piece of the vocabulary at a time.  dZ is
  * rounded to bfloat16 before the two products, whose sums are in single
- * precision.  The hidden states of tokens without a label enter d_weight with
+ * precision; what the rounding takes from the labels' entries is added back.  The hidden states of tokens without a label enter d_weight with
  * weight 0 and have to be finite.  Everything else is as for spec_linear_ce.
  */
 size_t spec_linear_ce_grad_workspace_bytes(int N, int V, int D);

@@ -13,7 +13,8 @@
 // gradients come out in bfloat16 anyway; every sum is in single precision.  The
 // label's entry, which is the largest of most rows and would pass its own rounding
 // on to a whole row of dW and dH, is made good: what the rounding took from it is
-// kept per token and added to both in single precision.
+// kept per token and added to both in single precision.  The other entries' roundings
+// stay: at most 2^-8 of their share of a row.
 //
 // Measured (V = 151936): loss of 2048 tokens, D = 2048, 735 us (1.73 PFLOP/s); loss and
 // gradients of 2048 tokens, D = 4096, 5.95 ms and of 512 tokens, D = 2048, 0.91 ms (1.72
@@ -32,9 +33,10 @@ constexpr int kCePartV = 128;      // and per (max, sum) pair
 constexpr int kCePieceBytes = 160 << 20;  // most bytes of a piece's dZ
 constexpr int kCeMaxTokens = SPEC_MAX_TOKENS;
 constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
+constexpr int kCeFixes = 4;  // tokens of a label that a tile of dW adds one by one
 
 struct CeLayout {
-  size_t partials, z_label, resid, in_rows, dz, dh_acc, total;
+  size_t partials, z_label, resid, in_rows, dz, dh_acc, label_sums, total;
   int tiles;   // vocabulary tiles
   int parts;   // (max, sum) pairs of a token
   int piece;   // vocabulary entries per piece (a multiple of kCeTileV)
@@ -112,6 +114,8 @@ inline CeLayout ce_layout(int N, int V, int D, bool grad) {
     l.direct = l.splits == 1 && l.piece >= V;
     l.dh_acc = o;
     if (!l.direct) o = align256(o + (size_t)l.splits * N * D * sizeof(float));
+    l.label_sums = o;
+    if (N > kCeFixes) o = align256(o + (size_t)N * D * sizeof(float));
   }
   l.total = o;
   return l;
@@ -171,6 +175,7 @@ struct CeParams {
   float* resid;            // [N]: the label's entry of dZ less its bf16 rounding
   uint32_t* in_rows;       // [piece / 32, N / 32]: tokens whose label is one of 32 entries
   float* dh_acc;           // [splits, N, D]
+  float* label_sums;       // [N, D]: row i for the label whose (kCeFixes + 1)-th token is i
   int dh_direct;           // dH comes out of one tile whole
   int first;               // first piece: dh_acc is set, not added to
   int splits, split_iters;  // slices of the piece in dH, 64-entry steps of a slice
@@ -360,6 +365,16 @@ __device__ __forceinline__ void ce_box_ready() {
   __syncwarp();
 }
 
+// The label's entry of dZ is g (exp(-nll) - 1): from the loss itself, because for a token
+// that is well predicted the difference of its logit and lse has few bits left.
+__device__ __forceinline__ float ce_label_entry(float nll, float g) {
+  return __fmul_rn(expm1f(-nll), g);
+}
+// What rounding to bf16 takes from it.
+__device__ __forceinline__ float ce_rounded_off(float x) {
+  return __fsub_rn(x, __uint_as_float(pack_bf16(x, 0.0f) << 16));
+}
+
 __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps, const CeTile& t,
                                            uint32_t addr, int row0, int half, CeOut& o) {
   const int lane = threadIdx.x & 31, m = t.m0 + row0 + lane;
@@ -369,10 +384,7 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
   const float l2 = has ? __fmul_rn(p.lse[m], kLog2e) : 0.0f;
   y = has ? y - p.v0 - t.n0 : -1;
   const int from = half * 128, cols = min(from + 128, p.nv - t.n0);
-  // The label's entry is exp(-nll) - 1: from the loss itself, because for a token that
-  // is well predicted the difference of its logit and lse has few bits left.
-  const float at_label =
-      has && y >= 0 && y < kMmN ? __fmul_rn(expm1f(-p.nll[m]), g) : 0.0f;
+  const float at_label = has && y >= 0 && y < kMmN ? ce_label_entry(p.nll[m], g) : 0.0f;
   // Which tokens have a label among each 32 entries of this warp's half.
   const int words = (p.N + 31) / 32;
 #pragma unroll
@@ -382,7 +394,7 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
       p.in_rows[(size_t)(t.n0 / 32 + from / 32 + k) * words + (t.m0 + row0) / 32] = tokens;
   }
   if (has && y >= from && y < from + 128)
-    p.resid[m] = __fsub_rn(at_label, __uint_as_float(pack_bf16(at_label, 0.0f) << 16));
+    p.resid[m] = ce_rounded_off(at_label);
   for (int c0 = from; c0 < cols; c0 += 64) {
     const uint32_t box = ce_box_begin(o);
 #pragma unroll
@@ -427,16 +439,17 @@ __device__ __forceinline__ void ce_add_row(float (&x)[32], const CeRow& row, flo
   }
 }
 
-// Whose rounding residual a lane's row takes: of dH the row's own token, of dW the
-// first kCeFixes tokens with this label, in order.  (What dW needs it for are rows with
-// one token or a few, which would carry one rounding as a whole; the roundings of
-// many are independent of one another, and stay as small in their sum as they are in one
-// term.)  `src`: where the row to add starts.
-constexpr int kCeFixes = 4;
+// Whose rounding residual a lane's row takes: of dH the row's own token's, of dW those
+// of all tokens with this label.  Their roundings are not independent: under a mean loss
+// every badly predicted token has -g there, rounded alike, and a frequent label's row
+// would be off as a whole by up to 2^-8.  Up to kCeFixes tokens are kept here, in
+// order (`src`: where the row to add starts); for a row with more, ce_label_kernel has
+// summed all of them (`sum`).
 struct CeFix {
   int toks;
   const uint16_t* src[kCeFixes];
   float r[kCeFixes];
+  const float* sum;  // or null
 };
 // The first 32 words of the map of labels for a warp's 32 entries of dW, one per lane
 // (read a tile ahead).
@@ -451,6 +464,7 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
   const int lane = threadIdx.x & 31, r0 = t.m0 + row0;
   CeFix f;
   f.toks = 0;
+  f.sum = nullptr;
   if (t.kind == 1) {
     // (Sums of several slices or pieces get theirs at the end.)
     const int y = p.dh_direct && r0 + lane < p.N ? p.labels[r0 + lane] : -1;
@@ -462,9 +476,9 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
     return f;
   }
   if (r0 >= p.nv) return f;
-  int tok[kCeFixes];
+  int tok[kCeFixes + 1];
 #pragma unroll
-  for (int k = 0; k < kCeFixes; ++k) tok[k] = 0;
+  for (int k = 0; k <= kCeFixes; ++k) tok[k] = 0;
   const int words = (p.N + 31) / 32;
   const uint32_t* in_rows = p.in_rows + (size_t)(r0 / 32) * words;
   for (int base = 0; base < words; base += 32) {
@@ -490,13 +504,17 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
           const int j = __ffs(m) - 1;
           if (__shfl_sync(0xffffffffu, rel[k], j) == lane) {
 #pragma unroll
-            for (int q = 0; q < kCeFixes; ++q)
+            for (int q = 0; q <= kCeFixes; ++q)
               if (f.toks == q) tok[q] = (base + first[k]) * 32 + j;
-            f.toks = min(f.toks + 1, kCeFixes);
+            ++f.toks;
           }
         }
       }
     }
+  }
+  if (f.toks > kCeFixes) {
+    f.sum = p.label_sums + (size_t)SPEC_CHECKED(tok[kCeFixes], p.N, kSiteLinearCe) * p.D;
+    f.toks = 0;
   }
 #pragma unroll
   for (int q = 0; q < kCeFixes; ++q)
@@ -534,6 +552,17 @@ __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& ma
 #pragma unroll
       for (int q = 1; q < kCeFixes; ++q)
         if (q < fix.toks) ce_add_row(x, ce_row(fix.src[q] + at, p.D - at), fix.r[q]);
+      if (fix.sum != nullptr) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q * 4 < p.D - at) {
+            const float4 a = reinterpret_cast<const float4*>(fix.sum + at)[q];
+            x[q * 4] = __fadd_rn(x[q * 4], a.x);
+            x[q * 4 + 1] = __fadd_rn(x[q * 4 + 1], a.y);
+            x[q * 4 + 2] = __fadd_rn(x[q * 4 + 2], a.z);
+            x[q * 4 + 3] = __fadd_rn(x[q * 4 + 3], a.w);
+          }
+      }
       if (sums) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) ce_box_put(box, q, pack_vec<float>(x + q * 4));
@@ -766,6 +795,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   cluster_sync();  // neither CTA leaves while the other may still reach its barriers
   tmem_fence_after();
   if (warp == kMmIssuer) tmem_free(tmem, 512);
+}
+
+// Labels with more than kCeFixes tokens: what rounding took from their entries of dZ,
+// times the tokens' hidden states, summed into the row of label_sums that belongs to the
+// label's (kCeFixes + 1)-th token.  Each of a CTA's eight warps looks whether its
+// token is such a one; the whole CTA then goes through the labels 1024 at a time, lists the
+// tokens in order and sums 512 columns, each 8 of them by one thread of each
+// quarter.  The additions' order depends on the sizes and labels alone.
+//
+// The kernel runs beside the first piece's dZ, on SMs that has none of or is done with: it
+// reads only what was there before that kernel, which lets its successor start after its
+// own wait for its predecessors.  It ends with a wait for that kernel, so that whoever
+// waits for this one has waited for both.
+// (Summing in dW's epilogue instead, the warp listing a row's tokens again for each 32
+// columns, took 1907 us where this takes 510, loss and gradients: 2048 tokens, V = 32000,
+// D = 1024, labels with p(v) ~ 1/v, whose many frequent labels share a few tiles.  Labels
+// that hardly repeat take 370 us there.)
+constexpr int kCeLabelThreads = 256, kCeLabelCols = 512, kCeLabelChunk = 1024;
+__global__ void __launch_bounds__(kCeLabelThreads)
+    ce_label_kernel(const __grid_constant__ CeParams p) {
+  constexpr int kWarps = kCeLabelThreads / 32, kGroups = kCeLabelCols / 8;
+  constexpr int kSubs = kCeLabelThreads / kGroups;
+  __shared__ int owner[kWarps];
+  __shared__ uint32_t bits[kCeLabelChunk / 32];
+  __shared__ int list[kCeLabelChunk];
+  __shared__ float weight[kCeLabelChunk];
+  __shared__ float part[kSubs][kGroups][9];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  {
+    const int i = blockIdx.x * kWarps + warp;
+    const int y = i < p.N ? p.labels[i] : -1;
+    int before = 0;  // tokens with this label before i
+    if (y >= 0 && y < p.V) {
+      for (int j0 = 0; j0 < i && before <= kCeFixes; j0 += 128) {
+        int l[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = j0 + k * 32 + lane;
+          l[k] = j < i ? p.labels[j] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) before += __popc(__ballot_sync(0xffffffffu, l[k] == y));
+      }
+    }
+    if (lane == 0) owner[warp] = before == kCeFixes ? y : -1;
+  }
+  __syncthreads();
+  const int group = tid % kGroups, sub = tid / kGroups;
+  const int col = blockIdx.y * kCeLabelCols + group * 8;
+  for (int w = 0; w < kWarps; ++w) {
+    const int y = owner[w];
+    if (y < 0) continue;
+    float s[8] = {};
+    for (int c = 0; c < p.N; c += kCeLabelChunk) {
+#pragma unroll
+      for (int k = 0; k < kCeLabelChunk / kCeLabelThreads; ++k) {
+        const int j = c + k * kCeLabelThreads + tid;
+        const uint32_t m = __ballot_sync(0xffffffffu, j < p.N && p.labels[j] == y);
+        if (lane == 0) bits[k * kWarps + warp] = m;
+      }
+      __syncthreads();
+      const uint32_t mine = bits[lane];  // the same in every warp
+      int at = __popc(mine);             // tokens up to this word: a scan over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += x;
+      }
+      const int n = __shfl_sync(0xffffffffu, at, 31);
+      if (warp == 0) {
+        at -= __popc(mine);
+        for (uint32_t m = mine; m != 0; m &= m - 1) list[at++] = c + lane * 32 + __ffs(m) - 1;
+      }
+      __syncthreads();
+      for (int k = tid; k < n; k += kCeLabelThreads) {
+        const int i = (int)SPEC_CHECKED(list[k], p.N, kSiteLinearCe);
+        weight[k] = ce_rounded_off(ce_label_entry(p.nll[i], p.g[i]));
+      }
+      __syncthreads();
+      if (col < p.D) {
+        for (int k = sub; k < n; k += 4 * kSubs) {
+          uint4 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            v[u] = k + u * kSubs < n ? *reinterpret_cast<const uint4*>(
+                                           p.h + (size_t)list[k + u * kSubs] * p.D + col)
+                                     : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float r = k + u * kSubs < n ? weight[k + u * kSubs] : 0.0f;
+            float a[8];
+            ElemTraits<uint16_t>::unpack(v[u], a);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = fmaf(r, a[e], s[e]);
+          }
+        }
+      }
+      __syncthreads();  // before the lists are written again
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[sub][group][e] = s[e];
+    __syncthreads();
+    if (sub == 0 && col < p.D) {
+#pragma unroll
+      for (int k = 1; k < kSubs; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = __fadd_rn(s[e], part[k][group][e]);
+      float4* out = reinterpret_cast<float4*>(
+          p.label_sums +
+          (size_t)SPEC_CHECKED(blockIdx.x * kWarps + w, p.N, kSiteLinearCe) * p.D + col);
+      out[0] = make_float4(s[0], s[1], s[2], s[3]);
+      out[1] = make_float4(s[4], s[5], s[6], s[7]);
+    }
+    __syncthreads();
+  }
+  pdl_wait();
 }
 
 // Tokens' pairs into lse and nll: `tokens` (a power of two up to 32) a CTA, the

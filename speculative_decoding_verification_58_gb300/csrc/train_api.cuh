@@ -75,7 +75,8 @@ inline cudaError_t ce_prepare(DeviceInfo* d) {
   if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads>, attr, kMmSmem)) != cudaSuccess) return e;
   // The small kernels between the products take the same split of L1, so that no SM has
   // to be idle to change it.
-  for (const void* k : {(const void*)ce_finish_kernel, (const void*)ce_round_kernel})
+  for (const void* k : {(const void*)ce_finish_kernel, (const void*)ce_round_kernel,
+                        (const void*)ce_label_kernel})
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
                                   cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
       return e;
@@ -111,6 +112,7 @@ inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLa
   p.dh_acc = reinterpret_cast<float*>(ws + lay.dh_acc);
   p.resid = reinterpret_cast<float*>(ws + lay.resid);
   p.in_rows = reinterpret_cast<uint32_t*>(ws + lay.in_rows);
+  p.label_sums = reinterpret_cast<float*>(ws + lay.label_sums);
   p.header = reinterpret_cast<WsHeader*>(ws);
   return p;
 }
@@ -181,6 +183,12 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
         !ce_map(&maps.dz_out, dz, N, p.nv, lay.piece, 32))
       return SPEC_ERR_CUDA;
     if (launch_ce<kCeDz>(d, maps, p, mb * blocks_of(p.nv, kMmN), s) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    // Once, beside the first piece's dZ; only labels of more tokens than kCeFixes need it.
+    if (p.first && d_weight != nullptr && N > kCeFixes &&
+        launch(ce_label_kernel,
+               dim3((unsigned)blocks_of(N, kCeLabelThreads / 32), (unsigned)blocks_of(D, kCeLabelCols)),
+               dim3(kCeLabelThreads), 0, s, true, p) != cudaSuccess)
       return SPEC_ERR_CUDA;
     if (launch_ce<kCeGrads>(d, maps, p, (long long)p.dh_units + p.dw_units, s) != cudaSuccess)
       return SPEC_ERR_CUDA;

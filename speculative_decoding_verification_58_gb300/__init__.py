@@ -682,7 +682,8 @@ class LinearCe:
     contents may change between calls, the tensors must stay alive.
 
     ``loss()`` fills and returns (nll, lse), ``grad()`` (d_hidden, d_weight)
-    from the nll and lse of the last ``loss()``.  ``need_hidden`` / ``need_weight``
+    from the nll and lse of the last ``loss()``, or from those that the caller
+    gave with both buffers; without either it is refused.  ``need_hidden`` / ``need_weight``
     False leaves that gradient out (None).  Both calls share one workspace:
     enqueue them on one stream.
     """
@@ -699,6 +700,8 @@ class LinearCe:
         _need(hidden, "hidden", hidden.dtype, (N, D), dev)
         _need(weight, "weight", hidden.dtype, (V, D), dev)
         _need(labels, "labels", torch.int32, (N,), dev)
+        # Whether grad() has a loss to start from: another call's, or loss() sets it.
+        self._filled = nll is not None and lse is not None
         with _alloc_on(stream, dev):
             if nll is None:
                 nll = torch.empty(N, dtype=torch.float32, device=dev)
@@ -742,12 +745,15 @@ class LinearCe:
     def loss(self):
         """Enqueue the loss; returns (nll, lse)."""
         _check(self._loss(*self._loss_args), "spec_linear_ce")
+        self._filled = True
         return self.nll, self.lse
 
     def grad(self):
         """Enqueue the gradients; returns (d_hidden, d_weight)."""
         if self._grad_args is None:
             raise ValueError("LinearCe was made without grad_nll")
+        if not self._filled:
+            raise ValueError("grad() needs nll and lse: call loss() first, or give both buffers")
         _check(self._grad(*self._grad_args), "spec_linear_ce_grad")
         return self.d_hidden, self.d_weight
 
@@ -772,6 +778,8 @@ def spec_linear_ce_grad(hidden, weight, labels, nll, lse, grad_nll, *, d_hidden=
     ``nll`` and ``lse`` are ``spec_linear_ce``'s on the same inputs; ``grad_nll`` float32 [N].
     ``need_hidden`` / ``need_weight`` False leaves that gradient out (None).
     """
+    if nll is None or lse is None:
+        raise ValueError("spec_linear_ce_grad needs spec_linear_ce's nll and lse")
     return LinearCe(hidden, weight, labels, grad_nll, nll=nll, lse=lse, d_hidden=d_hidden,
                     d_weight=d_weight, need_hidden=need_hidden, need_weight=need_weight,
                     workspace=workspace, stream=stream).grad()

@@ -402,6 +402,7 @@ spec_status_t spec_d3d_select(const int32_t* num_accepted, const int32_t* out_to
 
 #define SPEC_MAX_TOKENS (1 << 18) /* tokens per linear cross-entropy call */
 #define SPEC_MAX_WIDTH (1 << 15)  /* width of a hidden state */
+#define SPEC_TIMEOUT_NAN 0x7fc10557u /* bits of the NaN that a loss that timed out leaves */
 
 /*
  * Softmax cross entropy of a linear vocabulary head, without keeping the
@@ -428,7 +429,9 @@ spec_status_t spec_d3d_select(const int32_t* num_accepted, const int32_t* out_to
  *
  * Products and sums are in single precision.  A label >= V makes its token's
  * nll NaN (no gradient) and records SPEC_ERR_BAD_INPUT, readable with
- * spec_verify_device_status() on `workspace`.  A hidden state or weight that
+ * spec_verify_device_status() on `workspace`.  A device-side wait that runs out
+ * records SPEC_ERR_TIMEOUT there, and every nll and lse is the NaN with the bits
+ * SPEC_TIMEOUT_NAN.  A hidden state or weight that
  * is not finite makes the results it enters NaN, as the formula does.
  */
 size_t spec_linear_ce_workspace_bytes(int N, int V, int D);
@@ -451,7 +454,9 @@ spec_status_t spec_linear_ce(const void* hidden, const void* weight, spec_dtype_
  * The logits are formed again, a piece of the vocabulary at a time.  dZ is
  * rounded to bfloat16 before the two products, whose sums are in single
  * precision; what the rounding takes from the labels' entries is added back.  The hidden states of tokens without a label enter d_weight with
- * weight 0 and have to be finite.  Everything else is as for spec_linear_ce.
+ * weight 0 and have to be finite.  An lse of SPEC_TIMEOUT_NAN (the loss timed out)
+ * records SPEC_ERR_TIMEOUT, so that the loss's status is not lost where both
+ * calls share a workspace.  Everything else is as for spec_linear_ce.
  */
 size_t spec_linear_ce_grad_workspace_bytes(int N, int V, int D);
 spec_status_t spec_linear_ce_grad(const void* hidden, const void* weight, spec_dtype_t dtype,
@@ -549,6 +554,14 @@ int spec_debug_build(void);
  * reports 0 and SPEC_OK.  Returns SPEC_OK or SPEC_ERR_CUDA.
  */
 spec_status_t spec_debug_checks(int32_t* failures, int32_t* first_site, int reset, void* stream);
+
+/*
+ * Range-checking build: from now on the products of linear cross entropy on the
+ * current device record `status` (SPEC_ERR_TIMEOUT, as if a wait had run out; SPEC_OK
+ * ends it), so that what follows from a timeout can be tested without one.
+ * Waits for `stream`.  A release build returns SPEC_ERR_UNSUPPORTED.
+ */
+spec_status_t spec_debug_inject(spec_status_t status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -27,7 +27,8 @@ The functions keep the C names:
 ``spec_clip_grad_norm(...)``         the same, and the tensors scaled to a largest norm
 ``GradClipper(...)``                 the clip bound to fixed tensors
 ``spec_status_string(code)``
-``spec_debug_build()``, ``spec_debug_checks()``  the range-checking build (SPEC_VERIFY_DEBUG=1)
+``spec_debug_build()``, ``spec_debug_checks()``, ``spec_debug_inject()``
+                                     the range-checking build (SPEC_VERIFY_DEBUG=1)
 """
 
 from __future__ import annotations
@@ -53,6 +54,7 @@ SPEC_ERR_TIMEOUT = 6
 SPEC_ERR_INTERNAL = 7
 SPEC_F32 = 0
 SPEC_BF16 = 1
+SPEC_TIMEOUT_NAN = 0x7fc10557
 SPEC_FLAG_FULL_SWEEP = 1
 SPEC_FLAG_TEST_LATE_SLICES = 2
 
@@ -64,7 +66,8 @@ EXPORTS = ("spec_verify_workspace_bytes", "spec_verify", "spec_verify_ex", "spec
            "spec_verify_opd", "spec_d3d_select", "spec_linear_ce_workspace_bytes",
            "spec_linear_ce", "spec_linear_ce_grad_workspace_bytes", "spec_linear_ce_grad",
            "spec_opd_grad", "spec_grad_norm_workspace_bytes", "spec_grad_norm",
-           "spec_clip_grad_norm", "spec_debug_build", "spec_debug_checks")
+           "spec_clip_grad_norm", "spec_debug_build", "spec_debug_checks",
+           "spec_debug_inject")
 SPEC_STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -169,6 +172,8 @@ def lib() -> ctypes.CDLL:
     L.spec_debug_build.restype = ci
     L.spec_debug_checks.argtypes = [vp, vp, ci, vp]
     L.spec_debug_checks.restype = ci
+    L.spec_debug_inject.argtypes = [ci, vp]
+    L.spec_debug_inject.restype = ci
     _lib = L
     return L
 
@@ -199,6 +204,12 @@ def spec_debug_checks(reset: bool = False, stream=None) -> tuple[int, int]:
     if code != SPEC_OK:
         raise SpecVerifyError(code, "spec_debug_checks")
     return f.value, site.value
+
+
+def spec_debug_inject(status: int, stream=None) -> None:
+    """Range-checking build: linear cross entropy records ``status`` (SPEC_ERR_TIMEOUT, or
+    SPEC_OK to end it) as if a wait had run out; a release build refuses."""
+    _check(lib().spec_debug_inject(status, _stream_ptr(stream)), "spec_debug_inject")
 
 
 def status_string(code: int) -> str:

@@ -776,6 +776,9 @@ enum SpecDebugSite {
 
 __device__ int g_debug_failures;  // checks that failed since the last reset
 __device__ int g_debug_site;      // site of the first of them
+#ifdef SPEC_DEBUG
+__device__ int g_debug_inject;    // status that linear cross entropy records (spec_debug_inject)
+#endif
 
 __device__ __forceinline__ long long spec_debug_index(long long i, long long n, int site) {
   if (i >= 0 && i < n) return i;

@@ -183,7 +183,7 @@ struct CeParams {
   int dh_units, dw_units;  // units of the two products (0: not wanted)
   CeDeal deal;             // and how the pairs share them
   int a_rows;              // rows of A in a box (fewer than 128 where there are fewer tokens)
-  int check;               // CTA 0 checks the labels and writes the header
+  int check;               // CTA 0 checks labels and lse and writes the header (one kernel a call)
   WsHeader* header;
 };
 
@@ -232,7 +232,8 @@ struct CeBars {
   uint64_t full[kMmStages], empty[kMmStages], tfull[2], tempty[2];
   uint32_t tmem;
   int abort_flag;
-  int bad;  // labels outside the vocabulary
+  int bad;   // labels outside the vocabulary
+  int lost;  // tokens whose loss timed out (gradients)
 };
 
 struct CeTile {
@@ -581,18 +582,30 @@ __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& ma
   }
 }
 
-// Header of the workspace, and labels outside the vocabulary: the epilogue warps
-// of one CTA (its other warps go on).
-__device__ __forceinline__ void ce_check(const CeParams& p, int* bad) {
+// Header of the workspace: labels outside the vocabulary, and for the gradients a loss
+// that timed out, which lse tells (the loss's own status may have stood in this header).
+// Done by the epilogue warps of one CTA (its other warps go on).
+template <CeMode M>
+__device__ __forceinline__ void ce_check(const CeParams& p, CeBars& bars) {
   const int th = threadIdx.x - kMmEpilogue * 32, n = kMmThreads - kMmEpilogue * 32;
-  int mine = 0;
+  int bad = 0, lost = 0;
 #pragma unroll 4
-  for (int i = th; i < p.N; i += n) mine += p.labels[i] >= p.V ? 1 : 0;
-  if (mine) atomicAdd(bad, mine);
+  for (int i = th; i < p.N; i += n) {
+    bad += p.labels[i] >= p.V ? 1 : 0;
+    if (M == kCeDz) lost |= __float_as_uint(p.lse[i]) == SPEC_TIMEOUT_NAN ? 1 : 0;
+  }
+  if (bad) atomicAdd(&bars.bad, bad);
+  if (lost) atomicOr(&bars.lost, 1);
   asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
   if (th == 0) {
-    p.header->status = *bad ? SPEC_ERR_BAD_INPUT : SPEC_OK;
-    p.header->bad_requests = *bad;
+    const int found = *(volatile int*)&bars.bad;
+    int status = found ? SPEC_ERR_BAD_INPUT : SPEC_OK;
+    if (*(volatile int*)&bars.lost) status = SPEC_ERR_TIMEOUT;
+#ifdef SPEC_DEBUG
+    if (g_debug_inject != SPEC_OK) status = g_debug_inject;
+#endif
+    p.header->status = status;
+    p.header->bad_requests = found;
     p.header->first_bad = INT32_MAX;
   }
 }
@@ -615,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       mbar_init(&bars.tempty[a], 16);  // the epilogue warps of both CTAs
     }
     bars.abort_flag = 0;
-    bars.bad = 0;
+    bars.bad = bars.lost = 0;
     fence_mbar_init();
   }
   if (warp == kMmIssuer) tmem_alloc(&bars.tmem, 512);
@@ -720,7 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       }
     }
   } else {
-    if (p.check && blockIdx.x == 0) ce_check(p, &bars.bad);
+    if (p.check && blockIdx.x == 0) ce_check<M>(p, bars);
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
     const int half = (warp - kMmEpilogue) >> 2;
     CeOut out = {ring + kMmStages * kMmStageBytes + (warp - kMmEpilogue) * kMmBoxes * kMmBoxBytes, 0};
@@ -782,7 +795,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   }
   if (!ok) {
     *(volatile int*)&bars.abort_flag = 1;
-    if (lane == 0) record_status(p.header, SPEC_ERR_TIMEOUT);
+    if (lane == 0) atomicMax(&p.header->status, SPEC_ERR_TIMEOUT);  // over bad labels
     // Loads still on their way have to land before the CTAs end.
     if (warp == kMmProducer && lane == 0 && rank == 0) {
       int never = 0;
@@ -924,6 +937,7 @@ __global__ void __launch_bounds__(kCeFinishThreads)
   __shared__ float sm[2][kCeFinishThreads / 32][32];
   const int tid = threadIdx.x, tok = tid & (tokens - 1), groups = kCeFinishThreads / tokens;
   const int i = blockIdx.x * tokens + tok;
+  const bool lost = p.header->status == SPEC_ERR_TIMEOUT;
   const float2* part = p.partials + i;
   const float none = -FLT_MAX / 2;
   float m = none, s = 0.0f;
@@ -957,6 +971,10 @@ __global__ void __launch_bounds__(kCeFinishThreads)
   }
   __syncthreads();
   if (tid >= tokens || i >= p.N) return;
+  if (lost) {  // a wait ran out: some pairs are not this call's
+    nll[i] = lse[i] = __uint_as_float(SPEC_TIMEOUT_NAN);
+    return;
+  }
   float top = sm[0][0][tok];
 #pragma unroll
   for (int w = 1; w < kCeFinishThreads / 32; ++w) top = fmaxf(top, sm[0][w][tok]);

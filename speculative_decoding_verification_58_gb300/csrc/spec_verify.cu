@@ -605,6 +605,23 @@ int spec_debug_build(void) {
 #endif
 }
 
+spec_status_t spec_debug_inject(spec_status_t status, void* stream) {
+#ifdef SPEC_DEBUG
+  if (status != SPEC_OK && status != SPEC_ERR_TIMEOUT) return SPEC_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int32_t code = status;
+  if (cudaMemcpyToSymbolAsync(g_debug_inject, &code, sizeof code, 0, cudaMemcpyHostToDevice, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return SPEC_OK;
+#else
+  (void)status;
+  (void)stream;
+  return SPEC_ERR_UNSUPPORTED;
+#endif
+}
+
 spec_status_t spec_debug_checks(int32_t* failures, int32_t* first_site, int reset, void* stream) {
   int32_t f = 0, site = 0;
 #ifdef SPEC_DEBUG

@@ -184,6 +184,7 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
       return SPEC_ERR_CUDA;
     if (launch_ce<kCeDz>(d, maps, p, mb * blocks_of(p.nv, kMmN), s) != cudaSuccess)
       return SPEC_ERR_CUDA;
+    p.check = 0;  // the header is written once a call, or a timeout in dZ would be lost
     // Once, beside the first piece's dZ; only labels of more tokens than kCeFixes need it.
     if (p.first && d_weight != nullptr && N > kCeFixes &&
         launch(ce_label_kernel,

@@ -456,7 +456,8 @@ spec_status_t spec_linear_ce(const void* hidden, const void* weight, spec_dtype_
  * precision; what the rounding takes from the labels' entries is added back.  The hidden states of tokens without a label enter d_weight with
  * weight 0 and have to be finite.  An lse of SPEC_TIMEOUT_NAN (the loss timed out)
  * records SPEC_ERR_TIMEOUT, so that the loss's status is not lost where both
- * calls share a workspace.  Everything else is as for spec_linear_ce.
+ * calls share a workspace; entries that this or a timeout of the call's own kept from
+ * being computed are NaN.  Everything else is as for spec_linear_ce.
  */
 size_t spec_linear_ce_grad_workspace_bytes(int N, int V, int D);
 spec_status_t spec_linear_ce_grad(const void* hidden, const void* weight, spec_dtype_t dtype,

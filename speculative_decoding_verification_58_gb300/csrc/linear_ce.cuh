@@ -527,10 +527,11 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
 }
 
 // dH and dW: bf16 where the tile is the whole sum, else dH's sums in single
-// precision, set by the first piece and added to by the others.
+// precision, set by the first piece and added to by the others.  `dead`: a wait ran
+// out, here or before, and the result is NaN.
 __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& maps,
                                              const CeTile& t, uint32_t addr, int row0, int half,
-                                             CeOut& o, const CeFix& fix) {
+                                             CeOut& o, const CeFix& fix, bool dead) {
   const int lane = threadIdx.x & 31;
   const bool dh = t.kind == 1;
   const int rows = dh ? p.N : p.nv, r0 = t.m0 + row0;
@@ -548,6 +549,10 @@ __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& ma
       if (t.iters == 0) {  // a slice past the end of a short last piece
 #pragma unroll
         for (int c = 0; c < 32; ++c) x[c] = 0.0f;
+      }
+      if (dead) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = __int_as_float(0x7fc00000);
       }
       if (fix.toks > 0) ce_add_row(x, row, fix.r[0]);
 #pragma unroll
@@ -740,6 +745,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     CeTile next = ce_tile<M>(p, 0);
     next.m0 += rank * kMmHalf;
     uint32_t word = M == kCeGrads ? ce_fix_word(p, next, quarter * 32) : 0;
+    // After a timeout (the loss's, dZ's) nothing here is this call's: not the map of
+    // labels either, which then is not looked at.
+    bool dead = M == kCeGrads && p.header->status == SPEC_ERR_TIMEOUT;
     int sub = 0;
     auto filled = [&]() -> uint32_t {  // the next accumulator, once filled
       const int acc = sub & 1;
@@ -761,7 +769,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       next.m0 += rank * kMmHalf;
       CeFix fix;
       if (M == kCeGrads) {
-        fix = ce_fix(p, t, quarter * 32, word);
+        fix.toks = 0;
+        fix.sum = nullptr;
+        if (!dead) fix = ce_fix(p, t, quarter * 32, word);
         word = ce_fix_word(p, next, quarter * 32);
       }
       if constexpr (M == kCeLoss) {
@@ -784,12 +794,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         if (!ok) break;
         ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half, sum);
       } else {
-        const uint32_t addr = filled();
-        if (!ok) break;
-        if (M == kCeDz) ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);
-        else ce_grad_tile(p, maps, t, addr, quarter * 32, half, out, fix);
+        const uint32_t addr = ok ? filled() : tmem;
+        if (M == kCeDz) {
+          if (!ok) break;
+          ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);
+        } else {  // the tiles that are left become NaN
+          dead |= !ok;
+          ce_grad_tile(p, maps, t, addr, quarter * 32, half, out, fix, dead);
+        }
       }
-      drained();
+      if (ok) drained();
     }
     if (M != kCeLoss && lane == 0) bulk_wait_read<0>();
   }
@@ -1033,6 +1047,10 @@ __global__ void __launch_bounds__(256)
   for (int k = 1; k < min(8, p.splits); ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] += part[k][g][e];
+  if (p.header->status == SPEC_ERR_TIMEOUT) {  // some of the sums are not this call's
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __int_as_float(0x7fc00000);
+  }
   const int row = (int)(i / p.D), col = (int)(i - (long long)row * p.D);
   const int y = p.labels[row];
   if (y >= 0 && y < p.V) {

@@ -90,3 +90,46 @@ def test_the_release_build_injects_nothing():
     with pytest.raises(sv.SpecVerifyError) as e:
         sv.spec_debug_inject(sv.SPEC_ERR_TIMEOUT)
     assert e.value.code == sv.SPEC_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("N,V,D", SHAPES)
+def test_no_gradients_of_a_lost_loss(N, V, D):
+    h, w, y, g = inputs(N, V, D, seed=23)
+    ce = sv.LinearCe(h, w, y, g)
+    ce.loss()
+    want = [t.clone() for t in ce.grad()]
+    nll, lse = ce.nll.clone(), ce.lse.clone()
+    lse[y < 0] = 0.0  # (not read for a token without a label)
+    # An ordinary NaN spoils what it enters: every entry of the token's dZ but the
+    # label's, which is exp(-nll) - 1.
+    last = int((y >= 0).nonzero()[-1])
+    ce.lse[last] = float("nan")
+    dh, dw = ce.grad()
+    assert torch.isnan(dh).all(1).nonzero().tolist() == [[last]]
+    assert int(torch.isnan(dh).any(1).sum()) == 1
+    assert (~torch.isnan(dw)).any(1).nonzero().tolist() == [[int(y[last])]]
+    lse[0].view(torch.int32).fill_(sv.SPEC_TIMEOUT_NAN)
+    for kw in (dict(), dict(need_hidden=False), dict(need_weight=False)):
+        for t in sv.spec_linear_ce_grad(h, w, y, nll, lse, g, **kw):
+            assert t is None or bool(torch.isnan(t).all())
+    ce.loss()
+    assert all(torch.equal(a, b) for a, b in zip(want, ce.grad()))
+
+
+def test_gradients_that_timed_out():
+    run_debug("""
+for N, V, D in t.SHAPES:
+    h, w, y, g = t.inputs(N, V, D, seed=24)
+    ce = sv.LinearCe(h, w, y, g)
+    ce.loss()
+    want = [x.clone() for x in ce.grad()]
+    sv.spec_debug_inject(sv.SPEC_ERR_TIMEOUT)
+    for x in ce.grad():
+        assert bool(torch.isnan(x).all())
+    assert sv.spec_verify_device_status(ce.workspace) == sv.SPEC_ERR_TIMEOUT
+    sv.spec_debug_inject(sv.SPEC_OK)
+    for x, z in zip(ce.grad(), want):
+        assert torch.equal(x, z)
+    assert sv.spec_verify_device_status(ce.workspace) == sv.SPEC_OK
+assert sv.spec_debug_checks()[0] == 0
+""")

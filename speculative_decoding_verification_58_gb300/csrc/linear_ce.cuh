@@ -24,6 +24,7 @@
 #pragma once
 
 #include "grad_norm.cuh"
+#include "opd_grad.cuh"
 #include "tcgen05.cuh"
 
 namespace specv {
@@ -36,7 +37,7 @@ constexpr int kCeMaxWidth = SPEC_MAX_WIDTH;
 constexpr int kCeFixes = 4;  // tokens of a label that a tile of dW adds one by one
 
 struct CeLayout {
-  size_t partials, z_label, resid, in_rows, dz, dh_acc, label_sums, total;
+  size_t partials, resid, in_rows, dz, dh_acc, label_sums, total;
   int tiles;   // vocabulary tiles
   int parts;   // (max, sum) pairs of a token
   int piece;   // vocabulary entries per piece (a multiple of kCeTileV)
@@ -101,8 +102,6 @@ inline CeLayout ce_layout(int N, int V, int D, bool grad) {
   if (!grad) {
     l.partials = o;
     o = align256(o + (size_t)N * l.parts * sizeof(float2));
-    l.z_label = o;
-    o = align256(o + (size_t)N * sizeof(float));
   } else {
     l.resid = o;
     o = align256(o + (size_t)N * sizeof(float));
@@ -168,7 +167,6 @@ struct CeParams {
   const float* g;          // [N] (gradients)
   int N, V, D, parts;
   float2* partials;        // [parts, N]: (max log2 e, sum 2^(z log2 e - max log2 e))
-  float* z_label;          // [N]
   int piece, v0, nv;       // piece: buffer width, first entry, entries
   const uint16_t* h;       // [N, D]
   const uint16_t* w;       // [V, D]
@@ -288,7 +286,7 @@ __device__ __forceinline__ CeTile ce_tile(const CeParams& p, int i) {
 }
 
 // Epilogue of one thread: row `m` of the tile, one half of its columns in tensor memory.
-// The label's logit goes to z_label and is left out of the sums.
+// The label's logit is left out of the sums (ce_finish_kernel forms it itself).
 __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, uint32_t addr,
                                             int m, int half, const float (&sum)[kCePartV]) {
   const bool live = m < p.N;
@@ -311,14 +309,9 @@ __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, 
     }
     const int rel = y - t.n0 - c0;
     if (__any_sync(0xffffffffu, rel >= 0 && rel < 32)) {
-      float z = 0.0f;
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        if (c == rel) {
-          z = x[c];
-          x[c] = -INFINITY;
-        }
-      if (rel >= 0 && rel < 32) p.z_label[SPEC_CHECKED(m, p.N, kSiteLinearCe)] = z;
+        if (c == rel) x[c] = -INFINITY;
     }
     float mx = x[0];
 #pragma unroll
@@ -396,7 +389,10 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
   }
   if (has && y >= from && y < from + 128)
     p.resid[m] = ce_rounded_off(at_label);
-  for (int c0 = from; c0 < cols; c0 += 64) {
+#pragma unroll
+  for (int q0 = 0; q0 < kCePartV; q0 += 64) {
+    const int c0 = from + q0;
+    if (c0 >= cols) break;
     const uint32_t box = ce_box_begin(o);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -774,11 +770,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         if (!dead) fix = ce_fix(p, t, quarter * 32, word);
         word = ce_fix_word(p, next, quarter * 32);
       }
-      if constexpr (M == kCeLoss) {
+      if constexpr (M != kCeGrads) {
         float sum[kCePartV];
 #pragma unroll
         for (int c = 0; c < kCePartV; ++c) sum[c] = 0.0f;
-        for (int k = kMmChunk; k < t.iters && ok; k += kMmChunk) {
+        for (int k = kMmChunk; M == kCeLoss && k < t.iters && ok; k += kMmChunk) {
           const uint32_t addr = filled() + half * kCePartV;
           if (!ok) break;
 #pragma unroll
@@ -792,16 +788,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         }
         const uint32_t addr = ok ? filled() : 0;
         if (!ok) break;
-        ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half, sum);
+        if constexpr (M == kCeLoss)
+          ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half, sum);
+        else
+          ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);
       } else {
         const uint32_t addr = ok ? filled() : tmem;
-        if (M == kCeDz) {
-          if (!ok) break;
-          ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);
-        } else {  // the tiles that are left become NaN
-          dead |= !ok;
-          ce_grad_tile(p, maps, t, addr, quarter * 32, half, out, fix, dead);
-        }
+        dead |= !ok;  // the tiles that are left become NaN
+        ce_grad_tile(p, maps, t, addr, quarter * 32, half, out, fix, dead);
       }
       if (ok) drained();
     }
@@ -941,15 +935,47 @@ __global__ void __launch_bounds__(kCeLabelThreads)
   pdl_wait();
 }
 
+// h . w over D entries, by a warp, the sum in every lane.
+__device__ __forceinline__ float ce_dot(const uint16_t* h, const uint16_t* w, int D) {
+  const int lane = threadIdx.x & 31;
+  float2 a[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 4
+  for (int d = lane * 8; d < D; d += 256) {
+    float x[8], y[8];
+    ElemTraits<uint16_t>::unpack(*reinterpret_cast<const uint4*>(h + d), x);
+    ElemTraits<uint16_t>::unpack(*reinterpret_cast<const uint4*>(w + d), y);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+      a[(e >> 1) & 1] = f32x2_fma(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]),
+                                  a[(e >> 1) & 1]);
+  }
+  const float2 t = f32x2_add(a[0], a[1]);
+  return warp_sum(__fadd_rn(t.x, t.y));
+}
+
 // Tokens' pairs into lse and nll: `tokens` (a power of two up to 32) a CTA, the
-// other threads over each one's pairs, eight loads at a time.
+// other threads over each one's pairs, eight loads at a time.  The labels' logits are
+// formed here, a warp each, rounded to nearest: the tensor cores' sums are cut off
+// towards zero, which for the largest logit of a row, a long sum of one sign, is a
+// bias of 3e-7 of itself, and a small loss has all of it.  That comes before the wait for
+// the products, which start this kernel after their own wait: what the caller gave is
+// there.
 constexpr int kCeFinishThreads = 1024;
 __global__ void __launch_bounds__(kCeFinishThreads)
     ce_finish_kernel(const __grid_constant__ CeParams p, int tokens, float* nll, float* lse) {
+  __shared__ float sm[2][kCeFinishThreads / 32][32];
+  __shared__ float z_label[32];
+  const int tid = threadIdx.x, tok = tid & (tokens - 1), groups = kCeFinishThreads / tokens;
+  const int warp = tid >> 5;
+  if (warp < tokens && blockIdx.x * tokens + warp < p.N) {
+    const int at = blockIdx.x * tokens + warp, y = p.labels[at];
+    if (y >= 0 && y < p.V) {
+      const float dot = ce_dot(p.h + (size_t)at * p.D, p.w + (size_t)y * p.D, p.D);
+      if ((tid & 31) == 0) z_label[warp] = dot;
+    }
+  }
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float sm[2][kCeFinishThreads / 32][32];
-  const int tid = threadIdx.x, tok = tid & (tokens - 1), groups = kCeFinishThreads / tokens;
   const int i = blockIdx.x * tokens + tok;
   const bool lost = p.header->status == SPEC_ERR_TIMEOUT;
   const float2* part = p.partials + i;
@@ -972,7 +998,6 @@ __global__ void __launch_bounds__(kCeFinishThreads)
     }
   }
   // Each token's maximum and sum: over its lanes in a warp, then over the warps.
-  const int warp = tid >> 5;
   for (int o = 16; o >= tokens; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
     const float n = fmaxf(m, m2);
@@ -999,7 +1024,7 @@ __global__ void __launch_bounds__(kCeFinishThreads)
   const float nan = __int_as_float(0x7fc00000);
   const int y = p.labels[i];
   const bool has = y >= 0 && y < p.V;
-  const float z = has ? p.z_label[i] : -INFINITY;
+  const float z = has ? z_label[tok] : -INFINITY;
   // s = sum over the others of 2^(z_v log2 e - top); the label's own term is apart.
   // `gap` is how far the others' maximum lies above the label, in base 2:
   //   nll = log(1 + s 2^gap),  lse = log(s 2^top + 2^(z log2 e)).

@@ -72,7 +72,8 @@ inline cudaError_t ce_prepare(DeviceInfo* d) {
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeLoss>, attr, kMmSmem)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeDz>, attr, kMmSmem)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads>, attr, kMmSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads>, attr, kMmSmem)) != cudaSuccess)
+    return e;
   // The small kernels between the products take the same split of L1, so that no SM has
   // to be idle to change it.
   for (const void* k : {(const void*)ce_finish_kernel, (const void*)ce_round_kernel,
@@ -107,7 +108,6 @@ inline CeParams ce_params(const int32_t* labels, int N, int V, int D, const CeLa
   p.m_blocks = (N + kMmM - 1) / kMmM;
   p.a_rows = N < kMmHalf ? (N + 7) / 8 * 8 : kMmHalf;
   p.partials = reinterpret_cast<float2*>(ws + lay.partials);
-  p.z_label = reinterpret_cast<float*>(ws + lay.z_label);
   p.piece = lay.piece;
   p.dh_acc = reinterpret_cast<float*>(ws + lay.dh_acc);
   p.resid = reinterpret_cast<float*>(ws + lay.resid);
@@ -127,6 +127,8 @@ inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32
   if (device_info(&d) != cudaSuccess || ce_prepare(d) != cudaSuccess) return SPEC_ERR_CUDA;
   const CeLayout lay = ce_layout(N, V, D, false);
   CeParams p = ce_params(labels, N, V, D, lay, ws);
+  p.h = static_cast<const uint16_t*>(hidden);
+  p.w = static_cast<const uint16_t*>(weight);
   p.check = 1;
   CeMaps maps = {};
   if (!ce_map(&maps.h_k, hidden, N, D, D, p.a_rows) ||
@@ -182,8 +184,8 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
         !ce_map(&maps.dz_mn, dz, N, p.nv, lay.piece, 64) ||
         !ce_map(&maps.dz_out, dz, N, p.nv, lay.piece, 32))
       return SPEC_ERR_CUDA;
-    if (launch_ce<kCeDz>(d, maps, p, mb * blocks_of(p.nv, kMmN), s) != cudaSuccess)
-      return SPEC_ERR_CUDA;
+    const long long z_tiles = mb * blocks_of(p.nv, kMmN);
+    if (launch_ce<kCeDz>(d, maps, p, z_tiles, s) != cudaSuccess) return SPEC_ERR_CUDA;
     p.check = 0;  // the header is written once a call, or a timeout in dZ would be lost
     // Once, beside the first piece's dZ; only labels of more tokens than kCeFixes need it.
     if (p.first && d_weight != nullptr && N > kCeFixes &&
@@ -191,8 +193,8 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
                dim3((unsigned)blocks_of(N, kCeLabelThreads / 32), (unsigned)blocks_of(D, kCeLabelCols)),
                dim3(kCeLabelThreads), 0, s, true, p) != cudaSuccess)
       return SPEC_ERR_CUDA;
-    if (launch_ce<kCeGrads>(d, maps, p, (long long)p.dh_units + p.dw_units, s) != cudaSuccess)
-      return SPEC_ERR_CUDA;
+    const long long units = (long long)p.dh_units + p.dw_units;
+    if (launch_ce<kCeGrads>(d, maps, p, units, s) != cudaSuccess) return SPEC_ERR_CUDA;
   }
   if (d_hidden != nullptr && !lay.direct) {
     const long long n = (long long)N * D;

@@ -180,6 +180,7 @@ struct CeParams {
   int z_tiles, m_blocks;   // tiles of z, of which so many are one vocabulary tile's
   int dh_units, dw_units;  // units of the two products (0: not wanted)
   CeDeal deal;             // and how the pairs share them
+  int group;               // loss: rows of the product that the tokens take (32: one each)
   int a_rows;              // rows of A in a box (fewer than 128 where there are fewer tokens)
   int check;               // CTA 0 checks labels and lse and writes the header (one kernel a call)
   WsHeader* header;
@@ -209,6 +210,14 @@ constexpr int kMmM = 256, kMmN = 256, kMmK = 64, kMmStages = 6;
 // sums are cut off towards zero at every step, which over a long row is a bias (loss
 // of 2048 tokens, D = 2048: off by 1.1e-6 of itself in one chunk).
 constexpr int kMmChunk = 16;
+// Up to kCeFewTokens tokens leave rows of the product unused.  `group` of them (a power of
+// two) take one part of the sum over D, the next `group` rows the next part, and so on
+// over 32 rows: the hidden states are loaded that many rows lower, with zeros around
+// them, and a zero is added without a cut.  One token's logits so are sums of 32 parts,
+// joined in the epilogue (D = 1024, V = 151936: worst error of the loss of one token in
+// 24 4e-6 of itself, 8e-7 in parts; 59.8 us, 57.9 without; chunks of four steps
+// instead: 72).
+constexpr int kCeFewTokens = 16;
 constexpr int kMmHalf = 128;  // rows of A, of B and of the result in each CTA
 constexpr int kMmABytes = kMmHalf * kMmK * 2, kMmBBytes = kMmHalf * kMmK * 2;
 constexpr int kMmStageBytes = kMmABytes + kMmBBytes;  // each CTA's
@@ -330,6 +339,59 @@ __device__ __forceinline__ void ce_loss_row(const CeParams& p, const CeTile& t, 
   }
   if (live && from < cols)
     p.partials[(size_t)(t.n0 / kCePartV + half) * p.N + m] = make_float2(ms, s);
+}
+
+// The same for a few tokens, whose logits' parts lie in the 32 rows of a warp: lane l
+// has a part of token l mod group.  Each exchange adds the parts of two lanes and leaves
+// either with half of the columns, so that in the end a lane has `group` of 32
+// columns, whole.
+__device__ __forceinline__ void ce_loss_few(const CeParams& p, const CeTile& t, uint32_t addr,
+                                            int half, const float (&sum)[kCePartV]) {
+  const int lane = threadIdx.x & 31, group = p.group;
+  const int m = lane & (group - 1), first = lane & ~(group - 1);
+  const int y = m < p.N ? p.labels[m] : -1;
+  const int from = half * kCePartV, cols = min(from + kCePartV, p.V - t.n0);
+  float ms = -FLT_MAX / 2, s = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kCePartV; q += 32) {
+    const int c0 = from + q;
+    if (c0 >= cols) break;
+    float x[32];
+    tmem_load32(addr + c0, x);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x[c] = __fadd_rn(x[c], sum[q + c]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o < group) break;
+      const bool up = lane & o;
+#pragma unroll
+      for (int c = 0; c < o; ++c) {
+        const float mine = up ? x[c + o] : x[c], theirs = up ? x[c] : x[c + o];
+        x[c] = __fadd_rn(mine, __shfl_xor_sync(0xffffffffu, theirs, o));
+      }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kCeFewTokens; ++c) {
+      const int col = c0 + first + c;
+      if (c >= group || col >= cols || col == y - t.n0) x[c] = -INFINITY;
+      mx = fmaxf(mx, x[c]);
+    }
+    const float nms = fmaxf(ms, __fmul_rn(mx, kLog2e));
+    s = __fmul_rn(s, ex2(__fsub_rn(ms, nms)));
+#pragma unroll
+    for (int c = 0; c < kCeFewTokens; ++c)
+      if (c < group) s = __fadd_rn(s, ex2(fmaf(x[c], kLog2e, -nms)));
+    ms = nms;
+  }
+  for (int o = 16; o >= group; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, ms, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const float n = fmaxf(ms, m2);
+    s = __fadd_rn(__fmul_rn(s, ex2(__fsub_rn(ms, n))), __fmul_rn(s2, ex2(__fsub_rn(m2, n))));
+    ms = n;
+  }
+  if (lane < p.N && lane < group && from < cols)
+    p.partials[(size_t)(t.n0 / kCePartV + half) * p.N + lane] = make_float2(ms, s);
 }
 
 // A warp's results go through shared memory: a box of 32 rows x 128 bytes, its
@@ -659,6 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const CeTile t = ce_tile<M>(p, i);
         if (t.kind < 0) break;
         const int am = t.m0 + rank * kMmHalf, bn = t.n0 + rank * kMmHalf;
+        const int parts_len = M == kCeLoss ? (t.iters * p.group + 31) / 32 : 1;
         for (int k = 0; k < t.iters; ++k, ++loads) {
           const int s = loads % kMmStages, round = loads / kMmStages;
           if (round > 0 && !mbar_sleep(&bars.empty[s], (round - 1) & 1, &bars.abort_flag)) {
@@ -676,7 +739,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                                                                         : p.a_rows * kMmK * 2));
           const int k0 = t.k0 + k * kMmK;
           if (M != kCeGrads) {
-            if (all_a || rank == 0) tma_load(a, &maps.h_k, k0, am, bar);
+            // (Rows before the first and past the last token read as 0.)
+            const int part = M == kCeLoss && p.group < 32 ? k / parts_len * p.group : 0;
+            if (all_a || rank == 0) tma_load(a, &maps.h_k, k0, am - part, bar);
             tma_load(b, &maps.w_k, k0, (M == kCeDz ? p.v0 : 0) + bn, bar);
           } else {
             if (!a_mn) {
@@ -788,7 +853,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         }
         const uint32_t addr = ok ? filled() : 0;
         if (!ok) break;
-        if constexpr (M == kCeLoss)
+        if (M == kCeLoss && p.group < 32) {
+          if (t.m0 + quarter == 0) ce_loss_few(p, t, addr, half, sum);
+        } else if constexpr (M == kCeLoss)
           ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half, sum);
         else
           ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);

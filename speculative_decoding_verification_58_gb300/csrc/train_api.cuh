@@ -130,6 +130,11 @@ inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32
   p.h = static_cast<const uint16_t*>(hidden);
   p.w = static_cast<const uint16_t*>(weight);
   p.check = 1;
+  p.group = 32;
+  if (N <= kCeFewTokens) {
+    while (p.group / 2 >= N) p.group /= 2;
+    p.a_rows = 32;
+  }
   CeMaps maps = {};
   if (!ce_map(&maps.h_k, hidden, N, D, D, p.a_rows) ||
       !ce_map(&maps.w_k, weight, V, D, D, kMmHalf))

@@ -12,6 +12,7 @@ torch = pytest.importorskip("torch")
 
 import speculative_decoding_verification_58_gb300 as sv
 import train_ref as ref
+from test_gpu_linear_ce import check_grad, check_loss, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -33,6 +34,24 @@ def leaning(N, V, D, seed):
     return h, w, y
 
 
+@pytest.mark.parametrize("n,D", [(1, 1024), (1, 4096), (2, 2048), (3, 1000), (4, 1024)])
+def test_losses_of_a_few_tokens_have_no_bias(n, D):
+    V = 3000
+    h, w, y = leaning(96, V, D, seed=D + n)
+    nll, lse = (torch.cat(x) for x in zip(*[sv.spec_linear_ce(h[i:i + n].contiguous(), w,
+                                                              y[i:i + n].contiguous())
+                                            for i in range(0, 96, n)]))
+    rn, rl = ref.ce(h, w, y)
+    # Absolute, for lse as for the loss: half a step of the logit (2^-24 of 16) for each of the
+    # two logits that count, and the approximate exponentials and logarithms (2^-22).
+    bound = 2 * 2.0 ** -24 * float((h.double() @ w.double().t()).max()) + 2.0 ** -22
+    assert abs(float((lse.double() - rl).mean())) <= bound
+    # The losses are small (nearly all mass at the label), so that what is left of them is
+    # relative: the errors of both logits, the other entries' exponentials and sums.
+    rel = (nll.double() - rn) / rn
+    assert abs(float(rel.mean())) <= bound + 2.0 ** -21
+
+
 @pytest.mark.parametrize("N,D", [(300, 1024), (64, 4096)])
 def test_the_labels_logit_is_rounded_to_nearest(N, D):
     h, w, y = leaning(N, 2000, D, seed=N)
@@ -44,3 +63,25 @@ def test_the_labels_logit_is_rounded_to_nearest(N, D):
     # label's (2^-24 of itself) and the approximate functions.
     bound = 2.0 ** -21 * float(others) + 2.0 ** -24 * float(z.max()) + 2.0 ** -21
     assert abs(float(((nll.double() - rn) / rn).mean())) <= bound
+
+
+@pytest.mark.parametrize("N", range(1, 18))
+def test_few_tokens(N):
+    for V, D in ((1, 8), (300, 72), (5001, 1032), (257, 2056)):
+        h, w, y, g = inputs(N, V, D, seed=100 * N + D)
+        y[0] = V - 1
+        if N > 2:
+            y[1], y[2] = 0, -1
+        ce = sv.LinearCe(h, w, y, g)
+        nll, lse = ce.loss()
+        check_loss(h, w, y, nll, lse)
+        check_grad(h, w, y, g, *ce.grad())
+        one = [sv.spec_linear_ce(h[i:i + 1].contiguous(), w, y[i:i + 1].contiguous())
+               for i in range(N)]
+        check_loss(h, w, y, torch.cat([a for a, _ in one]), torch.cat([b for _, b in one]))
+    if N > 2:  # a bad token spoils its own results only
+        h[1, 3] = float("nan")
+        nll, lse = sv.spec_linear_ce(h, w, y)
+        assert torch.isnan(lse).nonzero().tolist() == [[1]]
+        keep = torch.arange(N, device="cuda") != 1
+        check_loss(h[keep], w, y[keep], nll[keep], lse[keep])

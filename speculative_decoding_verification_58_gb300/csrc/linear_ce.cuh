@@ -431,8 +431,11 @@ __device__ __forceinline__ float ce_rounded_off(float x) {
   return __fsub_rn(x, __uint_as_float(pack_bf16(x, 0.0f) << 16));
 }
 
+// `sum`: what earlier chunks of the sums over D gave (kChunks).
+template <bool kChunks>
 __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps, const CeTile& t,
-                                           uint32_t addr, int row0, int half, CeOut& o) {
+                                           uint32_t addr, int row0, int half, CeOut& o,
+                                           const float (&sum)[kCePartV]) {
   const int lane = threadIdx.x & 31, m = t.m0 + row0 + lane;
   int y = m < p.N ? p.labels[m] : -1;
   const bool has = y >= 0 && y < p.V;
@@ -463,6 +466,7 @@ __device__ __forceinline__ void ce_dz_tile(const CeParams& p, const CeMaps& maps
       const int rel = y - c0 - h * 32;
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
+        if (kChunks) x[c] = __fadd_rn(x[c], sum[q0 + h * 32 + c]);
         const float d = has ? __fmul_rn(ex2(fmaf(x[c], kLog2e, -l2)), g) : 0.0f;
         x[c] = c == rel && has ? at_label : d;
       }
@@ -673,7 +677,11 @@ __device__ __forceinline__ void ce_check(const CeParams& p, CeBars& bars) {
   }
 }
 
-template <CeMode M>
+// kChunks: sums are taken in chunks (the loss; dZ where D has more than one: the code for it
+// costs dZ's short form 1 us of a call of 15 us, 64 tokens, V = 1024, D = 128).  With
+// the 128 sums of a thread the compiler spills a few registers around the chunks' loop
+// (60 to 92 bytes of 168 registers, the share of ten warps on an SM).
+template <CeMode M, bool kChunks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     ce_mma_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CeParams p) {
   extern __shared__ unsigned char smem_raw[];
@@ -771,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
         int k = 0;
         do {  // (once where there is nothing to sum)
-          const int acc = sub & 1, end = M == kCeLoss ? min(t.iters, k + kMmChunk) : t.iters;
+          const int acc = sub & 1, end = kChunks ? min(t.iters, k + kMmChunk) : t.iters;
           if (sub >= 2 &&
               !mbar_sleep(&bars.tempty[acc], ((sub >> 1) - 1) & 1, &bars.abort_flag)) {
             ok = false;
@@ -839,7 +847,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         float sum[kCePartV];
 #pragma unroll
         for (int c = 0; c < kCePartV; ++c) sum[c] = 0.0f;
-        for (int k = kMmChunk; M == kCeLoss && k < t.iters && ok; k += kMmChunk) {
+        for (int k = kMmChunk; kChunks && k < t.iters && ok; k += kMmChunk) {
           const uint32_t addr = filled() + half * kCePartV;
           if (!ok) break;
 #pragma unroll
@@ -858,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         } else if constexpr (M == kCeLoss)
           ce_loss_row(p, t, addr, t.m0 + quarter * 32 + lane, half, sum);
         else
-          ce_dz_tile(p, maps, t, addr, quarter * 32, half, out);
+          ce_dz_tile<kChunks>(p, maps, t, addr, quarter * 32, half, out, sum);
       } else {
         const uint32_t addr = ok ? filled() : tmem;
         dead |= !ok;  // the tiles that are left become NaN

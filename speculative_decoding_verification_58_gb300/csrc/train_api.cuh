@@ -70,9 +70,11 @@ inline cudaError_t ce_prepare(DeviceInfo* d) {
   if (d->ce_ready) return cudaSuccess;
   cudaError_t e;
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeLoss>, attr, kMmSmem)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeDz>, attr, kMmSmem)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads>, attr, kMmSmem)) != cudaSuccess)
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeLoss, true>, attr, kMmSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeDz, false>, attr, kMmSmem)) != cudaSuccess)
+    return e;
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeDz, true>, attr, kMmSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads, false>, attr, kMmSmem)) != cudaSuccess)
     return e;
   // The small kernels between the products take the same split of L1, so that no SM has
   // to be idle to change it.
@@ -85,7 +87,7 @@ inline cudaError_t ce_prepare(DeviceInfo* d) {
   return cudaSuccess;
 }
 
-template <CeMode M>
+template <CeMode M, bool kChunks>
 cudaError_t launch_ce(const DeviceInfo* d, const CeMaps& maps, CeParams& p, long long tiles,
                       cudaStream_t stream) {
   const long long pairs = std::max<long long>(1, std::min<long long>(tiles, d->sms / 2));
@@ -93,7 +95,7 @@ cudaError_t launch_ce(const DeviceInfo* d, const CeMaps& maps, CeParams& p, long
     p.deal = ce_deal(p.dh_units, p.dw_units, p.split_iters, (p.N + kMmK - 1) / kMmK, (int)pairs);
   else
     p.z_tiles = (int)tiles;
-  return launch(ce_mma_kernel<M>, dim3((unsigned)(2 * pairs)), dim3(kMmThreads), kMmSmem, stream,
+  return launch(ce_mma_kernel<M, kChunks>, dim3((unsigned)(2 * pairs)), dim3(kMmThreads), kMmSmem, stream,
                 true, maps, p);
 }
 
@@ -139,7 +141,7 @@ inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32
   if (!ce_map(&maps.h_k, hidden, N, D, D, p.a_rows) ||
       !ce_map(&maps.w_k, weight, V, D, D, kMmHalf))
     return SPEC_ERR_CUDA;
-  if (launch_ce<kCeLoss>(d, maps, p, blocks_of(N, kMmM) * lay.tiles, s) != cudaSuccess)
+  if (launch_ce<kCeLoss, true>(d, maps, p, blocks_of(N, kMmM) * lay.tiles, s) != cudaSuccess)
     return SPEC_ERR_CUDA;
   int tokens = 1;
   while (tokens < 32 && tokens < N) tokens *= 2;
@@ -190,7 +192,9 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
         !ce_map(&maps.dz_out, dz, N, p.nv, lay.piece, 32))
       return SPEC_ERR_CUDA;
     const long long z_tiles = mb * blocks_of(p.nv, kMmN);
-    if (launch_ce<kCeDz>(d, maps, p, z_tiles, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    if ((D > kMmChunk * kMmK ? launch_ce<kCeDz, true>(d, maps, p, z_tiles, s)
+                             : launch_ce<kCeDz, false>(d, maps, p, z_tiles, s)) != cudaSuccess)
+      return SPEC_ERR_CUDA;
     p.check = 0;  // the header is written once a call, or a timeout in dZ would be lost
     // Once, beside the first piece's dZ; only labels of more tokens than kCeFixes need it.
     if (p.first && d_weight != nullptr && N > kCeFixes &&
@@ -199,7 +203,7 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
                dim3(kCeLabelThreads), 0, s, true, p) != cudaSuccess)
       return SPEC_ERR_CUDA;
     const long long units = (long long)p.dh_units + p.dw_units;
-    if (launch_ce<kCeGrads>(d, maps, p, units, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    if (launch_ce<kCeGrads, false>(d, maps, p, units, s) != cudaSuccess) return SPEC_ERR_CUDA;
   }
   if (d_hidden != nullptr && !lay.direct) {
     const long long n = (long long)N * D;

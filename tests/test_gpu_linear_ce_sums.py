@@ -85,3 +85,22 @@ def test_few_tokens(N):
         assert torch.isnan(lse).nonzero().tolist() == [[1]]
         keep = torch.arange(N, device="cuda") != 1
         check_loss(h[keep], w, y[keep], nll[keep], lse[keep])
+
+
+def test_probabilities_of_a_wide_head_sum_to_one():
+    # With a column of ones in the weight, that column of dH is g sum_v (p_v - [v = y]) = 0: what
+    # is there is what z, formed again, is off against lse.  All logits are about 16, sums of
+    # one sign over D = 8192.
+    N, V, D = 256, 4096, 8192
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    w = (0.5 + torch.rand((V, D), generator=gen, device="cuda")).to(torch.bfloat16)
+    w[:, 0] = 1.0
+    h = (16.0 / D * 2 * torch.rand((N, D), generator=gen, device="cuda")).to(torch.bfloat16)
+    y = torch.randint(0, V, (N,), generator=gen, device="cuda", dtype=torch.int32)
+    nll, lse = sv.spec_linear_ce(h, w, y)
+    dh, _ = sv.spec_linear_ce_grad(h, w, y, nll, lse, torch.ones(N, device="cuda"), need_weight=False)
+    # The means of N V roundings of dZ's entries (2^-8 of 1 / V at most, of random sign), six
+    # deviations; two logits' sums of eight chunks (2^-21 of themselves each, as above).
+    noise = 6 * 2.0 ** -8 / 3.0 ** 0.5 / (N * V) ** 0.5
+    top = float((h.double() @ w.double().t()).max())
+    assert abs(float(dh[:, 0].double().mean())) <= noise + 2.0 ** -21 * top / 4 + 2.0 ** -20

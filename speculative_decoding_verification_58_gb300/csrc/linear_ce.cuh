@@ -218,6 +218,10 @@ constexpr int kMmChunk = 16;
 // 24 4e-6 of itself, 8e-7 in parts; 59.8 us, 57.9 without; chunks of four steps
 // instead: 72).
 constexpr int kCeFewTokens = 16;
+// dW sums over the tokens and dH over a slice of the vocabulary; so long a sum of one sign
+// that the cuts would show beside the result's own rounding (up to 2^-8) is summed in
+// chunks as well (262144 tokens in one: short by 4.8e-4 of itself; 65536: 7e-5).
+constexpr int kMmGradChunk = 1024;
 constexpr int kMmHalf = 128;  // rows of A, of B and of the result in each CTA
 constexpr int kMmABytes = kMmHalf * kMmK * 2, kMmBBytes = kMmHalf * kMmK * 2;
 constexpr int kMmStageBytes = kMmABytes + kMmBBytes;  // each CTA's
@@ -590,10 +594,12 @@ __device__ __forceinline__ CeFix ce_fix(const CeParams& p, const CeTile& t, int 
 
 // dH and dW: bf16 where the tile is the whole sum, else dH's sums in single
 // precision, set by the first piece and added to by the others.  `dead`: a wait ran
-// out, here or before, and the result is NaN.
+// out, here or before, and the result is NaN.  `sum`: what earlier chunks gave (kChunks).
+template <bool kChunks>
 __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& maps,
                                              const CeTile& t, uint32_t addr, int row0, int half,
-                                             CeOut& o, const CeFix& fix, bool dead) {
+                                             CeOut& o, const CeFix& fix, bool dead,
+                                             const float* sum) {
   const int lane = threadIdx.x & 31;
   const bool dh = t.kind == 1;
   const int rows = dh ? p.N : p.nv, r0 = t.m0 + row0;
@@ -608,6 +614,10 @@ __device__ __forceinline__ void ce_grad_tile(const CeParams& p, const CeMaps& ma
       if (fix.toks > 0) row = ce_row(fix.src[0] + at, p.D - at);
       float x[32];
       tmem_load32(addr + c0 + h, x);
+      if (kChunks) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = __fadd_rn(x[c], sum[c0 - from + h + c]);
+      }
       if (t.iters == 0) {  // a slice past the end of a short last piece
 #pragma unroll
         for (int c = 0; c < 32; ++c) x[c] = 0.0f;
@@ -677,13 +687,15 @@ __device__ __forceinline__ void ce_check(const CeParams& p, CeBars& bars) {
   }
 }
 
-// kChunks: sums are taken in chunks (the loss; dZ where D has more than one: the code for it
-// costs dZ's short form 1 us of a call of 15 us, 64 tokens, V = 1024, D = 128).  With
-// the 128 sums of a thread the compiler spills a few registers around the chunks' loop
-// (60 to 92 bytes of 168 registers, the share of ten warps on an SM).
+// kChunks: sums are taken in chunks (the loss; dZ and the gradients where some sum has more
+// than one: the code for it costs dZ's short form 1 us of a call of 15 us, 64 tokens,
+// V = 1024, D = 128).  With the 128 sums of a thread the compiler spills a few registers
+// around the chunks' loop (60 to 92 bytes of 168 registers, the share of ten warps
+// on an SM), the gradients' form all of the sums: their loop turns once in 300 us.
 template <CeMode M, bool kChunks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     ce_mma_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CeParams p) {
+  constexpr int kChunk = M == kCeGrads ? kMmGradChunk : kMmChunk;
   extern __shared__ unsigned char smem_raw[];
   __shared__ CeBars bars;
   const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u;
@@ -779,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
         int k = 0;
         do {  // (once where there is nothing to sum)
-          const int acc = sub & 1, end = kChunks ? min(t.iters, k + kMmChunk) : t.iters;
+          const int acc = sub & 1, end = kChunks ? min(t.iters, k + kChunk) : t.iters;
           if (sub >= 2 &&
               !mbar_sleep(&bars.tempty[acc], ((sub >> 1) - 1) & 1, &bars.abort_flag)) {
             ok = false;
@@ -843,11 +855,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         if (!dead) fix = ce_fix(p, t, quarter * 32, word);
         word = ce_fix_word(p, next, quarter * 32);
       }
-      if constexpr (M != kCeGrads) {
-        float sum[kCePartV];
+      float sum[kCePartV];
+      if (kChunks) {
 #pragma unroll
         for (int c = 0; c < kCePartV; ++c) sum[c] = 0.0f;
-        for (int k = kMmChunk; kChunks && k < t.iters && ok; k += kMmChunk) {
+        for (int k = kChunk; k < t.iters && ok; k += kChunk) {
           const uint32_t addr = filled() + half * kCePartV;
           if (!ok) break;
 #pragma unroll
@@ -859,6 +871,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           }
           drained();
         }
+      }
+      if constexpr (M != kCeGrads) {
         const uint32_t addr = ok ? filled() : 0;
         if (!ok) break;
         if (M == kCeLoss && p.group < 32) {
@@ -870,7 +884,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       } else {
         const uint32_t addr = ok ? filled() : tmem;
         dead |= !ok;  // the tiles that are left become NaN
-        ce_grad_tile(p, maps, t, addr, quarter * 32, half, out, fix, dead);
+        ce_grad_tile<kChunks>(p, maps, t, addr, quarter * 32, half, out, fix, dead, sum);
       }
       if (ok) drained();
     }

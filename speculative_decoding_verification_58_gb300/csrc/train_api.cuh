@@ -76,6 +76,8 @@ inline cudaError_t ce_prepare(DeviceInfo* d) {
   if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeDz, true>, attr, kMmSmem)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads, false>, attr, kMmSmem)) != cudaSuccess)
     return e;
+  if ((e = cudaFuncSetAttribute(ce_mma_kernel<kCeGrads, true>, attr, kMmSmem)) != cudaSuccess)
+    return e;
   // The small kernels between the products take the same split of L1, so that no SM has
   // to be idle to change it.
   for (const void* k : {(const void*)ce_finish_kernel, (const void*)ce_round_kernel,
@@ -203,7 +205,11 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
                dim3(kCeLabelThreads), 0, s, true, p) != cudaSuccess)
       return SPEC_ERR_CUDA;
     const long long units = (long long)p.dh_units + p.dw_units;
-    if (launch_ce<kCeGrads, false>(d, maps, p, units, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    const bool chunks = (p.dh_units > 0 && p.split_iters > kMmGradChunk) ||
+                        (p.dw_units > 0 && N > kMmGradChunk * kMmK);
+    if ((chunks ? launch_ce<kCeGrads, true>(d, maps, p, units, s)
+                : launch_ce<kCeGrads, false>(d, maps, p, units, s)) != cudaSuccess)
+      return SPEC_ERR_CUDA;
   }
   if (d_hidden != nullptr && !lay.direct) {
     const long long n = (long long)N * D;

@@ -104,3 +104,31 @@ def test_probabilities_of_a_wide_head_sum_to_one():
     noise = 6 * 2.0 ** -8 / 3.0 ** 0.5 / (N * V) ** 0.5
     top = float((h.double() @ w.double().t()).max())
     assert abs(float(dh[:, 0].double().mean())) <= noise + 2.0 ** -21 * top / 4 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("N,D", [(262144, 1024), (100000, 136)])
+def test_weight_gradients_of_very_many_tokens(N, D):
+    # W = 0: every entry of dZ but the labels' is 1 / V exactly, and a row of dW without labels
+    # the mean of the hidden states, all positive.  A cut takes less than a step (2^-23) of the
+    # running sum, which over a chunk of 4096 steps is half its end on average: 2^-12 of it.
+    V = 64
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    scale = 0.5 + torch.rand((1, D), generator=gen, device="cuda")
+    h = (torch.rand((N, D), generator=gen, device="cuda") * scale).to(torch.bfloat16)
+    w = torch.zeros((V, D), dtype=torch.bfloat16, device="cuda")
+    y = (torch.arange(N, device="cuda") % 3).to(torch.int32)
+    ce = sv.LinearCe(h, w, y, torch.ones(N, device="cuda"), need_hidden=False)
+    ce.loss()
+    _, dw = ce.grad()
+    want = torch.zeros(V, D, dtype=torch.float64, device="cuda")
+    for r in range(0, N, 8192):
+        part = h[r:r + 8192].double()
+        want += part.sum(0) / V
+        for k in range(3):
+            want[k] -= part[y[r:r + 8192] == k].sum(0)
+    err = (dw.double() - want).abs()
+    assert torch.all(err <= (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -18) * want.abs())
+    row, x = want[5], dw[5].double()
+    step = torch.ldexp(torch.ones_like(row), torch.frexp(row)[1] - 9)
+    noise = 6 * float((step * row).square().sum().sqrt() / row.square().sum()) / 3.0 ** 0.5
+    assert abs(float(((x - row) * row).sum() / row.square().sum())) <= 2.0 ** -12 + noise

@@ -910,7 +910,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 // Labels with more than kCeFixes tokens: what rounding took from their entries of dZ,
 // times the tokens' hidden states, summed into the row of label_sums that belongs to the
 // label's (kCeFixes + 1)-th token.  Each of a CTA's eight warps looks whether its
-// token is such a one; the whole CTA then goes through the labels 1024 at a time, lists the
+// token is such a one; the whole CTA then goes through the labels 4096 at a time, lists the
 // tokens in order and sums 512 columns, each 8 of them by one thread of each
 // quarter.  The additions' order depends on the sizes and labels alone.
 //
@@ -921,14 +921,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 // (Summing in dW's epilogue instead, the warp listing a row's tokens again for each 32
 // columns, took 1907 us where this takes 510, loss and gradients: 2048 tokens, V = 32000,
 // D = 1024, labels with p(v) ~ 1/v, whose many frequent labels share a few tiles.  Labels
-// that hardly repeat take 370 us there.)
-constexpr int kCeLabelThreads = 256, kCeLabelCols = 512, kCeLabelChunk = 1024;
+// that hardly repeat take 370 us there.  65536 tokens, V = 1000, D = 512, gradients: 854 us,
+// 653 without this kernel; with lists of 1024 labels 1020.)
+constexpr int kCeLabelThreads = 256, kCeLabelCols = 512, kCeLabelChunk = 4096;
 __global__ void __launch_bounds__(kCeLabelThreads)
     ce_label_kernel(const __grid_constant__ CeParams p) {
   constexpr int kWarps = kCeLabelThreads / 32, kGroups = kCeLabelCols / 8;
   constexpr int kSubs = kCeLabelThreads / kGroups;
+  constexpr int kWords = kCeLabelChunk / kCeLabelThreads;  // 32 labels each, of a warp
   __shared__ int owner[kWarps];
-  __shared__ uint32_t bits[kCeLabelChunk / 32];
+  __shared__ int found[kWarps];
   __shared__ int list[kCeLabelChunk];
   __shared__ float weight[kCeLabelChunk];
   __shared__ float part[kSubs][kGroups][9];
@@ -939,15 +941,15 @@ __global__ void __launch_bounds__(kCeLabelThreads)
     const int y = i < p.N ? p.labels[i] : -1;
     int before = 0;  // tokens with this label before i
     if (y >= 0 && y < p.V) {
-      for (int j0 = 0; j0 < i && before <= kCeFixes; j0 += 128) {
-        int l[4];
+      for (int j0 = 0; j0 < i && before <= kCeFixes; j0 += 256) {
+        int l[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const int j = j0 + k * 32 + lane;
           l[k] = j < i ? p.labels[j] : -1;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) before += __popc(__ballot_sync(0xffffffffu, l[k] == y));
+        for (int k = 0; k < 8; ++k) before += __popc(__ballot_sync(0xffffffffu, l[k] == y));
       }
     }
     if (lane == 0) owner[warp] = before == kCeFixes ? y : -1;
@@ -960,29 +962,35 @@ __global__ void __launch_bounds__(kCeLabelThreads)
     if (y < 0) continue;
     float s[8] = {};
     for (int c = 0; c < p.N; c += kCeLabelChunk) {
+      // Each warp takes 512 labels in a row.
+      const int c0 = c + warp * (kWords * 32) + lane;
+      uint32_t hits = 0;  // the lane's own labels, one bit a word
 #pragma unroll
-      for (int k = 0; k < kCeLabelChunk / kCeLabelThreads; ++k) {
-        const int j = c + k * kCeLabelThreads + tid;
-        const uint32_t m = __ballot_sync(0xffffffffu, j < p.N && p.labels[j] == y);
-        if (lane == 0) bits[k * kWarps + warp] = m;
-      }
-      __syncthreads();
-      const uint32_t mine = bits[lane];  // the same in every warp
-      int at = __popc(mine);             // tokens up to this word: a scan over the lanes
+      for (int k = 0; k < kWords; ++k)
+        hits |= (uint32_t)(c0 + k * 32 < p.N && p.labels[c0 + k * 32] == y) << k;
+      int mine = 0;  // the warp's tokens
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += x;
-      }
-      const int n = __shfl_sync(0xffffffffu, at, 31);
-      if (warp == 0) {
-        at -= __popc(mine);
-        for (uint32_t m = mine; m != 0; m &= m - 1) list[at++] = c + lane * 32 + __ffs(m) - 1;
-      }
+      for (int k = 0; k < kWords; ++k)
+        mine += __popc(__ballot_sync(0xffffffffu, (hits >> k) & 1));
+      if (lane == 0) found[warp] = mine;
       __syncthreads();
-      for (int k = tid; k < n; k += kCeLabelThreads) {
-        const int i = (int)SPEC_CHECKED(list[k], p.N, kSiteLinearCe);
-        weight[k] = ce_rounded_off(ce_label_entry(p.nll[i], p.g[i]));
+      int at = 0, n = 0;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        at += k < warp ? found[k] : 0;
+        n += found[k];
+      }
+      if (mine > 0) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          const uint32_t m = __ballot_sync(0xffffffffu, (hits >> k) & 1);
+          if ((hits >> k) & 1) {
+            const int slot = at + __popc(m & ((1u << lane) - 1)), i = c0 + k * 32;
+            list[slot] = i;
+            weight[slot] = ce_rounded_off(ce_label_entry(p.nll[i], p.g[i]));
+          }
+          at += __popc(m);
+        }
       }
       __syncthreads();
       if (col < p.D) {
@@ -990,9 +998,11 @@ __global__ void __launch_bounds__(kCeLabelThreads)
           uint4 v[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            v[u] = k + u * kSubs < n ? *reinterpret_cast<const uint4*>(
-                                           p.h + (size_t)list[k + u * kSubs] * p.D + col)
-                                     : make_uint4(0, 0, 0, 0);
+            v[u] = k + u * kSubs < n
+                       ? *reinterpret_cast<const uint4*>(
+                             p.h + (size_t)SPEC_CHECKED(list[k + u * kSubs], p.N, kSiteLinearCe) *
+                                       p.D + col)
+                       : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const float r = k + u * kSubs < n ? weight[k + u * kSubs] : 0.0f;

@@ -145,8 +145,12 @@ inline spec_status_t ce_loss(const void* hidden, const void* weight, const int32
     return SPEC_ERR_CUDA;
   if (launch_ce<kCeLoss, true>(d, maps, p, blocks_of(N, kMmM) * lay.tiles, s) != cudaSuccess)
     return SPEC_ERR_CUDA;
+  // Tokens of a CTA of the join: a sector's worth of partials (4), more only where the CTAs
+  // still cover the SMs, so that the labels' logits are formed by many at once (512 tokens,
+  // D = 2048: 8 us with 4 a CTA, 14 with 32; 2048 tokens, D = 4096: 12 with 16, 17
+  // with 32).
   int tokens = 1;
-  while (tokens < 32 && tokens < N) tokens *= 2;
+  while (tokens < 32 && tokens < N && (tokens < 4 || blocks_of(N, tokens) > d->sms)) tokens *= 2;
   if (launch(ce_finish_kernel, dim3((unsigned)blocks_of(N, tokens)), dim3(kCeFinishThreads), 0, s,
              true, p, tokens, nll, lse) != cudaSuccess)
     return SPEC_ERR_CUDA;

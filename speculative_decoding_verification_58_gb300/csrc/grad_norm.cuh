@@ -9,7 +9,7 @@
 // run of units.  The second pass goes through a CTA's run backwards: what the
 // first read last is still in L2.  A few units are done by one cluster of CTAs in one
 // launch, with the sums exchanged through distributed shared memory (12 tensors of
-// 20000 entries in all: 7.0 us as two launches).  The order of every addition is
+// 20000 entries in all: 8.5 to 11 us, 11.8 as two launches).  The order of every addition is
 // fixed by sizes and alignments alone, so two calls on the same tensors give the
 // same bits.
 //
@@ -22,7 +22,9 @@
 // The three kinds of sums are carried apart, as float-float pairs, and joined in double
 // precision at the end.
 // Infinities and NaN, which a float-float pair cannot carry, go into a plain sum
-// of their own; a norm that is not finite leaves every tensor as it is.
+// of their own: where an entry is one, the norm is, and every tensor stays as it is.  (A sum of
+// finite entries whose root is above the largest float gives an infinite norm, and the
+// tensors are scaled all the same.)
 //
 // Tensors are read by plain loads, here and in the other training kernels: the read-only
 // path is for data that nobody writes while the kernel lives, and a clip in place

@@ -16,11 +16,12 @@
 // kept per token and added to both in single precision.  The other entries' roundings
 // stay: at most 2^-8 of their share of a row.
 //
-// Measured (V = 151936): loss of 2048 tokens, D = 2048, 735 us (1.73 PFLOP/s); loss and
-// gradients of 2048 tokens, D = 4096, 5.95 ms and of 512 tokens, D = 2048, 0.91 ms (1.72
-// and 1.40 PFLOP/s, the logits formed twice).  Bound by the tensor cores (92 to 95 % of
-// their cycles) where there are many tokens, by dW's epilogue and stores at 512, by
-// reading W at a few (loss of one token, D = 1024: 57 us, 5.5 TB/s).
+// Measured (V = 151936): loss of 2048 tokens, D = 2048, 727 to 746 us on several boxes
+// (1.71 to 1.75 PFLOP/s); loss and gradients of 2048 tokens, D = 4096, 5.9 to 6.1 ms and of
+// 512 tokens, D = 2048, 0.91 to 0.95 ms (1.7 and 1.37 PFLOP/s, the logits formed twice).
+// Bound by the tensor cores (88 to 94 % of their cycles) where there are many tokens, by
+// dW's epilogue and stores at 512, by reading W at a few (loss of one token, D = 1024:
+// 60 us, 5.2 TB/s).
 #pragma once
 
 #include "grad_norm.cuh"
@@ -208,14 +209,15 @@ constexpr int kMmM = 256, kMmN = 256, kMmK = 64, kMmStages = 6;
 // The loss sums a logit in chunks of kMmChunk steps, each from zero in an accumulator of
 // its own, and adds the chunks in registers, rounded to nearest: the tensor cores'
 // sums are cut off towards zero at every step, which over a long row is a bias (loss
-// of 2048 tokens, D = 2048: off by 1.1e-6 of itself in one chunk).
+// of 2048 tokens, D = 2048: off by 1.1e-6 of itself in one chunk, 5e-7 in chunks of 16
+// steps; of 8 or 4 half and a fourth of that, but 772 and 881 us instead of 739).
 constexpr int kMmChunk = 16;
 // Up to kCeFewTokens tokens leave rows of the product unused.  `group` of them (a power of
 // two) take one part of the sum over D, the next `group` rows the next part, and so on
 // over 32 rows: the hidden states are loaded that many rows lower, with zeros around
 // them, and a zero is added without a cut.  One token's logits so are sums of 32 parts,
 // joined in the epilogue (D = 1024, V = 151936: worst error of the loss of one token in
-// 24 4e-6 of itself, 8e-7 in parts; 59.8 us, 57.9 without; chunks of four steps
+// 24 4e-6 of itself, 8e-7 in parts; 60.9 us, 58.7 without; chunks of four steps
 // instead: 72).
 constexpr int kCeFewTokens = 16;
 // dW sums over the tokens and dH over a slice of the vocabulary; so long a sum of one sign

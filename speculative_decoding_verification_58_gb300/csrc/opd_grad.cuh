@@ -33,11 +33,12 @@
 // window of each row.  The target row, which then lies differently, is read as the
 // aligned blocks around a window and shifted into place.
 //
-// Measured: 128 requests of up to 16 rows of 151936 bf16, 310 us (1.28 GB read and
-// written once: 189 us); DRAM at 45 % and issue at 56 % of their peaks: a third of the
+// Measured: 128 requests of up to 16 rows of 151936 bf16, 313 to 331 us on several boxes
+// (1.28 GB read and written once: 189 us; 370 us where every position sums entry by
+// entry); DRAM at 45 % and issue at 56 % of their peaks: a third of the
 // time lies between the passes (copies, cluster barriers), which three CTAs an SM
-// overlap in part.  192, 224, 288 or 320 threads a CTA took 319 to 327 us (352 and more,
-// 375 and up), 16-CTA clusters 394 to 409, resident clusters that copy ahead 359, three
+// overlap in part.  Where 256 threads a CTA took 311 us, 192, 224, 288 or 320 took 319 to 327
+// (352 and more, 375 and up), 16-CTA clusters 394 to 409, resident clusters that copy ahead 359, three
 // passes over L2 453.
 #pragma once
 

@@ -231,9 +231,9 @@ inline spec_status_t ce_grad(const void* hidden, const void* weight, const int32
 // share them at kOgSliceBytes each, so that three fit an SM (a CTA's own
 // variables and what the system keeps are in the difference to a third of 228 KB).
 // Longer ones are read from memory in every pass, one CTA per 4096 entries up to eight
-// (measured: 128 requests of up to 16 rows of 151936 bf16 336 us from shared memory,
-// 453 us without; 32 requests in float, which would leave one CTA per SM, 241 and
-// 193 us; 60 requests of 32000 bf16 41 and 58 us).
+// (measured, before the passes over shared memory came to 313 us: 128 requests of up to 16
+// rows of 151936 bf16 336 us, 453 us without; 32 requests in float, which would leave one
+// CTA per SM, 241 and 193 us; 60 requests of 32000 bf16 41 and 58 us).
 constexpr int kOgSliceBytes = 76000;
 
 inline size_t opd_grad_slice(int V, int cs, size_t es) {

@@ -33,7 +33,7 @@
 // window of each row.  The target row, which then lies differently, is read as the
 // aligned blocks around a window and shifted into place.
 //
-// Measured: 128 requests of up to 16 rows of 151936 bf16, 313 to 331 us on several boxes
+// Measured: 128 requests of up to 16 rows of 151936 bf16, 313 to 335 us on several boxes
 // (1.28 GB read and written once: 189 us; 370 us where every position sums entry by
 // entry); DRAM at 45 % and issue at 56 % of their peaks: a third of the
 // time lies between the passes (copies, cluster barriers), which three CTAs an SM

@@ -517,6 +517,143 @@ spec_status_t spec_clip_grad_norm(const void* const* grads, void* const* outs,
                                   float max_norm, float* norm, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/*
+ * The calls around a verification round: tokens drawn under a request's sampling
+ * settings, the same truncation of logits, and the pass of new tokens over a paged
+ * key-value cache.  As everywhere, the calls are asynchronous on `stream`, allocate
+ * nothing and can be captured into a graph (after a first call of each on the
+ * device, which sets its kernels up).  Host-detectable errors return before
+ * anything is enqueued; among them is an output that shares memory with an input
+ * or another output (SPEC_ERR_INVALID_ARG), but for what is said below.
+ */
+
+#define SPEC_MAX_ROWS (1 << 24) /* rows of a sampling call, new tokens of a cache call */
+
+/*
+ * Sampling with temperature, top-k, top-p and min-p by inverse CDF.  For a row of
+ * logits z at temperature T > 0, let p = softmax(z / T) and order the entries by z
+ * from the largest down, equal ones by index from the lowest up:
+ *   K1 = the first top_k entries                            (top_k = 0: all)
+ *   K2 = the shortest prefix of K1 of at least top_p of K1's mass  (top_p = 1: K1)
+ *   K  = the entries of K2 with p_v >= min_p max p
+ * The token is the first index, ascending, whose cumulative mass over K exceeds
+ * u times the mass of K.  At T = 0 it is the argmax (lowest index), K that entry
+ * alone, and the other settings and u are not used.
+ *
+ *   logits       [rows, V] dtype, row-major contiguous, aligned to the entry
+ *   group        rows per request: row r takes the settings r / group.  Padded
+ *                logits [B, n, V] are B * n rows in groups of n
+ *   temperature  [rows / group, rounded up] float: 0 or finite and >= 2^-126
+ *   top_k        int32 >= 0, or NULL (off), per request like temperature
+ *   top_p        float in (0, 1], or NULL (1)
+ *   min_p        float in [0, 1], or NULL (0)
+ *   uniforms     [rows] float in [0, 1)
+ *   rows, V      below 1: SPEC_ERR_INVALID_ARG; rows > SPEC_MAX_ROWS or
+ *                V > SPEC_MAX_V: SPEC_ERR_UNSUPPORTED
+ *   tokens       [rows] int32 out
+ *   kept         [rows, V] dtype out, or NULL: the row truncated as by spec_truncate
+ *                (may be `logits` itself, in place)
+ *
+ * All buffers are device memory.  A row whose settings are out of range, whose
+ * entries hold a NaN or (T > 0) +inf, or none above -inf, gets token -1 and a kept
+ * row of NaN (which verification reports as invalid); at T = 0 a NaN is never the
+ * maximum, as for spec_verify.  A uniform out of range gives token -1 alone.
+ * The masses are summed as whole numbers (units of 2^-42 of the largest or finer), so
+ * that a row's result does not depend on the order of its additions: the same row
+ * gives the same token on every call and in every batch.
+ */
+spec_status_t spec_sample(const void* logits, spec_dtype_t dtype, int rows, int V, int group,
+                          const float* temperature, const int32_t* top_k, const float* top_p,
+                          const float* min_p, const float* uniforms, int32_t* tokens, void* kept,
+                          void* stream);
+
+/*
+ * The truncation on its own: kept[r][v] = logits[r][v] for v in K, -inf elsewhere.
+ * spec_verify on target and draft rows truncated with the settings of their
+ * requests accepts and resamples losslessly for truncated sampling (draft
+ * tokens drawn by spec_sample with the same settings).  Arguments as for
+ * spec_sample; kept may be `logits` itself (in place), else may not overlap it.
+ */
+spec_status_t spec_truncate(const void* logits, spec_dtype_t dtype, int rows, int V, int group,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, void* kept, void* stream);
+
+/*
+ * A paged key-value cache and the new tokens of a batch of requests.  Entry `pos` of
+ * request b lies in page page_table[b][pos / page_size], slot pos % page_size.
+ * Request b's new tokens are rows new_start[b] .. new_start[b + 1] - 1 of a
+ * packed batch (its L_b drafts and the token before them, say: the rows of
+ * spec_verify_packed), and its last entries: token t is entry
+ * kv_len[b] - (number of new tokens) + t.
+ */
+typedef struct {
+  void* k_cache;  /* [num_pages, page_size, kv_heads, width], 16-byte aligned, entries of a */
+  void* v_cache;  /* head contiguous, the other strides as given */
+  long long k_page, k_slot, k_head;  /* entries from page to page, slot to slot, head to */
+  long long v_page, v_slot, v_head;  /* head: multiples of 8, width or more */
+  int num_pages;
+  int page_size;  /* a power of two, 8 to 1024 */
+  int kv_heads;   /* 1 to 1024 */
+  int width;      /* entries of a head: 64 or 128 */
+  const int32_t* page_table;  /* [B, max_pages] (device); what no request uses is not read */
+  int max_pages;              /* max_pages * page_size <= INT32_MAX */
+  const int32_t* new_start;   /* [B + 1] (device), not decreasing */
+  const int32_t* kv_len;      /* [B] (device): entries with the new tokens' */
+  int B;
+} spec_paged_cache_t;
+
+/*
+ * Write the new tokens' keys and values into the cache.
+ *   k_new, v_new  [rows, kv_heads, width] dtype, 16-byte aligned, rows k_stride and
+ *                 v_stride entries apart (multiples of 8), heads `width` apart
+ *   dtype         SPEC_BF16; SPEC_F32 is SPEC_ERR_UNSUPPORTED
+ * A request whose rows lie outside 0 .. rows - 1, whose kv_len is less than its
+ * number of new tokens or more than max_pages * page_size, and a token whose page
+ * lies outside the cache are left out (spec_paged_attention on the same arrays
+ * reports them).  Other entries of the cache keep their values.
+ */
+spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype,
+                             const void* k_new, const void* v_new, int rows, long long k_stride,
+                             long long v_stride, void* stream);
+
+/*
+ * Attention of the new tokens over the cache (their own entries are in it):
+ *   s_j = scale q_t . k_j     out_t = sum_j exp(s_j - lse) v_j     lse = log sum_j exp s_j
+ * over the entries j that token t of request b sees: j < kv_len[b]; with causal,
+ * j <= P = kv_len[b] - n + t (n: its new tokens); with a window W > 0, j > P - W.
+ * Query head h reads key-value head h / (heads / kv_heads).
+ *
+ *   q          [rows, heads, width] dtype, 16-byte aligned, rows q_stride entries
+ *              apart (a multiple of 8), heads `width` apart
+ *   dtype      SPEC_BF16; SPEC_F32 is SPEC_ERR_UNSUPPORTED
+ *   heads      a multiple of kv_heads, at most 1024
+ *   causal     0 or 1: a target's pass over a chain of tokens is causal, the block
+ *              of a diffusion drafter is not
+ *   window     0 (none) or the number of entries a token sees; needs causal
+ *   scale      finite, > 0
+ *   out        [rows, heads, width] dtype out, contiguous, 16-byte aligned
+ *   lse        [rows, heads] float out, or NULL
+ *   workspace  >= spec_paged_attention_workspace_bytes(rows, heads, kv_heads, width)
+ *              bytes (0 for unsupported sizes), 256-byte aligned; not shared by calls
+ *              that may overlap; needs no initialisation
+ *
+ * Scores, softmax and sums are in single precision; the weights exp(s_j - max) are
+ * rounded to bfloat16 for the product with the values.  A token that sees no
+ * entry gets out 0 and lse -inf.  Rows of no request keep their values.  What the
+ * pages hold past kv_len is not used, whatever it is; an entry below kv_len that
+ * is not finite makes the rows NaN whose tiles it lies in, among them rows of its request
+ * that do not see it.  A request whose rows or kv_len are
+ * out of range gets NaN rows as far as they lie in 0 .. rows - 1, and so do rows that
+ * read a page outside the cache; both record SPEC_ERR_BAD_INPUT, readable with
+ * spec_verify_device_status() on `workspace`.  A device-side wait that runs out records
+ * SPEC_ERR_TIMEOUT and leaves NaN.
+ */
+size_t spec_paged_attention_workspace_bytes(int rows, int heads, int kv_heads, int width);
+spec_status_t spec_paged_attention(const spec_paged_cache_t* cache, spec_dtype_t dtype,
+                                   const void* q, int rows, int heads, long long q_stride,
+                                   int causal, int window, float scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* spec_status_string(spec_status_t status);
 
@@ -540,7 +677,8 @@ int spec_abi_version(void);
  *    5 sweep: completion counter   11 OPD: output element
  *    6 sweep: decided position     12 D3D: branch slot
  *   13 OPD gradient: logit row     14 linear cross entropy: label, dZ or gradient element
- *   15 gradient norm: tensor of a unit
+ *   15 gradient norm: tensor of a unit  16 sampling: entry of a row
+ *   17 paged cache: page
  */
 
 /* 1 if the loaded library is the range-checking build, else 0. */

@@ -26,6 +26,12 @@ The functions keep the C names:
 ``spec_grad_norm(...)``              global norm of many gradient tensors
 ``spec_clip_grad_norm(...)``         the same, and the tensors scaled to a largest norm
 ``GradClipper(...)``                 the clip bound to fixed tensors
+``spec_sample(...)``                 tokens drawn under temperature, top-k, top-p and min-p
+``spec_truncate(...)``               the same truncation, written as logits
+``Sampler(...)``                     both bound to fixed buffers
+``spec_kv_append(...)``              new tokens' keys and values into a paged cache
+``spec_paged_attention(...)``        attention of the new tokens over their pages
+``PagedCache(...)``                  both bound to fixed buffers
 ``spec_status_string(code)``
 ``spec_debug_build()``, ``spec_debug_checks()``, ``spec_debug_inject()``
                                      the range-checking build (SPEC_VERIFY_DEBUG=1)
@@ -66,8 +72,9 @@ EXPORTS = ("spec_verify_workspace_bytes", "spec_verify", "spec_verify_ex", "spec
            "spec_verify_opd", "spec_d3d_select", "spec_linear_ce_workspace_bytes",
            "spec_linear_ce", "spec_linear_ce_grad_workspace_bytes", "spec_linear_ce_grad",
            "spec_opd_grad", "spec_grad_norm_workspace_bytes", "spec_grad_norm",
-           "spec_clip_grad_norm", "spec_debug_build", "spec_debug_checks",
-           "spec_debug_inject")
+           "spec_clip_grad_norm", "spec_sample", "spec_truncate", "spec_kv_append",
+           "spec_paged_attention_workspace_bytes", "spec_paged_attention",
+           "spec_debug_build", "spec_debug_checks", "spec_debug_inject")
 SPEC_STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -84,6 +91,16 @@ class _Report(ctypes.Structure):
                 ("chunk_elems", ctypes.c_int32), ("final_rows", ctypes.c_int64),
                 ("residual_zero", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("sweep_bytes", ctypes.c_int64), ("final_bytes", ctypes.c_int64)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_cache", "v_cache")]
+                + [(n, ctypes.c_longlong) for n in ("k_page", "k_slot", "k_head", "v_page",
+                                                    "v_slot", "v_head")]
+                + [(n, ctypes.c_int) for n in ("num_pages", "page_size", "kv_heads", "width")]
+                + [("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int),
+                   ("new_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                   ("B", ctypes.c_int)])
 
 
 @dataclass
@@ -164,6 +181,18 @@ def lib() -> ctypes.CDLL:
     L.spec_grad_norm.restype = ci
     L.spec_clip_grad_norm.argtypes = [vp, vp, vp, vp, ci, ctypes.c_float, f32p, vp, csz, vp]
     L.spec_clip_grad_norm.restype = ci
+    L.spec_sample.argtypes = [vp, ci, ci, ci, ci, f32p, i32p, f32p, f32p, f32p, i32p, vp, vp]
+    L.spec_sample.restype = ci
+    L.spec_truncate.argtypes = [vp, ci, ci, ci, ci, f32p, i32p, f32p, f32p, vp, vp]
+    L.spec_truncate.restype = ci
+    cll = ctypes.c_longlong
+    L.spec_kv_append.argtypes = [vp, ci, vp, vp, ci, cll, cll, vp]
+    L.spec_kv_append.restype = ci
+    L.spec_paged_attention_workspace_bytes.argtypes = [ci, ci, ci, ci]
+    L.spec_paged_attention_workspace_bytes.restype = csz
+    L.spec_paged_attention.argtypes = [vp, ci, vp, ci, ci, cll, ci, ci, ctypes.c_float, vp, f32p, vp,
+                                       csz, vp]
+    L.spec_paged_attention.restype = ci
     L.spec_status_string.argtypes = [ci]
     L.spec_status_string.restype = ctypes.c_char_p
     L.spec_abi_version.argtypes = []
@@ -889,6 +918,238 @@ def spec_clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None,
     """
     return GradClipper(grads, max_norm, out=out, norm=norm, workspace=workspace,
                        stream=stream)()
+
+
+class Sampler:
+    """Truncated sampling bound to fixed buffers.
+
+    ``logits`` [B, n, V] or [B, V] (float32 or bfloat16), one set of settings per request:
+    ``temperature`` float32 [B] (0: greedy), ``top_k`` int32 [B] (0: off), ``top_p`` float32
+    [B] (1: off), ``min_p`` float32 [B] (0: off); None leaves a setting off.  ``uniforms``
+    float32 [B, n] or [B].  Like ``Verifier``, the object checks its buffers once; their
+    contents may change between calls, the tensors must stay alive.
+
+    ``sample()`` fills and returns ``tokens`` (int32, the shape of ``uniforms``); where
+    ``kept`` was given it writes the truncated logits as well.  ``truncate()`` only writes
+    and returns them (``kept``; made on the first call if None, ``logits`` itself truncates
+    in place).
+    """
+
+    def __init__(self, logits, temperature, uniforms=None, *, top_k=None, top_p=None, min_p=None,
+                 tokens=None, kept=None, stream=None):
+        torch = _torch()
+        if logits.dim() not in (2, 3):
+            raise ValueError(f"logits must have shape [B, n, V] or [B, V], got {tuple(logits.shape)}")
+        shape, V = tuple(logits.shape[:-1]), logits.shape[-1]
+        B, n = shape[0], shape[1] if len(shape) == 2 else 1
+        dev = logits.device
+        _need_cuda(logits, "logits")
+        dt = _dtype_code(logits)
+        _need(logits, "logits", logits.dtype, shape + (V,), dev)
+        _need(temperature, "temperature", torch.float32, (B,), dev)
+        for name, t, dtype in (("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
+                               ("min_p", min_p, torch.float32)):
+            if t is not None:
+                _need(t, name, dtype, (B,), dev)
+        if uniforms is not None:
+            _need(uniforms, "uniforms", torch.float32, shape, dev)
+            if tokens is None:
+                with _alloc_on(stream, dev):
+                    tokens = torch.empty(shape, dtype=torch.int32, device=dev)
+            _need(tokens, "tokens", torch.int32, shape, dev)
+        if kept is not None:
+            _need(kept, "kept", logits.dtype, shape + (V,), dev)
+        self._keep = (logits, temperature, uniforms, top_k, top_p, min_p)
+        self._stream = stream
+        self.tokens, self.kept = tokens if uniforms is not None else None, kept
+        self._head = (logits.data_ptr(), dt, B * n, V, n, temperature.data_ptr(),
+                      *(None if t is None else t.data_ptr() for t in (top_k, top_p, min_p)))
+        self._st = _stream_on(stream, dev)
+        self._sample, self._truncate = lib().spec_sample, lib().spec_truncate
+        self._bind()
+
+    def _bind(self):
+        kept = None if self.kept is None else self.kept.data_ptr()
+        uniforms = self._keep[2]
+        self._sample_args = None if uniforms is None else self._head + (
+            uniforms.data_ptr(), self.tokens.data_ptr(), kept, self._st)
+        self._truncate_args = None if kept is None else self._head + (kept, self._st)
+
+    def sample(self):
+        """Enqueue the draw; returns the tokens, or (tokens, kept) where ``kept`` was given."""
+        if self._sample_args is None:
+            raise ValueError("Sampler was made without uniforms")
+        _check(self._sample(*self._sample_args), "spec_sample")
+        return self.tokens if self._sample_args[-2] is None else (self.tokens, self.kept)
+
+    def truncate(self):
+        """Enqueue the truncation; returns the truncated logits."""
+        if self._truncate_args is None:
+            logits = self._keep[0]
+            with _alloc_on(self._stream, logits.device):
+                self.kept = _torch().empty_like(logits)
+            self._truncate_args = self._head + (self.kept.data_ptr(), self._st)
+        _check(self._truncate(*self._truncate_args), "spec_truncate")
+        return self.kept
+
+
+def spec_sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None, tokens=None,
+                kept=None, stream=None):
+    """Tokens drawn by inverse CDF under temperature, top-k, top-p and min-p.
+
+    Arguments as ``Sampler``.  Returns int32 tokens of ``uniforms``' shape (-1 where a
+    request's settings or a row are invalid), with ``kept`` also the truncated logits.
+    """
+    if uniforms is None:
+        raise ValueError("spec_sample needs uniforms (spec_truncate does not)")
+    return Sampler(logits, temperature, uniforms, top_k=top_k, top_p=top_p, min_p=min_p,
+                   tokens=tokens, kept=kept, stream=stream).sample()
+
+
+def spec_truncate(logits, temperature, *, top_k=None, top_p=None, min_p=None, kept=None,
+                  stream=None):
+    """The logits that truncated sampling may draw, -inf elsewhere (NaN rows: invalid).
+
+    Target and draft rows truncated with their requests' settings make ``spec_verify``
+    lossless for truncated sampling.  ``kept`` may be ``logits`` itself (in place).
+    """
+    return Sampler(logits, temperature, top_k=top_k, top_p=top_p, min_p=min_p, kept=kept,
+                   stream=stream).truncate()
+
+
+def _need_rows(t, name, dtype, shape, device):
+    """Rows of heads, contiguous within a row; rows may lie apart (a slice of a fused
+    projection, say)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+        raise ValueError(f"{name} must be contiguous within a row")
+
+
+class PagedCache:
+    """A paged key-value cache, a batch's new tokens, and the calls on them, bound to fixed buffers.
+
+    ``k_cache``, ``v_cache`` [pages, page_size, kv_heads, width] bfloat16, any strides with
+    contiguous heads (a permuted [pages, kv_heads, page_size, width] too); ``page_table``
+    int32 [B, max_pages]; ``new_start`` int32 [B + 1], request b's new tokens being rows
+    new_start[b] .. new_start[b + 1] - 1 of the batch; ``kv_len`` int32 [B], its entries
+    with the new ones, which are the last.
+
+    ``append()`` writes ``k_new``, ``v_new`` [rows, kv_heads, width] into the pages and
+    returns the caches.  ``attend()`` is the attention of ``q`` [rows, heads, width] over
+    them; returns ``out`` (bfloat16, as ``q``), with ``need_lse`` (out, lse float32
+    [rows, heads]).  ``causal`` False lets a request's new tokens see each other;
+    ``window`` > 0 is the number of entries a token sees; ``scale`` None is
+    1 / sqrt(width).  Like ``Verifier``, the object checks its buffers once; their contents
+    may change between calls, the tensors must stay alive.
+    """
+
+    def __init__(self, k_cache, v_cache, page_table, new_start, kv_len, *, k_new=None, v_new=None,
+                 q=None, causal: bool = True, window: int = 0, scale=None, out=None, lse=None,
+                 need_lse: bool = False, workspace=None, stream=None):
+        torch = _torch()
+        if k_cache.dim() != 4:
+            raise ValueError("k_cache must have shape [pages, page_size, kv_heads, width], got "
+                             f"{tuple(k_cache.shape)}")
+        pages, P, Hk, D = k_cache.shape
+        dev = k_cache.device
+        _need_cuda(k_cache, "k_cache")
+        dt = _dtype_code(k_cache)
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t.dtype != k_cache.dtype:
+                raise TypeError(f"{name} must be {k_cache.dtype}, got {t.dtype}")
+            if t.shape != k_cache.shape:
+                raise ValueError(f"{name} must have shape {tuple(k_cache.shape)}, got "
+                                 f"{tuple(t.shape)}")
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, expected {dev}")
+            if t.stride(3) != 1:
+                raise ValueError(f"{name} must be contiguous within a head")
+        B, i32 = kv_len.shape[0], torch.int32
+        _need(kv_len, "kv_len", i32, (B,), dev)
+        _need(new_start, "new_start", i32, (B + 1,), dev)
+        _need(page_table, "page_table", i32, (B, page_table.shape[-1]), dev)
+        self._keep = (k_cache, v_cache, page_table, new_start, kv_len, k_new, v_new, q)
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self._c = _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
+                              *v_cache.stride()[:3], pages, P, Hk, D, page_table.data_ptr(),
+                              page_table.shape[1], new_start.data_ptr(), kv_len.data_ptr(), B)
+        c = ctypes.addressof(self._c)
+        st = _stream_on(stream, dev)
+        self._append_args = self._attend_args = None
+        if (k_new is None) != (v_new is None):
+            raise ValueError("k_new and v_new are given together")
+        if k_new is not None:
+            rows = k_new.shape[0]
+            _need_rows(k_new, "k_new", k_cache.dtype, (rows, Hk, D), dev)
+            _need_rows(v_new, "v_new", k_cache.dtype, (rows, Hk, D), dev)
+            self._append = lib().spec_kv_append
+            self._append_args = (c, dt, k_new.data_ptr(), v_new.data_ptr(), rows, k_new.stride(0),
+                                 v_new.stride(0), st)
+        self.out = self.lse = self.workspace = None
+        if q is not None:
+            rows, H = q.shape[:2]
+            _need_rows(q, "q", k_cache.dtype, (rows, H, D), dev)
+            with _alloc_on(stream, dev):
+                if out is None:
+                    out = torch.empty((rows, H, D), dtype=q.dtype, device=dev)
+                if lse is None and need_lse:
+                    lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
+            _need(out, "out", q.dtype, (rows, H, D), dev)
+            if lse is not None:
+                _need(lse, "lse", torch.float32, (rows, H), dev)
+            n = int(lib().spec_paged_attention_workspace_bytes(rows, H, Hk, D))
+            # Unsupported sizes (n == 0) reach the library, which says so.
+            ws = _need_workspace(workspace, "workspace", max(n, 256), dev, stream)
+            self.out, self.lse, self.workspace = out, lse, ws
+            self._attend = lib().spec_paged_attention
+            self._attend_args = (c, dt, q.data_ptr(), rows, H, q.stride(0), int(causal), int(window),
+                                 D ** -0.5 if scale is None else float(scale), out.data_ptr(),
+                                 None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), st)
+
+    def append(self):
+        """Enqueue the writes of the new keys and values; returns (k_cache, v_cache)."""
+        if self._append_args is None:
+            raise ValueError("PagedCache was made without k_new and v_new")
+        _check(self._append(*self._append_args), "spec_kv_append")
+        return self.k_cache, self.v_cache
+
+    def attend(self):
+        """Enqueue the attention; returns out, or (out, lse) where lse is wanted."""
+        if self._attend_args is None:
+            raise ValueError("PagedCache was made without q")
+        _check(self._attend(*self._attend_args), "spec_paged_attention")
+        return self.out if self.lse is None else (self.out, self.lse)
+
+
+def spec_kv_append(k_new, v_new, k_cache, v_cache, page_table, new_start, kv_len, *, stream=None):
+    """Write new tokens' keys and values into their pages; returns (k_cache, v_cache).
+
+    Arguments as ``PagedCache``.
+    """
+    if k_new is None or v_new is None:
+        raise ValueError("spec_kv_append needs k_new and v_new")
+    return PagedCache(k_cache, v_cache, page_table, new_start, kv_len, k_new=k_new, v_new=v_new,
+                      stream=stream).append()
+
+
+def spec_paged_attention(q, k_cache, v_cache, page_table, new_start, kv_len, *,
+                         causal: bool = True, window: int = 0, scale=None, out=None, lse=None,
+                         need_lse: bool = False, workspace=None, stream=None):
+    """Attention of new tokens over a paged cache that holds their own entries already.
+
+    Arguments as ``PagedCache``.  Returns out, or (out, lse) with ``need_lse`` or ``lse``.
+    """
+    if q is None:
+        raise ValueError("spec_paged_attention needs q")
+    return PagedCache(k_cache, v_cache, page_table, new_start, kv_len, q=q, causal=causal,
+                      window=window, scale=scale, out=out, lse=lse, need_lse=need_lse,
+                      workspace=workspace, stream=stream).attend()
 
 
 def to_device(inputs, device="cuda"):

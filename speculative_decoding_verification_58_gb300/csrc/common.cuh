@@ -772,6 +772,8 @@ enum SpecDebugSite {
   kSiteOpdGradRow = 13,   // OPD gradient: logit row < rows of the draft buffer
   kSiteLinearCe = 14,     // linear cross entropy: logit column, label or gradient element
   kSiteNormUnit = 15,     // gradient norm: tensor of a unit < tensors
+  kSiteSample = 16,       // sampling: entry of a row < V
+  kSitePage = 17,         // paged cache: page < pages of the cache
 };
 
 __device__ int g_debug_failures;  // checks that failed since the last reset

@@ -18,7 +18,9 @@
 #include "linear_ce.cuh"
 #include "opd.cuh"
 #include "opd_grad.cuh"
+#include "paged.cuh"
 #include "plan.cuh"
+#include "sample.cuh"
 #include "sweep.cuh"
 
 namespace specv {
@@ -212,6 +214,7 @@ class DeviceOf {
     err_ = cudaPointerGetAttributes(&a, p);
     if (err_ != cudaSuccess) return;
     if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return;
+    device_ = true;
     if ((err_ = cudaGetDevice(&prev_)) != cudaSuccess) return;
     if (a.device >= 0 && a.device != prev_) {
       err_ = cudaSetDevice(a.device);
@@ -222,9 +225,11 @@ class DeviceOf {
     if (switched_) cudaSetDevice(prev_);
   }
   bool ok() const { return err_ == cudaSuccess; }
+  bool device() const { return device_; }  // device or managed memory
 
  private:
   cudaError_t err_ = cudaSuccess;
+  bool device_ = false;
   int prev_ = -1;
   bool switched_ = false;
 };
@@ -1050,3 +1055,5 @@ extern "C" spec_status_t spec_verify_static(const void* target_logits, const voi
 }
 
 #include "train_api.cuh"
+
+#include "round_api.cuh"

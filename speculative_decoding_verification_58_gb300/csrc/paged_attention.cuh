@@ -1,0 +1,895 @@
+// Attention of a chunk of new tokens over a paged key-value cache.
+//
+//   s_tj = scale q_t . k_j     m_t = max_j s_tj     l_t = sum_j exp(s_tj - m_t)
+//   out_t = sum_j exp(s_tj - m_t) v_j / l_t         lse_t = m_t + log l_t
+//
+// The query heads that share a key-value head are rows of one product: row r of a request
+// and key-value head is token r / group, head r % group, so that a few tokens of many
+// heads fill the 128 rows of a tensor-core tile that one token would leave empty.  A
+// unit of work is up to 256 such rows against the tiles of 128 entries that some of
+// them sees.  All units' tiles form one line, which the CTAs (one per SM) share out evenly:
+// a unit that lies across a border is done in parts, each leaving unnormalised
+// sums with its maximum, and a second kernel joins them (in the CTAs' order: the result's
+// bits do not depend on timing).
+//
+// In a CTA: a warp that loads pages by TMA into a ring of tiles, one that issues the
+// products, one that loads queries, one that works out the units, and two
+// warpgroups of softmax, a row per thread.  Each warpgroup has a stream of its own, with
+// scores and sums in tensor memory: in a unit of more than 128 rows, a half of the
+// rows each, over the same tiles; in a smaller one the same rows, the even tiles
+// and the odd ones, joined at the end.  One stream's softmax so runs under the other's
+// products.  The weights exp(s - m) go back to tensor memory as bfloat16 (relative 2^-8: the
+// products take both operands in one type) over the scores they come from, and are
+// the product's first operand there.  The running maximum is only raised when a score
+// passes it by more than 2^8, which leaves the sums' scaling out of almost every tile.
+#pragma once
+
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace specv {
+
+constexpr int kAtThreads = 384;
+constexpr int kAtProducer = 0, kAtIssuer = 1, kAtQueries = 2, kAtPlanner = 3, kAtSoftmax = 4;
+constexpr int kAtTile = 128;      // entries per tile, rows per stream
+constexpr int kAtUnitRows = 256;  // rows per unit
+constexpr int kAtUnits = 4;       // units planned ahead
+constexpr int kAtMaxCtas = 160;
+constexpr int kAtReaders = 11;    // warps that read a planned unit
+constexpr float kAtRaise = 8.0f;  // log2 of how far a score may pass the maximum in use
+
+template <int D>
+struct AtSizes {
+  static constexpr int kTileBytes = kAtTile * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kRing = 2 * kTileBytes;  // behind two buffers of queries
+};
+
+struct AtUnit {
+  int b, h;        // request (-1: no more), key-value head
+  int first, n;    // its first row in the batch, its new tokens
+  int len;         // its entries
+  int r0, rows;    // rows of the unit
+  int lo, hi;      // entries that some row sees
+  int tile0, nt;   // tiles done here
+  int slot;        // where the part goes, -1: the result itself
+  int bad;         // a page outside the cache
+};
+
+struct AtControl {
+  uint64_t full[10], empty[10];
+  uint64_t s_full[2], p_ready[2], o_full[2], q_full[2], q_empty[2];
+  uint64_t u_full[kAtUnits], u_empty[kAtUnits];
+  uint64_t meet;  // of both warpgroups
+  AtUnit unit[kAtUnits];
+  float2 stats[2][kAtTile];
+  long long scan[kAtThreads / 32];
+  long long start_off, start_left;
+  int start_b;
+  int abort_flag, bad_page;
+  uint32_t tmem;
+};
+
+template <int D>
+constexpr int at_smem() {
+  return (2 + AtSizes<D>::kStages) * AtSizes<D>::kTileBytes + (int)sizeof(AtControl);
+}
+static_assert(at_smem<128>() <= 232448 && at_smem<64>() <= 232448, "shared memory of an SM");
+
+// What a CTA leaves for the join: its two parts of units that lie across borders, the
+// last of one (0) and the first of another (1).
+struct AtPart {
+  int used, ends;  // ends: the unit's last part
+  int b, h, first, r0, rows, pad;
+};
+struct AtCta {
+  AtPart part[2];
+  int timeout, bad_page;
+  int pad[14];
+};
+static_assert(sizeof(AtCta) == 128, "one line per CTA");
+
+struct AtParams {
+  PagedParams p;
+  int group;       // query heads per key-value head
+  int slot_rows;   // rows of a part
+  float scale2;    // scale log2 e
+  AtCta* ctas;     // [kAtMaxCtas]
+  float2* stats;   // [2 kAtMaxCtas, slot_rows]: (m, l)
+  float* parts;    // [2 kAtMaxCtas, slot_rows, D]
+  int main_ctas;
+};
+struct AtMaps {
+  CUtensorMap k, v;
+};
+
+// Entries lo .. hi - 1 are those that tokens t0 .. t1 of a request see between them.
+__device__ __forceinline__ void at_span(const PagedParams& p, int n, int len, int t0, int t1,
+                                        int& lo, int& hi) {
+  hi = p.causal ? min(max(len - n + t1 + 1, 0), len) : len;
+  lo = p.window > 0 ? max(len - n + t0 - p.window + 1, 0) : 0;
+}
+// Tiles of the unit of rows r0 .. and what one costs: two streams' products or one's.
+struct AtSpan {
+  int rows, lo, hi, tile0, tiles, cost;
+};
+__device__ __forceinline__ AtSpan at_unit_span(const AtParams& a, int n, int len, int r0) {
+  AtSpan s;
+  s.rows = (int)min((long long)n * a.group - r0, (long long)kAtUnitRows);
+  at_span(a.p, n, len, r0 / a.group, (r0 + s.rows - 1) / a.group, s.lo, s.hi);
+  s.tile0 = s.lo / kAtTile;
+  s.tiles = s.hi > s.lo ? (s.hi + kAtTile - 1) / kAtTile - s.tile0 : 0;
+  s.cost = s.rows > kAtTile ? 2 : 1;
+  return s;
+}
+// Cost of all units of a request and one key-value head (0: nothing to do, or out of range).
+__device__ __forceinline__ long long at_head_cost(const AtParams& a, int b) {
+  const int first = a.p.c.new_start[b], last = a.p.c.new_start[b + 1], len = a.p.c.kv_len[b];
+  if (!request_ok(a.p, first, last, len)) return 0;
+  const int n = last - first;
+  long long cost = 0;
+  for (int r0 = 0; r0 < n * a.group; r0 += kAtUnitRows) {
+    const AtSpan s = at_unit_span(a, n, len, r0);
+    cost += (long long)s.tiles * s.cost;
+  }
+  return cost;
+}
+
+// The share of the line that this CTA does: from start_off within request start_b on.
+__device__ __forceinline__ void at_share(const AtParams& a, AtControl& ctl) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = a.p.c.B;
+  const int each = (B + kAtThreads - 1) / kAtThreads;
+  const int b0 = min(tid * each, B), b1 = min(b0 + each, B);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += at_head_cost(a, b);
+  mine *= a.p.c.kv_heads;
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) ctl.scan[warp] = upto;
+  if (tid == 0) ctl.start_left = 0;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kAtThreads / 32; ++w) {
+    if (w < warp) before += ctl.scan[w];
+    total += ctl.scan[w];
+  }
+  before += upto - mine;
+  const long long c = blockIdx.x, G = gridDim.x;
+  const long long start = total * c / G, end = total * (c + 1) / G;
+  if (start < end && before <= start && start < before + mine) {
+    for (int b = b0; b < b1; ++b) {
+      const long long x = at_head_cost(a, b) * a.p.c.kv_heads;
+      if (start < before + x) {
+        ctl.start_b = b;
+        ctl.start_off = start - before;
+        ctl.start_left = end - start;
+        break;
+      }
+      before += x;
+    }
+  }
+  __syncthreads();
+}
+
+// One thread hands the units of the CTA's share to the other warps, and notes the parts.
+__device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
+  AtPart parts[2];
+  parts[0].used = parts[1].used = 0;
+  long long left = ctl.start_left, off = ctl.start_off;
+  int slot = 0, round = 0;  // of the ring
+  bool ok = true;
+  auto publish = [&](const AtUnit& u) {
+    if (round > 0 && !mbar_sleep(&ctl.u_empty[slot], (round - 1) & 1, &ctl.abort_flag)) ok = false;
+    if (!ok) return;
+    ctl.unit[slot] = u;
+    mbar_arrive(&ctl.u_full[slot]);
+    if (++slot == kAtUnits) {
+      slot = 0;
+      ++round;
+    }
+  };
+  AtUnit u;
+  u.bad = 0;
+  for (int b = ctl.start_b; ok && left > 0 && b < a.p.c.B; ++b, off = 0) {
+    const long long cost = at_head_cost(a, b);
+    if (cost == 0) continue;
+    u.b = b;
+    u.first = a.p.c.new_start[b];
+    u.n = a.p.c.new_start[b + 1] - u.first;
+    u.len = a.p.c.kv_len[b];
+    u.h = (int)(off / cost);
+    off -= u.h * cost;
+    for (; ok && left > 0 && u.h < a.p.c.kv_heads; ++u.h) {
+      for (u.r0 = 0; ok && left > 0 && u.r0 < u.n * a.group; u.r0 += kAtUnitRows) {
+        const AtSpan s = at_unit_span(a, u.n, u.len, u.r0);
+        const long long c = (long long)s.tiles * s.cost;
+        if (off >= c) {
+          off -= c;
+          continue;
+        }
+        const long long take = min(c - off, left);
+        const int from = (int)((off + s.cost - 1) / s.cost);
+        const int to = (int)((off + take + s.cost - 1) / s.cost);
+        left -= take;
+        off = 0;
+        if (to == from) continue;
+        u.rows = s.rows;
+        u.lo = s.lo;
+        u.hi = s.hi;
+        u.tile0 = s.tile0 + from;
+        u.nt = to - from;
+        u.slot = -1;
+        if (from > 0 || to < s.tiles) {
+          const int k = from > 0 ? 0 : 1;
+          u.slot = 2 * blockIdx.x + k;
+          parts[k] = {1, to == s.tiles, u.b, u.h, u.first, u.r0, u.rows, 0};
+        }
+        publish(u);
+      }
+    }
+  }
+  u.b = -1;
+  if (ok) publish(u);
+  a.ctas[blockIdx.x].part[0] = parts[0];
+  a.ctas[blockIdx.x].part[1] = parts[1];
+  return ok;
+}
+
+// A warp's way through the planned units.
+struct AtWalk {
+  int slot = 0, round = 0;
+  __device__ __forceinline__ bool next(AtControl& ctl, AtUnit& u, bool& ok) {
+    if (!mbar_sleep(&ctl.u_full[slot], round & 1, &ctl.abort_flag)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    u = ctl.unit[slot];
+    return u.b >= 0;
+  }
+  __device__ __forceinline__ void done(AtControl& ctl) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.u_empty[slot]);
+    if (++slot == kAtUnits) {
+      slot = 0;
+      ++round;
+    }
+  }
+};
+
+// Stages of the ring in order.
+template <int kStages>
+struct AtRing {
+  int stage = 0, round = 0;
+  __device__ __forceinline__ void step() {
+    if (++stage == kStages) {
+      stage = 0;
+      ++round;
+    }
+  }
+};
+
+// Keys then values of each tile; where the streams take the tiles in turn, the values two
+// tiles later, as the products want them.
+template <int D>
+__device__ __forceinline__ bool at_produce(const AtParams& a, const AtMaps& maps, AtControl& ctl,
+                                           uint32_t base) {
+  using S = AtSizes<D>;
+  const int lane = threadIdx.x & 31;
+  const int P = a.p.c.page_size, box = min(P, kAtTile), per_tile = kAtTile / box;
+  const int piece = lane % per_tile, half = lane / per_tile;
+  const bool mine = half < D / 64;
+  AtWalk walk;
+  AtRing<S::kStages> ring;
+  int loads = 0;
+  bool ok = true;
+  AtUnit u;
+  while (walk.next(ctl, u, ok)) {
+    const int32_t* table = a.p.c.page_table + (size_t)u.b * a.p.c.max_pages;
+    bool bad = false;
+    // This lane's page of a tile: its number, -1 for one not to be loaded.
+    auto page_of = [&](int j) -> int {
+      const int pos = (u.tile0 + j) * kAtTile + piece * box;
+      if (j >= u.nt || !mine || pos >= u.hi || pos + box <= u.lo) return -1;
+      const int id = table[pos / P];
+      if (id >= 0 && id < a.p.c.num_pages) return id;
+      bad = true;
+      return -1;
+    };
+    auto load = [&](const CUtensorMap* map, int j, int id) {
+      if (ring.round > 0 &&
+          !mbar_sleep(&ctl.empty[ring.stage], (ring.round - 1) & 1, &ctl.abort_flag))
+        ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box * 128;
+      if (__any_sync(0xffffffffu, bad) && lane == 0) {  // known before the tile is
+        *(volatile int*)&ctl.unit[walk.slot].bad = 1;
+        ctl.bad_page = 1;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[ring.stage], bytes);
+      __syncwarp();
+      if (id >= 0)
+        tma_load4(base + S::kRing + ring.stage * S::kTileBytes + half * (kAtTile * 128) +
+                      piece * box * 128,
+                  map, half * 64, ((u.tile0 + j) * kAtTile + piece * box) % P, u.h,
+                  (int)SPEC_CHECKED(id, a.p.c.num_pages, kSitePage), &ctl.full[ring.stage]);
+      ring.step();
+      ++loads;
+    };
+    if (u.rows > kAtTile) {
+      int id = page_of(0);
+      for (int j = 0; ok && j < u.nt; ++j) {
+        const int next = page_of(j + 1);
+        load(&maps.k, j, id);
+        if (ok) load(&maps.v, j, id);
+        id = next;
+      }
+    } else {
+      int id = page_of(0), id1 = -1, id2 = -1;
+      for (int j = 0; ok && j < u.nt + 2; ++j) {
+        const int next = page_of(j + 1);
+        if (j >= 2) load(&maps.v, j - 2, id2);
+        if (ok && j < u.nt) load(&maps.k, j, id);
+        id2 = id1;
+        id1 = id;
+        id = next;
+      }
+    }
+    if (!ok) break;
+    walk.done(ctl);
+  }
+  // The products' last arrivals come before the CTA ends; after a timeout, the loads that
+  // are still on their way.
+  int never = 0;
+  for (int l = max(0, loads - S::kStages); l < loads; ++l) {
+    if (ok) ok = mbar_sleep(&ctl.empty[l % S::kStages], (l / S::kStages) & 1, &ctl.abort_flag);
+    if (!ok) mbar_sleep(&ctl.full[l % S::kStages], (l / S::kStages) & 1, &never);
+  }
+  return ok;
+}
+
+// Queries of a unit into shared memory, 128 rows to a buffer, swizzled as TMA would.
+template <int D>
+__device__ __forceinline__ bool at_load_queries(const AtParams& a, AtControl& ctl, uint32_t base) {
+  using S = AtSizes<D>;
+  const int lane = threadIdx.x & 31;
+  AtWalk walk;
+  int used = 0;
+  bool ok = true;
+  AtUnit u;
+  while (walk.next(ctl, u, ok)) {
+    for (int r = 0; r < u.rows; r += kAtTile, ++used) {
+      const int buf = used & 1;
+      if (used >= 2 && !mbar_sleep(&ctl.q_empty[buf], ((used >> 1) - 1) & 1, &ctl.abort_flag))
+        ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t dst = base + buf * S::kTileBytes;
+      const int chunks = min(u.rows - r, kAtTile) * (D / 8);
+      for (int i = lane; i < chunks; i += 32) {
+        const int row = i / (D / 8), e = i % (D / 8);
+        const int at = u.r0 + r + row;
+        const uint16_t* src = a.p.q + (u.first + at / a.group) * a.p.q_stride +
+                              (u.h * a.group + at % a.group) * D + e * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         dst + (e >> 3) * (kAtTile * 128) + row * 128 + (((e ^ row) & 7) << 4)),
+                     "l"(src)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.q_full[buf]);
+    }
+    if (!ok) break;
+    walk.done(ctl);
+  }
+  for (int l = max(0, used - 2); ok && l < used; ++l)
+    ok = mbar_sleep(&ctl.q_empty[l & 1], (l >> 1) & 1, &ctl.abort_flag);
+  return ok;
+}
+
+// The products: S = Q K^T and O += P V, of the streams in turn.
+template <int D>
+__device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint32_t base,
+                                         uint32_t tmem) {
+  using S = AtSizes<D>;
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kPv = mma_idesc(128, D, false, true);
+  AtWalk walk;
+  AtRing<S::kStages> ring;
+  int q_used = 0, p_count[2] = {0, 0};
+  bool ok = true;
+  AtUnit u = {};
+  auto wait = [&](uint64_t* bar, int parity) {
+    if (ok && !mbar_sleep(bar, parity & 1, &ctl.abort_flag)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    tmem_fence_after();
+  };
+  auto take = [&]() -> int {  // the next stage, filled
+    const int s = ring.stage;
+    wait(&ctl.full[s], ring.round);
+    ring.step();
+    return s;
+  };
+  auto scores = [&](int s, int buf, int stage, int j) {
+    const int cols = min(u.hi - (u.tile0 + j) * kAtTile, kAtTile);
+    const uint32_t idesc = mma_idesc(128, (cols + 15) / 16 * 16, false, false);
+    const uint32_t q = base + buf * S::kTileBytes, k = base + S::kRing + stage * S::kTileBytes;
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t off = (i >> 2) * (kAtTile * 128) + (i & 3) * 32;
+        mma1_f16(tmem + s * kAtTile, mma_desc(q + off, 0, 1024), mma_desc(k + off, 0, 1024), idesc,
+                 i > 0);
+      }
+      mma1_commit(&ctl.s_full[s]);
+    }
+    __syncwarp();
+  };
+  // Values of entries that nobody sees are set to 0 as far as the product reads them: their
+  // weights are 0, but what lies there may not be finite.
+  auto clear = [&](int stage, int j) {
+    const int from = max(u.lo - (u.tile0 + j) * kAtTile, 0);
+    const int to = min(u.hi - (u.tile0 + j) * kAtTile, kAtTile);
+    if ((from | to) % 16 == 0) return;
+    const uint32_t v = base + S::kRing + stage * S::kTileBytes;
+    const int head = from % 16, tail = (16 - to % 16) % 16;
+    for (int i = lane; i < (head + tail) * (D / 8); i += 32) {
+      const int r = i / (D / 8), e = i % (D / 8);
+      const int row = r < head ? from - head + r : to + r - head;
+      st_shared16(v + (e >> 3) * (kAtTile * 128) + row * 128 + ((e & 7) << 4),
+                  make_uint4(0, 0, 0, 0));
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+  };
+  auto values = [&](int s, int stage, int j, bool first) {
+    wait(&ctl.p_ready[s], p_count[s]++);
+    if (!ok) return;
+    const int from = max(u.lo - (u.tile0 + j) * kAtTile, 0) / 16;
+    const int to = (min(u.hi - (u.tile0 + j) * kAtTile, kAtTile) + 15) / 16;
+    const uint32_t v = base + S::kRing + stage * S::kTileBytes;
+    if (lane == 0) {
+      for (int i = from; i < to; ++i)
+        mma1_f16_ta(tmem + 2 * kAtTile + s * D, tmem + s * kAtTile + i * 8,
+                    mma_desc(v + i * 2048, kAtTile * 128, 1024), kPv, !first || i > from);
+    }
+    __syncwarp();
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (lane == 0) mma1_commit(bar);
+  };
+  while (ok && walk.next(ctl, u, ok)) {
+    const int buf = q_used & 1;
+    wait(&ctl.q_full[buf], q_used >> 1);
+    ++q_used;
+    if (u.rows > kAtTile) {
+      wait(&ctl.q_full[buf ^ 1], q_used >> 1);
+      ++q_used;
+      int k = ok ? take() : 0;
+      if (!ok) break;
+      scores(0, buf, k, 0);
+      scores(1, buf ^ 1, k, 0);
+      commit(&ctl.empty[k]);
+      for (int j = 0; ok && j < u.nt; ++j) {
+        const int v = take();
+        if (!ok) break;
+        clear(v, j);
+        values(0, v, j, j == 0);
+        if (!ok) break;
+        if (j + 1 < u.nt) {
+          k = take();
+          if (!ok) break;
+          scores(0, buf, k, j + 1);
+        } else {
+          commit(&ctl.o_full[0]);
+        }
+        values(1, v, j, j == 0);
+        if (!ok) break;
+        commit(&ctl.empty[v]);
+        if (j + 1 < u.nt) {
+          scores(1, buf ^ 1, k, j + 1);
+          commit(&ctl.empty[k]);
+        } else {
+          commit(&ctl.q_empty[buf]);
+          commit(&ctl.q_empty[buf ^ 1]);
+          commit(&ctl.o_full[1]);
+        }
+      }
+    } else {
+      for (int j = 0; ok && j < u.nt + 2; ++j) {
+        if (j >= 2) {
+          const int v = take();
+          if (!ok) break;
+          clear(v, j - 2);
+          values(j & 1, v, j - 2, j < 4);
+          if (!ok) break;
+          commit(&ctl.empty[v]);
+        }
+        if (j < u.nt) {
+          const int k = take();
+          if (!ok) break;
+          scores(j & 1, buf, k, j);
+          commit(&ctl.empty[k]);
+        }
+        if (j + 1 == u.nt) commit(&ctl.q_empty[buf]);
+      }
+      if (!ok) break;
+      commit(&ctl.o_full[0]);
+      commit(&ctl.o_full[1]);
+    }
+    walk.done(ctl);
+  }
+  return ok;
+}
+
+// 32 results of a row, scaled.
+template <int kWords>
+__device__ __forceinline__ void at_store_row(uint16_t* out, const float (&x)[kWords]) {
+#pragma unroll
+  for (int c = 0; c < kWords; c += 8)
+    *reinterpret_cast<uint4*>(out + c) = pack_vec<uint16_t>(x + c);
+}
+
+template <int D>
+__device__ __forceinline__ bool at_softmax(const AtParams& a, AtControl& ctl, uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3;
+  const int s = (warp - kAtSoftmax) >> 2;  // the stream
+  const int row = quarter * 32 + lane;
+  const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+  const uint32_t scores = tmem + s * kAtTile + lanes, sums = tmem + 2 * kAtTile + lanes;
+  const float nan = __int_as_float(0x7fc00000);
+  AtWalk walk;
+  int tiles = 0, units = 0, meets = 0;
+  bool ok = true;
+  AtUnit u = {};
+  auto wait = [&](uint64_t* bar, int parity) {
+    if (!mbar_sleep(bar, parity & 1, &ctl.abort_flag)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    tmem_fence_after();
+  };
+  auto meet = [&]() {  // with the other warpgroup (a barrier whose wait is bounded)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.meet);
+    wait(&ctl.meet, meets++);
+  };
+  while (walk.next(ctl, u, ok)) {
+    const bool two = u.rows > kAtTile;  // a half of the rows each
+    const int r = two ? s * kAtTile + row : row;
+    const bool live = r < u.rows;
+    const bool dead = r - lane >= u.rows;  // the whole warp
+    int lo, hi;
+    {
+      const int t = (u.r0 + r) / a.group;
+      at_span(a.p, u.n, u.len, t, t, lo, hi);
+      if (!live) hi = 0;
+    }
+    float m = -INFINITY, l = 0.0f;
+    for (int j = two ? 0 : s; j < u.nt; j += two ? 1 : 2, ++tiles) {
+      wait(&ctl.s_full[s], tiles);
+      if (!ok) break;
+      if (!dead) {
+        // Twice through the scores, 64 registers of them at a time: for the maximum, and for
+        // the weights.
+        const int at = (u.tile0 + j) * kAtTile;
+        const bool edge = !__all_sync(0xffffffffu, lo <= at && at + kAtTile <= hi);
+        const int from = lo - at, to = hi - at;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < kAtTile; h += 64) {
+          uint32_t x[64];
+          tmem_issue32(scores + h, x);
+          tmem_issue32(scores + h + 32, x + 32);
+          tmem_wait_load(x);
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (h + c < from || h + c >= to) x[c] = 0xff800000u;  // -inf
+          }
+#pragma unroll
+          for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+        }
+        const float top =
+            __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale2);
+        float fix = 1.0f;
+        if (m == -INFINITY) {
+          m = top;  // no sums yet
+        } else if (top > m + kAtRaise) {
+          fix = ex2(__fsub_rn(m, top));
+          m = top;
+        }
+        if (__any_sync(0xffffffffu, fix != 1.0f)) {
+          // (All earlier products are done: this tile's scores came behind them.)
+          l = __fmul_rn(l, fix);
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_issue32(sums + s * D + c, o);
+            tmem_wait_load(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), fix));
+            tmem_store32(sums + s * D + c, o);
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const float2 sc = make_float2(a.scale2, a.scale2), mm = make_float2(-ref, -ref);
+        float2 add[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) add[c] = make_float2(0.0f, 0.0f);
+        // (The weights take the first half of the columns, those of scores read already.)
+#pragma unroll
+        for (int h = 0; h < kAtTile; h += 64) {
+          uint32_t x[64];
+          tmem_issue32(scores + h, x);
+          tmem_issue32(scores + h + 32, x + 32);
+          tmem_wait_load(x);
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (h + c < from || h + c >= to) x[c] = 0xff800000u;
+          }
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float2 e = ex2x2(
+                f32x2_fma(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc, mm));
+            add[(c >> 1) & 3] = f32x2_add(add[(c >> 1) & 3], e);
+            x[c >> 1] = pack_bf16(e.x, e.y);
+          }
+          tmem_store32(scores + h / 2, x);
+        }
+        const float2 t = f32x2_add(f32x2_add(add[0], add[1]), f32x2_add(add[2], add[3]));
+        l = __fadd_rn(l, __fadd_rn(t.x, t.y));
+        tmem_wait_store();
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.p_ready[s]);
+    }
+    if (!ok) break;
+    wait(&ctl.o_full[s], units++);
+    if (!ok) break;
+    const bool bad = *(volatile int*)&ctl.unit[walk.slot].bad;
+    // The two streams of the same rows are joined: each warpgroup takes half of the width.
+    float w0 = 1.0f, w1 = 0.0f, top = m;
+    if (!two) {
+      ctl.stats[s][row] = make_float2(m, l);
+      meet();
+      if (!ok) break;
+      const float2 other = ctl.stats[s ^ 1][row];
+      top = fmaxf(m, other.x);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      w0 = ex2(__fsub_rn(m, ref));
+      w1 = ex2(__fsub_rn(other.x, ref));
+      l = __fadd_rn(__fmul_rn(l, w0), __fmul_rn(other.y, w1));
+    }
+    if (bad) l = nan;
+    if (!dead) {
+      const bool whole = u.slot < 0;
+      const float inv = whole ? (l == 0.0f ? 0.0f : __fdividef(1.0f, l)) : 1.0f;
+      w0 = __fmul_rn(w0, inv);
+      w1 = __fmul_rn(w1, inv);
+      const int from = two ? 0 : s * (D / 2), to = two ? D : from + D / 2;
+      const int at = u.r0 + r;
+      const long long head =
+          ((long long)u.first + at / a.group) * a.p.heads + u.h * a.group + at % a.group;
+      const int slot_row = u.slot * a.slot_rows + r;
+#pragma unroll 1
+      for (int c = from; c < to; c += 32) {
+        uint32_t o[32], o2[32];
+        tmem_issue32(sums + s * D + c, o);
+        if (!two) tmem_issue32(sums + (s ^ 1) * D + c, o2);
+        tmem_wait_load(o);
+        tmem_wait_load(o2);
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          // (A stream without tiles left nothing in tensor memory.)
+          const float p0 = w0 == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o[e]), w0);
+          const float p1 = w1 == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o2[e]), w1);
+          y[e] = __fadd_rn(p0, p1);
+          if (bad) y[e] = nan;
+        }
+        if (live) {
+          if (whole) {
+            at_store_row<32>(a.p.out + head * D + c, y);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.parts + (size_t)slot_row * D + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          }
+        }
+      }
+      if (live && (two || s == 0)) {
+        if (!whole) a.stats[slot_row] = make_float2(top, l);
+        else if (a.p.lse != nullptr)
+          a.p.lse[head] = __fmul_rn(__fadd_rn(top, log2f(l)), kLn2f);
+      }
+    }
+    tmem_fence_before();
+    // Neither warpgroup's next products may write sums that the other still reads.
+    if (!two) meet();
+    if (!ok) break;
+    walk.done(ctl);
+  }
+  return ok;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    paged_attention_kernel(const __grid_constant__ AtMaps maps, const __grid_constant__ AtParams a) {
+  using S = AtSizes<D>;
+  extern __shared__ __align__(1024) unsigned char at_smem_raw[];
+  const uint32_t base = smem_addr(at_smem_raw);
+  AtControl& ctl =
+      *reinterpret_cast<AtControl*>(at_smem_raw + (2 + S::kStages) * S::kTileBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_ready[i], 4);
+      mbar_init(&ctl.o_full[i], 1);
+      mbar_init(&ctl.q_full[i], 1);
+      mbar_init(&ctl.q_empty[i], 1);
+    }
+    for (int i = 0; i < kAtUnits; ++i) {
+      mbar_init(&ctl.u_full[i], 1);
+      mbar_init(&ctl.u_empty[i], kAtReaders);
+    }
+    mbar_init(&ctl.meet, 8);
+    ctl.abort_flag = ctl.bad_page = 0;
+    fence_mbar_init();
+  }
+  if (warp == kAtIssuer) tmem1_alloc(&ctl.tmem, 512);
+  if (warp == kAtProducer && lane < 2) tma_prefetch_map(lane ? &maps.v : &maps.k);
+  pdl_wait();
+  pdl_launch_dependents();
+  tmem_fence_before();
+  at_share(a, ctl);
+  tmem_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  bool ok = (base & 1023) == 0;  // (the tiles' swizzle counts from there)
+  if (ok) {
+    if (warp == kAtProducer) ok = at_produce<D>(a, maps, ctl, base);
+    else if (warp == kAtIssuer) ok = at_issue<D>(a, ctl, base, tmem);
+    else if (warp == kAtQueries) ok = at_load_queries<D>(a, ctl, base);
+    else if (warp >= kAtSoftmax) ok = at_softmax<D>(a, ctl, tmem);
+    else if (lane == 0) ok = at_plan(a, ctl);
+  }
+  if (!ok) *(volatile int*)&ctl.abort_flag = 1;
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (threadIdx.x == 0) {
+    a.ctas[blockIdx.x].timeout = ctl.abort_flag;
+    a.ctas[blockIdx.x].bad_page = ctl.bad_page;
+  }
+  if (warp == kAtIssuer) tmem1_free(tmem, 512);
+}
+
+// Joins the parts of units that lie across CTAs' borders, one warp per row; then the
+// rows that belong to no unit: of requests out of range (NaN), and those that see nothing.
+// The first CTA writes the workspace's header.
+constexpr int kAtJoinThreads = 256, kAtJoinShare = 4;  // CTAs per CTA of the first kernel
+
+template <int D>
+__device__ __forceinline__ void at_fill(const AtParams& a, long long row, float x, float lse,
+                                        int from, int step) {
+  const uint32_t w = pack_bf16(x, x);
+  uint4* out = reinterpret_cast<uint4*>(a.p.out + row * a.p.heads * D);
+  for (int i = from; i < a.p.heads * (D / 8); i += step) out[i] = make_uint4(w, w, w, w);
+  if (a.p.lse != nullptr)
+    for (int i = from; i < a.p.heads; i += step) a.p.lse[row * a.p.heads + i] = lse;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAtJoinThreads)
+    paged_join_kernel(const __grid_constant__ AtParams a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x / kAtJoinShare, share = blockIdx.x % kAtJoinShare;
+  const float nan = __int_as_float(0x7fc00000);
+  pdl_wait();
+  pdl_launch_dependents();
+  const PagedParams& p = a.p;
+  int late = 0, bad_page = 0;
+  for (int i = threadIdx.x; i < a.main_ctas; i += kAtJoinThreads) {
+    late |= a.ctas[i].timeout;
+    bad_page |= a.ctas[i].bad_page;
+  }
+#ifdef SPEC_DEBUG
+  late |= g_debug_inject == SPEC_ERR_TIMEOUT;
+#endif
+  late = __syncthreads_or(late);
+  bad_page = __syncthreads_or(bad_page);
+  if (blockIdx.x == 0) {
+    int bad = 0;
+    for (int b = threadIdx.x; b < p.c.B; b += kAtJoinThreads)
+      bad += !request_ok(p, p.c.new_start[b], p.c.new_start[b + 1], p.c.kv_len[b]);
+    __shared__ int count;
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    if (bad) atomicAdd(&count, bad);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      p.header->status = late               ? SPEC_ERR_TIMEOUT
+                         : count || bad_page ? SPEC_ERR_BAD_INPUT
+                                             : SPEC_OK;
+      p.header->bad_requests = count;
+      p.header->first_bad = INT32_MAX;
+    }
+  }
+  // Rows that nobody computed.
+  for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
+    const int first = p.c.new_start[b], last = p.c.new_start[b + 1], len = p.c.kv_len[b];
+    const bool good = request_ok(p, first, last, len);
+    if (late || !good) {
+      for (int r = max(first, 0); r < min(last, p.rows); ++r)
+        at_fill<D>(a, r, nan, nan, threadIdx.x, kAtJoinThreads);
+      continue;
+    }
+    const int n = last - first;
+    for (int r0 = 0; r0 < n * a.group; r0 += kAtUnitRows) {
+      const AtSpan s = at_unit_span(a, n, len, r0);
+      if (s.tiles > 0) break;  // (and none behind it)
+      for (int i = threadIdx.x; i < s.rows * p.c.kv_heads * (D / 8); i += kAtJoinThreads) {
+        const int e = i % (D / 8), x = i / (D / 8), r = r0 + x % s.rows, h = x / s.rows;
+        const long long head =
+            ((long long)first + r / a.group) * p.heads + h * a.group + r % a.group;
+        reinterpret_cast<uint4*>(p.out + head * D)[e] = make_uint4(0, 0, 0, 0);
+        if (e == 0 && p.lse != nullptr) p.lse[head] = -INFINITY;
+      }
+    }
+  }
+  if (late || c >= a.main_ctas) return;
+  const AtPart u = a.ctas[c].part[1];
+  if (!u.used) return;
+  int end = c + 1;  // CTAs c .. end have parts
+  while (end < a.main_ctas - 1 && !(a.ctas[end].part[0].used && a.ctas[end].part[0].ends)) ++end;
+  auto stat_of = [&](int i, int r) -> float2 {  // part i of the unit
+    if (i > 0 && !a.ctas[c + i].part[0].used) return make_float2(-INFINITY, 0.0f);
+    return a.stats[(size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r];
+  };
+  const int parts = end - c + 1;
+  for (int r = share * (kAtJoinThreads / 32) + warp; r < u.rows;
+       r += kAtJoinShare * (kAtJoinThreads / 32)) {
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, stat_of(i, r).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, x[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+      const float2 st = stat_of(i, r);
+      const float w = ex2(__fsub_rn(st.x, ref));
+      if (w == 0.0f && st.y == st.y) continue;  // (nothing there, or nothing that counts)
+      l = fmaf(st.y, w, l);
+      const float* src =
+          a.parts + ((size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r) * D;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) x[e] = fmaf(src[e * 32 + lane], w, x[e]);
+    }
+    const int at = u.r0 + r;
+    const long long head =
+        ((long long)u.first + at / a.group) * p.heads + u.h * a.group + at % a.group;
+    const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+      p.out[head * D + e * 32 + lane] =
+          (uint16_t)(pack_bf16(l == 0.0f ? 0.0f : __fmul_rn(x[e], inv), 0.0f) & 0xffff);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[head] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2f);
+  }
+}
+
+}  // namespace specv

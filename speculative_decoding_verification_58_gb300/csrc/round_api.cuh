@@ -120,17 +120,81 @@ inline bool row_stride_ok(long long stride, long long row) {
   return stride >= row && stride % 8 == 0 && stride <= (1ll << 38);
 }
 
-inline size_t attn_workspace(int rows, int heads, int kv_heads, int width) {
-  (void)rows;
-  (void)heads;
-  (void)kv_heads;
-  (void)width;
-  return align256(sizeof(WsHeader));
-}
-
 inline bool attn_sizes_ok(int rows, int heads, int kv_heads, int width) {
   return rows >= 1 && heads >= 1 && kv_heads >= 1 && rows <= SPEC_MAX_ROWS && heads <= 1024 &&
-         heads % kv_heads == 0 && (width == 64 || width == 128);
+         heads % kv_heads == 0 && (width == 64 || width == 128) &&
+         (long long)rows * heads <= (1 << 30);
+}
+
+struct AttnLayout {
+  size_t ctas, stats, parts, total;
+  int slot_rows;
+};
+inline AttnLayout attn_layout(int rows, int heads, int kv_heads, int width) {
+  AttnLayout l;
+  l.slot_rows = (int)std::min<long long>(kAtUnitRows, (long long)rows * (heads / kv_heads));
+  l.ctas = align256(sizeof(WsHeader));
+  l.stats = l.ctas + align256(kAtMaxCtas * sizeof(AtCta));
+  l.parts = l.stats + align256((size_t)2 * kAtMaxCtas * l.slot_rows * sizeof(float2));
+  l.total = l.parts + align256((size_t)2 * kAtMaxCtas * l.slot_rows * width * sizeof(float));
+  return l;
+}
+
+// Tensor map of a cache: [pages, heads, slots, width] in boxes of up to 128 slots x 64 entries
+// with the 128-byte swizzle.
+inline bool attn_map(CUtensorMap* m, const spec_paged_cache_t& c, void* base, long long page,
+                     long long slot, long long head) {
+  EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.width, (cuuint64_t)c.page_size,
+                              (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)slot * 2, (cuuint64_t)head * 2, (cuuint64_t)page * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(c.page_size, kAtTile), 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline cudaError_t attn_prepare(DeviceInfo* d) {
+  std::lock_guard<std::mutex> lock(g_dev_mu);
+  if (d->attn_ready) return cudaSuccess;
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(paged_attention_kernel<64>, attr, at_smem<64>())) != cudaSuccess)
+    return e;
+  if ((e = cudaFuncSetAttribute(paged_attention_kernel<128>, attr, at_smem<128>())) != cudaSuccess)
+    return e;
+  d->attn_ready = true;
+  return cudaSuccess;
+}
+
+template <int D>
+spec_status_t attn_run(const PagedParams& p, unsigned char* ws, cudaStream_t s) {
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != cudaSuccess || attn_prepare(d) != cudaSuccess) return SPEC_ERR_CUDA;
+  const AttnLayout lay = attn_layout(p.rows, p.heads, p.c.kv_heads, D);
+  AtParams a = {};
+  a.p = p;
+  a.p.header = reinterpret_cast<WsHeader*>(ws);
+  a.group = p.heads / p.c.kv_heads;
+  a.slot_rows = lay.slot_rows;
+  a.scale2 = p.scale * kLog2e;
+  a.ctas = reinterpret_cast<AtCta*>(ws + lay.ctas);
+  a.stats = reinterpret_cast<float2*>(ws + lay.stats);
+  a.parts = reinterpret_cast<float*>(ws + lay.parts);
+  a.main_ctas = std::min(d->sms, kAtMaxCtas);
+  AtMaps maps;
+  if (!attn_map(&maps.k, p.c, p.c.k_cache, p.c.k_page, p.c.k_slot, p.c.k_head) ||
+      !attn_map(&maps.v, p.c, p.c.v_cache, p.c.v_page, p.c.v_slot, p.c.v_head))
+    return SPEC_ERR_CUDA;
+  if (launch(paged_attention_kernel<D>, dim3((unsigned)a.main_ctas), dim3(kAtThreads), at_smem<D>(),
+             s, true, maps, a) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return launch(paged_join_kernel<D>, dim3((unsigned)(a.main_ctas * kAtJoinShare)),
+                dim3(kAtJoinThreads), 0, s, true, a) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
 }
 
 }  // namespace specv
@@ -188,8 +252,8 @@ spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype
 }
 
 size_t spec_paged_attention_workspace_bytes(int rows, int heads, int kv_heads, int width) {
-  return attn_sizes_ok(rows, heads, kv_heads, width) ? attn_workspace(rows, heads, kv_heads, width)
-                                                     : 0;
+  if (!attn_sizes_ok(rows, heads, kv_heads, width)) return 0;
+  return attn_layout(rows, heads, kv_heads, width).total;
 }
 
 spec_status_t spec_paged_attention(const spec_paged_cache_t* cache, spec_dtype_t dtype,
@@ -212,7 +276,7 @@ spec_status_t spec_paged_attention(const spec_paged_cache_t* cache, spec_dtype_t
   if (!row_stride_ok(q_stride, row)) return SPEC_ERR_INVALID_ARG;
   const size_t nq = ((size_t)(rows - 1) * q_stride + row) * 2, no = (size_t)rows * row * 2;
   const size_t nl = lse ? (size_t)rows * heads * 4 : 0;
-  const size_t nw = attn_workspace(rows, heads, p.c.kv_heads, p.c.width);
+  const size_t nw = attn_layout(rows, heads, p.c.kv_heads, p.c.width).total;
   for (const auto& o : {std::make_pair((const void*)out, no), std::make_pair((const void*)lse, nl)})
     if (overlap(o.first, o.second, q, nq) || overlap(o.first, o.second, p.c.k_cache, nk) ||
         overlap(o.first, o.second, p.c.v_cache, nv) || meets_tables(p.c, o.first, o.second))
@@ -231,15 +295,9 @@ spec_status_t spec_paged_attention(const spec_paged_cache_t* cache, spec_dtype_t
   p.scale = scale;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
-  p.header = static_cast<WsHeader*>(workspace);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch(paged_header_kernel, dim3(1), dim3(1024), 0, s, true, p) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  const long long blocks = blocks_of((long long)rows * heads, kAttnWarps);
-  return launch(paged_attention_kernel, dim3((unsigned)blocks), dim3(kAttnWarps * 32), 0, s, true,
-                p) == cudaSuccess
-             ? SPEC_OK
-             : SPEC_ERR_CUDA;
+  return p.c.width == 64 ? attn_run<64>(p, ws, s) : attn_run<128>(p, ws, s);
 }
 
 }  // extern "C"

@@ -19,6 +19,7 @@
 #include "opd.cuh"
 #include "opd_grad.cuh"
 #include "paged.cuh"
+#include "paged_attention.cuh"
 #include "plan.cuh"
 #include "sample.cuh"
 #include "sweep.cuh"
@@ -122,6 +123,7 @@ struct DeviceInfo {
   bool opd_ready = false;
   bool ce_ready = false;
   bool opd_grad_ready = false;
+  bool attn_ready = false;
   int opd_clusters[2][4] = {};  // [dtype][cluster size - 1]: co-resident OPD clusters
 };
 

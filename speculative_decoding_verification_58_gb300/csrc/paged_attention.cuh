@@ -25,6 +25,7 @@
 #pragma once
 
 #include "paged.cuh"
+#include "sample.cuh"
 #include "tcgen05.cuh"
 
 namespace specv {
@@ -33,16 +34,31 @@ constexpr int kAtThreads = 384;
 constexpr int kAtProducer = 0, kAtIssuer = 1, kAtQueries = 2, kAtPlanner = 3, kAtSoftmax = 4;
 constexpr int kAtTile = 128;      // entries per tile, rows per stream
 constexpr int kAtUnitRows = 256;  // rows per unit
+constexpr int kAtFewRows = 64;    // rows per stream where the tiles are transposed
 constexpr int kAtUnits = 4;       // units planned ahead
 constexpr int kAtMaxCtas = 160;
 constexpr int kAtReaders = 11;    // warps that read a planned unit
 constexpr float kAtRaise = 8.0f;  // log2 of how far a score may pass the maximum in use
 
+// A bounded wait that looks at the clock only when it has to wait long.
+__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try_wait_cluster(bar, parity) || mbar_sleep(bar, parity, abort);
+}
+
+// Shared memory: the ring of tiles, then the queries of a unit's streams (two buffers), and
+// for units of few rows the weights of both streams.
 template <int D>
 struct AtSizes {
   static constexpr int kTileBytes = kAtTile * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr int kRing = 2 * kTileBytes;  // behind two buffers of queries
+  static constexpr int kQ = kStages * kTileBytes;       // queries of up to 128 rows each
+  static constexpr int kFewHalf = kAtFewRows * 128;     // few rows: 64 entries of each
+  static constexpr int kFewQ = kAtFewRows * D * 2;
+  static constexpr int kWeights = kQ + 2 * kFewQ;       // few rows: weights of a stream
+  static constexpr int kFewWeights = kAtTile * 128;     // [entries, 64 rows]
+  static constexpr int kTotal =
+      kQ + (2 * kFewQ + 2 * kFewWeights > 2 * kTileBytes ? 2 * kFewQ + 2 * kFewWeights
+                                                         : 2 * kTileBytes);
 };
 
 struct AtUnit {
@@ -62,24 +78,35 @@ struct AtControl {
   uint64_t u_full[kAtUnits], u_empty[kAtUnits];
   uint64_t meet;  // of both warpgroups
   AtUnit unit[kAtUnits];
-  float2 stats[2][kAtTile];
+  // Few rows, per stream and row: the maximum in use, negated (inf: none yet), and what scores
+  // take for it; what the sums are multiplied by.
+  __align__(16) float above[2][kAtFewRows];  // (read four at a time)
+  __align__(16) float ref[2][kAtFewRows];
+  float fix[2][kAtFewRows];
+  int raise[2][2];
+  uint64_t vote[2];
+  uint64_t few_done;
   long long scan[kAtThreads / 32];
-  long long start_off, start_left;
+  long long start_off, start_left, start_line, total;
   int start_b;
   int abort_flag, bad_page;
   uint32_t tmem;
 };
 
+static_assert(offsetof(AtControl, above) % 16 == 0 && offsetof(AtControl, ref) % 16 == 0 &&
+                  AtSizes<64>::kTotal % 16 == 0 && AtSizes<128>::kTotal % 16 == 0,
+              "16-byte loads");
+
 template <int D>
 constexpr int at_smem() {
-  return (2 + AtSizes<D>::kStages) * AtSizes<D>::kTileBytes + (int)sizeof(AtControl);
+  return AtSizes<D>::kTotal + (int)sizeof(AtControl);
 }
 static_assert(at_smem<128>() <= 232448 && at_smem<64>() <= 232448, "shared memory of an SM");
 
 // What a CTA leaves for the join: its two parts of units that lie across borders, the
 // last of one (0) and the first of another (1).
 struct AtPart {
-  int used, ends;  // ends: the unit's last part
+  int used, end;  // end: the CTA with the unit's last part
   int b, h, first, r0, rows, pad;
 };
 struct AtCta {
@@ -92,6 +119,9 @@ static_assert(sizeof(AtCta) == 128, "one line per CTA");
 struct AtParams {
   PagedParams p;
   int group;       // query heads per key-value head
+  uint32_t magic;  // x / group = x magic >> shift for x < 2^31
+  int shift;
+  int page_bits;   // log2 of the page size
   int slot_rows;   // rows of a part
   float scale2;    // scale log2 e
   AtCta* ctas;     // [kAtMaxCtas]
@@ -109,6 +139,9 @@ __device__ __forceinline__ void at_span(const PagedParams& p, int n, int len, in
   hi = p.causal ? min(max(len - n + t1 + 1, 0), len) : len;
   lo = p.window > 0 ? max(len - n + t0 - p.window + 1, 0) : 0;
 }
+__device__ __forceinline__ int at_token(const AtParams& a, int row) {
+  return (int)(((unsigned long long)(uint32_t)row * a.magic) >> a.shift);
+}
 // Tiles of the unit of rows r0 .. and what one costs: two streams' products or one's.
 struct AtSpan {
   int rows, lo, hi, tile0, tiles, cost;
@@ -116,11 +149,24 @@ struct AtSpan {
 __device__ __forceinline__ AtSpan at_unit_span(const AtParams& a, int n, int len, int r0) {
   AtSpan s;
   s.rows = (int)min((long long)n * a.group - r0, (long long)kAtUnitRows);
-  at_span(a.p, n, len, r0 / a.group, (r0 + s.rows - 1) / a.group, s.lo, s.hi);
+  at_span(a.p, n, len, at_token(a, r0), at_token(a, r0 + s.rows - 1), s.lo, s.hi);
   s.tile0 = s.lo / kAtTile;
   s.tiles = s.hi > s.lo ? (s.hi + kAtTile - 1) / kAtTile - s.tile0 : 0;
-  s.cost = s.rows > kAtTile ? 2 : 1;
+  s.cost = s.rows > 2 * kAtFewRows ? 2 : 1;
   return s;
+}
+// How a unit is done.  Up to kAtFewRows rows: both streams have all rows and take the
+// tiles in turn.  Else each stream has a part of the rows, the first at_first_rows of them.
+__device__ __forceinline__ bool at_in_turn(const AtUnit& u) { return u.rows <= kAtFewRows; }
+__device__ __forceinline__ bool at_few(const AtUnit& u) { return u.rows <= 2 * kAtFewRows; }
+__device__ __forceinline__ int at_first_rows(const AtUnit& u) {
+  return at_in_turn(u) ? u.rows : at_few(u) ? ((u.rows + 1) / 2 + 15) / 16 * 16 : kAtTile;
+}
+
+// The head of a unit's row among all rows' heads.
+__device__ __forceinline__ long long at_head(const AtParams& a, int first, int h, int row) {
+  const int t = at_token(a, row);
+  return ((long long)first + t) * a.p.heads + h * a.group + (row - t * a.group);
 }
 // Cost of all units of a request and one key-value head (0: nothing to do, or out of range).
 __device__ __forceinline__ long long at_head_cost(const AtParams& a, int b) {
@@ -133,6 +179,15 @@ __device__ __forceinline__ long long at_head_cost(const AtParams& a, int b) {
     cost += (long long)s.tiles * s.cost;
   }
   return cost;
+}
+
+// x * c / g, and the CTA whose share entry x of the line is in.
+__device__ __forceinline__ long long at_border(long long x, int c, int g) {
+  return x < (1 << 23) ? (int)x * c / g : x * c / g;
+}
+__device__ __forceinline__ int at_owner(long long x, long long total, int g) {
+  return total < (1 << 23) ? (((int)x + 1) * g - 1) / (int)total
+                           : (int)(((x + 1) * g - 1) / total);
 }
 
 // The share of the line that this CTA does: from start_off within request start_b on.
@@ -158,15 +213,17 @@ __device__ __forceinline__ void at_share(const AtParams& a, AtControl& ctl) {
     total += ctl.scan[w];
   }
   before += upto - mine;
-  const long long c = blockIdx.x, G = gridDim.x;
-  const long long start = total * c / G, end = total * (c + 1) / G;
+  const int c = blockIdx.x, G = gridDim.x;
+  const long long start = at_border(total, c, G), end = at_border(total, c + 1, G);
   if (start < end && before <= start && start < before + mine) {
     for (int b = b0; b < b1; ++b) {
-      const long long x = at_head_cost(a, b) * a.p.c.kv_heads;
+      const long long x = each == 1 ? mine : at_head_cost(a, b) * a.p.c.kv_heads;
       if (start < before + x) {
         ctl.start_b = b;
         ctl.start_off = start - before;
         ctl.start_left = end - start;
+        ctl.start_line = start;
+        ctl.total = total;
         break;
       }
       before += x;
@@ -179,11 +236,11 @@ __device__ __forceinline__ void at_share(const AtParams& a, AtControl& ctl) {
 __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
   AtPart parts[2];
   parts[0].used = parts[1].used = 0;
-  long long left = ctl.start_left, off = ctl.start_off;
+  long long left = ctl.start_left, off = ctl.start_off, line = ctl.start_line;
   int slot = 0, round = 0;  // of the ring
   bool ok = true;
   auto publish = [&](const AtUnit& u) {
-    if (round > 0 && !mbar_sleep(&ctl.u_empty[slot], (round - 1) & 1, &ctl.abort_flag)) ok = false;
+    if (round > 0 && !at_wait(&ctl.u_empty[slot], (round - 1) & 1, &ctl.abort_flag)) ok = false;
     if (!ok) return;
     ctl.unit[slot] = u;
     mbar_arrive(&ctl.u_full[slot]);
@@ -201,7 +258,7 @@ __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
     u.first = a.p.c.new_start[b];
     u.n = a.p.c.new_start[b + 1] - u.first;
     u.len = a.p.c.kv_len[b];
-    u.h = (int)(off / cost);
+    u.h = off == 0 ? 0 : off < INT32_MAX ? (int)off / (int)min(cost, (long long)INT32_MAX) : (int)(off / cost);
     off -= u.h * cost;
     for (; ok && left > 0 && u.h < a.p.c.kv_heads; ++u.h) {
       for (u.r0 = 0; ok && left > 0 && u.r0 < u.n * a.group; u.r0 += kAtUnitRows) {
@@ -214,7 +271,9 @@ __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
         const long long take = min(c - off, left);
         const int from = (int)((off + s.cost - 1) / s.cost);
         const int to = (int)((off + take + s.cost - 1) / s.cost);
+        const long long unit_end = line + c - off;  // on the line
         left -= take;
+        line += take;
         off = 0;
         if (to == from) continue;
         u.rows = s.rows;
@@ -226,7 +285,8 @@ __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
         if (from > 0 || to < s.tiles) {
           const int k = from > 0 ? 0 : 1;
           u.slot = 2 * blockIdx.x + k;
-          parts[k] = {1, to == s.tiles, u.b, u.h, u.first, u.r0, u.rows, 0};
+          parts[k] = {1, at_owner(unit_end - 1, ctl.total, gridDim.x), u.b, u.h, u.first, u.r0,
+                      u.rows, 0};
         }
         publish(u);
       }
@@ -243,7 +303,7 @@ __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
 struct AtWalk {
   int slot = 0, round = 0;
   __device__ __forceinline__ bool next(AtControl& ctl, AtUnit& u, bool& ok) {
-    if (!mbar_sleep(&ctl.u_full[slot], round & 1, &ctl.abort_flag)) ok = false;
+    if (!at_wait(&ctl.u_full[slot], round & 1, &ctl.abort_flag)) ok = false;
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
     u = ctl.unit[slot];
@@ -293,14 +353,14 @@ __device__ __forceinline__ bool at_produce(const AtParams& a, const AtMaps& maps
     auto page_of = [&](int j) -> int {
       const int pos = (u.tile0 + j) * kAtTile + piece * box;
       if (j >= u.nt || !mine || pos >= u.hi || pos + box <= u.lo) return -1;
-      const int id = table[pos / P];
+      const int id = table[pos >> a.page_bits];
       if (id >= 0 && id < a.p.c.num_pages) return id;
       bad = true;
       return -1;
     };
     auto load = [&](const CUtensorMap* map, int j, int id) {
       if (ring.round > 0 &&
-          !mbar_sleep(&ctl.empty[ring.stage], (ring.round - 1) & 1, &ctl.abort_flag))
+          !at_wait(&ctl.empty[ring.stage], (ring.round - 1) & 1, &ctl.abort_flag))
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
@@ -312,14 +372,14 @@ __device__ __forceinline__ bool at_produce(const AtParams& a, const AtMaps& maps
       if (lane == 0) mbar_arrive_expect_tx(&ctl.full[ring.stage], bytes);
       __syncwarp();
       if (id >= 0)
-        tma_load4(base + S::kRing + ring.stage * S::kTileBytes + half * (kAtTile * 128) +
+        tma_load4(base + ring.stage * S::kTileBytes + half * (kAtTile * 128) +
                       piece * box * 128,
-                  map, half * 64, ((u.tile0 + j) * kAtTile + piece * box) % P, u.h,
+                  map, half * 64, ((u.tile0 + j) * kAtTile + piece * box) & (P - 1), u.h,
                   (int)SPEC_CHECKED(id, a.p.c.num_pages, kSitePage), &ctl.full[ring.stage]);
       ring.step();
       ++loads;
     };
-    if (u.rows > kAtTile) {
+    if (!at_in_turn(u)) {
       int id = page_of(0);
       for (int j = 0; ok && j < u.nt; ++j) {
         const int next = page_of(j + 1);
@@ -345,8 +405,8 @@ __device__ __forceinline__ bool at_produce(const AtParams& a, const AtMaps& maps
   // are still on their way.
   int never = 0;
   for (int l = max(0, loads - S::kStages); l < loads; ++l) {
-    if (ok) ok = mbar_sleep(&ctl.empty[l % S::kStages], (l / S::kStages) & 1, &ctl.abort_flag);
-    if (!ok) mbar_sleep(&ctl.full[l % S::kStages], (l / S::kStages) & 1, &never);
+    if (ok) ok = at_wait(&ctl.empty[l % S::kStages], (l / S::kStages) & 1, &ctl.abort_flag);
+    if (!ok) at_wait(&ctl.full[l % S::kStages], (l / S::kStages) & 1, &never);
   }
   return ok;
 }
@@ -357,38 +417,61 @@ __device__ __forceinline__ bool at_load_queries(const AtParams& a, AtControl& ct
   using S = AtSizes<D>;
   const int lane = threadIdx.x & 31;
   AtWalk walk;
-  int used = 0;
-  bool ok = true;
+  int used = 0, few_units = 0;
+  bool ok = true, was_few = false;
   AtUnit u;
-  while (walk.next(ctl, u, ok)) {
-    for (int r = 0; r < u.rows; r += kAtTile, ++used) {
-      const int buf = used & 1;
-      if (used >= 2 && !mbar_sleep(&ctl.q_empty[buf], ((used >> 1) - 1) & 1, &ctl.abort_flag))
-        ok = false;
+  auto empty = [&](int l) {  // the buffer's l-th use is over
+    if (l >= 0 && !at_wait(&ctl.q_empty[l & 1], (l >> 1) & 1, &ctl.abort_flag)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+  };
+  int done = 0;
+  auto few_over = [&](int f) {  // the first f units of few rows are (their phases in order)
+    for (; ok && done < f; ++done) {
+      if (!at_wait(&ctl.few_done, done & 1, &ctl.abort_flag)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
+    }
+  };
+  while (walk.next(ctl, u, ok)) {
+    // Buffers and weights of units of few rows lie over the others' buffers.
+    const bool few = at_few(u);
+    if (few) few_over(few_units++ - 1);
+    if (few != was_few) {
+      if (was_few) few_over(few_units);
+      if (ok) empty(used - 1);
+    }
+    was_few = few;
+    const int half = few ? S::kFewHalf : kAtTile * 128, size = few ? S::kFewQ : S::kTileBytes;
+    const int first = at_first_rows(u);
+    for (int r = 0; ok && r < u.rows; r += first, ++used) {
+      empty(used - 2);
       if (!ok) break;
-      const uint32_t dst = base + buf * S::kTileBytes;
-      const int chunks = min(u.rows - r, kAtTile) * (D / 8);
+      const uint32_t dst = base + S::kQ + (used & 1) * size;
+      const int rows = min(u.rows - r, first), chunks = rows * (D / 8);
+      // (Columns of the product without a row are 0.)
+      const int all = few ? (rows + 15) / 16 * 16 * (D / 8) : chunks;
+      for (int i = chunks + lane; i < all; i += 32)
+        st_shared16(dst + ((i % (D / 8)) >> 3) * half + i / (D / 8) * 128 + ((i & 7) << 4),
+                    make_uint4(0, 0, 0, 0));
       for (int i = lane; i < chunks; i += 32) {
         const int row = i / (D / 8), e = i % (D / 8);
-        const int at = u.r0 + r + row;
-        const uint16_t* src = a.p.q + (u.first + at / a.group) * a.p.q_stride +
-                              (u.h * a.group + at % a.group) * D + e * 8;
+        const int at = u.r0 + r + row, t = at_token(a, at);
+        const uint16_t* src = a.p.q + (u.first + t) * a.p.q_stride +
+                              (u.h * a.group + at - t * a.group) * D + e * 8;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         dst + (e >> 3) * (kAtTile * 128) + row * 128 + (((e ^ row) & 7) << 4)),
+                         dst + (e >> 3) * half + row * 128 + (((e ^ row) & 7) << 4)),
                      "l"(src)
                      : "memory");
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.q_full[buf]);
+      if (lane == 0) mbar_arrive(&ctl.q_full[used & 1]);
     }
     if (!ok) break;
     walk.done(ctl);
   }
-  for (int l = max(0, used - 2); ok && l < used; ++l)
-    ok = mbar_sleep(&ctl.q_empty[l & 1], (l >> 1) & 1, &ctl.abort_flag);
+  if (ok) empty(used - 2);
+  if (ok) empty(used - 1);
   return ok;
 }
 
@@ -405,7 +488,7 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
   bool ok = true;
   AtUnit u = {};
   auto wait = [&](uint64_t* bar, int parity) {
-    if (ok && !mbar_sleep(bar, parity & 1, &ctl.abort_flag)) ok = false;
+    if (ok && !at_wait(bar, parity & 1, &ctl.abort_flag)) ok = false;
     ok = __all_sync(0xffffffffu, ok);
     tmem_fence_after();
   };
@@ -415,10 +498,44 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     ring.step();
     return s;
   };
+  // Few rows: S^T = K Q^T and O^T += V^T P^T, so that the product's 128 rows are entries and
+  // the width, and its columns as many as the stream has rows.
+  auto few_cols = [&](int s) {
+    const int first = at_first_rows(u);
+    return ((s == 0 || at_in_turn(u) ? first : u.rows - first) + 15) / 16 * 16;
+  };
+  auto scores_few = [&](int s, int buf, int stage) {
+    const uint32_t idesc = mma_idesc(128, few_cols(s), false, false);
+    const uint32_t q = base + S::kQ + buf * S::kFewQ, k = base + stage * S::kTileBytes;
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        mma1_f16(tmem + s * kAtTile,
+                 mma_desc(k + (i >> 2) * (kAtTile * 128) + (i & 3) * 32, 0, 1024),
+                 mma_desc(q + (i >> 2) * S::kFewHalf + (i & 3) * 32, 0, 1024), idesc, i > 0);
+      mma1_commit(&ctl.s_full[s]);
+    }
+    __syncwarp();
+  };
+  auto values_few = [&](int s, int stage, int j, bool first) {
+    wait(&ctl.p_ready[s], p_count[s]++);
+    if (!ok) return;
+    const uint32_t idesc = mma_idesc(128, few_cols(s), true, true);
+    const int from = max(u.lo - (u.tile0 + j) * kAtTile, 0) / 16;
+    const int to = (min(u.hi - (u.tile0 + j) * kAtTile, kAtTile) + 15) / 16;
+    const uint32_t v = base + stage * S::kTileBytes, w = base + S::kWeights + s * S::kFewWeights;
+    if (lane == 0) {
+      // (Of a width of 64 the lower half of the product's rows is another tile's, and not used.)
+      for (int i = from; i < to; ++i)
+        mma1_f16(tmem + (2 + s) * kAtTile, mma_desc(v + i * 2048, kAtTile * 128, 1024),
+                 mma_desc(w + i * 2048, 0, 1024), idesc, !first || i > from);
+    }
+    __syncwarp();
+  };
   auto scores = [&](int s, int buf, int stage, int j) {
     const int cols = min(u.hi - (u.tile0 + j) * kAtTile, kAtTile);
     const uint32_t idesc = mma_idesc(128, (cols + 15) / 16 * 16, false, false);
-    const uint32_t q = base + buf * S::kTileBytes, k = base + S::kRing + stage * S::kTileBytes;
+    const uint32_t q = base + S::kQ + buf * S::kTileBytes, k = base + stage * S::kTileBytes;
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -436,7 +553,7 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     const int from = max(u.lo - (u.tile0 + j) * kAtTile, 0);
     const int to = min(u.hi - (u.tile0 + j) * kAtTile, kAtTile);
     if ((from | to) % 16 == 0) return;
-    const uint32_t v = base + S::kRing + stage * S::kTileBytes;
+    const uint32_t v = base + stage * S::kTileBytes;
     const int head = from % 16, tail = (16 - to % 16) % 16;
     for (int i = lane; i < (head + tail) * (D / 8); i += 32) {
       const int r = i / (D / 8), e = i % (D / 8);
@@ -452,10 +569,10 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     if (!ok) return;
     const int from = max(u.lo - (u.tile0 + j) * kAtTile, 0) / 16;
     const int to = (min(u.hi - (u.tile0 + j) * kAtTile, kAtTile) + 15) / 16;
-    const uint32_t v = base + S::kRing + stage * S::kTileBytes;
+    const uint32_t v = base + stage * S::kTileBytes;
     if (lane == 0) {
       for (int i = from; i < to; ++i)
-        mma1_f16_ta(tmem + 2 * kAtTile + s * D, tmem + s * kAtTile + i * 8,
+        mma1_f16_ta(tmem + (2 + s) * kAtTile, tmem + s * kAtTile + i * 8,
                     mma_desc(v + i * 2048, kAtTile * 128, 1024), kPv, !first || i > from);
     }
     __syncwarp();
@@ -467,36 +584,47 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     const int buf = q_used & 1;
     wait(&ctl.q_full[buf], q_used >> 1);
     ++q_used;
-    if (u.rows > kAtTile) {
+    if (!at_in_turn(u)) {
+      const bool few = at_few(u);
       wait(&ctl.q_full[buf ^ 1], q_used >> 1);
       ++q_used;
+      auto score = [&](int s, int stage, int j) {
+        if (few) scores_few(s, buf ^ s, stage);
+        else scores(s, buf ^ s, stage, j);
+      };
+      auto value = [&](int s, int stage, int j) {
+        if (few) values_few(s, stage, j, j == 0);
+        else values(s, stage, j, j == 0);
+      };
       int k = ok ? take() : 0;
       if (!ok) break;
-      scores(0, buf, k, 0);
-      scores(1, buf ^ 1, k, 0);
+      score(0, k, 0);
+      score(1, k, 0);
       commit(&ctl.empty[k]);
       for (int j = 0; ok && j < u.nt; ++j) {
+        if (j + 1 == u.nt) {  // the last scores are under way
+          commit(&ctl.q_empty[buf]);
+          commit(&ctl.q_empty[buf ^ 1]);
+        }
         const int v = take();
         if (!ok) break;
         clear(v, j);
-        values(0, v, j, j == 0);
+        value(0, v, j);
         if (!ok) break;
         if (j + 1 < u.nt) {
           k = take();
           if (!ok) break;
-          scores(0, buf, k, j + 1);
+          score(0, k, j + 1);
         } else {
           commit(&ctl.o_full[0]);
         }
-        values(1, v, j, j == 0);
+        value(1, v, j);
         if (!ok) break;
         commit(&ctl.empty[v]);
         if (j + 1 < u.nt) {
-          scores(1, buf ^ 1, k, j + 1);
+          score(1, k, j + 1);
           commit(&ctl.empty[k]);
         } else {
-          commit(&ctl.q_empty[buf]);
-          commit(&ctl.q_empty[buf ^ 1]);
           commit(&ctl.o_full[1]);
         }
       }
@@ -506,14 +634,14 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
           const int v = take();
           if (!ok) break;
           clear(v, j - 2);
-          values(j & 1, v, j - 2, j < 4);
+          values_few(j & 1, v, j - 2, j < 4);
           if (!ok) break;
           commit(&ctl.empty[v]);
         }
         if (j < u.nt) {
           const int k = take();
           if (!ok) break;
-          scores(j & 1, buf, k, j);
+          scores_few(j & 1, buf, k);
           commit(&ctl.empty[k]);
         }
         if (j + 1 == u.nt) commit(&ctl.q_empty[buf]);
@@ -535,189 +663,462 @@ __device__ __forceinline__ void at_store_row(uint16_t* out, const float (&x)[kWo
     *reinterpret_cast<uint4*>(out + c) = pack_vec<uint16_t>(x + c);
 }
 
-template <int D>
-__device__ __forceinline__ bool at_softmax(const AtParams& a, AtControl& ctl, uint32_t tmem) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3;
-  const int s = (warp - kAtSoftmax) >> 2;  // the stream
-  const int row = quarter * 32 + lane;
-  const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-  const uint32_t scores = tmem + s * kAtTile + lanes, sums = tmem + 2 * kAtTile + lanes;
-  const float nan = __int_as_float(0x7fc00000);
-  AtWalk walk;
-  int tiles = 0, units = 0, meets = 0;
-  bool ok = true;
-  AtUnit u = {};
-  auto wait = [&](uint64_t* bar, int parity) {
-    if (!mbar_sleep(bar, parity & 1, &ctl.abort_flag)) ok = false;
+// A softmax warp: which lanes of tensor memory it has, and how often it has waited for what.
+struct AtSoft {
+  int s, quarter;  // the stream; the warp's 32 lanes
+  int tiles, units, meets, votes;
+  bool ok;
+  __device__ __forceinline__ void wait(AtControl& ctl, uint64_t* bar, int parity) {
+    if (!at_wait(bar, parity & 1, &ctl.abort_flag)) ok = false;
     ok = __all_sync(0xffffffffu, ok);
     tmem_fence_after();
-  };
-  auto meet = [&]() {  // with the other warpgroup (a barrier whose wait is bounded)
+  }
+  // All warps of both streams, or of one: barriers whose waits are bounded.
+  __device__ __forceinline__ void meet(AtControl& ctl) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl.meet);
-    wait(&ctl.meet, meets++);
-  };
-  while (walk.next(ctl, u, ok)) {
-    const bool two = u.rows > kAtTile;  // a half of the rows each
-    const int r = two ? s * kAtTile + row : row;
-    const bool live = r < u.rows;
-    const bool dead = r - lane >= u.rows;  // the whole warp
-    int lo, hi;
-    {
-      const int t = (u.r0 + r) / a.group;
-      at_span(a.p, u.n, u.len, t, t, lo, hi);
-      if (!live) hi = 0;
-    }
-    float m = -INFINITY, l = 0.0f;
-    for (int j = two ? 0 : s; j < u.nt; j += two ? 1 : 2, ++tiles) {
-      wait(&ctl.s_full[s], tiles);
-      if (!ok) break;
-      if (!dead) {
-        // Twice through the scores, 64 registers of them at a time: for the maximum, and for
-        // the weights.
-        const int at = (u.tile0 + j) * kAtTile;
-        const bool edge = !__all_sync(0xffffffffu, lo <= at && at + kAtTile <= hi);
-        const int from = lo - at, to = hi - at;
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int h = 0; h < kAtTile; h += 64) {
-          uint32_t x[64];
-          tmem_issue32(scores + h, x);
-          tmem_issue32(scores + h + 32, x + 32);
-          tmem_wait_load(x);
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (h + c < from || h + c >= to) x[c] = 0xff800000u;  // -inf
-          }
-#pragma unroll
-          for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
-        }
-        const float top =
-            __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale2);
-        float fix = 1.0f;
-        if (m == -INFINITY) {
-          m = top;  // no sums yet
-        } else if (top > m + kAtRaise) {
-          fix = ex2(__fsub_rn(m, top));
-          m = top;
-        }
-        if (__any_sync(0xffffffffu, fix != 1.0f)) {
-          // (All earlier products are done: this tile's scores came behind them.)
-          l = __fmul_rn(l, fix);
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_issue32(sums + s * D + c, o);
-            tmem_wait_load(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), fix));
-            tmem_store32(sums + s * D + c, o);
-          }
-        }
-        const float ref = m == -INFINITY ? 0.0f : m;
-        const float2 sc = make_float2(a.scale2, a.scale2), mm = make_float2(-ref, -ref);
-        float2 add[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) add[c] = make_float2(0.0f, 0.0f);
-        // (The weights take the first half of the columns, those of scores read already.)
-#pragma unroll
-        for (int h = 0; h < kAtTile; h += 64) {
-          uint32_t x[64];
-          tmem_issue32(scores + h, x);
-          tmem_issue32(scores + h + 32, x + 32);
-          tmem_wait_load(x);
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (h + c < from || h + c >= to) x[c] = 0xff800000u;
-          }
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float2 e = ex2x2(
-                f32x2_fma(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc, mm));
-            add[(c >> 1) & 3] = f32x2_add(add[(c >> 1) & 3], e);
-            x[c >> 1] = pack_bf16(e.x, e.y);
-          }
-          tmem_store32(scores + h / 2, x);
-        }
-        const float2 t = f32x2_add(f32x2_add(add[0], add[1]), f32x2_add(add[2], add[3]));
-        l = __fadd_rn(l, __fadd_rn(t.x, t.y));
-        tmem_wait_store();
-      }
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.p_ready[s]);
-    }
-    if (!ok) break;
-    wait(&ctl.o_full[s], units++);
-    if (!ok) break;
-    const bool bad = *(volatile int*)&ctl.unit[walk.slot].bad;
-    // The two streams of the same rows are joined: each warpgroup takes half of the width.
-    float w0 = 1.0f, w1 = 0.0f, top = m;
-    if (!two) {
-      ctl.stats[s][row] = make_float2(m, l);
-      meet();
-      if (!ok) break;
-      const float2 other = ctl.stats[s ^ 1][row];
-      top = fmaxf(m, other.x);
-      const float ref = top == -INFINITY ? 0.0f : top;
-      w0 = ex2(__fsub_rn(m, ref));
-      w1 = ex2(__fsub_rn(other.x, ref));
-      l = __fadd_rn(__fmul_rn(l, w0), __fmul_rn(other.y, w1));
-    }
-    if (bad) l = nan;
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.meet);
+    wait(ctl, &ctl.meet, meets++);
+  }
+  __device__ __forceinline__ void vote(AtControl& ctl) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.vote[s]);
+    wait(ctl, &ctl.vote[s], votes++);
+  }
+};
+
+// Units of many rows: a thread has a row of its stream's half.
+template <int D>
+__device__ __forceinline__ void at_unit_rows(const AtParams& a, AtControl& ctl, uint32_t tmem,
+                                             AtSoft& w, const AtUnit& u, int slot) {
+  const int lane = threadIdx.x & 31, s = w.s, row = w.quarter * 32 + lane;
+  const uint32_t lanes = (uint32_t)(w.quarter * 32) << 16;
+  const uint32_t scores = tmem + s * kAtTile + lanes, sums = tmem + 2 * kAtTile + lanes;
+  const float nan = __int_as_float(0x7fc00000);
+  const int r = s * kAtTile + row;
+  const bool live = r < u.rows;
+  const bool dead = r - lane >= u.rows;  // the whole warp
+  int lo, hi;
+  {
+    const int t = at_token(a, u.r0 + r);
+    at_span(a.p, u.n, u.len, t, t, lo, hi);
+    if (!live) hi = 0;
+  }
+  float m = -INFINITY, l = 0.0f;
+  for (int j = 0; j < u.nt; ++j, ++w.tiles) {
+    w.wait(ctl, &ctl.s_full[s], w.tiles);
+    if (!w.ok) return;
     if (!dead) {
-      const bool whole = u.slot < 0;
-      const float inv = whole ? (l == 0.0f ? 0.0f : __fdividef(1.0f, l)) : 1.0f;
-      w0 = __fmul_rn(w0, inv);
-      w1 = __fmul_rn(w1, inv);
-      const int from = two ? 0 : s * (D / 2), to = two ? D : from + D / 2;
-      const int at = u.r0 + r;
-      const long long head =
-          ((long long)u.first + at / a.group) * a.p.heads + u.h * a.group + at % a.group;
-      const int slot_row = u.slot * a.slot_rows + r;
-#pragma unroll 1
-      for (int c = from; c < to; c += 32) {
-        uint32_t o[32], o2[32];
-        tmem_issue32(sums + s * D + c, o);
-        if (!two) tmem_issue32(sums + (s ^ 1) * D + c, o2);
-        tmem_wait_load(o);
-        tmem_wait_load(o2);
-        float y[32];
+      // Twice through the scores, 64 registers of them at a time: for the maximum, and for
+      // the weights.
+      const int at = (u.tile0 + j) * kAtTile;
+      const bool edge = !__all_sync(0xffffffffu, lo <= at && at + kAtTile <= hi);
+      const int from = lo - at, to = hi - at;
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          // (A stream without tiles left nothing in tensor memory.)
-          const float p0 = w0 == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o[e]), w0);
-          const float p1 = w1 == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o2[e]), w1);
-          y[e] = __fadd_rn(p0, p1);
-          if (bad) y[e] = nan;
+      for (int h = 0; h < kAtTile; h += 64) {
+        uint32_t x[64];
+        tmem_issue32(scores + h, x);
+        tmem_issue32(scores + h + 32, x + 32);
+        tmem_wait_load(x);
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (h + c < from || h + c >= to) x[c] = 0xff800000u;  // -inf
         }
-        if (live) {
-          if (whole) {
-            at_store_row<32>(a.p.out + head * D + c, y);
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.parts + (size_t)slot_row * D + c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-          }
+        for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+      }
+      const float top =
+          __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale2);
+      float fix = 1.0f;
+      if (m == -INFINITY) {
+        m = top;  // no sums yet
+      } else if (top > m + kAtRaise) {
+        fix = ex2(__fsub_rn(m, top));
+        m = top;
+      }
+      if (__any_sync(0xffffffffu, fix != 1.0f)) {
+        // (All earlier products are done: this tile's scores came behind them.)
+        l = __fmul_rn(l, fix);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_issue32(sums + s * kAtTile + c, o);
+          tmem_wait_load(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), fix));
+          tmem_store32(sums + s * kAtTile + c, o);
         }
       }
-      if (live && (two || s == 0)) {
-        if (!whole) a.stats[slot_row] = make_float2(top, l);
-        else if (a.p.lse != nullptr)
-          a.p.lse[head] = __fmul_rn(__fadd_rn(top, log2f(l)), kLn2f);
+      const float ref = m == -INFINITY ? 0.0f : m;
+      const float2 sc = make_float2(a.scale2, a.scale2), mm = make_float2(-ref, -ref);
+      float2 add[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) add[c] = make_float2(0.0f, 0.0f);
+      // (The weights take the first half of the columns, those of scores read already.)
+#pragma unroll
+      for (int h = 0; h < kAtTile; h += 64) {
+        uint32_t x[64];
+        tmem_issue32(scores + h, x);
+        tmem_issue32(scores + h + 32, x + 32);
+        tmem_wait_load(x);
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (h + c < from || h + c >= to) x[c] = 0xff800000u;
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 e = ex2x2(
+              f32x2_fma(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc, mm));
+          add[(c >> 1) & 3] = f32x2_add(add[(c >> 1) & 3], e);
+          x[c >> 1] = pack_bf16(e.x, e.y);
+        }
+        tmem_store32(scores + h / 2, x);
       }
+      const float2 t = f32x2_add(f32x2_add(add[0], add[1]), f32x2_add(add[2], add[3]));
+      l = __fadd_rn(l, __fadd_rn(t.x, t.y));
+      tmem_wait_store();
     }
     tmem_fence_before();
-    // Neither warpgroup's next products may write sums that the other still reads.
-    if (!two) meet();
-    if (!ok) break;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.p_ready[s]);
+  }
+  if (!w.ok) return;
+  w.wait(ctl, &ctl.o_full[s], w.units++);
+  if (!w.ok) return;
+  const bool bad = *(volatile int*)&ctl.unit[slot].bad;
+  if (bad) l = nan;
+  if (!dead) {
+    const bool whole = u.slot < 0;
+    const float inv = whole ? (l == 0.0f ? 0.0f : __fdividef(1.0f, l)) : 1.0f;
+    const long long head = at_head(a, u.first, u.h, u.r0 + r);
+    const int slot_row = u.slot * a.slot_rows + r;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      tmem_issue32(sums + s * kAtTile + c, o);
+      tmem_wait_load(o);
+      float y[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        y[e] = bad ? nan : l == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o[e]), inv);
+      if (live) {
+        if (whole) {
+          at_store_row<32>(a.p.out + head * D + c, y);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.parts + (size_t)slot_row * D + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        }
+      }
+    }
+    if (live) {
+      if (!whole) a.stats[slot_row] = make_float2(m, l);
+      else if (a.p.lse != nullptr)
+        a.p.lse[head] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2f);
+    }
+  }
+  tmem_fence_before();
+}
+
+// 16 columns of the warp's 32 lanes without the wait, and 16 written.
+__device__ __forceinline__ void at_issue16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void at_store16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
+// Units of few rows: a thread has an entry of the tile in the scores, an element of the
+// width in the sums, and all rows of either; so a few rows keep all threads busy, where a
+// row per thread leaves most of them idle and the others with 128 scores each.
+// The maximum in use is the stream's, in shared memory: the warps vote on whether a score
+// passes one by more than 2^8, and only then look for the new ones.
+template <int D>
+__device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
+                                            unsigned char* smem, uint32_t tmem, AtSoft& w,
+                                            const AtUnit& u, int slot) {
+  using S = AtSizes<D>;
+  constexpr int kChunks = kAtFewRows / 16;
+  const int lane = threadIdx.x & 31, s = w.s, row = w.quarter * 32 + lane;
+  const bool turn = at_in_turn(u);
+  // The stream's rows.
+  const int r0 = u.r0 + (turn || s == 0 ? 0 : at_first_rows(u));
+  const int rows = turn || s == 0 ? at_first_rows(u) : u.rows - at_first_rows(u);
+  const int chunks = (rows + 15) / 16;
+  const uint32_t lanes = (uint32_t)(w.quarter * 32) << 16;
+  const uint32_t scores = tmem + s * kAtTile + lanes, sums = tmem + 2 * kAtTile + lanes;
+  const float nan = __int_as_float(0x7fc00000);
+  // This entry's line of weights: 8 rows to 16 bytes, swizzled by the entry.
+  unsigned char* store = smem + S::kWeights + s * S::kFewWeights;
+  const uint32_t line = smem_addr(store) + row * 128, turnover = (uint32_t)(row & 7) << 4;
+  // While no weights are there, what the stream's four warps have found for each row.
+  float* found[2] = {reinterpret_cast<float*>(smem + S::kWeights),
+                     reinterpret_cast<float*>(smem + S::kWeights + S::kFewWeights)};
+  // Entries that every row sees.
+  int lo_all, hi_all, unused;
+  at_span(a.p, u.n, u.len, 0, at_token(a, r0), unused, hi_all);
+  at_span(a.p, u.n, u.len, at_token(a, r0 + rows - 1), 0, lo_all, unused);
+  float2 l[kAtFewRows / 2];
+#pragma unroll
+  for (int c = 0; c < kAtFewRows / 2; ++c) l[c] = make_float2(0.0f, 0.0f);
+  if (row < kAtFewRows) {
+    ctl.above[s][row] = row < rows ? INFINITY : -FLT_MAX;  // (no row: no weight, no vote)
+    ctl.ref[s][row] = row < rows ? 0.0f : -FLT_MAX;
+  }
+  const float2 sc = make_float2(a.scale2, a.scale2);
+  bool first = true;
+  for (int j = turn ? s : 0; j < u.nt; j += turn ? 2 : 1, ++w.tiles, first = false) {
+    w.wait(ctl, &ctl.s_full[s], w.tiles);
+    if (!w.ok) return;
+    const int at = (u.tile0 + j) * kAtTile;
+    if (at < lo_all || at + kAtTile > hi_all) {
+      // Some row does not see all of the tile: what it does not see becomes -inf.
+      const int pos = at + row;
+#pragma unroll 1
+      for (int c = 0; c < chunks * 16; c += 16) {
+        uint32_t x[16];
+        at_issue16(scores + c, x);
+        tmem_wait_load(x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          int lo, hi;
+          const int t = at_token(a, r0 + c + e);
+          at_span(a.p, u.n, u.len, t, t, lo, hi);
+          if (pos < lo || pos >= hi) x[e] = 0xff800000u;
+        }
+        at_store16(scores + c, x);
+      }
+      tmem_wait_store();
+    }
+    bool raise = first;
+    if (!first) {
+      float most = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q) {
+        if (q >= chunks) break;
+        uint32_t x[16];
+        at_issue16(scores + q * 16, x);
+        tmem_wait_load(x);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&ctl.above[s][q * 16 + e]);
+          const float2 y0 = f32x2_fma(
+              make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc, make_float2(m.x, m.y));
+          const float2 y1 =
+              f32x2_fma(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sc,
+                        make_float2(m.z, m.w));
+          most = fmaxf(fmaxf(fmaxf(most, y0.x), fmaxf(y0.y, y1.x)), y1.y);
+        }
+      }
+      raise = __any_sync(0xffffffffu, most > kAtRaise);
+      // (The word of two tiles ago is read by all before any comes here again.)
+      if (raise && lane == 0) *(volatile int*)&ctl.raise[s][w.tiles & 1] = w.tiles;
+      w.vote(ctl);
+      if (!w.ok) return;
+      raise = *(volatile int*)&ctl.raise[s][w.tiles & 1] == w.tiles;
+    }
+    if (raise) {
+#pragma unroll 1
+      for (int c = 0; c < chunks * 16; c += 16) {
+        uint32_t x[16];
+        at_issue16(scores + c, x);
+        tmem_wait_load(x);
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float y = __fmul_rn(__uint_as_float(x[e]), a.scale2);
+          const uint32_t most = __reduce_max_sync(0xffffffffu, y != y ? 0u : order_bits(y));
+          if (lane == e) top = from_order_bits(most);
+        }
+        if (lane < 16) found[s][w.quarter * kAtFewRows + c + lane] = top;
+      }
+      w.vote(ctl);
+      if (!w.ok) return;
+      if (row < kAtFewRows) {
+        float fix = 1.0f;
+        if (row < rows) {
+          const float m = -ctl.above[s][row];
+          const float top =
+              fmaxf(fmaxf(found[s][row], found[s][kAtFewRows + row]),
+                    fmaxf(found[s][2 * kAtFewRows + row], found[s][3 * kAtFewRows + row]));
+          if (m == -INFINITY || top > m + kAtRaise) {
+            if (m != -INFINITY) fix = ex2(__fsub_rn(m, top));
+            ctl.above[s][row] = -top;
+            ctl.ref[s][row] = top == -INFINITY ? 0.0f : -top;
+          }
+        }
+        ctl.fix[s][row] = fix;
+      }
+      w.vote(ctl);
+      if (!w.ok) return;
+      if (!first) {
+        // (All earlier products are done: this tile's scores came behind them.)
+#pragma unroll
+        for (int q = 0; q < kChunks; ++q) {
+          if (q >= chunks) break;
+          uint32_t o[16];
+          at_issue16(sums + s * kAtTile + q * 16, o);
+          tmem_wait_load(o);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float f0 = ctl.fix[s][q * 16 + e], f1 = ctl.fix[s][q * 16 + e + 1];
+            l[q * 8 + e / 2] = f32x2_mul(l[q * 8 + e / 2], make_float2(f0, f1));
+            o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), f0));
+            o[e + 1] = __float_as_uint(__fmul_rn(__uint_as_float(o[e + 1]), f1));
+          }
+          at_store16(sums + s * kAtTile + q * 16, o);
+        }
+        tmem_wait_store();
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q) {
+      if (q >= chunks) break;
+      uint32_t x[16];
+      at_issue16(scores + q * 16, x);
+      tmem_wait_load(x);
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(&ctl.ref[s][q * 16 + e]);
+        const float2 p0 = ex2x2(f32x2_fma(
+            make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc, make_float2(m.x, m.y)));
+        const float2 p1 =
+            ex2x2(f32x2_fma(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sc,
+                            make_float2(m.z, m.w)));
+        l[q * 8 + e / 2] = f32x2_add(l[q * 8 + e / 2], p0);
+        l[q * 8 + e / 2 + 1] = f32x2_add(l[q * 8 + e / 2 + 1], p1);
+        x[e / 2] = pack_bf16(p0.x, p0.y);
+        x[e / 2 + 1] = pack_bf16(p1.x, p1.y);
+      }
+      st_shared16(line + ((uint32_t)(q * 32) ^ turnover), make_uint4(x[0], x[1], x[2], x[3]));
+      st_shared16(line + ((uint32_t)(q * 32 + 16) ^ turnover), make_uint4(x[4], x[5], x[6], x[7]));
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tmem_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.p_ready[s]);
+  }
+  w.wait(ctl, &ctl.o_full[s], w.units++);
+  if (!w.ok) return;
+  // (No product reads weights any more.)  The sums of the weights, over the 32 lanes: each
+  // exchange leaves a lane half of the columns, in the end the one of its number.
+#pragma unroll
+  for (int g = 0; g < kAtFewRows; g += 32) {
+    if (g >= rows) break;
+    float y[32];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      y[c] = l[(g + c) / 2].x;
+      y[c + 1] = l[(g + c) / 2].y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int c = 0; c < o; ++c) {
+        const float mine = up ? y[c + o] : y[c], theirs = up ? y[c] : y[c + o];
+        y[c] = __fadd_rn(mine, __shfl_xor_sync(0xffffffffu, theirs, o));
+      }
+    }
+    found[s][w.quarter * kAtFewRows + g + lane] = y[0];
+  }
+  const bool bad = *(volatile int*)&ctl.unit[slot].bad, whole = u.slot < 0;
+  if (turn) w.meet(ctl);
+  else w.vote(ctl);
+  if (!w.ok) return;
+  // What either stream's sums are multiplied by, a thread per row; where both have the same
+  // rows, they are joined.
+  if (row < rows) {
+    const float m0 = -ctl.above[turn ? 0 : s][row], m1 = turn ? -ctl.above[1][row] : -INFINITY;
+    const float top = fmaxf(m0, m1), ref = top == -INFINITY ? 0.0f : top;
+    const float w0 = ex2(__fsub_rn(m0, ref)), w1 = ex2(__fsub_rn(m1, ref));
+    float all = 0.0f;
+    if (w0 != 0.0f) {
+      const float* f = found[turn ? 0 : s] + row;
+      all = __fadd_rn(__fadd_rn(f[0], f[kAtFewRows]), __fadd_rn(f[2 * kAtFewRows], f[3 * kAtFewRows]));
+      all = __fmul_rn(all, w0);
+    }
+    if (w1 != 0.0f) {
+      const float* f = found[1] + row;
+      const float l1 =
+          __fadd_rn(__fadd_rn(f[0], f[kAtFewRows]), __fadd_rn(f[2 * kAtFewRows], f[3 * kAtFewRows]));
+      all = fmaf(l1, w1, all);
+    }
+    if (bad) all = nan;
+    const float inv = whole ? (all == 0.0f ? 0.0f : __fdividef(1.0f, all)) : 1.0f;
+    ctl.fix[s][row] = bad ? nan : __fmul_rn(turn && s == 1 ? w1 : w0, inv);
+    if (!turn || s == 0) {
+      if (!whole)
+        a.stats[(size_t)u.slot * a.slot_rows + r0 - u.r0 + row] = make_float2(top, all);
+      else if (a.p.lse != nullptr)
+        a.p.lse[at_head(a, u.first, u.h, r0 + row)] = __fmul_rn(__fadd_rn(top, log2f(all)), kLn2f);
+    }
+  }
+  if (turn) w.meet(ctl);
+  else w.vote(ctl);
+  if (!w.ok) return;
+  // (In turn: the streams' threads share the chunks of 16 rows.)
+#pragma unroll 1
+  for (int c = turn ? s * 16 : 0; c < rows; c += turn ? 32 : 16) {
+    uint32_t o0[16], o1[16];
+    at_issue16(sums + (turn ? 0 : s * kAtTile) + c, o0);
+    at_issue16(sums + kAtTile + c, o1);
+    tmem_wait_load(o0);
+    tmem_wait_load(o1);
+    if (row >= D) continue;  // (a width of 64: the product's other rows)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int r = c + e;
+      if (r >= rows) break;
+      const float w0 = ctl.fix[turn ? 0 : s][r], w1 = turn ? ctl.fix[1][r] : 0.0f;
+      // (A stream without tiles left nothing in tensor memory.)
+      const float y = __fadd_rn(w0 == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o0[e]), w0),
+                                w1 == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o1[e]), w1));
+      if (whole)
+        a.p.out[at_head(a, u.first, u.h, r0 + r) * D + row] =
+            (uint16_t)(pack_bf16(y, 0.0f) & 0xffff);
+      else
+        a.parts[((size_t)u.slot * a.slot_rows + r0 - u.r0 + r) * D + row] = y;
+    }
+  }
+  tmem_fence_before();
+  // Neither stream's next products may write sums that the other still reads, nor queries
+  // what is in the weights' place.
+  if (turn) w.meet(ctl);
+  else w.vote(ctl);
+  if (w.ok && w.quarter == 0 && lane == 0) mbar_arrive(&ctl.few_done);
+}
+
+template <int D>
+__device__ __forceinline__ bool at_softmax(const AtParams& a, AtControl& ctl, unsigned char* smem,
+                                           uint32_t tmem) {
+  const int warp = threadIdx.x >> 5;
+  AtWalk walk;
+  AtSoft w = {(warp - kAtSoftmax) >> 2, warp & 3, 0, 0, 0, 0, true};
+  AtUnit u;
+  while (walk.next(ctl, u, w.ok)) {
+    if (at_few(u)) at_unit_few<D>(a, ctl, smem, tmem, w, u, walk.slot);
+    else at_unit_rows<D>(a, ctl, tmem, w, u, walk.slot);
+    if (!w.ok) break;
     walk.done(ctl);
   }
-  return ok;
+  return w.ok;
 }
 
 template <int D>
@@ -727,7 +1128,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   extern __shared__ __align__(1024) unsigned char at_smem_raw[];
   const uint32_t base = smem_addr(at_smem_raw);
   AtControl& ctl =
-      *reinterpret_cast<AtControl*>(at_smem_raw + (2 + S::kStages) * S::kTileBytes);
+      *reinterpret_cast<AtControl*>(at_smem_raw + S::kTotal);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -746,6 +1147,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&ctl.u_empty[i], kAtReaders);
     }
     mbar_init(&ctl.meet, 8);
+    mbar_init(&ctl.few_done, 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.vote[i], 4);
+      ctl.raise[i][0] = ctl.raise[i][1] = 0;
+    }
     ctl.abort_flag = ctl.bad_page = 0;
     fence_mbar_init();
   }
@@ -762,7 +1168,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     if (warp == kAtProducer) ok = at_produce<D>(a, maps, ctl, base);
     else if (warp == kAtIssuer) ok = at_issue<D>(a, ctl, base, tmem);
     else if (warp == kAtQueries) ok = at_load_queries<D>(a, ctl, base);
-    else if (warp >= kAtSoftmax) ok = at_softmax<D>(a, ctl, tmem);
+    else if (warp >= kAtSoftmax) ok = at_softmax<D>(a, ctl, at_smem_raw, tmem);
     else if (lane == 0) ok = at_plan(a, ctl);
   }
   if (!ok) *(volatile int*)&ctl.abort_flag = 1;
@@ -842,8 +1248,7 @@ __global__ void __launch_bounds__(kAtJoinThreads)
       if (s.tiles > 0) break;  // (and none behind it)
       for (int i = threadIdx.x; i < s.rows * p.c.kv_heads * (D / 8); i += kAtJoinThreads) {
         const int e = i % (D / 8), x = i / (D / 8), r = r0 + x % s.rows, h = x / s.rows;
-        const long long head =
-            ((long long)first + r / a.group) * p.heads + h * a.group + r % a.group;
+        const long long head = at_head(a, first, h, r);
         reinterpret_cast<uint4*>(p.out + head * D)[e] = make_uint4(0, 0, 0, 0);
         if (e == 0 && p.lse != nullptr) p.lse[head] = -INFINITY;
       }
@@ -852,36 +1257,58 @@ __global__ void __launch_bounds__(kAtJoinThreads)
   if (late || c >= a.main_ctas) return;
   const AtPart u = a.ctas[c].part[1];
   if (!u.used) return;
-  int end = c + 1;  // CTAs c .. end have parts
-  while (end < a.main_ctas - 1 && !(a.ctas[end].part[0].used && a.ctas[end].part[0].ends)) ++end;
-  auto stat_of = [&](int i, int r) -> float2 {  // part i of the unit
-    if (i > 0 && !a.ctas[c + i].part[0].used) return make_float2(-INFINITY, 0.0f);
-    return a.stats[(size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r];
-  };
-  const int parts = end - c + 1;
+  const int parts = u.end - c + 1;  // CTAs c .. end have parts (but for such with none)
   for (int r = share * (kAtJoinThreads / 32) + warp; r < u.rows;
        r += kAtJoinShare * (kAtJoinThreads / 32)) {
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, stat_of(i, r).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, x[D / 32];
+    // 32 parts at a time, a lane the statistics of each; of further ones the sums so far are
+    // rescaled.
+    float m = -INFINITY, l = 0.0f, x[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-      const float2 st = stat_of(i, r);
-      const float w = ex2(__fsub_rn(st.x, ref));
-      if (w == 0.0f && st.y == st.y) continue;  // (nothing there, or nothing that counts)
-      l = fmaf(st.y, w, l);
-      const float* src =
-          a.parts + ((size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r) * D;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const int i = i0 + lane;
+      float2 st = make_float2(-INFINITY, 0.0f);
+      if (i < parts && (i == 0 || a.ctas[c + i].part[0].used))
+        st = a.stats[(size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r];
+      float top = st.x;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) x[e] = fmaf(src[e * 32 + lane], w, x[e]);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmaxf(top, m);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float fix = ex2(__fsub_rn(m, ref));
+      m = top;
+      const float w = ex2(__fsub_rn(st.x, ref));
+      // (A NaN in the statistics marks a part that read a page outside the cache.)
+      const bool counts = w != 0.0f || st.y != st.y;
+      float add = counts ? __fmul_rn(st.y, w) : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) add = __fadd_rn(add, __shfl_xor_sync(0xffffffffu, add, o));
+      l = fmaf(l, fix, add);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) x[e] = __fmul_rn(x[e], fix);
+      uint32_t some = __ballot_sync(0xffffffffu, counts);
+      while (some != 0) {
+        // Four parts' sums at a time: their loads go together.
+        float v[4][D / 32], wk[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = some != 0 ? __ffs(some) - 1 : -1;
+          some &= some - 1;
+          wk[k] = __shfl_sync(0xffffffffu, w, max(j, 0));
+          const float* src =
+              a.parts +
+              ((size_t)(2 * (c + i0 + j) + (i0 + j == 0 ? 1 : 0)) * a.slot_rows + r) * D;
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) v[k][e] = j >= 0 ? src[e * 32 + lane] : 0.0f;
+          if (j < 0) wk[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) x[e] = fmaf(v[k][e], wk[k], x[e]);
+      }
     }
-    const int at = u.r0 + r;
-    const long long head =
-        ((long long)u.first + at / a.group) * p.heads + u.h * a.group + at % a.group;
+    const long long head = at_head(a, u.first, u.h, u.r0 + r);
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e)

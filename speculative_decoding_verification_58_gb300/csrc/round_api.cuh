@@ -178,6 +178,11 @@ spec_status_t attn_run(const PagedParams& p, unsigned char* ws, cudaStream_t s) 
   a.p = p;
   a.p.header = reinterpret_cast<WsHeader*>(ws);
   a.group = p.heads / p.c.kv_heads;
+  int bits = 0;
+  while ((1 << bits) < a.group) ++bits;
+  a.shift = 31 + bits;
+  a.magic = (uint32_t)(((1ull << a.shift) + a.group - 1) / a.group);
+  while ((1 << a.page_bits) < p.c.page_size) ++a.page_bits;
   a.slot_rows = lay.slot_rows;
   a.scale2 = p.scale * kLog2e;
   a.ctas = reinterpret_cast<AtCta*>(ws + lay.ctas);

@@ -41,6 +41,9 @@ __device__ __forceinline__ uint32_t order_bits(float z) {
   const uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float from_order_bits(uint32_t b) {
+  return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
+}
 __device__ __forceinline__ unsigned long long entry_rank(float z, int v) {
   return ((unsigned long long)order_bits(z) << 32) | (uint32_t)~v;
 }

@@ -144,6 +144,10 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+__device__ __forceinline__ void st_shared2(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+
 // The same for a single CTA: an M = 128 product.
 __device__ __forceinline__ void mma1_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          bool accumulate) {

@@ -484,6 +484,7 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
   constexpr uint32_t kPv = mma_idesc(128, D, false, true);
   AtWalk walk;
   AtRing<S::kStages> ring;
+  const uint32_t one = mma1_elect();
   int q_used = 0, p_count[2] = {0, 0};
   bool ok = true;
   AtUnit u = {};
@@ -498,6 +499,15 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     ring.step();
     return s;
   };
+  // Whether every entry of a tile is seen; else the steps of 16 that are, in part.
+  auto whole = [&](int j) {
+    const int at = (u.tile0 + j) * kAtTile;
+    return at >= u.lo && at + kAtTile <= u.hi;
+  };
+  auto first_step = [&](int j) { return max(u.lo - (u.tile0 + j) * kAtTile, 0) / 16; };
+  auto last_step = [&](int j) {
+    return (min(u.hi - (u.tile0 + j) * kAtTile, kAtTile) + 15) / 16;
+  };
   // Few rows: S^T = K Q^T and O^T += V^T P^T, so that the product's 128 rows are entries and
   // the width, and its columns as many as the stream has rows.
   auto few_cols = [&](int s) {
@@ -506,46 +516,43 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
   };
   auto scores_few = [&](int s, int buf, int stage) {
     const uint32_t idesc = mma_idesc(128, few_cols(s), false, false);
-    const uint32_t q = base + S::kQ + buf * S::kFewQ, k = base + stage * S::kTileBytes;
-    if (lane == 0) {
+    const uint32_t q = mma1_desc(base + S::kQ + buf * S::kFewQ, 0);
+    const uint32_t k = mma1_desc(base + stage * S::kTileBytes, 0);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        mma1_f16(tmem + s * kAtTile,
-                 mma_desc(k + (i >> 2) * (kAtTile * 128) + (i & 3) * 32, 0, 1024),
-                 mma_desc(q + (i >> 2) * S::kFewHalf + (i & 3) * 32, 0, 1024), idesc, i > 0);
-      mma1_commit(&ctl.s_full[s]);
-    }
-    __syncwarp();
+    for (int i = 0; i < D / 16; ++i)
+      mma1_f16(tmem + s * kAtTile, k + ((i >> 2) * (kAtTile * 128) + (i & 3) * 32) / 16,
+               q + ((i >> 2) * S::kFewHalf + (i & 3) * 32) / 16, idesc, i > 0, one);
+    mma1_commit(&ctl.s_full[s], one);
   };
   auto values_few = [&](int s, int stage, int j, bool first) {
     wait(&ctl.p_ready[s], p_count[s]++);
     if (!ok) return;
     const uint32_t idesc = mma_idesc(128, few_cols(s), true, true);
-    const int from = max(u.lo - (u.tile0 + j) * kAtTile, 0) / 16;
-    const int to = (min(u.hi - (u.tile0 + j) * kAtTile, kAtTile) + 15) / 16;
-    const uint32_t v = base + stage * S::kTileBytes, w = base + S::kWeights + s * S::kFewWeights;
-    if (lane == 0) {
-      // (Of a width of 64 the lower half of the product's rows is another tile's, and not used.)
+    // (Of a width of 64 the lower half of the product's rows is another tile's, and not used.)
+    const uint32_t v = mma1_desc(base + stage * S::kTileBytes, kAtTile * 128);
+    const uint32_t w = mma1_desc(base + S::kWeights + s * S::kFewWeights, 0);
+    const uint32_t d = tmem + (2 + s) * kAtTile;
+    if (whole(j)) {
+#pragma unroll
+      for (int i = 0; i < kAtTile / 16; ++i)
+        mma1_f16(d, v + i * 128, w + i * 128, idesc, i > 0 || !first, one);
+    } else {
+      const int from = first_step(j), to = last_step(j);
       for (int i = from; i < to; ++i)
-        mma1_f16(tmem + (2 + s) * kAtTile, mma_desc(v + i * 2048, kAtTile * 128, 1024),
-                 mma_desc(w + i * 2048, 0, 1024), idesc, !first || i > from);
+        mma1_f16(d, v + i * 128, w + i * 128, idesc, i > from || !first, one);
     }
-    __syncwarp();
   };
   auto scores = [&](int s, int buf, int stage, int j) {
-    const int cols = min(u.hi - (u.tile0 + j) * kAtTile, kAtTile);
-    const uint32_t idesc = mma_idesc(128, (cols + 15) / 16 * 16, false, false);
-    const uint32_t q = base + S::kQ + buf * S::kTileBytes, k = base + stage * S::kTileBytes;
-    if (lane == 0) {
+    const int cols = whole(j) ? kAtTile : last_step(j) * 16;
+    const uint32_t idesc = mma_idesc(128, cols, false, false);
+    const uint32_t q = mma1_desc(base + S::kQ + buf * S::kTileBytes, 0);
+    const uint32_t k = mma1_desc(base + stage * S::kTileBytes, 0);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t off = (i >> 2) * (kAtTile * 128) + (i & 3) * 32;
-        mma1_f16(tmem + s * kAtTile, mma_desc(q + off, 0, 1024), mma_desc(k + off, 0, 1024), idesc,
-                 i > 0);
-      }
-      mma1_commit(&ctl.s_full[s]);
+    for (int i = 0; i < D / 16; ++i) {
+      const uint32_t off = ((i >> 2) * (kAtTile * 128) + (i & 3) * 32) / 16;
+      mma1_f16(tmem + s * kAtTile, q + off, k + off, idesc, i > 0, one);
     }
-    __syncwarp();
+    mma1_commit(&ctl.s_full[s], one);
   };
   // Values of entries that nobody sees are set to 0 as far as the product reads them: their
   // weights are 0, but what lies there may not be finite.
@@ -567,19 +574,19 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
   auto values = [&](int s, int stage, int j, bool first) {
     wait(&ctl.p_ready[s], p_count[s]++);
     if (!ok) return;
-    const int from = max(u.lo - (u.tile0 + j) * kAtTile, 0) / 16;
-    const int to = (min(u.hi - (u.tile0 + j) * kAtTile, kAtTile) + 15) / 16;
-    const uint32_t v = base + stage * S::kTileBytes;
-    if (lane == 0) {
+    const uint32_t v = mma1_desc(base + stage * S::kTileBytes, kAtTile * 128);
+    const uint32_t p = tmem + s * kAtTile, d = tmem + (2 + s) * kAtTile;
+    if (whole(j)) {
+#pragma unroll
+      for (int i = 0; i < kAtTile / 16; ++i)
+        mma1_f16_ta(d, p + i * 8, v + i * 128, kPv, i > 0 || !first, one);
+    } else {
+      const int from = first_step(j), to = last_step(j);
       for (int i = from; i < to; ++i)
-        mma1_f16_ta(tmem + (2 + s) * kAtTile, tmem + s * kAtTile + i * 8,
-                    mma_desc(v + i * 2048, kAtTile * 128, 1024), kPv, !first || i > from);
+        mma1_f16_ta(d, p + i * 8, v + i * 128, kPv, i > from || !first, one);
     }
-    __syncwarp();
   };
-  auto commit = [&](uint64_t* bar) {
-    if (lane == 0) mma1_commit(bar);
-  };
+  auto commit = [&](uint64_t* bar) { mma1_commit(bar, one); };
   while (ok && walk.next(ctl, u, ok)) {
     const int buf = q_used & 1;
     wait(&ctl.q_full[buf], q_used >> 1);

@@ -148,28 +148,51 @@ __device__ __forceinline__ void st_shared2(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
 
-// The same for a single CTA: an M = 128 product.
-__device__ __forceinline__ void mma1_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         bool accumulate) {
+// The same for a single CTA: an M = 128 product, called by a whole warp, of which `one`
+// lane issues (nonzero in it alone).  A descriptor's upper word is its layout, a constant; the
+// lower one has the address in units of 16 bytes, so that steps along a tile are
+// additions.  Code that all lanes run, on values that are the same in all, keeps both in
+// uniform registers, from which the instruction takes them: issued from a branch of lane
+// 0, with whole descriptors formed for each, a product of 128 x 128 x 16 took 130 cycles.
+__device__ __forceinline__ uint32_t mma1_elect() {
+  uint32_t one;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(one));
+  return one;
+}
+__device__ __forceinline__ uint32_t mma1_desc(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3fff) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t kMma1Layout = (1024u >> 4) | (1u << 14) | (2u << 29);  // see mma_desc
+__device__ __forceinline__ void mma1_f16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(one), "n"(kMma1Layout)
       : "memory");
 }
 // A in tensor memory (two bf16 of a row per column).
-__device__ __forceinline__ void mma1_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            bool accumulate) {
+__device__ __forceinline__ void mma1_f16_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(one), "n"(kMma1Layout)
       : "memory");
 }
-__device__ __forceinline__ void mma1_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
-               : "memory");
+__device__ __forceinline__ void mma1_commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"(one)
+      : "memory");
 }
 __device__ __forceinline__ void tmem1_alloc(uint32_t* out, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(

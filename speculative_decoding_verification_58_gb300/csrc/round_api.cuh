@@ -8,13 +8,36 @@ namespace specv {
 // Sampling and truncation.
 // ---------------------------------------------------------------------------
 
-inline spec_status_t sample_run(const SampleParams& p, bool f32, cudaStream_t s) {
+// CTAs per row: one where the rows cover the SMs, else as many as do, each with some
+// thousand entries.
+constexpr size_t kSampleRunBytes = 16384;
+inline int sample_cluster(const SampleParams& p, size_t es, int sms) {
+  int c = 1;
+  while (c < kSampleMaxCluster && (long long)p.rows * c < sms &&
+         (size_t)p.V * es >= 2 * c * kSampleRunBytes)
+    c *= 2;
+  return c;
+}
+
+template <typename TIn>
+spec_status_t sample_run(const SampleParams& p, cudaStream_t stream) {
   DeviceInfo* d = nullptr;
   if (device_info(&d) != cudaSuccess) return SPEC_ERR_CUDA;
-  const dim3 grid((unsigned)p.rows), block(kSampleThreads);
-  const cudaError_t e = f32 ? launch(sample_kernel<float>, grid, block, 0, s, true, p)
-                            : launch(sample_kernel<uint16_t>, grid, block, 0, s, true, p);
-  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  const int c = sample_cluster(p, sizeof(TIn), d->sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)p.rows * c));
+  cfg.blockDim = dim3(kSampleThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<TIn>, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 inline spec_status_t sample_entry(const char* name, const void* logits, spec_dtype_t dtype,
@@ -62,7 +85,8 @@ inline spec_status_t sample_entry(const char* name, const void* logits, spec_dty
   p.V = V;
   p.group = group;
   p.unit_bits = sample_unit_bits(V);
-  return sample_run(p, dtype == SPEC_F32, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == SPEC_F32 ? sample_run<float>(p, s) : sample_run<uint16_t>(p, s);
 }
 
 // ---------------------------------------------------------------------------

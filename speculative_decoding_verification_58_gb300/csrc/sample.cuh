@@ -48,14 +48,24 @@ __device__ __forceinline__ unsigned long long entry_rank(float z, int v) {
   return ((unsigned long long)order_bits(z) << 32) | (uint32_t)~v;
 }
 
-// 2^(j / 256) in units of 2^-39, j = 0 .. 255: formed by each CTA in double precision.
+// 2^(j / 256) in units of 2^-39, j = 0 .. 255, from the exponential's series.
 struct MassTable {
   unsigned long long e[256];
 };
-__device__ __forceinline__ void mass_table_fill(MassTable& t) {
-  for (int j = threadIdx.x; j < 256; j += blockDim.x)
-    t.e[j] = (unsigned long long)__double2ll_rn(exp2((double)j * (1.0 / 256.0)) * 549755813888.0);
+constexpr MassTable mass_table() {
+  MassTable t = {};
+  for (int j = 0; j < 256; ++j) {
+    const double x = j * 0.69314718055994530942 / 256;
+    double sum = 1.0, term = 1.0;
+    for (int n = 1; n < 24; ++n) {
+      term *= x / n;
+      sum += term;
+    }
+    t.e[j] = (unsigned long long)(sum * 549755813888.0 + 0.5);
+  }
+  return t;
 }
+__device__ const MassTable g_mass_table = mass_table();
 
 // exp((z - max) / T) in units of 2^-unit_bits, rounded.  x = (z - max) log2(e) / T is formed
 // in float-float and split as n + j / 256 + g, g < 2^-8 in units of 2^-40;
@@ -93,6 +103,16 @@ __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, con
   if (shift <= 0) return m << -shift;
   if (shift > 41) return 0;
   return (m + (1ull << (shift - 1))) >> shift;
+}
+
+// NaN in either half of the result once an entry of the vectors so far is: maxima that keep it.
+__device__ __forceinline__ uint32_t nan_of(const uint4& v, uint32_t before) {
+  uint32_t d;
+  asm("{\n\t.reg .b32 t, u;\n\tmax.NaN.bf16x2 t, %1, %2;\n\tmax.NaN.bf16x2 u, %3, %4;\n\t"
+      "max.NaN.bf16x2 t, t, u;\n\tmax.NaN.bf16x2 %0, t, %5;\n\t}"
+      : "=r"(d)
+      : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(before));
+  return d;
 }
 
 // ceil(p * m) and floor(p * m) for a float 0 <= p <= 1.
@@ -147,130 +167,1054 @@ __device__ __forceinline__ RowSettings row_settings(const SampleParams& p, int r
   return s;
 }
 
-// One CTA per row; every sum is a pass over the row.
+// ---------------------------------------------------------------------------
+// One CTA per row, or a cluster of them where there are few rows, each with a run of the
+// row's 16-byte vectors (the entries before the first go with the first run, those
+// behind the last with the last).
+//
+//   top_k up to kSampleFew: one pass.  The top_k-th largest of the maxima of half vectors, over
+//     the first vectors of the run, bounds the top_k-th largest entry from below; what
+//     is not below goes to a list in shared memory, which is cut to its own top_k-th
+//     when it fills.  The list, sorted, has all of K: no mass of any other entry is needed.
+//   top_p alone: a pass for the maximum and the mass, roughly; one for the mass and a
+//     histogram of the distances from the maximum, which shows where about the border
+//     is; then the exact mass above that place, and of its entries by their bits, in finer and
+//     finer bins until a bin's entries fit the list.
+//   Larger top_k: the same bins over all entries, counted.
+// Passes after the first find the row in L2.
+// ---------------------------------------------------------------------------
+constexpr int kSampleMaxCluster = 8;
+constexpr int kSampleFew = 512;
+constexpr int kSampleList = 2048;    // entries of the list
+constexpr int kSampleCut = 1024;     // and how many make it be cut
+constexpr int kSampleLong = 96;
+constexpr int kSampleBins = 4096;    // of the first histogram
+constexpr int kSampleFine = 1024;    // of the others
+constexpr int kSampleWarps = kSampleThreads / 32;
+constexpr int kSampleBatch = 4;      // vectors a thread has on their way
+
+struct SamplePeer {  // what a CTA tells the others
+  unsigned long long a, b;
+  float x, y;
+  int i, j;
+};
+struct SampleShared {
+  union {
+    unsigned long long list[kSampleList];
+    uint32_t hist[kSampleBins];
+  };
+  union {
+    unsigned long long mass[kSampleList];  // sums up to and with an entry of the sorted list
+    unsigned long long fine[kSampleFine];
+  };
+  MassTable table;
+  SamplePeer peer[2][kSampleMaxCluster];
+  unsigned long long red[2][kSampleWarps];
+  SamplePeer mine[kSampleWarps];
+  uint32_t digit[256];
+  FF inv;          // log2(e) / T
+  double min_off;  // T log(min_p)
+  int count, kth, rest, border;
+};
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dsmem_st_u64(uint32_t a, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t dsmem_ld_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long dsmem_ld_u64(uint32_t a) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// The first of n ascending sums that is at least `want`, n if none.
+__device__ __forceinline__ int first_reaching(const unsigned long long* sums, int n,
+                                              unsigned long long want) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] >= want) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// What a border is looked for by: the entries' number or their mass.
+struct SampleGoal {
+  bool by_count;
+  unsigned long long want;
+};
+
+// A CTA's part in one row.
 template <typename TIn>
-__global__ void __launch_bounds__(kSampleThreads) sample_kernel(SampleParams p) {
+struct SampleJob {
   using Tr = ElemTraits<TIn>;
-  __shared__ MassTable table;
-  __shared__ unsigned long long red[2][kSampleThreads / 32];
-  __shared__ unsigned long long best;
-  __shared__ float sh_min;
-  __shared__ FF sh_inv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_launch_dependents();
-  mass_table_fill(table);
-  const int V = p.V;
-  const int row = blockIdx.x;
-  const TIn* in = static_cast<const TIn*>(p.logits) + (size_t)row * V;
-  const RowSettings st = row_settings(p, row);
-  const bool greedy = st.T == 0.0f;
-  // The largest entry's rank; whether the row holds what it may not.
-  unsigned long long top = 0;
-  bool bad = !st.ok;
-  for (int v = threadIdx.x; v < V; v += kSampleThreads) {
-    const float z = Tr::to_float(in[SPEC_CHECKED(v, V, kSiteSample)]);
-    if (z != z) {
-      bad |= !greedy;
-      continue;
+  static constexpr int kPer = 16 / (int)sizeof(TIn);
+  SampleShared& sh;
+  const SampleParams& p;
+  const TIn* row;       // the whole row
+  const uint4* run;     // this CTA's vectors
+  int nvec, first;      // how many, index of their first entry
+  int head, tail;       // entries before and behind them that are this CTA's
+  int rank, ctas, round;
+  MassScale s;
+
+  // f(values, index of the first, how many) for all of the run, threads in turn.
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    for (int i0 = threadIdx.x; i0 < nvec; i0 += kSampleBatch * kSampleThreads) {
+      uint4 v[kSampleBatch];
+#pragma unroll
+      for (int j = 0; j < kSampleBatch; ++j) {
+        const int i = i0 + j * kSampleThreads;
+        if (i < nvec) v[j] = run[i];
+      }
+#pragma unroll
+      for (int j = 0; j < kSampleBatch; ++j) {
+        const int i = i0 + j * kSampleThreads;
+        if (i >= nvec) break;
+        float x[kPer];
+        Tr::unpack(v[j], x);
+        f(x, first + i * kPer, kPer);
+      }
     }
-    bad |= !greedy && z > FLT_MAX;
-    const unsigned long long rk = z < -FLT_MAX ? 0 : entry_rank(z, v);
-    top = rk > top ? rk : top;
+    if ((int)threadIdx.x < head + tail) {
+      float x[kPer];
+      const int v = edge(threadIdx.x);
+      x[0] = Tr::to_float(row[SPEC_CHECKED(v, p.V, kSiteSample)]);
+      f(x, v, 1);
+    }
   }
-  if (threadIdx.x == 0) {
-    best = 0;
-    const double inv = greedy ? 0.0 : 1.4426950408889634074 / (double)st.T;
-    sh_inv.hi = (float)inv;
-    sh_inv.lo = (float)(inv - (double)sh_inv.hi);
+  // The t-th entry outside the vectors.
+  __device__ __forceinline__ int edge(int t) const {
+    return t < head ? first - head + t : first + nvec * kPer + t - head;
   }
-  bad = __syncthreads_or(bad);
-  top = warp_max_u64(top);
-  if (lane == 0) atomicMax(&best, top);
-  __syncthreads();
-  top = best;
-  bad = bad || top == 0;
-  int token = bad ? -1 : (int)~(uint32_t)top;
-  unsigned long long limit = top;
-  if (!greedy && !bad) {
-    MassScale s;
-    s.max = Tr::to_float(in[token]);
-    s.inv = sh_inv;
-    s.unit_bits = p.unit_bits;
-    auto sums = [&](unsigned long long from, int last) -> CountMass {  // ranks >= from, indices <= last
-      unsigned long long c = 0, m = 0;
-      for (int v = threadIdx.x; v <= last; v += kSampleThreads) {
-        const float z = Tr::to_float(in[v]);
-        if (entry_rank(z, v) >= from) {
-          ++c;
-          m += entry_mass(s, table, z);
+
+  // Every CTA's word for all of them, in rank order; thread 0's argument counts.
+  __device__ __forceinline__ const SamplePeer* exchange(const SamplePeer& word) {
+    SamplePeer* slot = sh.peer[round++ & 1];
+    __syncthreads();
+    if (ctas == 1) {
+      if (threadIdx.x == 0) slot[0] = word;
+      __syncthreads();
+      return slot;
+    }
+    if (threadIdx.x == 0) sh.mine[0] = word;
+    __syncthreads();
+    if ((int)threadIdx.x < ctas) {
+      const uint32_t to = dsmem_map(&slot[rank], threadIdx.x);
+      const SamplePeer m = sh.mine[0];
+      dsmem_st_u64(to, m.a);
+      dsmem_st_u64(to + 8, m.b);
+      dsmem_st_u64(to + 16, ((unsigned long long)__float_as_uint(m.y) << 32) | __float_as_uint(m.x));
+      dsmem_st_u64(to + 24, ((unsigned long long)(uint32_t)m.j << 32) | (uint32_t)m.i);
+    }
+    cluster_arrive();
+    cluster_wait();
+    return slot;
+  }
+  __device__ __forceinline__ void sync_all() {
+    if (ctas == 1) {
+      __syncthreads();
+    } else {
+      cluster_arrive();
+      cluster_wait();
+    }
+  }
+  // Sums over the CTA's threads, for all of them.
+  __device__ __forceinline__ CountMass block_sums(unsigned long long c, unsigned long long m) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    c = warp_sum_u64(c);
+    m = warp_sum_u64(m);
+    __syncthreads();
+    if (lane == 0) {
+      sh.red[0][warp] = c;
+      sh.red[1][warp] = m;
+    }
+    __syncthreads();
+    CountMass r = {0, 0};
+#pragma unroll
+    for (int w = 0; w < kSampleWarps; ++w) {
+      r.count += sh.red[0][w];
+      r.mass += sh.red[1][w];
+    }
+    return r;
+  }
+  __device__ __forceinline__ CountMass cluster_sums(unsigned long long c, unsigned long long m) {
+    const CountMass r = block_sums(c, m);
+    SamplePeer w = {};
+    w.a = r.count;
+    w.b = r.mass;
+    const SamplePeer* all = exchange(w);
+    CountMass t = {0, 0};
+    for (int i = 0; i < ctas; ++i) {
+      t.count += all[i].a;
+      t.mass += all[i].b;
+    }
+    return t;
+  }
+
+  // The largest 16-bit number that at least k of the threads' kN numbers reach, 0 if there are
+  // fewer (but for zeros): by their upper 8 bits, then the lower ones.
+  template <int kN>
+  __device__ __forceinline__ uint32_t kth(const uint32_t (&g)[kN], int k) {
+    const int tid = threadIdx.x;
+    uint32_t upper = 0;
+    int rest = k;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+      __syncthreads();
+      if (tid < 256) sh.digit[tid] = 0;
+      if (tid == 0) sh.kth = -1;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (level == 0 ? g[i] != 0 : g[i] >> 8 == upper)
+          atomicAdd(&sh.digit[level == 0 ? g[i] >> 8 : g[i] & 255], 1u);
+      __syncthreads();
+      if (tid < 32) {
+        // From the top: lane l has the bins 255 - 8 l down.
+        int n[8], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine += n[i] = (int)sh.digit[255 - 8 * tid - i];
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (tid >= o) upto += x;
+        }
+        int before = upto - mine;
+        if (before < rest && upto >= rest) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (before < rest && before + n[i] >= rest) {
+              sh.kth = 255 - 8 * tid - i;
+              sh.rest = rest - before;
+            }
+            before += n[i];
+          }
         }
       }
-      c = warp_sum_u64(c);
-      m = warp_sum_u64(m);
       __syncthreads();
-      if (lane == 0) {
-        red[0][warp] = c;
-        red[1][warp] = m;
+      if (sh.kth < 0) return 0;
+      if (level == 0) {
+        upper = (uint32_t)sh.kth;
+        rest = sh.rest;
       }
-      __syncthreads();
-      CountMass r = {0, 0};
-      for (int w = 0; w < kSampleThreads / 32; ++w) {
-        r.count += red[0][w];
-        r.mass += red[1][w];
+    }
+    return (upper << 8) | (uint32_t)sh.kth;
+  }
+
+  __device__ __forceinline__ void append(float z, int v) {
+    const int k = atomicAdd(&sh.count, 1);
+    if (k < kSampleList) sh.list[k] = entry_rank(z, v);
+  }
+  // What of the list is at least `least` (an order's upper 16 bits).
+  __device__ __forceinline__ void cut_list(uint32_t least) {
+    constexpr int kEach = kSampleList / kSampleThreads;
+    unsigned long long x[kEach];
+    __syncthreads();
+    const int n = min(sh.count, kSampleList);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + e * kSampleThreads;
+      x[e] = i < n ? sh.list[i] : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (x[e] != 0 && (uint32_t)(x[e] >> 48) >= least) sh.list[atomicAdd(&sh.count, 1)] = x[e];
+    __syncthreads();
+  }
+  __device__ __forceinline__ uint32_t list_kth(int k) {
+    constexpr int kEach = kSampleList / kSampleThreads;
+    uint32_t g[kEach];
+    __syncthreads();
+    const int n = min(sh.count, kSampleList);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + e * kSampleThreads;
+      g[e] = i < n ? (uint32_t)(sh.list[i] >> 48) : 0;
+    }
+    return kth(g, k);
+  }
+  // The CTAs' lists one behind the other in the first one's.  Returns their length, -1 if they
+  // do not fit.
+  __device__ __forceinline__ int gather() {
+    __syncthreads();
+    if (ctas == 1) return sh.count <= kSampleList ? sh.count : -1;
+    SamplePeer w = {};
+    w.i = sh.count;
+    const SamplePeer* all = exchange(w);
+    int before = 0, total = 0;
+    bool fits = true;
+    for (int i = 0; i < ctas; ++i) {
+      fits = fits && all[i].i <= kSampleList;
+      if (i < rank) before += all[i].i;
+      total += fits ? all[i].i : 0;
+    }
+    if (!fits || total > kSampleList) return -1;
+    if (rank > 0)
+      for (int i = threadIdx.x; i < sh.count; i += kSampleThreads)
+        dsmem_st_u64(dsmem_map(&sh.list[before + i], 0), sh.list[i]);
+    sync_all();
+    return total;
+  }
+  // Sorts the list (descending); the first CTA alone.
+  __device__ __forceinline__ void sort(int n) {
+    int size = 32;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += kSampleThreads) sh.list[i] = 0;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+      for (int j = k / 2; j > 0; j /= 2) {
+        for (int i = threadIdx.x; i < size / 2; i += kSampleThreads) {
+          const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+          const unsigned long long x = sh.list[lo], y = sh.list[hi];
+          if (((lo & k) == 0) == (x < y)) {
+            sh.list[lo] = y;
+            sh.list[hi] = x;
+          }
+        }
+        if (j > 32 || j == 1) __syncthreads();  // (else a warp has both of each pair)
+        else __syncwarp();
       }
-      return r;
+    __syncthreads();
+  }
+  // In sh.mass the masses of the sorted list's entries, summed up.
+  __device__ __forceinline__ void list_masses(int n) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kEach = kSampleList / kSampleThreads;
+    unsigned long long m[kEach], mine = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x * kEach + e;
+      m[e] = i < n ? entry_mass(s, sh.table, from_order_bits((uint32_t)(sh.list[i] >> 32))) : 0;
+      mine += m[e];
+    }
+    unsigned long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) sh.red[0][warp] = upto;
+    __syncthreads();
+    unsigned long long before = upto - mine;
+    for (int w = 0; w < warp; ++w) before += sh.red[0][w];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      before += m[e];
+      const int i = threadIdx.x * kEach + e;
+      if (i < n) sh.mass[i] = before;
+    }
+    __syncthreads();
+  }
+
+  // The first index, ascending, whose weight with all lower ones' exceeds `level(total)`; -1
+  // if none does.  Weights of the warps' runs first; the warp in whose run the level is passed
+  // goes through it again.
+  template <typename W, typename L>
+  __device__ __forceinline__ int locate(W&& weight, L&& level_of) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w0 = (int)((long long)nvec * warp / kSampleWarps);
+    const int w1 = (int)((long long)nvec * (warp + 1) / kSampleWarps);
+    const int heads = warp == 0 ? head : 0, tails = warp == kSampleWarps - 1 ? tail : 0;
+    const int tail0 = first + nvec * kPer;
+    auto single = [&](int v, bool here) -> unsigned long long {
+      return here ? weight(Tr::to_float(row[v]), v) : 0;
     };
-    limit = 0;
-    if (st.top_k > 0 && st.top_k < V) {
-      for (int b = 63; b >= 0; --b) {
-        const unsigned long long c = limit | (1ull << b);
-        if (sums(c, V - 1).count >= (unsigned long long)st.top_k) limit = c;
-      }
+    unsigned long long m =
+        single(first - head + lane, lane < heads) + single(tail0 + lane, lane < tails);
+#pragma unroll 2
+    for (int i = w0 + lane; i < w1; i += 32) {
+      float x[kPer];
+      Tr::unpack(run[i], x);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) m += weight(x[e], first + i * kPer + e);
     }
-    if (st.top_p < 1.0f) {
-      const unsigned long long want = mass_part(st.top_p, sums(limit, V - 1).mass, true);
-      unsigned long long at = 0;
-      for (int b = 63; b >= 0; --b) {
-        const unsigned long long c = at | (1ull << b);
-        if (c <= limit || sums(c, V - 1).mass >= want) at = c;
-      }
-      limit = at > limit ? at : limit;
+    m = warp_sum_u64(m);
+    __syncthreads();
+    if (lane == 0) sh.red[0][warp] = m;
+    if (threadIdx.x == 0) sh.border = -1;
+    __syncthreads();
+    SamplePeer w = {};
+    unsigned long long mine = 0, upto = 0;
+    for (int i = 0; i < kSampleWarps; ++i) {
+      if (i < warp) upto += sh.red[0][i];
+      mine += sh.red[0][i];
     }
-    if (st.min_p > 0.0f) {
-      if (threadIdx.x == 0)
-        sh_min = __double2float_ru((double)s.max + (double)st.T * log((double)st.min_p));
+    w.a = mine;
+    const SamplePeer* all = exchange(w);
+    unsigned long long total = 0;
+    for (int i = 0; i < ctas; ++i) {
+      if (i < rank) upto += all[i].a;
+      total += all[i].a;
+    }
+    const unsigned long long level = level_of(total);
+    if (upto <= level && level < upto + m) {
+      int found = -1;
+      auto look = [&](unsigned long long x, auto&& finish) {  // the lanes' weights, in order
+        unsigned long long sum = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long y = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += y;
+        }
+        const uint32_t over = __ballot_sync(0xffffffffu, upto + sum > level);
+        if (over != 0) {
+          const int l = __ffs(over) - 1;
+          if (lane == l) found = finish(upto + sum - x);
+          found = __shfl_sync(0xffffffffu, found, l);
+        }
+        upto += __shfl_sync(0xffffffffu, sum, 31);
+      };
+      if (heads > 0) {
+        const int v = first - head + lane;
+        look(single(v, lane < heads), [&](unsigned long long) { return v; });
+      }
+      for (int i0 = w0; i0 < w1 && found < 0; i0 += 32) {
+        const int i = i0 + lane;
+        float x[kPer];
+        unsigned long long sum = 0;
+        if (i < w1) {
+          Tr::unpack(run[i], x);
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) sum += weight(x[e], first + i * kPer + e);
+        }
+        look(sum, [&](unsigned long long c) {
+          int v = first + i * kPer;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            c += weight(x[e], first + i * kPer + e);
+            if (c <= level) ++v;
+          }
+          return v;
+        });
+      }
+      if (tails > 0 && found < 0) {
+        const int v = tail0 + lane;
+        look(single(v, lane < tails), [&](unsigned long long) { return v; });
+      }
+      if (lane == 0) sh.border = found;
+    }
+    __syncthreads();
+    SamplePeer w2 = {};
+    w2.i = sh.border;
+    all = exchange(w2);
+    int found = -1;
+    for (int i = 0; i < ctas; ++i) found = ::max(found, all[i].i);
+    return found;
+  }
+
+  // The largest rank from which on the entries of rank `from` and more reach the goal (all of
+  // them together do).  lo .. hi: order bits between which it is thought to be; taken to be
+  // anywhere if it is not.
+  __device__ __forceinline__ unsigned long long border_rank(SampleGoal goal, unsigned long long from,
+                                                            uint32_t lo, uint32_t hi) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // bfloat16: the lower 16 bits say nothing.
+    constexpr int kDrop = sizeof(TIn) == 2 ? 16 : 0;
+    bool widened = false;
+    for (;;) {
+      const uint32_t k0 = lo >> kDrop, k1 = hi >> kDrop;
+      int shift = 0;
+      while (((k1 - k0) >> shift) >= (uint32_t)kSampleFine) ++shift;
       __syncthreads();
-      const unsigned long long c = (unsigned long long)order_bits(sh_min) << 32;
-      limit = c > limit ? c : limit;
-    }
-    if (p.tokens != nullptr) {
-      const float u = p.uniforms[row];
-      const unsigned long long level = mass_part(u, sums(limit, V - 1).mass, false);
-      int lo = 0, hi = V - 1;  // the token is in lo .. hi
-      while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (sums(limit, mid).mass > level) hi = mid;
-        else lo = mid + 1;
+      for (int i = tid; i < kSampleFine; i += kSampleThreads) {
+        sh.hist[i] = 0;
+        sh.fine[i] = 0;
       }
-      token = u >= 0.0f && u < 1.0f ? lo : -1;
+      __syncthreads();
+      unsigned long long count = 0, mass = 0;  // above hi
+      each([&](const float* x, int v, int n) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          if (e >= n) continue;
+          const uint32_t k = order_bits(x[e]) >> kDrop;
+          if (k < k0 || entry_rank(x[e], v + e) < from) continue;
+          const unsigned long long m = goal.by_count ? 0 : entry_mass(s, sh.table, x[e]);
+          if (k > k1) {
+            ++count;
+            mass += m;
+          } else {
+            const int b = (int)((k - k0) >> shift);
+            atomicAdd(&sh.hist[b], 1u);
+            if (m != 0) atomicAdd(&sh.fine[b], m);
+          }
+        }
+      });
+      const CountMass above = cluster_sums(count, mass);
+      // From the top bin down: thread t has two bins, and what is above them.
+      const unsigned long long start = goal.by_count ? above.count : above.mass;
+      SamplePeer w = {};
+      w.i = -1;
+      if (rank == 0) {
+        constexpr int kEach = kSampleFine / kSampleThreads;
+        unsigned long long n[kEach], mine = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const int b = kSampleFine - 1 - (tid * kEach + e);
+          n[e] = 0;
+          for (int i = 0; i < ctas; ++i)
+            n[e] += goal.by_count ? dsmem_ld_u32(dsmem_map(&sh.hist[b], i))
+                                  : dsmem_ld_u64(dsmem_map(&sh.fine[b], i));
+          mine += n[e];
+        }
+        unsigned long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        if (lane == 31) sh.red[0][warp] = upto;
+        if (tid == 0) sh.border = -1;
+        __syncthreads();
+        unsigned long long before = start + upto - mine;
+        for (int q = 0; q < warp; ++q) before += sh.red[0][q];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          if (before < goal.want && before + n[e] >= goal.want) {
+            sh.border = kSampleFine - 1 - (tid * kEach + e);
+            sh.red[1][0] = before;
+          }
+          before += n[e];
+        }
+        __syncthreads();
+        if (tid == 0 && sh.border >= 0) {
+          w.i = sh.border;
+          w.a = sh.red[1][0];
+          int c = 0;
+          for (int i = 0; i < ctas; ++i) c += (int)dsmem_ld_u32(dsmem_map(&sh.hist[sh.border], i));
+          w.j = c;
+        }
+      }
+      const SamplePeer* all = exchange(w);
+      const int bin = all[0].i, entries = all[0].j;
+      const unsigned long long before = all[0].a;
+      if (bin < 0) {
+        if (widened) return from;  // (does not happen: all entries together reach the goal)
+        widened = true;
+        lo = 0;
+        hi = 0xffffffffu;
+        continue;
+      }
+      const uint32_t b0 = k0 + ((uint32_t)bin << shift);
+      const uint32_t b1 = ::min(k1, b0 + ((1u << shift) - 1));
+      if (entries <= kSampleList) {
+        __syncthreads();
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        each([&](const float* x, int v, int n) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            if (e >= n) continue;
+            const uint32_t k = order_bits(x[e]) >> kDrop;
+            if (k >= b0 && k <= b1 && entry_rank(x[e], v + e) >= from) append(x[e], v + e);
+          }
+        });
+        const int n = gather();
+        SamplePeer w2 = {};
+        if (rank == 0) {
+          sort(n);
+          int i;
+          if (goal.by_count) {
+            i = (int)(goal.want - before) - 1;
+          } else {
+            list_masses(n);
+            i = first_reaching(sh.mass, n, goal.want - before);
+          }
+          w2.a = sh.list[::min(i, n - 1)];
+        }
+        return exchange(w2)[0].a;
+      }
+      if (shift == 0) {
+        // All equal: the lowest indices, as many as are wanted.
+        // (The bits that bfloat16 does not have are ones in a negative number's order.)
+        const float z = from_order_bits((b0 << kDrop) | (kDrop && !(b0 & 0x8000u) ? 0xffffu : 0u));
+        unsigned long long nth = goal.want - before;
+        if (!goal.by_count) {
+          const unsigned long long m = entry_mass(s, sh.table, z);
+          nth = (nth + m - 1) / m;
+        }
+        const int v = locate(
+            [&](float y, int at) -> unsigned long long {
+              return order_bits(y) >> kDrop == b0 && entry_rank(y, at) >= from ? 1 : 0;
+            },
+            [&](unsigned long long) { return nth - 1; });
+        return entry_rank(z, v);
+      }
+      lo = b0 << kDrop;
+      hi = (b1 << kDrop) | (kDrop ? 0xffffu : 0u);
     }
   }
-  if (p.tokens != nullptr && threadIdx.x == 0) p.tokens[row] = token;
-  if (p.kept == nullptr) return;
-  TIn* out = static_cast<TIn*>(p.kept) + (size_t)row * V;
-  TIn nan, off;
+};
+
+template <typename TIn>
+__global__ void __launch_bounds__(kSampleThreads, 2)
+    sample_kernel(const __grid_constant__ SampleParams p) {
+  using Tr = ElemTraits<TIn>;
+  constexpr int kPer = SampleJob<TIn>::kPer;
+  __shared__ __align__(16) SampleShared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+  const int V = p.V, r = blockIdx.x / ctas;
+  if (ctas > 1) cluster_arrive();  // (waited for before the first word to another CTA)
+  if (tid == 0) sh.count = 0;
+  if (tid < 256) sh.table.e[tid] = g_mass_table.e[tid];
+  pdl_wait();
+  pdl_launch_dependents();
+  SampleJob<TIn> job = {sh, p};
+  job.rank = rank;
+  job.ctas = ctas;
+  job.round = 0;
+  job.row = static_cast<const TIn*>(p.logits) + (size_t)r * V;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(job.row);
+  const int before = min((int)((16 - at % 16) % 16 / sizeof(TIn)), V);
+  const int nv = (V - before) / kPer;
+  const int v0 = (int)((long long)nv * rank / ctas), v1 = (int)((long long)nv * (rank + 1) / ctas);
+  job.nvec = v1 - v0;
+  job.first = before + v0 * kPer;
+  job.head = rank == 0 ? before : 0;
+  job.tail = rank == ctas - 1 ? V - before - nv * kPer : 0;
+  job.run = reinterpret_cast<const uint4*>(job.row + job.first);
+  const int nvec = job.nvec, edges = job.head + job.tail;
+
+  // The first vectors are on their way while the settings are read.
+  uint4 next[kSampleBatch];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kSampleBatch; ++j) {
+      const int i = i0 + j * kSampleThreads + tid;
+      if (i < nvec) next[j] = job.run[i];
+    }
+  };
+  load(0);
+  const RowSettings st = row_settings(p, r);
+  const bool greedy = st.T == 0.0f;
+  const bool cut_k = !greedy && st.top_k > 0 && st.top_k < V, cut_p = !greedy && st.top_p < 1.0f;
+  const bool few = cut_k && st.top_k <= kSampleFew;
+  const bool estimate = cut_p && !cut_k;  // the row's mass, roughly
+  if (st.ok && !greedy) {
+    if (tid == 32) {  // (in double precision, which is slow: beside the loads)
+      const double inv = 1.4426950408889634074 / (double)st.T;
+      sh.inv.hi = (float)inv;
+      sh.inv.lo = (float)(inv - (double)sh.inv.hi);
+    }
+    if (tid == 64 && st.min_p > 0.0f) sh.min_off = (double)st.T * log((double)st.min_p);
+  }
+  if (estimate) __syncthreads();
+
+  // First pass.
+  bool bad = !st.ok, overflow = false;
+  float top = -INFINITY;  // the largest entry of the vectors
+  float edge = tid < edges ? Tr::to_float(job.row[SPEC_CHECKED(job.edge(tid), V, kSiteSample)])
+                           : -INFINITY;
+  bad |= edge != edge && !greedy;
+  int top_vec = -1;  // greedy: the vector it is in, the first
+  SoftAcc acc;
+  soft_init(acc);
+  float nan = 0.0f;  // NaN once an entry is
+  uint32_t least_bits = 0;
+  constexpr int kStep = kSampleBatch * kSampleThreads;
+  if (few) {
+    float half[2 * kSampleBatch];
+#pragma unroll
+    for (int j = 0; j < kSampleBatch; ++j) {
+      half[2 * j] = half[2 * j + 1] = -INFINITY;
+      if (j * kSampleThreads + tid < nvec) {
+        float x[kPer];
+        Tr::unpack(next[j], x);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) half[2 * j + (e >= kPer / 2)] = fmaxf(half[2 * j + (e >= kPer / 2)], x[e]);
+      }
+    }
+    uint32_t g[2 * kSampleBatch];
+#pragma unroll
+    for (int j = 0; j < 2 * kSampleBatch; ++j)
+      g[j] = half[j] < -FLT_MAX ? 0 : order_bits(half[j]) >> 16;
+    least_bits = job.kth(g, st.top_k);
+  }
+  // (An entry of -inf has no mass, and is -inf in the result too.)
+  float least = fmaxf(from_order_bits(least_bits << 16), -FLT_MAX);
+  if (few && edge >= least) job.append(edge, job.edge(tid));
+  for (int i0 = 0; i0 < nvec; i0 += kStep) {
+    uint4 v[kSampleBatch];
+#pragma unroll
+    for (int j = 0; j < kSampleBatch; ++j) v[j] = next[j];
+    if (i0 + kStep < nvec) load(i0 + kStep);
+#pragma unroll
+    for (int j = 0; j < kSampleBatch; ++j) {
+      const int i = i0 + j * kSampleThreads + tid;
+      if (i >= nvec) break;
+      float x[kPer];
+      Tr::unpack(v[j], x);
+      float most = x[0];
+#pragma unroll
+      for (int e = 1; e < kPer; ++e) most = fmaxf(most, x[e]);
+      if constexpr (sizeof(TIn) == 2) {
+        nan = __uint_as_float(nan_of(v[j], __float_as_uint(nan)));
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) nan = x[e] != x[e] ? x[e] : nan;
+      }
+      if (most > top) {
+        top = most;
+        top_vec = i;
+      }
+      if (few) {
+        if (most >= least) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            if (x[e] >= least) job.append(x[e], job.first + i * kPer + e);
+        }
+      } else if (estimate && most > -1e37f) {  // (what is below has no mass)
+        soft_add_vec<TIn>(acc, v[j], sh.inv.hi);
+      }
+    }
+    if (few && !overflow && i0 + kStep < nvec) {
+      __syncthreads();
+      const int n = sh.count;
+      __syncthreads();  // (all have read it before any adds to it)
+      if (n > kSampleList) {
+        overflow = true;
+        least = INFINITY;  // (no more entries)
+      } else if (n > kSampleCut) {
+        least_bits = ::max(least_bits, job.list_kth(st.top_k));
+        job.cut_list(least_bits);
+        least = fmaxf(from_order_bits(least_bits << 16), -FLT_MAX);
+      }
+    }
+  }
+  if (estimate && edge > -1e37f) soft_add1(acc, edge, sh.inv.hi);
+  if constexpr (sizeof(TIn) == 2) {
+    const float other = __uint_as_float(__float_as_uint(nan) << 16);
+    nan = other != other ? other : nan;
+  }
+  const float vec_top = top;
+  top = fmaxf(top, edge);
+  bad |= !greedy && (nan != nan || top > FLT_MAX);
+  bad = __syncthreads_or(bad);
+  if (few && !bad) {
+    // A long list is cut before it is sorted.
+    overflow = sh.count > kSampleList;
+    if (!overflow && sh.count > kSampleLong) least_bits = ::max(least_bits, job.list_kth(st.top_k));
+  }
+
+  // What the CTAs have found.
+  SamplePeer word = {};
+  {
+    unsigned long long best = 0;
+    if (greedy && top >= -FLT_MAX) {
+      // The lowest index of the thread's largest.
+      if (tid < edges && edge == top) best = entry_rank(edge, job.edge(tid));
+      if (top_vec >= 0 && vec_top == top) {
+        float x[kPer];
+        Tr::unpack(job.run[top_vec], x);
+#pragma unroll
+        for (int e = kPer - 1; e >= 0; --e)
+          if (x[e] == top) {
+            const unsigned long long rk = entry_rank(top, job.first + top_vec * kPer + e);
+            best = rk > best ? rk : best;
+          }
+      }
+    }
+    float m = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (estimate) {
+        SoftAcc b;
+        b.m = __shfl_xor_sync(0xffffffffu, acc.m, o);
+        b.ms = __shfl_xor_sync(0xffffffffu, acc.ms, o);
+        b.s = __shfl_xor_sync(0xffffffffu, acc.s, o);
+        soft_merge(acc, b);
+      }
+    }
+    if (greedy) best = warp_max_u64(best);
+    __syncthreads();
+    if (lane == 0) {
+      sh.mine[warp].x = m;
+      sh.mine[warp].y = acc.ms;
+      sh.mine[warp].a = greedy ? best : __float_as_uint(acc.s);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const SamplePeer q = sh.mine[lane % kSampleWarps];
+      word.x = q.x;
+      acc.m = acc.ms = lane < kSampleWarps ? q.y : -FLT_MAX;
+      acc.s = lane < kSampleWarps ? __uint_as_float((uint32_t)q.a) : 0.0f;
+      best = q.a;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        word.x = fmaxf(word.x, __shfl_xor_sync(0xffffffffu, word.x, o));
+        SoftAcc b;
+        b.m = b.ms = __shfl_xor_sync(0xffffffffu, acc.ms, o);
+        b.s = __shfl_xor_sync(0xffffffffu, acc.s, o);
+        if (estimate) soft_merge(acc, b);
+      }
+      if (greedy) best = warp_max_u64(best);
+    }
+    word.y = acc.ms;
+    word.a = greedy ? best : __float_as_uint(acc.s);
+    word.b = least_bits;
+    word.i = bad;
+    word.j = overflow;
+  }
+  if (ctas > 1) cluster_wait();
+  const SamplePeer* all = job.exchange(word);
+  float most = -INFINITY, mass_ms = -FLT_MAX, mass_s = 0.0f;
+  unsigned long long limit = 0;
+  overflow = false;
+  for (int i = 0; i < ctas; ++i) {
+    most = fmaxf(most, all[i].x);
+    bad |= all[i].i != 0;
+    overflow |= all[i].j != 0;
+    least_bits = ::max(least_bits, (uint32_t)all[i].b);
+    mass_ms = fmaxf(mass_ms, all[i].y);
+    if (greedy) limit = all[i].a > limit ? all[i].a : limit;
+  }
+  if (estimate)
+    for (int i = 0; i < ctas; ++i)
+      mass_s += __uint_as_float((uint32_t)all[i].a) * ex2(all[i].y - mass_ms);
+  bad |= !(most >= -FLT_MAX);
+
+  job.s.max = most;
+  job.s.inv = sh.inv;
+  job.s.unit_bits = p.unit_bits;
+  int token = -1;
+  int listed = -1;  // entries of K in the first CTA's list, if it has all of K
+  const bool want_kept = p.kept != nullptr, want_token = p.tokens != nullptr;
+  float u = want_token ? p.uniforms[r] : 0.0f;
+  const bool u_ok = u >= 0.0f && u < 1.0f;
+  if (!u_ok) u = 0.0f;
+  if (bad) {
+  } else if (greedy) {
+    token = (int)~(uint32_t)limit;
+  } else {
+    unsigned long long min_rank = 0;
+    if (st.min_p > 0.0f)
+      min_rank = (unsigned long long)order_bits(__double2float_ru((double)most + sh.min_off)) << 32;
+    int n = -1;
+    if (few && !overflow) {
+      if (sh.count > kSampleLong || ctas > 1) job.cut_list(least_bits);
+      n = job.gather();
+    }
+    if (n >= 0) {
+      if (rank == 0) {
+        job.sort(n);
+        job.list_masses(n);
+        int kept = min(n, st.top_k);
+        if (cut_p) {
+          const unsigned long long want = mass_part(st.top_p, sh.mass[kept - 1], true);
+          kept = min(first_reaching(sh.mass, kept, want) + 1, kept);
+        }
+        if (min_rank > 0) {
+          int lo = 0, hi = kept;  // entries of min_rank and more
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (sh.list[mid] >= min_rank) lo = mid + 1;
+            else hi = mid;
+          }
+          kept = lo;
+        }
+        listed = kept;
+        limit = sh.list[kept - 1];
+        if (want_token && u_ok) {
+          const unsigned long long level = mass_part(u, sh.mass[kept - 1], false);
+          token = V;
+          if (kept <= 128) {
+            // Each entry's mass with those of all lower indices; the lowest that passes.
+            if (tid == 0) sh.border = V;
+            __syncthreads();
+            if (tid < kept) {
+              const uint32_t mine = (uint32_t)sh.list[tid];
+              unsigned long long m = 0, last = 0;
+              for (int i = 0; i < kept; ++i) {
+                const unsigned long long upto = sh.mass[i];
+                if ((uint32_t)sh.list[i] >= mine) m += upto - last;  // (~index)
+                last = upto;
+              }
+              if (m > level) atomicMin(&sh.border, (int)~mine);
+            }
+            __syncthreads();
+            token = sh.border;
+          } else {
+            // By bisection of the index; a thread has an entry (kept <= kSampleFew).
+            const int idx = tid < kept ? (int)~(uint32_t)sh.list[tid] : V;
+            const unsigned long long m =
+                tid < kept ? sh.mass[tid] - (tid > 0 ? sh.mass[tid - 1] : 0) : 0;
+            int lo = 0, hi = V - 1;
+            while (lo < hi) {
+              const int mid = lo + (hi - lo) / 2;
+              if (job.block_sums(0, idx <= mid ? m : 0).mass > level) hi = mid;
+              else lo = mid + 1;
+            }
+            token = lo;
+          }
+        }
+      }
+      if (want_kept && ctas > 1) {
+        SamplePeer w = {};
+        w.a = limit;
+        limit = job.exchange(w)[0].a;
+      }
+    } else {
+      const uint32_t top_bits = order_bits(most);
+      if (cut_k)
+        limit = job.border_rank({true, (unsigned long long)st.top_k}, 0, 0, top_bits);
+      if (cut_p) {
+        // The border is among the entries whose mass is at least their share of what may be
+        // left out; where about, a histogram of the distances from the maximum shows.
+        uint32_t lo = (uint32_t)(limit >> 32), hi = top_bits;
+        unsigned long long total = 0;
+        if (estimate) {
+          const float range = logf((float)V / ((1.0f - st.top_p) * mass_s)) + 0.001f -
+                              (mass_ms - __fmul_rn(most, job.s.inv.hi)) * kLn2f;
+          const float per =
+              __fmul_rn(__fmul_rn(job.s.inv.hi, kLn2f), (float)kSampleBins / range);
+          __syncthreads();
+          for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.hist[i] = 0;
+          __syncthreads();
+          unsigned long long m = 0;
+          job.each([&](const float* x, int v, int k) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              if (e < k) {
+                m += entry_mass(job.s, sh.table, x[e]);
+                const float f = __fmul_rn(__fsub_rn(most, x[e]), per);
+                if (f >= 0.0f && f < (float)kSampleBins) atomicAdd(&sh.hist[(int)f], 1u);
+              }
+          });
+          total = job.cluster_sums(0, m).mass;
+          SamplePeer w = {};
+          if (rank == 0) {
+            // The masses of the bins, taken at their middles, up to what is wanted.
+            constexpr int kEach = kSampleBins / kSampleThreads;
+            const float width = range / (float)kSampleBins;
+            float mine = 0.0f, bin[kEach];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+              const int b = tid * kEach + e;
+              uint32_t c = 0;
+              for (int i = 0; i < ctas; ++i) c += dsmem_ld_u32(dsmem_map(&sh.hist[b], i));
+              bin[e] = (float)c * expf(-((float)b + 0.5f) * width);
+              mine += bin[e];
+            }
+            float upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const float x = __shfl_up_sync(0xffffffffu, upto, o);
+              if (lane >= o) upto += x;
+            }
+            if (tid == 0) sh.border = kSampleBins - 1;
+            if (lane == 31) sh.mine[warp].x = upto;
+            __syncthreads();
+            float sum = upto - mine;
+            for (int q = 0; q < warp; ++q) sum += sh.mine[q].x;
+            const float goal =
+                st.top_p * (float)((double)total * exp2(-(double)p.unit_bits));
+            for (int e = 0; e < kEach; ++e) {
+              sum += bin[e];
+              if (sum >= goal) {
+                atomicMin(&sh.border, tid * kEach + e);
+                break;
+              }
+            }
+            __syncthreads();
+            w.i = sh.border;
+          }
+          const int border = job.exchange(w)[0].i;
+          // (Where exactly the places of the bins' ends lie does not matter: what is found
+          // outside of them is looked for everywhere.)
+          lo = order_bits(fmaxf(most - (float)(border + 2) / per, -FLT_MAX));
+          hi = order_bits(fmaxf(most - (float)::max(border - 1, 0) / per, -FLT_MAX));
+          if (!(per > 0.0f) || !(per <= FLT_MAX)) {
+            lo = 0;
+            hi = top_bits;
+          }
+        } else {
+          unsigned long long m = 0;
+          job.each([&](const float* x, int v, int k) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              if (e < k && entry_rank(x[e], v + e) >= limit) m += entry_mass(job.s, sh.table, x[e]);
+          });
+          total = job.cluster_sums(0, m).mass;
+        }
+        const unsigned long long rk =
+            job.border_rank({false, mass_part(st.top_p, total, true)}, limit, lo, hi);
+        limit = rk > limit ? rk : limit;
+      }
+      limit = min_rank > limit ? min_rank : limit;
+      if (want_token)
+        token = job.locate(
+            [&](float z, int v) -> unsigned long long {
+              return entry_rank(z, v) >= limit ? entry_mass(job.s, sh.table, z) : 0;
+            },
+            [&](unsigned long long total) { return mass_part(u, total, false); });
+    }
+    if (!u_ok) token = -1;
+  }
+  if (want_token && rank == 0 && tid == 0) p.tokens[r] = token;
+  if (!want_kept) return;
+  TIn* out = static_cast<TIn*>(p.kept) + (size_t)r * V;
+  TIn none, off;
   if constexpr (sizeof(TIn) == 4) {
-    nan = __int_as_float(0x7fc00000);
+    none = __int_as_float(0x7fc00000);
     off = -INFINITY;
   } else {
-    nan = 0x7fc0;
+    none = 0x7fc0;
     off = 0xff80;
   }
-  for (int v = threadIdx.x; v < V; v += kSampleThreads) {
-    const TIn x = in[v];
+  __syncthreads();  // (in place: nobody reads the row any more)
+  auto result = [&](TIn x, int v) -> TIn {
     const float z = Tr::to_float(x);
-    out[v] = bad ? nan : z == z && entry_rank(z, v) >= limit ? x : off;
+    return bad ? none : z == z && entry_rank(z, v) >= limit ? x : off;
+  };
+  const bool lines = reinterpret_cast<uintptr_t>(out + job.first) % 16 == 0;
+  // K is all in the list: the row is not read again.
+  const bool fill = ctas == 1 && listed >= 0;
+  const uint32_t off2 = sizeof(TIn) == 4 ? 0xff800000u : 0xff80ff80u;
+  if (fill && lines) {
+    uint4* dst = reinterpret_cast<uint4*>(out + job.first);
+    const int kept_at = tid < listed ? (int)~(uint32_t)sh.list[tid] : -1;
+    const TIn x = kept_at >= 0 ? job.row[kept_at] : off;
+    __syncthreads();
+    for (int i = tid; i < nvec; i += kSampleThreads) dst[i] = make_uint4(off2, off2, off2, off2);
+    if (tid < edges) out[job.edge(tid)] = off;
+    __syncthreads();
+    if (kept_at >= 0) out[kept_at] = x;
+    return;
+  }
+  for (int i = tid; i < nvec; i += kSampleThreads) {
+    const uint4 v = job.run[i];
+    TIn x[kPer];
+    *reinterpret_cast<uint4*>(x) = v;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = result(x[e], job.first + i * kPer + e);
+    if (lines) {
+      *reinterpret_cast<uint4*>(out + job.first + i * kPer) = *reinterpret_cast<uint4*>(x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) out[job.first + i * kPer + e] = x[e];
+    }
+  }
+  if (tid < edges) {
+    const int v = job.edge(tid);
+    out[v] = result(job.row[v], v);
   }
 }
 

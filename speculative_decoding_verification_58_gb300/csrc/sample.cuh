@@ -1104,7 +1104,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
             // The masses of the bins, taken at their middles, up to what is wanted.
             constexpr int kEach = kSampleBins / kSampleThreads;
             const float width = range / (float)kSampleBins;
-            float mine = 0.0f, bin[kEach];
+            float mine = 0.0f, squares = 0.0f, bin[kEach];
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
               const int b = tid * kEach + e;
@@ -1112,35 +1112,50 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
               for (int i = 0; i < ctas; ++i) c += dsmem_ld_u32(dsmem_map(&sh.hist[b], i));
               bin[e] = (float)c * expf(-((float)b + 0.5f) * width);
               mine += bin[e];
+              squares = fmaf(bin[e], bin[e], squares);
             }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(0xffffffffu, squares, o);
             float upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
               const float x = __shfl_up_sync(0xffffffffu, upto, o);
               if (lane >= o) upto += x;
             }
-            if (tid == 0) sh.border = kSampleBins - 1;
-            if (lane == 31) sh.mine[warp].x = upto;
-            __syncthreads();
-            float sum = upto - mine;
-            for (int q = 0; q < warp; ++q) sum += sh.mine[q].x;
-            const float goal =
-                st.top_p * (float)((double)total * exp2(-(double)p.unit_bits));
-            for (int e = 0; e < kEach; ++e) {
-              sum += bin[e];
-              if (sum >= goal) {
-                atomicMin(&sh.border, tid * kEach + e);
-                break;
-              }
+            if (tid == 0) sh.border = sh.rest = kSampleBins - 1;
+            if (lane == 31) {
+              sh.mine[warp].x = upto;
+              sh.mine[warp].y = squares;
             }
             __syncthreads();
-            w.i = sh.border;
+            float sum = upto - mine;
+            squares = 0.0f;
+            for (int q = 0; q < kSampleWarps; ++q) {
+              if (q < warp) sum += sh.mine[q].x;
+              squares += sh.mine[q].y;
+            }
+            // A bin's entries are off its middle by up to half a width, all alike at worst: four
+            // standard deviations of that.
+            const float slack = 1.2f * width * sqrtf(squares);
+            const float goal = st.top_p * ((float)total * exp2f(-(float)p.unit_bits));
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+              const float next = sum + bin[e];
+              if (sum < goal - slack && next >= goal - slack) atomicMin(&sh.border, tid * kEach + e);
+              if (sum < goal + slack && next >= goal + slack) atomicMin(&sh.rest, tid * kEach + e);
+              sum = next;
+            }
+            if (tid == 0 && goal - slack <= 0.0f) sh.border = 0;
+            __syncthreads();
+            w.i = ::max(sh.border - 1, 0);
+            w.j = sh.rest + 2;
           }
-          const int border = job.exchange(w)[0].i;
+          const SamplePeer* bins = job.exchange(w);
+          const int bin_lo = bins[0].i, bin_hi = bins[0].j;
           // (Where exactly the places of the bins' ends lie does not matter: what is found
           // outside of them is looked for everywhere.)
-          lo = order_bits(fmaxf(most - (float)(border + 2) / per, -FLT_MAX));
-          hi = order_bits(fmaxf(most - (float)::max(border - 1, 0) / per, -FLT_MAX));
+          lo = order_bits(fmaxf(most - (float)bin_hi / per, -FLT_MAX));
+          hi = order_bits(fmaxf(most - (float)bin_lo / per, -FLT_MAX));
           if (!(per > 0.0f) || !(per <= FLT_MAX)) {
             lo = 0;
             hi = top_bits;

@@ -74,6 +74,7 @@ struct MassScale {
   float max;
   FF inv;  // log2(e) / T
   int unit_bits;
+  float low;  // distances below it are without mass
 };
 __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, const MassTable& t,
                                                          float z) {
@@ -103,6 +104,17 @@ __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, con
   if (shift <= 0) return m << -shift;
   if (shift > 41) return 0;
   return (m + (1ull << (shift - 1))) >> shift;
+}
+
+// The same in single precision, to about 2^-22 of itself, for sums that only have to tell on
+// which side of a border they are, and for the draw.
+__device__ __forceinline__ float near_mass(const MassScale& s, float z) {
+  const float d = fmaxf(__fsub_rn(z, s.max), s.low);
+  return z < -FLT_MAX ? 0.0f : ex2(__fmaf_rn(d, s.inv.hi, __fmul_rn(d, s.inv.lo)));
+}
+// In whole units of 2^-32 (the largest entry's 2^32 - 1 then), for the draw.
+__device__ __forceinline__ uint32_t draw_mass(const MassScale& s, float z) {
+  return __float2uint_rn(__fmul_rn(near_mass(s, z), 4294967040.0f));
 }
 
 // NaN in either half of the result once an entry of the vectors so far is: maxima that keep it.
@@ -247,6 +259,13 @@ __device__ __forceinline__ int first_reaching(const unsigned long long* sums, in
     else lo = mid + 1;
   }
   return lo;
+}
+
+// A sum of near masses in units of 2^-kNearBits.
+constexpr int kNearBits = 40;
+__device__ __forceinline__ unsigned long long units_of(FF x) {
+  const float up = 1099511627776.0f;
+  return (unsigned long long)(__float2ll_rn(__fmul_rn(x.hi, up)) + __float2ll_rn(__fmul_rn(x.lo, up)));
 }
 
 // What a border is looked for by: the entries' number or their mass.
@@ -994,6 +1013,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   job.s.max = most;
   job.s.inv = sh.inv;
   job.s.unit_bits = p.unit_bits;
+  job.s.low = fmaxf(__fdiv_rn(-200.0f, sh.inv.hi), -FLT_MAX);
   int token = -1;
   int listed = -1;  // entries of K in the first CTA's list, if it has all of K
   const bool want_kept = p.kept != nullptr, want_token = p.tokens != nullptr;
@@ -1079,7 +1099,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
         // The border is among the entries whose mass is at least their share of what may be
         // left out; where about, a histogram of the distances from the maximum shows.
         uint32_t lo = (uint32_t)(limit >> 32), hi = top_bits;
-        unsigned long long total = 0;
+        bool cut_p_done = false;
         if (estimate) {
           const float range = logf((float)V / ((1.0f - st.top_p) * mass_s)) + 0.001f -
                               (mass_ms - __fmul_rn(most, job.s.inv.hi)) * kLn2f;
@@ -1088,17 +1108,19 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
           __syncthreads();
           for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.hist[i] = 0;
           __syncthreads();
-          unsigned long long m = 0;
+          FF sum = {0.0f, 0.0f};
           job.each([&](const float* x, int v, int k) {
+            float part = 0.0f;
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
               if (e < k) {
-                m += entry_mass(job.s, sh.table, x[e]);
+                part = __fadd_rn(part, near_mass(job.s, x[e]));
                 const float f = __fmul_rn(__fsub_rn(most, x[e]), per);
                 if (f >= 0.0f && f < (float)kSampleBins) atomicAdd(&sh.hist[(int)f], 1u);
               }
+            sum = ff_add_f(sum, part);
           });
-          total = job.cluster_sums(0, m).mass;
+          const unsigned long long about = job.cluster_sums(0, units_of(sum)).mass;
           SamplePeer w = {};
           if (rank == 0) {
             // The masses of the bins, taken at their middles, up to what is wanted.
@@ -1110,7 +1132,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
               const int b = tid * kEach + e;
               uint32_t c = 0;
               for (int i = 0; i < ctas; ++i) c += dsmem_ld_u32(dsmem_map(&sh.hist[b], i));
-              bin[e] = (float)c * expf(-((float)b + 0.5f) * width);
+              bin[e] = (float)c * ex2(__fmul_rn(-((float)b + 0.5f) * width, kLog2e));
               mine += bin[e];
               squares = fmaf(bin[e], bin[e], squares);
             }
@@ -1128,22 +1150,24 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
               sh.mine[warp].y = squares;
             }
             __syncthreads();
-            float sum = upto - mine;
+            float before = upto - mine;
             squares = 0.0f;
             for (int q = 0; q < kSampleWarps; ++q) {
-              if (q < warp) sum += sh.mine[q].x;
+              if (q < warp) before += sh.mine[q].x;
               squares += sh.mine[q].y;
             }
             // A bin's entries are off its middle by up to half a width, all alike at worst: four
             // standard deviations of that.
             const float slack = 1.2f * width * sqrtf(squares);
-            const float goal = st.top_p * ((float)total * exp2f(-(float)p.unit_bits));
+            const float goal = st.top_p * ((float)about * exp2f(-(float)kNearBits));
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
-              const float next = sum + bin[e];
-              if (sum < goal - slack && next >= goal - slack) atomicMin(&sh.border, tid * kEach + e);
-              if (sum < goal + slack && next >= goal + slack) atomicMin(&sh.rest, tid * kEach + e);
-              sum = next;
+              const float next = before + bin[e];
+              if (before < goal - slack && next >= goal - slack)
+                atomicMin(&sh.border, tid * kEach + e);
+              if (before < goal + slack && next >= goal + slack)
+                atomicMin(&sh.rest, tid * kEach + e);
+              before = next;
             }
             if (tid == 0 && goal - slack <= 0.0f) sh.border = 0;
             __syncthreads();
@@ -1151,33 +1175,79 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
             w.j = sh.rest + 2;
           }
           const SamplePeer* bins = job.exchange(w);
-          const int bin_lo = bins[0].i, bin_hi = bins[0].j;
-          // (Where exactly the places of the bins' ends lie does not matter: what is found
-          // outside of them is looked for everywhere.)
-          lo = order_bits(fmaxf(most - (float)bin_hi / per, -FLT_MAX));
-          hi = order_bits(fmaxf(most - (float)bin_lo / per, -FLT_MAX));
-          if (!(per > 0.0f) || !(per <= FLT_MAX)) {
-            lo = 0;
-            hi = top_bits;
+          // (Where exactly the places of the bins' ends lie does not matter.)
+          const float z_lo = fmaxf(most - (float)bins[0].j / per, -FLT_MAX);
+          const float z_hi = bins[0].i == 0 ? INFINITY : most - (float)bins[0].i / per;
+          unsigned long long rk = 0;
+          if (per > 0.0f && per <= FLT_MAX) {
+            // What is above those bins, and their entries one by one.
+            __syncthreads();
+            if (tid == 0) sh.count = 0;
+            __syncthreads();
+            sum = {0.0f, 0.0f};
+            job.each([&](const float* x, int v, int k) {
+              float part = 0.0f;
+#pragma unroll
+              for (int e = 0; e < kPer; ++e)
+                if (e < k && x[e] >= z_lo) {
+                  if (x[e] > z_hi) part = __fadd_rn(part, near_mass(job.s, x[e]));
+                  else job.append(x[e], v + e);
+                }
+              sum = ff_add_f(sum, part);
+            });
+            const unsigned long long above = job.cluster_sums(0, units_of(sum)).mass;
+            const int n = job.gather();
+            SamplePeer w2 = {};
+            if (rank == 0 && n > 0) {
+              job.sort(n);
+              job.list_masses(n);
+              // Both sums are right to a few parts in 10^9 (errors of thousands of entries, of
+              // 10^-7 each): if the border is not a hundred times as far, the exact sums decide.
+              const int down = p.unit_bits - kNearBits;
+              const unsigned long long want = mass_part(st.top_p, about, true), doubt = about >> 22;
+              if (want > above) {
+                const int i = first_reaching(sh.mass, n, (want - above) << down);
+                if (i < n) {
+                  const unsigned long long upto = above + (sh.mass[i] >> down);
+                  const unsigned long long less = above + (i > 0 ? sh.mass[i - 1] >> down : 0);
+                  if (upto - want > doubt && want - less > doubt) w2.a = sh.list[i];
+                }
+              }
+            }
+            rk = job.exchange(w2)[0].a;
           }
-        } else {
+          if (rk != 0) {
+            limit = rk;
+            cut_p_done = true;
+          } else if (per > 0.0f && per <= FLT_MAX) {
+            lo = order_bits(z_lo);
+            hi = order_bits(fminf(z_hi, most));
+          } else {
+            lo = 0;
+          }
+        }
+        if (!cut_p_done) {
           unsigned long long m = 0;
           job.each([&](const float* x, int v, int k) {
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
               if (e < k && entry_rank(x[e], v + e) >= limit) m += entry_mass(job.s, sh.table, x[e]);
           });
-          total = job.cluster_sums(0, m).mass;
+          const unsigned long long total = job.cluster_sums(0, m).mass;
+          const unsigned long long rk =
+              job.border_rank({false, mass_part(st.top_p, total, true)}, limit, lo, hi);
+          limit = rk > limit ? rk : limit;
         }
-        const unsigned long long rk =
-            job.border_rank({false, mass_part(st.top_p, total, true)}, limit, lo, hi);
-        limit = rk > limit ? rk : limit;
       }
       limit = min_rank > limit ? min_rank : limit;
+      const float limit_z = limit > 0 ? from_order_bits((uint32_t)(limit >> 32)) : -INFINITY;
       if (want_token)
+        // (z itself decides but for the entries equal to the last one kept.)
         token = job.locate(
             [&](float z, int v) -> unsigned long long {
-              return entry_rank(z, v) >= limit ? entry_mass(job.s, sh.table, z) : 0;
+              return z >= limit_z && (z > limit_z || entry_rank(z, v) >= limit)
+                         ? draw_mass(job.s, z)
+                         : 0;
             },
             [&](unsigned long long total) { return mass_part(u, total, false); });
     }

@@ -198,12 +198,14 @@ __device__ __forceinline__ RowSettings row_settings(const SampleParams& p, int r
 constexpr int kSampleMaxCluster = 8;
 constexpr int kSampleFew = 512;
 constexpr int kSampleList = 2048;    // entries of the list
-constexpr int kSampleCut = 1024;     // and how many make it be cut
+constexpr int kSampleTop = 1024;     // of top_p, about what is listed
+constexpr int kSampleCut = 1024;     // how many make the list be cut
 constexpr int kSampleLong = 96;
 constexpr int kSampleBins = 4096;    // of the first histogram
 constexpr int kSampleFine = 1024;    // of the others
 constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kSampleBatch = 4;      // vectors a thread has on their way
+constexpr int kSamplePerSm = 2;      // CTAs
 
 struct SamplePeer {  // what a CTA tells the others
   unsigned long long a, b;
@@ -288,9 +290,10 @@ struct SampleJob {
   int rank, ctas, round;
   MassScale s;
 
-  // f(values, index of the first, how many) for all of the run, threads in turn.
+  // f(values, index of the first, how many) for all of the run, threads in turn, but for
+  // vectors whose entries are all below `least`.
   template <typename F>
-  __device__ __forceinline__ void each(F&& f) const {
+  __device__ __forceinline__ void each(float least, F&& f) const {
     for (int i0 = threadIdx.x; i0 < nvec; i0 += kSampleBatch * kSampleThreads) {
       uint4 v[kSampleBatch];
 #pragma unroll
@@ -304,7 +307,7 @@ struct SampleJob {
         if (i >= nvec) break;
         float x[kPer];
         Tr::unpack(v[j], x);
-        f(x, first + i * kPer, kPer);
+        if (reaches(x, least)) f(x, first + i * kPer, kPer);
       }
     }
     if ((int)threadIdx.x < head + tail) {
@@ -313,6 +316,12 @@ struct SampleJob {
       x[0] = Tr::to_float(row[SPEC_CHECKED(v, p.V, kSiteSample)]);
       f(x, v, 1);
     }
+  }
+  static __device__ __forceinline__ bool reaches(const float* x, float least) {
+    float most = x[0];
+#pragma unroll
+    for (int e = 1; e < kPer; ++e) most = fmaxf(most, x[e]);
+    return most >= least;
   }
   // The t-th entry outside the vectors.
   __device__ __forceinline__ int edge(int t) const {
@@ -512,15 +521,17 @@ struct SampleJob {
       }
     __syncthreads();
   }
-  // In sh.mass the masses of the sorted list's entries, summed up.
-  __device__ __forceinline__ void list_masses(int n) {
+  // In sh.mass the masses of the sorted list's entries, summed up; `near`: those in single
+  // precision, in units of 2^-kNearBits.
+  __device__ __forceinline__ void list_masses(int n, bool near) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kEach = kSampleList / kSampleThreads;
     unsigned long long m[kEach], mine = 0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int i = threadIdx.x * kEach + e;
-      m[e] = i < n ? entry_mass(s, sh.table, from_order_bits((uint32_t)(sh.list[i] >> 32))) : 0;
+      const float z = i < n ? from_order_bits((uint32_t)(sh.list[i] >> 32)) : -INFINITY;
+      m[e] = near ? units_of({near_mass(s, z), 0.0f}) : entry_mass(s, sh.table, z);
       mine += m[e];
     }
     unsigned long long upto = mine;
@@ -546,7 +557,7 @@ struct SampleJob {
   // if none does.  Weights of the warps' runs first; the warp in whose run the level is passed
   // goes through it again.
   template <typename W, typename L>
-  __device__ __forceinline__ int locate(W&& weight, L&& level_of) {
+  __device__ __forceinline__ int locate(float least, W&& weight, L&& level_of) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w0 = (int)((long long)nvec * warp / kSampleWarps);
     const int w1 = (int)((long long)nvec * (warp + 1) / kSampleWarps);
@@ -557,10 +568,11 @@ struct SampleJob {
     };
     unsigned long long m =
         single(first - head + lane, lane < heads) + single(tail0 + lane, lane < tails);
-#pragma unroll 2
+#pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) {
       float x[kPer];
       Tr::unpack(run[i], x);
+      if (!reaches(x, least)) continue;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) m += weight(x[e], first + i * kPer + e);
     }
@@ -608,8 +620,8 @@ struct SampleJob {
         const int i = i0 + lane;
         float x[kPer];
         unsigned long long sum = 0;
-        if (i < w1) {
-          Tr::unpack(run[i], x);
+        if (i < w1) Tr::unpack(run[i], x);
+        if (i < w1 && reaches(x, least)) {
 #pragma unroll
           for (int e = 0; e < kPer; ++e) sum += weight(x[e], first + i * kPer + e);
         }
@@ -658,7 +670,8 @@ struct SampleJob {
       }
       __syncthreads();
       unsigned long long count = 0, mass = 0;  // above hi
-      each([&](const float* x, int v, int n) {
+      const float low = from_order_bits(k0 << kDrop);  // (NaN: no bound)
+      each(low == low ? low : -INFINITY, [&](const float* x, int v, int n) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
           if (e >= n) continue;
@@ -736,7 +749,7 @@ struct SampleJob {
         __syncthreads();
         if (tid == 0) sh.count = 0;
         __syncthreads();
-        each([&](const float* x, int v, int n) {
+        each(low == low ? low : -INFINITY, [&](const float* x, int v, int n) {
 #pragma unroll
           for (int e = 0; e < kPer; ++e) {
             if (e >= n) continue;
@@ -752,7 +765,7 @@ struct SampleJob {
           if (goal.by_count) {
             i = (int)(goal.want - before) - 1;
           } else {
-            list_masses(n);
+            list_masses(n, false);
             i = first_reaching(sh.mass, n, goal.want - before);
           }
           w2.a = sh.list[::min(i, n - 1)];
@@ -769,7 +782,7 @@ struct SampleJob {
           nth = (nth + m - 1) / m;
         }
         const int v = locate(
-            [&](float y, int at) -> unsigned long long {
+            z, [&](float y, int at) -> unsigned long long {
               return order_bits(y) >> kDrop == b0 && entry_rank(y, at) >= from ? 1 : 0;
             },
             [&](unsigned long long) { return nth - 1; });
@@ -782,7 +795,7 @@ struct SampleJob {
 };
 
 template <typename TIn>
-__global__ void __launch_bounds__(kSampleThreads, 2)
+__global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
     sample_kernel(const __grid_constant__ SampleParams p) {
   using Tr = ElemTraits<TIn>;
   constexpr int kPer = SampleJob<TIn>::kPer;
@@ -792,7 +805,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   const int V = p.V, r = blockIdx.x / ctas;
   if (ctas > 1) cluster_arrive();  // (waited for before the first word to another CTA)
   if (tid == 0) sh.count = 0;
-  if (tid < 256) sh.table.e[tid] = g_mass_table.e[tid];
+  for (int i = tid; i < 256; i += kSampleThreads) sh.table.e[i] = g_mass_table.e[i];
   pdl_wait();
   pdl_launch_dependents();
   SampleJob<TIn> job = {sh, p};
@@ -825,7 +838,15 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   const bool greedy = st.T == 0.0f;
   const bool cut_k = !greedy && st.top_k > 0 && st.top_k < V, cut_p = !greedy && st.top_p < 1.0f;
   const bool few = cut_k && st.top_k <= kSampleFew;
-  const bool estimate = cut_p && !cut_k;  // the row's mass, roughly
+  const bool share = cut_p && !cut_k;  // a share of the whole row's mass
+  const bool listing = st.ok && (few || share);
+  constexpr int kStep = kSampleBatch * kSampleThreads;
+  // With `share` any bound will do: one that leaves about kSampleTop entries of all CTAs, as far
+  // as the first vectors tell.
+  const int target =
+      few ? st.top_k
+          : ::max(1, (int)min((long long)kSampleTop,
+                              (long long)kSampleTop * kStep / ((long long)::max(nvec, kStep) * ctas)));
   if (st.ok && !greedy) {
     if (tid == 32) {  // (in double precision, which is slow: beside the loads)
       const double inv = 1.4426950408889634074 / (double)st.T;
@@ -834,22 +855,21 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     }
     if (tid == 64 && st.min_p > 0.0f) sh.min_off = (double)st.T * log((double)st.min_p);
   }
-  if (estimate) __syncthreads();
 
-  // First pass.
+  // First pass: the list, the largest, and with `share` the row's mass in single precision,
+  // next to the largest of the first vectors.
   bool bad = !st.ok, overflow = false;
   float top = -INFINITY;  // the largest entry of the vectors
-  float edge = tid < edges ? Tr::to_float(job.row[SPEC_CHECKED(job.edge(tid), V, kSiteSample)])
-                           : -INFINITY;
+  const float edge = tid < edges ? Tr::to_float(job.row[SPEC_CHECKED(job.edge(tid), V, kSiteSample)])
+                                 : -INFINITY;
   bad |= edge != edge && !greedy;
   int top_vec = -1;  // greedy: the vector it is in, the first
-  SoftAcc acc;
-  soft_init(acc);
   float nan = 0.0f;  // NaN once an entry is
   uint32_t least_bits = 0;
-  constexpr int kStep = kSampleBatch * kSampleThreads;
-  if (few) {
-    float half[2 * kSampleBatch];
+  MassScale s0 = {};
+  FF sum = {0.0f, 0.0f};
+  if (listing) {
+    float half[2 * kSampleBatch], most = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kSampleBatch; ++j) {
       half[2 * j] = half[2 * j + 1] = -INFINITY;
@@ -857,18 +877,31 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
         float x[kPer];
         Tr::unpack(next[j], x);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) half[2 * j + (e >= kPer / 2)] = fmaxf(half[2 * j + (e >= kPer / 2)], x[e]);
+        for (int e = 0; e < kPer; ++e)
+          half[2 * j + (e >= kPer / 2)] = fmaxf(half[2 * j + (e >= kPer / 2)], x[e]);
       }
+      most = fmaxf(most, fmaxf(half[2 * j], half[2 * j + 1]));
     }
     uint32_t g[2 * kSampleBatch];
 #pragma unroll
     for (int j = 0; j < 2 * kSampleBatch; ++j)
       g[j] = half[j] < -FLT_MAX ? 0 : order_bits(half[j]) >> 16;
-    least_bits = job.kth(g, st.top_k);
+    least_bits = job.kth(g, target);
+    if (share) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      if (lane == 0) sh.mine[warp].x = most;
+      __syncthreads();
+      for (int w = 0; w < kSampleWarps; ++w) most = fmaxf(most, sh.mine[w].x);
+      s0.max = most >= -FLT_MAX && most <= FLT_MAX ? most : 0.0f;
+      s0.inv = sh.inv;
+      s0.low = fmaxf(__fdiv_rn(-200.0f, sh.inv.hi), -FLT_MAX);
+      if (tid < edges) sum.hi = near_mass(s0, edge);
+    }
   }
   // (An entry of -inf has no mass, and is -inf in the result too.)
   float least = fmaxf(from_order_bits(least_bits << 16), -FLT_MAX);
-  if (few && edge >= least) job.append(edge, job.edge(tid));
+  if (listing && edge >= least) job.append(edge, job.edge(tid));
   for (int i0 = 0; i0 < nvec; i0 += kStep) {
     uint4 v[kSampleBatch];
 #pragma unroll
@@ -893,31 +926,32 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
         top = most;
         top_vec = i;
       }
-      if (few) {
-        if (most >= least) {
+      if (listing && most >= least) {
 #pragma unroll
-          for (int e = 0; e < kPer; ++e)
-            if (x[e] >= least) job.append(x[e], job.first + i * kPer + e);
-        }
-      } else if (estimate && most > -1e37f) {  // (what is below has no mass)
-        soft_add_vec<TIn>(acc, v[j], sh.inv.hi);
+        for (int e = 0; e < kPer; ++e)
+          if (x[e] >= least) job.append(x[e], job.first + i * kPer + e);
+      }
+      if (share) {
+        float part[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) part[e & 1] = __fadd_rn(part[e & 1], near_mass(s0, x[e]));
+        sum = ff_add_f(sum, __fadd_rn(part[0], part[1]));
       }
     }
-    if (few && !overflow && i0 + kStep < nvec) {
+    if (listing && !overflow && i0 + kStep < nvec) {
       __syncthreads();
       const int n = sh.count;
       __syncthreads();  // (all have read it before any adds to it)
       if (n > kSampleList) {
         overflow = true;
         least = INFINITY;  // (no more entries)
-      } else if (n > kSampleCut) {
-        least_bits = ::max(least_bits, job.list_kth(st.top_k));
+      } else if (few && n > kSampleCut) {
+        least_bits = ::max(least_bits, job.list_kth(target));
         job.cut_list(least_bits);
         least = fmaxf(from_order_bits(least_bits << 16), -FLT_MAX);
       }
     }
   }
-  if (estimate && edge > -1e37f) soft_add1(acc, edge, sh.inv.hi);
   if constexpr (sizeof(TIn) == 2) {
     const float other = __uint_as_float(__float_as_uint(nan) << 16);
     nan = other != other ? other : nan;
@@ -926,10 +960,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   top = fmaxf(top, edge);
   bad |= !greedy && (nan != nan || top > FLT_MAX);
   bad = __syncthreads_or(bad);
-  if (few && !bad) {
+  if (listing && !bad) {
     // A long list is cut before it is sorted.
     overflow = sh.count > kSampleList;
-    if (!overflow && sh.count > kSampleLong) least_bits = ::max(least_bits, job.list_kth(st.top_k));
+    if (few && !overflow && sh.count > kSampleLong) least_bits = ::max(least_bits, job.list_kth(target));
   }
 
   // What the CTAs have found.
@@ -950,51 +984,37 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
           }
       }
     }
+    if (greedy) best = warp_max_u64(best);
     float m = top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (estimate) {
-        SoftAcc b;
-        b.m = __shfl_xor_sync(0xffffffffu, acc.m, o);
-        b.ms = __shfl_xor_sync(0xffffffffu, acc.ms, o);
-        b.s = __shfl_xor_sync(0xffffffffu, acc.s, o);
-        soft_merge(acc, b);
-      }
-    }
-    if (greedy) best = warp_max_u64(best);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (share) sum = warp_sum_ff(sum);
     __syncthreads();
     if (lane == 0) {
       sh.mine[warp].x = m;
-      sh.mine[warp].y = acc.ms;
-      sh.mine[warp].a = greedy ? best : __float_as_uint(acc.s);
+      sh.mine[warp].a = best;
+      sh.mine[warp].b = ((unsigned long long)__float_as_uint(sum.lo) << 32) | __float_as_uint(sum.hi);
     }
     __syncthreads();
-    if (warp == 0) {
-      const SamplePeer q = sh.mine[lane % kSampleWarps];
-      word.x = q.x;
-      acc.m = acc.ms = lane < kSampleWarps ? q.y : -FLT_MAX;
-      acc.s = lane < kSampleWarps ? __uint_as_float((uint32_t)q.a) : 0.0f;
-      best = q.a;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        word.x = fmaxf(word.x, __shfl_xor_sync(0xffffffffu, word.x, o));
-        SoftAcc b;
-        b.m = b.ms = __shfl_xor_sync(0xffffffffu, acc.ms, o);
-        b.s = __shfl_xor_sync(0xffffffffu, acc.s, o);
-        if (estimate) soft_merge(acc, b);
+    if (tid == 0) {
+      word.x = -INFINITY;
+      FF all = {0.0f, 0.0f};
+      for (int w = 0; w < kSampleWarps; ++w) {
+        const SamplePeer q = sh.mine[w];
+        word.x = fmaxf(word.x, q.x);
+        word.a = q.a > word.a ? q.a : word.a;
+        if (share)
+          all = ff_add(all, {__uint_as_float((uint32_t)q.b), __uint_as_float((uint32_t)(q.b >> 32))});
       }
-      if (greedy) best = warp_max_u64(best);
+      sum = all;
+      word.b = least_bits;
+      word.i = bad;
+      word.j = overflow;
     }
-    word.y = acc.ms;
-    word.a = greedy ? best : __float_as_uint(acc.s);
-    word.b = least_bits;
-    word.i = bad;
-    word.j = overflow;
   }
   if (ctas > 1) cluster_wait();
   const SamplePeer* all = job.exchange(word);
-  float most = -INFINITY, mass_ms = -FLT_MAX, mass_s = 0.0f;
+  float most = -INFINITY;
   unsigned long long limit = 0;
   overflow = false;
   for (int i = 0; i < ctas; ++i) {
@@ -1002,59 +1022,90 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     bad |= all[i].i != 0;
     overflow |= all[i].j != 0;
     least_bits = ::max(least_bits, (uint32_t)all[i].b);
-    mass_ms = fmaxf(mass_ms, all[i].y);
     if (greedy) limit = all[i].a > limit ? all[i].a : limit;
   }
-  if (estimate)
-    for (int i = 0; i < ctas; ++i)
-      mass_s += __uint_as_float((uint32_t)all[i].a) * ex2(all[i].y - mass_ms);
   bad |= !(most >= -FLT_MAX);
-
   job.s.max = most;
   job.s.inv = sh.inv;
   job.s.unit_bits = p.unit_bits;
   job.s.low = fmaxf(__fdiv_rn(-200.0f, sh.inv.hi), -FLT_MAX);
+  // The row's mass next to its largest entry's, in units of 2^-kNearBits; 0: not known.
+  unsigned long long about = 0;
+  if (share && !bad) {
+    SamplePeer w = {};
+    if (tid == 0) {
+      double x = (double)sum.hi + (double)sum.lo;
+      if (s0.max != most)
+        x *= exp2(((double)s0.max - (double)most) * ((double)sh.inv.hi + (double)sh.inv.lo));
+      x *= 1099511627776.0;
+      w.a = x > 0.0 && x < 4611686018427387904.0 ? (unsigned long long)x : 0;
+      w.i = !(x < 4611686018427387904.0);
+    }
+    all = job.exchange(w);
+    bool known = true;
+    for (int i = 0; i < ctas; ++i) {
+      about += all[i].a;
+      known = known && all[i].i == 0;
+    }
+    if (!known) about = 0;
+  }
+
   int token = -1;
   int listed = -1;  // entries of K in the first CTA's list, if it has all of K
   const bool want_kept = p.kept != nullptr, want_token = p.tokens != nullptr;
   float u = want_token ? p.uniforms[r] : 0.0f;
   const bool u_ok = u >= 0.0f && u < 1.0f;
   if (!u_ok) u = 0.0f;
+  // Sums in single precision on both sides: what they are off by in common (the exponential's
+  // mean error is -5e-8) does not matter, and what is left of it is a few parts in 10^9 of
+  // the mass (thousands of entries, 10^-7 each).  Unless the border is some six times as far,
+  // the exact sums decide.
+  const unsigned long long want = mass_part(st.top_p, about, true), doubt = about >> 25;
+  auto border_of = [&](int n, unsigned long long above) -> int {  // in the sorted list, or -1
+    if (n <= 0 || want <= above) return -1;
+    const int i = first_reaching(sh.mass, n, want - above);
+    if (i >= n) return -1;
+    const unsigned long long upto = above + sh.mass[i];
+    const unsigned long long less = above + (i > 0 ? sh.mass[i - 1] : 0);
+    return upto - want > doubt && want - less > doubt ? i : -1;
+  };
   if (bad) {
   } else if (greedy) {
     token = (int)~(uint32_t)limit;
+    if (tid == 0) sh.list[0] = limit;
+    listed = 1;
   } else {
     unsigned long long min_rank = 0;
     if (st.min_p > 0.0f)
       min_rank = (unsigned long long)order_bits(__double2float_ru((double)most + sh.min_off)) << 32;
-    int n = -1;
-    if (few && !overflow) {
-      if (sh.count > kSampleLong || ctas > 1) job.cut_list(least_bits);
-      n = job.gather();
-    }
-    if (n >= 0) {
-      if (rank == 0) {
+    bool done = false;
+    if (listing && !overflow && (few || about != 0)) {
+      if ((few && sh.count > kSampleLong) || ctas > 1) job.cut_list(least_bits);
+      const int n = job.gather();
+      if (n >= 0 && rank == 0) {
         job.sort(n);
-        job.list_masses(n);
-        int kept = min(n, st.top_k);
-        if (cut_p) {
-          const unsigned long long want = mass_part(st.top_p, sh.mass[kept - 1], true);
-          kept = min(first_reaching(sh.mass, kept, want) + 1, kept);
+        job.list_masses(n, share);
+        int kept = few ? min(n, st.top_k) : border_of(n, 0) + 1;
+        if (few && cut_p) {
+          const unsigned long long part = mass_part(st.top_p, sh.mass[kept - 1], true);
+          kept = min(first_reaching(sh.mass, kept, part) + 1, kept);
         }
-        if (min_rank > 0) {
-          int lo = 0, hi = kept;  // entries of min_rank and more
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (sh.list[mid] >= min_rank) lo = mid + 1;
-            else hi = mid;
+        if (kept > 0) {
+          if (min_rank > 0) {
+            int lo = 0, hi = kept;  // entries of min_rank and more
+            while (lo < hi) {
+              const int mid = (lo + hi) >> 1;
+              if (sh.list[mid] >= min_rank) lo = mid + 1;
+              else hi = mid;
+            }
+            kept = lo;
           }
-          kept = lo;
+          done = true;
+          listed = kept;
+          limit = sh.list[kept - 1];
         }
-        listed = kept;
-        limit = sh.list[kept - 1];
-        if (want_token && u_ok) {
+        if (done && want_token && u_ok) {
           const unsigned long long level = mass_part(u, sh.mass[kept - 1], false);
-          token = V;
           if (kept <= 128) {
             // Each entry's mass with those of all lower indices; the lowest that passes.
             if (tid == 0) sh.border = V;
@@ -1072,55 +1123,55 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
             __syncthreads();
             token = sh.border;
           } else {
-            // By bisection of the index; a thread has an entry (kept <= kSampleFew).
-            const int idx = tid < kept ? (int)~(uint32_t)sh.list[tid] : V;
-            const unsigned long long m =
-                tid < kept ? sh.mass[tid] - (tid > 0 ? sh.mass[tid - 1] : 0) : 0;
+            // By bisection of the index.
             int lo = 0, hi = V - 1;
             while (lo < hi) {
               const int mid = lo + (hi - lo) / 2;
-              if (job.block_sums(0, idx <= mid ? m : 0).mass > level) hi = mid;
+              unsigned long long m = 0;
+              for (int i = tid; i < kept; i += kSampleThreads)
+                if ((int)~(uint32_t)sh.list[i] <= mid) m += sh.mass[i] - (i > 0 ? sh.mass[i - 1] : 0);
+              if (job.block_sums(0, m).mass > level) hi = mid;
               else lo = mid + 1;
             }
             token = lo;
           }
         }
       }
-      if (want_kept && ctas > 1) {
+      if (n >= 0 && ctas > 1 && (share || want_kept)) {
         SamplePeer w = {};
         w.a = limit;
-        limit = job.exchange(w)[0].a;
+        w.i = done;
+        all = job.exchange(w);
+        limit = all[0].a;
+        done = all[0].i != 0;
+      } else if (few) {
+        done = n >= 0;
       }
-    } else {
+    }
+    if (!done) {
       const uint32_t top_bits = order_bits(most);
-      if (cut_k)
-        limit = job.border_rank({true, (unsigned long long)st.top_k}, 0, 0, top_bits);
+      if (cut_k) limit = job.border_rank({true, (unsigned long long)st.top_k}, 0, 0, top_bits);
       if (cut_p) {
         // The border is among the entries whose mass is at least their share of what may be
         // left out; where about, a histogram of the distances from the maximum shows.
         uint32_t lo = (uint32_t)(limit >> 32), hi = top_bits;
-        bool cut_p_done = false;
-        if (estimate) {
-          const float range = logf((float)V / ((1.0f - st.top_p) * mass_s)) + 0.001f -
-                              (mass_ms - __fmul_rn(most, job.s.inv.hi)) * kLn2f;
-          const float per =
-              __fmul_rn(__fmul_rn(job.s.inv.hi, kLn2f), (float)kSampleBins / range);
+        unsigned long long found = 0;
+        const float mass = (float)about * exp2f(-(float)kNearBits);
+        const float range = logf((float)V / ((1.0f - st.top_p) * mass)) + 0.001f;
+        const float per = __fmul_rn(__fmul_rn(job.s.inv.hi, kLn2f), (float)kSampleBins / range);
+        if (about != 0 && range > 0.0f && per > 0.0f && per <= FLT_MAX) {
           __syncthreads();
           for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.hist[i] = 0;
           __syncthreads();
-          FF sum = {0.0f, 0.0f};
-          job.each([&](const float* x, int v, int k) {
-            float part = 0.0f;
+          job.each(most - (float)kSampleBins / per * 1.0001f, [&](const float* x, int v, int k) {
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
               if (e < k) {
-                part = __fadd_rn(part, near_mass(job.s, x[e]));
                 const float f = __fmul_rn(__fsub_rn(most, x[e]), per);
                 if (f >= 0.0f && f < (float)kSampleBins) atomicAdd(&sh.hist[(int)f], 1u);
               }
-            sum = ff_add_f(sum, part);
           });
-          const unsigned long long about = job.cluster_sums(0, units_of(sum)).mass;
+          job.sync_all();
           SamplePeer w = {};
           if (rank == 0) {
             // The masses of the bins, taken at their middles, up to what is wanted.
@@ -1150,24 +1201,24 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
               sh.mine[warp].y = squares;
             }
             __syncthreads();
-            float before = upto - mine;
+            float below = upto - mine;
             squares = 0.0f;
             for (int q = 0; q < kSampleWarps; ++q) {
-              if (q < warp) before += sh.mine[q].x;
+              if (q < warp) below += sh.mine[q].x;
               squares += sh.mine[q].y;
             }
             // A bin's entries are off its middle by up to half a width, all alike at worst: four
             // standard deviations of that.
             const float slack = 1.2f * width * sqrtf(squares);
-            const float goal = st.top_p * ((float)about * exp2f(-(float)kNearBits));
+            const float goal = st.top_p * mass;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
-              const float next = before + bin[e];
-              if (before < goal - slack && next >= goal - slack)
+              const float upper = below + bin[e];
+              if (below < goal - slack && upper >= goal - slack)
                 atomicMin(&sh.border, tid * kEach + e);
-              if (before < goal + slack && next >= goal + slack)
+              if (below < goal + slack && upper >= goal + slack)
                 atomicMin(&sh.rest, tid * kEach + e);
-              before = next;
+              below = upper;
             }
             if (tid == 0 && goal - slack <= 0.0f) sh.border = 0;
             __syncthreads();
@@ -1178,78 +1229,146 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
           // (Where exactly the places of the bins' ends lie does not matter.)
           const float z_lo = fmaxf(most - (float)bins[0].j / per, -FLT_MAX);
           const float z_hi = bins[0].i == 0 ? INFINITY : most - (float)bins[0].i / per;
-          unsigned long long rk = 0;
-          if (per > 0.0f && per <= FLT_MAX) {
-            // What is above those bins, and their entries one by one.
+          // bfloat16: the entries between are counted by their bits, of which there are few (a
+          // flat row may have thousands of the same).
+          const uint32_t k0 = order_bits(z_lo) >> 16, k1 = order_bits(fminf(z_hi, most)) >> 16;
+          if (sizeof(TIn) == 2 && k1 - k0 < (uint32_t)kSampleFine) {
             __syncthreads();
-            if (tid == 0) sh.count = 0;
+            for (int i = tid; i < kSampleFine; i += kSampleThreads) sh.hist[i] = 0;
             __syncthreads();
             sum = {0.0f, 0.0f};
-            job.each([&](const float* x, int v, int k) {
+            job.each(z_lo, [&](const float* x, int v, int k) {
               float part = 0.0f;
 #pragma unroll
               for (int e = 0; e < kPer; ++e)
                 if (e < k && x[e] >= z_lo) {
-                  if (x[e] > z_hi) part = __fadd_rn(part, near_mass(job.s, x[e]));
-                  else job.append(x[e], v + e);
+                  const uint32_t key = order_bits(x[e]) >> 16;
+                  if (key > k1) part = __fadd_rn(part, near_mass(job.s, x[e]));
+                  else if (key >= k0) atomicAdd(&sh.hist[key - k0], 1u);
                 }
               sum = ff_add_f(sum, part);
             });
             const unsigned long long above = job.cluster_sums(0, units_of(sum)).mass;
-            const int n = job.gather();
+            // Thread t has two keys, from the top down.
             SamplePeer w2 = {};
-            if (rank == 0 && n > 0) {
-              job.sort(n);
-              job.list_masses(n);
-              // Both sums are right to a few parts in 10^9 (errors of thousands of entries, of
-              // 10^-7 each): if the border is not a hundred times as far, the exact sums decide.
-              const int down = p.unit_bits - kNearBits;
-              const unsigned long long want = mass_part(st.top_p, about, true), doubt = about >> 22;
-              if (want > above) {
-                const int i = first_reaching(sh.mass, n, (want - above) << down);
-                if (i < n) {
-                  const unsigned long long upto = above + (sh.mass[i] >> down);
-                  const unsigned long long less = above + (i > 0 ? sh.mass[i - 1] >> down : 0);
-                  if (upto - want > doubt && want - less > doubt) w2.a = sh.list[i];
+            if (rank == 0) {
+              constexpr int kEach = kSampleFine / kSampleThreads;
+              unsigned long long m[kEach], mine = 0;
+              uint32_t c[kEach];
+#pragma unroll
+              for (int e = 0; e < kEach; ++e) {
+                const int b = (int)(k1 - k0) - (tid * kEach + e);
+                c[e] = 0;
+                m[e] = 0;
+                if (b >= 0) {
+                  for (int i = 0; i < ctas; ++i) c[e] += dsmem_ld_u32(dsmem_map(&sh.hist[b], i));
+                  const uint32_t key = k0 + b;
+                  m[e] = units_of({near_mass(job.s, from_order_bits(
+                                                        (key << 16) | (key & 0x8000u ? 0 : 0xffffu))),
+                                   0.0f});
                 }
+                mine += c[e] * m[e];
               }
+              unsigned long long upto = mine;
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+              }
+              if (lane == 31) sh.red[0][warp] = upto;
+              if (tid == 0) sh.border = -1;
+              __syncthreads();
+              unsigned long long less = above + upto - mine;
+              for (int q = 0; q < warp; ++q) less += sh.red[0][q];
+#pragma unroll
+              for (int e = 0; e < kEach; ++e) {
+                if (less < want && less + c[e] * m[e] >= want) {
+                  const unsigned long long nth = (want - less + m[e] - 1) / m[e];
+                  const unsigned long long over = less + nth * m[e];
+                  if (over - want > doubt && want - (over - m[e]) > doubt) {
+                    sh.border = (int)(k1 - k0) - (tid * kEach + e);
+                    sh.red[1][0] = nth;
+                    sh.rest = nth == c[e];
+                  }
+                }
+                less += c[e] * m[e];
+              }
+              __syncthreads();
+              w2.i = sh.border;
+              w2.a = sh.border >= 0 ? sh.red[1][0] : 0;
+              w2.j = sh.border >= 0 ? sh.rest : 0;
             }
-            rk = job.exchange(w2)[0].a;
-          }
-          if (rk != 0) {
-            limit = rk;
-            cut_p_done = true;
-          } else if (per > 0.0f && per <= FLT_MAX) {
-            lo = order_bits(z_lo);
-            hi = order_bits(fminf(z_hi, most));
+            const SamplePeer* got = job.exchange(w2);
+            const int bin = got[0].i, whole = got[0].j;
+            const unsigned long long nth = got[0].a;
+            if (bin >= 0) {
+              const uint32_t key = k0 + bin;
+              const float z = from_order_bits((key << 16) | (key & 0x8000u ? 0 : 0xffffu));
+              // The lowest indices of those equal to the last.
+              found = whole ? (unsigned long long)order_bits(z) << 32
+                            : entry_rank(z, job.locate(
+                                                z,
+                                                [&](float y, int) -> unsigned long long {
+                                                  return order_bits(y) >> 16 == key ? 1 : 0;
+                                                },
+                                                [&](unsigned long long) { return nth - 1; }));
+            }
           } else {
-            lo = 0;
+          // What is above those bins, and their entries one by one.
+          __syncthreads();
+          if (tid == 0) sh.count = 0;
+          __syncthreads();
+          sum = {0.0f, 0.0f};
+          job.each(z_lo, [&](const float* x, int v, int k) {
+            float part = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              if (e < k && x[e] >= z_lo) {
+                if (x[e] > z_hi) part = __fadd_rn(part, near_mass(job.s, x[e]));
+                else job.append(x[e], v + e);
+              }
+            sum = ff_add_f(sum, part);
+          });
+          const unsigned long long above = job.cluster_sums(0, units_of(sum)).mass;
+          const int n = job.gather();
+          SamplePeer w2 = {};
+          if (rank == 0 && n > 0) {
+            job.sort(n);
+            job.list_masses(n, true);
+            const int i = border_of(n, above);
+            if (i >= 0) w2.a = sh.list[i];
           }
+          found = job.exchange(w2)[0].a;
+          }
+          lo = order_bits(z_lo);
+          hi = order_bits(fminf(z_hi, most));
         }
-        if (!cut_p_done) {
+        if (found == 0) {
           unsigned long long m = 0;
-          job.each([&](const float* x, int v, int k) {
+          const float z = limit > 0 ? from_order_bits((uint32_t)(limit >> 32)) : -INFINITY;
+          job.each(z, [&](const float* x, int v, int k) {
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
               if (e < k && entry_rank(x[e], v + e) >= limit) m += entry_mass(job.s, sh.table, x[e]);
           });
           const unsigned long long total = job.cluster_sums(0, m).mass;
-          const unsigned long long rk =
-              job.border_rank({false, mass_part(st.top_p, total, true)}, limit, lo, hi);
-          limit = rk > limit ? rk : limit;
+          found = job.border_rank({false, mass_part(st.top_p, total, true)}, limit, lo, hi);
         }
+        limit = found > limit ? found : limit;
       }
       limit = min_rank > limit ? min_rank : limit;
-      const float limit_z = limit > 0 ? from_order_bits((uint32_t)(limit >> 32)) : -INFINITY;
-      if (want_token)
+      if (want_token) {
         // (z itself decides but for the entries equal to the last one kept.)
+        const float z_least = limit > 0 ? from_order_bits((uint32_t)(limit >> 32)) : -INFINITY;
         token = job.locate(
+            z_least,
             [&](float z, int v) -> unsigned long long {
-              return z >= limit_z && (z > limit_z || entry_rank(z, v) >= limit)
+              return z >= z_least && (z > z_least || entry_rank(z, v) >= limit)
                          ? draw_mass(job.s, z)
                          : 0;
             },
             [&](unsigned long long total) { return mass_part(u, total, false); });
+      }
     }
     if (!u_ok) token = -1;
   }
@@ -1265,25 +1384,40 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     off = 0xff80;
   }
   __syncthreads();  // (in place: nobody reads the row any more)
+  const bool lines = reinterpret_cast<uintptr_t>(out + job.first) % 16 == 0;
+  if (lines && (bad || (listed >= 0 && (ctas == 1 || greedy)))) {
+    // All of K is in the list: the row is not read again, but for those entries.
+    const TIn all_over = bad ? none : off;
+    uint32_t two;
+    if constexpr (sizeof(TIn) == 4) two = __float_as_uint(all_over);
+    else two = (uint32_t)all_over * 0x10001u;
+    constexpr int kEach = kSampleList / kSampleThreads;
+    TIn keep[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = tid + e * kSampleThreads;
+      if (i < listed) keep[e] = job.row[(int)~(uint32_t)sh.list[i]];
+    }
+    if (ctas > 1) job.sync_all();  // (in place: the one entry is read by all)
+    else __syncthreads();
+    uint4* dst = reinterpret_cast<uint4*>(out + job.first);
+    for (int i = tid; i < nvec; i += kSampleThreads) dst[i] = make_uint4(two, two, two, two);
+    if (tid < edges) out[job.edge(tid)] = all_over;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = tid + e * kSampleThreads;
+      if (i >= listed) break;
+      const int v = (int)~(uint32_t)sh.list[i];
+      const bool mine = v >= job.first - job.head && v < job.first + nvec * kPer + job.tail;
+      if (mine) out[v] = keep[e];
+    }
+    return;
+  }
   auto result = [&](TIn x, int v) -> TIn {
     const float z = Tr::to_float(x);
     return bad ? none : z == z && entry_rank(z, v) >= limit ? x : off;
   };
-  const bool lines = reinterpret_cast<uintptr_t>(out + job.first) % 16 == 0;
-  // K is all in the list: the row is not read again.
-  const bool fill = ctas == 1 && listed >= 0;
-  const uint32_t off2 = sizeof(TIn) == 4 ? 0xff800000u : 0xff80ff80u;
-  if (fill && lines) {
-    uint4* dst = reinterpret_cast<uint4*>(out + job.first);
-    const int kept_at = tid < listed ? (int)~(uint32_t)sh.list[tid] : -1;
-    const TIn x = kept_at >= 0 ? job.row[kept_at] : off;
-    __syncthreads();
-    for (int i = tid; i < nvec; i += kSampleThreads) dst[i] = make_uint4(off2, off2, off2, off2);
-    if (tid < edges) out[job.edge(tid)] = off;
-    __syncthreads();
-    if (kept_at >= 0) out[kept_at] = x;
-    return;
-  }
   for (int i = tid; i < nvec; i += kSampleThreads) {
     const uint4 v = job.run[i];
     TIn x[kPer];

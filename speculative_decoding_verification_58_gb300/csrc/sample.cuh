@@ -74,7 +74,7 @@ struct MassScale {
   float max;
   FF inv;  // log2(e) / T
   int unit_bits;
-  float low;  // distances below it are without mass
+  float floor;
 };
 __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, const MassTable& t,
                                                          float z) {
@@ -107,14 +107,23 @@ __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, con
 }
 
 // The same in single precision, to about 2^-22 of itself, for sums that only have to tell on
-// which side of a border they are, and for the draw.
+// which side of a border they are.  (What is below `floor` has no mass.)
 __device__ __forceinline__ float near_mass(const MassScale& s, float z) {
-  const float d = fmaxf(__fsub_rn(z, s.max), s.low);
-  return z < -FLT_MAX ? 0.0f : ex2(__fmaf_rn(d, s.inv.hi, __fmul_rn(d, s.inv.lo)));
+  const float d = __fsub_rn(fmaxf(z, s.floor), s.max);
+  return ex2(__fmaf_rn(d, s.inv.hi, __fmul_rn(d, s.inv.lo)));
 }
 // In whole units of 2^-32 (the largest entry's 2^32 - 1 then), for the draw.
 __device__ __forceinline__ uint32_t draw_mass(const MassScale& s, float z) {
-  return __float2uint_rn(__fmul_rn(near_mass(s, z), 4294967040.0f));
+  return __float2uint_rn(__fmul_rn(ex2(__fmul_rn(__fsub_rn(z, s.max), s.inv.hi)), 4294967296.0f));
+}
+// A scale next to `max`; false where the temperature is too high for `floor` to leave out
+// entries of -inf.
+__device__ __forceinline__ bool mass_scale(MassScale& s, float max, FF inv, int unit_bits) {
+  s.max = max;
+  s.inv = inv;
+  s.unit_bits = unit_bits;
+  s.floor = __fsub_rn(max, __fdiv_rn(200.0f, inv.hi));
+  return s.floor >= -FLT_MAX;
 }
 
 // NaN in either half of the result once an entry of the vectors so far is: maxima that keep it.
@@ -199,8 +208,7 @@ constexpr int kSampleMaxCluster = 8;
 constexpr int kSampleFew = 512;
 constexpr int kSampleList = 2048;    // entries of the list
 constexpr int kSampleTop = 1024;     // of top_p, about what is listed
-constexpr int kSampleCut = 1024;     // how many make the list be cut
-constexpr int kSampleLong = 96;
+constexpr int kSampleLong = 256;     // what is not cut before it is sorted
 constexpr int kSampleBins = 4096;    // of the first histogram
 constexpr int kSampleFine = 1024;    // of the others
 constexpr int kSampleWarps = kSampleThreads / 32;
@@ -225,10 +233,11 @@ struct SampleShared {
   SamplePeer peer[2][kSampleMaxCluster];
   unsigned long long red[2][kSampleWarps];
   SamplePeer mine[kSampleWarps];
-  uint32_t digit[256];
+  uint32_t digit[kSampleWarps];
+  int counts[17];
   FF inv;          // log2(e) / T
   double min_off;  // T log(min_p)
-  int count, kth, rest, border;
+  int count, rest, border;
 };
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -323,6 +332,13 @@ struct SampleJob {
     for (int e = 1; e < kPer; ++e) most = fmaxf(most, x[e]);
     return most >= least;
   }
+  // Of CTA i's shared memory.
+  __device__ __forceinline__ uint32_t peek(const uint32_t* x, int i) const {
+    return ctas == 1 ? *x : dsmem_ld_u32(dsmem_map(x, i));
+  }
+  __device__ __forceinline__ unsigned long long peek(const unsigned long long* x, int i) const {
+    return ctas == 1 ? *x : dsmem_ld_u64(dsmem_map(x, i));
+  }
   // The t-th entry outside the vectors.
   __device__ __forceinline__ int edge(int t) const {
     return t < head ? first - head + t : first + nvec * kPer + t - head;
@@ -393,54 +409,39 @@ struct SampleJob {
   }
 
   // The largest 16-bit number that at least k of the threads' kN numbers reach, 0 if there are
-  // fewer (but for zeros): by their upper 8 bits, then the lower ones.
+  // fewer (but for zeros).  Each warp finds the one that its share of the k reach among its
+  // own; the result is between the least and the largest of those, and the CTA's counts
+  // are needed only for the bits in which they differ.
   template <int kN>
   __device__ __forceinline__ uint32_t kth(const uint32_t (&g)[kN], int k) {
-    const int tid = threadIdx.x;
-    uint32_t upper = 0;
-    int rest = k;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int share = (k + kSampleWarps - 1) / kSampleWarps;
+    auto count = [&](uint32_t c) -> int {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) n += g[i] >= c ? 1 : 0;
+      return __reduce_add_sync(0xffffffffu, n);
+    };
+    uint32_t mine = 0;
 #pragma unroll 1
-    for (int level = 0; level < 2; ++level) {
+    for (int b = 15; b >= 0; --b)
+      if (count(mine | (1u << b)) >= share) mine |= 1u << b;
+    __syncthreads();
+    if (lane == 0) sh.digit[warp] = mine;
+    if (threadIdx.x < 17) sh.counts[threadIdx.x] = 0;
+    __syncthreads();
+    const uint32_t least = __reduce_min_sync(0xffffffffu, sh.digit[lane % kSampleWarps]);
+    // (At least k reach `least`: every warp has its share.)
+    uint32_t at = least, over = __reduce_max_sync(0xffffffffu, sh.digit[lane % kSampleWarps]) + 1;
+    for (int round = 0; over - at > 1; ++round) {
+      const uint32_t mid = (at + over) >> 1;
+      const int n = count(mid);
+      if (lane == 0 && n) atomicAdd(&sh.counts[round], n);
       __syncthreads();
-      if (tid < 256) sh.digit[tid] = 0;
-      if (tid == 0) sh.kth = -1;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (level == 0 ? g[i] != 0 : g[i] >> 8 == upper)
-          atomicAdd(&sh.digit[level == 0 ? g[i] >> 8 : g[i] & 255], 1u);
-      __syncthreads();
-      if (tid < 32) {
-        // From the top: lane l has the bins 255 - 8 l down.
-        int n[8], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine += n[i] = (int)sh.digit[255 - 8 * tid - i];
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, upto, o);
-          if (tid >= o) upto += x;
-        }
-        int before = upto - mine;
-        if (before < rest && upto >= rest) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (before < rest && before + n[i] >= rest) {
-              sh.kth = 255 - 8 * tid - i;
-              sh.rest = rest - before;
-            }
-            before += n[i];
-          }
-        }
-      }
-      __syncthreads();
-      if (sh.kth < 0) return 0;
-      if (level == 0) {
-        upper = (uint32_t)sh.kth;
-        rest = sh.rest;
-      }
+      if (sh.counts[round] >= k) at = mid;
+      else over = mid;
     }
-    return (upper << 8) | (uint32_t)sh.kth;
+    return at;
   }
 
   __device__ __forceinline__ void append(float z, int v) {
@@ -701,8 +702,8 @@ struct SampleJob {
           const int b = kSampleFine - 1 - (tid * kEach + e);
           n[e] = 0;
           for (int i = 0; i < ctas; ++i)
-            n[e] += goal.by_count ? dsmem_ld_u32(dsmem_map(&sh.hist[b], i))
-                                  : dsmem_ld_u64(dsmem_map(&sh.fine[b], i));
+            n[e] += goal.by_count ? peek(&sh.hist[b], i)
+                                  : peek(&sh.fine[b], i);
           mine += n[e];
         }
         unsigned long long upto = mine;
@@ -729,7 +730,7 @@ struct SampleJob {
           w.i = sh.border;
           w.a = sh.red[1][0];
           int c = 0;
-          for (int i = 0; i < ctas; ++i) c += (int)dsmem_ld_u32(dsmem_map(&sh.hist[sh.border], i));
+          for (int i = 0; i < ctas; ++i) c += (int)peek(&sh.hist[sh.border], i);
           w.j = c;
         }
       }
@@ -824,7 +825,8 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   job.run = reinterpret_cast<const uint4*>(job.row + job.first);
   const int nvec = job.nvec, edges = job.head + job.tail;
 
-  // The first vectors are on their way while the settings are read.
+  // The sample, 512 bytes here and there of the whole run, and the first vectors are on
+  // their way while the settings are read.
   uint4 next[kSampleBatch];
   auto load = [&](int i0) {
 #pragma unroll
@@ -833,20 +835,29 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
       if (i < nvec) next[j] = job.run[i];
     }
   };
-  load(0);
+  // (A run shorter than the sample is all of it.)
+  constexpr int kPieces = kSampleBatch * kSampleWarps;
+  auto sample_at = [&](int j) -> int {
+    const int piece = j * kSampleWarps + warp;
+    const int at = nvec <= kPieces * 32 ? piece * 32
+                                        : (int)((long long)(nvec - 32) * piece / (kPieces - 1));
+    return at + lane;
+  };
   const RowSettings st = row_settings(p, r);
   const bool greedy = st.T == 0.0f;
   const bool cut_k = !greedy && st.top_k > 0 && st.top_k < V, cut_p = !greedy && st.top_p < 1.0f;
   const bool few = cut_k && st.top_k <= kSampleFew;
   const bool share = cut_p && !cut_k;  // a share of the whole row's mass
   const bool listing = st.ok && (few || share);
+  // How many of the sample's entries the list's bound is to leave: with `share` any bound will
+  // do, and one that leaves about kSampleTop entries of all CTAs is taken; top_k's has to
+  // leave top_k, so that what the sample should have of them is taken five standard
+  // deviations and some more (if that does not do, all entries are counted).
   constexpr int kStep = kSampleBatch * kSampleThreads;
-  // With `share` any bound will do: one that leaves about kSampleTop entries of all CTAs, as far
-  // as the first vectors tell.
-  const int target =
-      few ? st.top_k
-          : ::max(1, (int)min((long long)kSampleTop,
-                              (long long)kSampleTop * kStep / ((long long)::max(nvec, kStep) * ctas)));
+  const float part_of = fminf(1.0f, (float)kStep / (float)::max(nvec, 1));
+  const float mean = (float)(few ? st.top_k : kSampleTop) * part_of / (float)ctas;
+  const int target = part_of == 1.0f && ctas == 1 ? (few ? st.top_k : kSampleTop)
+                                                   : (int)(mean + (few ? 5.0f * sqrtf(mean) + 8.0f : 1.0f));
   if (st.ok && !greedy) {
     if (tid == 32) {  // (in double precision, which is slow: beside the loads)
       const double inv = 1.4426950408889634074 / (double)st.T;
@@ -857,7 +868,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   }
 
   // First pass: the list, the largest, and with `share` the row's mass in single precision,
-  // next to the largest of the first vectors.
+  // next to the largest of the sample.
   bool bad = !st.ok, overflow = false;
   float top = -INFINITY;  // the largest entry of the vectors
   const float edge = tid < edges ? Tr::to_float(job.row[SPEC_CHECKED(job.edge(tid), V, kSiteSample)])
@@ -867,13 +878,20 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   float nan = 0.0f;  // NaN once an entry is
   uint32_t least_bits = 0;
   MassScale s0 = {};
+  bool scaled = true;
+  if (!listing) load(0);
   FF sum = {0.0f, 0.0f};
   if (listing) {
     float half[2 * kSampleBatch], most = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kSampleBatch; ++j) {
+      const int i = sample_at(j);
+      if (i < nvec) next[j] = job.run[i];
+    }
+#pragma unroll
+    for (int j = 0; j < kSampleBatch; ++j) {
       half[2 * j] = half[2 * j + 1] = -INFINITY;
-      if (j * kSampleThreads + tid < nvec) {
+      if (sample_at(j) < nvec) {
         float x[kPer];
         Tr::unpack(next[j], x);
 #pragma unroll
@@ -882,6 +900,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
       }
       most = fmaxf(most, fmaxf(half[2 * j], half[2 * j + 1]));
     }
+    load(0);
     uint32_t g[2 * kSampleBatch];
 #pragma unroll
     for (int j = 0; j < 2 * kSampleBatch; ++j)
@@ -893,9 +912,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
       if (lane == 0) sh.mine[warp].x = most;
       __syncthreads();
       for (int w = 0; w < kSampleWarps; ++w) most = fmaxf(most, sh.mine[w].x);
-      s0.max = most >= -FLT_MAX && most <= FLT_MAX ? most : 0.0f;
-      s0.inv = sh.inv;
-      s0.low = fmaxf(__fdiv_rn(-200.0f, sh.inv.hi), -FLT_MAX);
+      scaled = mass_scale(s0, most >= -FLT_MAX && most <= FLT_MAX ? most : 0.0f, sh.inv, p.unit_bits);
       if (tid < edges) sum.hi = near_mass(s0, edge);
     }
   }
@@ -938,19 +955,6 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
         sum = ff_add_f(sum, __fadd_rn(part[0], part[1]));
       }
     }
-    if (listing && !overflow && i0 + kStep < nvec) {
-      __syncthreads();
-      const int n = sh.count;
-      __syncthreads();  // (all have read it before any adds to it)
-      if (n > kSampleList) {
-        overflow = true;
-        least = INFINITY;  // (no more entries)
-      } else if (few && n > kSampleCut) {
-        least_bits = ::max(least_bits, job.list_kth(target));
-        job.cut_list(least_bits);
-        least = fmaxf(from_order_bits(least_bits << 16), -FLT_MAX);
-      }
-    }
   }
   if constexpr (sizeof(TIn) == 2) {
     const float other = __uint_as_float(__float_as_uint(nan) << 16);
@@ -963,7 +967,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   if (listing && !bad) {
     // A long list is cut before it is sorted.
     overflow = sh.count > kSampleList;
-    if (few && !overflow && sh.count > kSampleLong) least_bits = ::max(least_bits, job.list_kth(target));
+    if (few && !overflow && sh.count > kSampleLong) least_bits = ::max(least_bits, job.list_kth(st.top_k));
   }
 
   // What the CTAs have found.
@@ -1025,10 +1029,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
     if (greedy) limit = all[i].a > limit ? all[i].a : limit;
   }
   bad |= !(most >= -FLT_MAX);
-  job.s.max = most;
-  job.s.inv = sh.inv;
-  job.s.unit_bits = p.unit_bits;
-  job.s.low = fmaxf(__fdiv_rn(-200.0f, sh.inv.hi), -FLT_MAX);
+  scaled &= mass_scale(job.s, most, sh.inv, p.unit_bits);
   // The row's mass next to its largest entry's, in units of 2^-kNearBits; 0: not known.
   unsigned long long about = 0;
   if (share && !bad) {
@@ -1039,7 +1040,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
         x *= exp2(((double)s0.max - (double)most) * ((double)sh.inv.hi + (double)sh.inv.lo));
       x *= 1099511627776.0;
       w.a = x > 0.0 && x < 4611686018427387904.0 ? (unsigned long long)x : 0;
-      w.i = !(x < 4611686018427387904.0);
+      w.i = !(x < 4611686018427387904.0) || !scaled;
     }
     all = job.exchange(w);
     bool known = true;
@@ -1082,7 +1083,15 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
     if (listing && !overflow && (few || about != 0)) {
       if ((few && sh.count > kSampleLong) || ctas > 1) job.cut_list(least_bits);
       const int n = job.gather();
-      if (n >= 0 && rank == 0) {
+      bool enough = true;  // of a share's mass, to hold the border
+      if (n >= 0 && rank == 0 && share) {
+        unsigned long long m = 0;
+        for (int i = tid; i < n; i += kSampleThreads)
+          m += units_of({near_mass(job.s, from_order_bits((uint32_t)(sh.list[i] >> 32))), 0.0f});
+        enough = job.block_sums(0, m).mass >= want;
+      }
+      if (few && n < min(st.top_k, V) && !(n >= 0 && least_bits == 0)) enough = false;
+      if (n >= 0 && rank == 0 && enough) {
         job.sort(n);
         job.list_masses(n, share);
         int kept = few ? min(n, st.top_k) : border_of(n, 0) + 1;
@@ -1145,7 +1154,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
         limit = all[0].a;
         done = all[0].i != 0;
       } else if (few) {
-        done = n >= 0;
+        done = n >= 0 && enough;
       }
     }
     if (!done) {
@@ -1165,11 +1174,10 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
           __syncthreads();
           job.each(most - (float)kSampleBins / per * 1.0001f, [&](const float* x, int v, int k) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e)
-              if (e < k) {
-                const float f = __fmul_rn(__fsub_rn(most, x[e]), per);
-                if (f >= 0.0f && f < (float)kSampleBins) atomicAdd(&sh.hist[(int)f], 1u);
-              }
+            for (int e = 0; e < kPer; ++e) {
+              const float f = __fmul_rn(__fsub_rn(most, x[e]), per);
+              if ((e < k) & (f >= 0.0f) & (f < (float)kSampleBins)) atomicAdd(&sh.hist[(int)f], 1u);
+            }
           });
           job.sync_all();
           SamplePeer w = {};
@@ -1182,7 +1190,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
             for (int e = 0; e < kEach; ++e) {
               const int b = tid * kEach + e;
               uint32_t c = 0;
-              for (int i = 0; i < ctas; ++i) c += dsmem_ld_u32(dsmem_map(&sh.hist[b], i));
+              for (int i = 0; i < ctas; ++i) c += job.peek(&sh.hist[b], i);
               bin[e] = (float)c * ex2(__fmul_rn(-((float)b + 0.5f) * width, kLog2e));
               mine += bin[e];
               squares = fmaf(bin[e], bin[e], squares);
@@ -1240,12 +1248,12 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
             job.each(z_lo, [&](const float* x, int v, int k) {
               float part = 0.0f;
 #pragma unroll
-              for (int e = 0; e < kPer; ++e)
-                if (e < k && x[e] >= z_lo) {
-                  const uint32_t key = order_bits(x[e]) >> 16;
-                  if (key > k1) part = __fadd_rn(part, near_mass(job.s, x[e]));
-                  else if (key >= k0) atomicAdd(&sh.hist[key - k0], 1u);
-                }
+              for (int e = 0; e < kPer; ++e) {
+                const uint32_t key = order_bits(x[e]) >> 16;
+                const float m = near_mass(job.s, x[e]);
+                part = __fadd_rn(part, (e < k) & (key > k1) ? m : 0.0f);
+                if ((e < k) & (key >= k0) & (key <= k1)) atomicAdd(&sh.hist[key - k0], 1u);
+              }
               sum = ff_add_f(sum, part);
             });
             const unsigned long long above = job.cluster_sums(0, units_of(sum)).mass;
@@ -1261,7 +1269,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
                 c[e] = 0;
                 m[e] = 0;
                 if (b >= 0) {
-                  for (int i = 0; i < ctas; ++i) c[e] += dsmem_ld_u32(dsmem_map(&sh.hist[b], i));
+                  for (int i = 0; i < ctas; ++i) c[e] += job.peek(&sh.hist[b], i);
                   const uint32_t key = k0 + b;
                   m[e] = units_of({near_mass(job.s, from_order_bits(
                                                         (key << 16) | (key & 0x8000u ? 0 : 0xffffu))),
@@ -1322,11 +1330,11 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
           job.each(z_lo, [&](const float* x, int v, int k) {
             float part = 0.0f;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e)
-              if (e < k && x[e] >= z_lo) {
-                if (x[e] > z_hi) part = __fadd_rn(part, near_mass(job.s, x[e]));
-                else job.append(x[e], v + e);
-              }
+            for (int e = 0; e < kPer; ++e) {
+              const float m = near_mass(job.s, x[e]);
+              part = __fadd_rn(part, (e < k) & (x[e] > z_hi) ? m : 0.0f);
+              if ((e < k) & (x[e] >= z_lo) & (x[e] <= z_hi)) job.append(x[e], v + e);
+            }
             sum = ff_add_f(sum, part);
           });
           const unsigned long long above = job.cluster_sums(0, units_of(sum)).mass;
@@ -1360,12 +1368,12 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
       if (want_token) {
         // (z itself decides but for the entries equal to the last one kept.)
         const float z_least = limit > 0 ? from_order_bits((uint32_t)(limit >> 32)) : -INFINITY;
+        const uint32_t last = ~(uint32_t)limit;
         token = job.locate(
             z_least,
             [&](float z, int v) -> unsigned long long {
-              return z >= z_least && (z > z_least || entry_rank(z, v) >= limit)
-                         ? draw_mass(job.s, z)
-                         : 0;
+              const uint32_t m = draw_mass(job.s, z);
+              return (z > z_least) | ((z == z_least) & ((uint32_t)v <= last)) ? m : 0;
             },
             [&](unsigned long long total) { return mass_part(u, total, false); });
       }

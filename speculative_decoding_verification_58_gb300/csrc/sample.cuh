@@ -230,6 +230,7 @@ struct SampleShared {
     unsigned long long fine[kSampleFine];
   };
   MassTable table;
+  unsigned long long sums[256];  // of a draw from the list
   SamplePeer peer[2][kSampleMaxCluster];
   unsigned long long red[2][kSampleWarps];
   SamplePeer mine[kSampleWarps];
@@ -501,10 +502,33 @@ struct SampleJob {
     sync_all();
     return total;
   }
-  // Sorts the list (descending); the first CTA alone.
+  // Sorts the list (descending); the first CTA alone.  A short one by counting for each entry
+  // those before it, several threads to an entry (138 entries 0.6 us, by exchanges 3).
   __device__ __forceinline__ void sort(int n) {
     int size = 32;
     while (size < n) size *= 2;
+    if (size <= 256) {
+      const int i = threadIdx.x & (size - 1), part = threadIdx.x / size;
+      const int parts = kSampleThreads / size, each = (n + parts - 1) / parts;
+      const unsigned long long x = i < n ? sh.list[i] : 0;
+      int* place = reinterpret_cast<int*>(sh.mass);
+      __syncthreads();
+      if ((int)threadIdx.x < n) place[threadIdx.x] = 0;
+      __syncthreads();
+      int before = 0;
+      if (i < n)
+        for (int j = part * each; j < min(n, (part + 1) * each); ++j) before += sh.list[j] > x ? 1 : 0;
+      if (before > 0) atomicAdd(&place[i], before);
+      __syncthreads();
+      if ((int)threadIdx.x < n) {
+        const int to = place[threadIdx.x];
+        before = to;
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < n) sh.list[before] = x;
+      __syncthreads();
+      return;
+    }
     for (int i = n + threadIdx.x; i < size; i += kSampleThreads) sh.list[i] = 0;
     __syncthreads();
     for (int k = 2; k <= size; k *= 2)
@@ -554,93 +578,156 @@ struct SampleJob {
     __syncthreads();
   }
 
+  // The lowest index among the list's first n entries whose mass with those of all lower ones
+  // exceeds the level; the first CTA alone.
+  __device__ __forceinline__ int draw_listed(int n, unsigned long long level) {
+    const int tid = threadIdx.x;
+    if (tid == 0) sh.border = p.V;
+    __syncthreads();
+    int size = 32;
+    while (size < n) size *= 2;
+    if (size <= 256) {
+      // Each entry's sum, several threads to an entry.
+      const int i = tid & (size - 1), part = tid / size;
+      const int parts = kSampleThreads / size, each = (n + parts - 1) / parts;
+      if (tid < n) sh.sums[tid] = 0;
+      __syncthreads();
+      const uint32_t mine = i < n ? (uint32_t)sh.list[i] : 0xffffffffu;  // (~index)
+      unsigned long long m = 0;
+      if (i < n) {
+        const int j0 = part * each, j1 = min(n, j0 + each);
+        unsigned long long last = j0 > 0 && j0 < j1 ? sh.mass[j0 - 1] : 0;
+        for (int j = j0; j < j1; ++j) {
+          const unsigned long long upto = sh.mass[j];
+          if ((uint32_t)sh.list[j] >= mine) m += upto - last;
+          last = upto;
+        }
+      }
+      if (m != 0) atomicAdd(&sh.sums[i], m);
+      __syncthreads();
+      if (tid < n && sh.sums[tid] > level) atomicMin(&sh.border, (int)~(uint32_t)sh.list[tid]);
+      __syncthreads();
+      return sh.border;
+    }
+    // By bisection of the index.
+    int lo = 0, hi = p.V - 1;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      unsigned long long m = 0;
+      for (int i = tid; i < n; i += kSampleThreads)
+        if ((int)~(uint32_t)sh.list[i] <= mid) m += sh.mass[i] - (i > 0 ? sh.mass[i - 1] : 0);
+      if (block_sums(0, m).mass > level) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  }
+
   // The first index, ascending, whose weight with all lower ones' exceeds `level(total)`; -1
   // if none does.  Weights of the warps' runs first; the warp in whose run the level is passed
   // goes through it again.
+  // Then the CTA in whose run the level is passed goes through that warp's run again, shared
+  // out among its warps, and one of these through its share (one warp through all of the
+  // run, a load after the other, took 17 us of a row of 151936).
   template <typename W, typename L>
   __device__ __forceinline__ int locate(float least, W&& weight, L&& level_of) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w0 = (int)((long long)nvec * warp / kSampleWarps);
-    const int w1 = (int)((long long)nvec * (warp + 1) / kSampleWarps);
-    const int heads = warp == 0 ? head : 0, tails = warp == kSampleWarps - 1 ? tail : 0;
     const int tail0 = first + nvec * kPer;
     auto single = [&](int v, bool here) -> unsigned long long {
       return here ? weight(Tr::to_float(row[v]), v) : 0;
     };
-    unsigned long long m =
-        single(first - head + lane, lane < heads) + single(tail0 + lane, lane < tails);
-#pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) {
+    auto vector_weight = [&](int i) -> unsigned long long {
       float x[kPer];
       Tr::unpack(run[i], x);
-      if (!reaches(x, least)) continue;
+      unsigned long long m = 0;
+      if (reaches(x, least)) {
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) m += weight(x[e], first + i * kPer + e);
-    }
-    m = warp_sum_u64(m);
-    __syncthreads();
-    if (lane == 0) sh.red[0][warp] = m;
-    if (threadIdx.x == 0) sh.border = -1;
-    __syncthreads();
+        for (int e = 0; e < kPer; ++e) m += weight(x[e], first + i * kPer + e);
+      }
+      return m;
+    };
+    // Vectors from .. to - 1, the entries before all and behind all: of this warp.
+    int from = (int)((long long)nvec * warp / kSampleWarps);
+    int to = (int)((long long)nvec * (warp + 1) / kSampleWarps);
+    int heads = warp == 0 ? head : 0, tails = warp == kSampleWarps - 1 ? tail : 0;
+    // The warps' sums, and for all threads what is before each.
+    auto sums = [&]() -> unsigned long long {
+      unsigned long long m =
+          single(first - head + lane, lane < heads) + single(tail0 + lane, lane < tails);
+#pragma unroll 4
+      for (int i = from + lane; i < to; i += 32) m += vector_weight(i);
+      m = warp_sum_u64(m);
+      __syncthreads();
+      if (lane == 0) sh.red[0][warp] = m;
+      if (threadIdx.x == 0) sh.border = -1;
+      __syncthreads();
+      unsigned long long all = 0;
+      for (int i = 0; i < kSampleWarps; ++i) all += sh.red[0][i];
+      return all;
+    };
     SamplePeer w = {};
-    unsigned long long mine = 0, upto = 0;
-    for (int i = 0; i < kSampleWarps; ++i) {
-      if (i < warp) upto += sh.red[0][i];
-      mine += sh.red[0][i];
-    }
-    w.a = mine;
+    w.a = sums();
     const SamplePeer* all = exchange(w);
-    unsigned long long total = 0;
+    unsigned long long total = 0, upto = 0;
     for (int i = 0; i < ctas; ++i) {
       if (i < rank) upto += all[i].a;
       total += all[i].a;
     }
     const unsigned long long level = level_of(total);
-    if (upto <= level && level < upto + m) {
-      int found = -1;
-      auto look = [&](unsigned long long x, auto&& finish) {  // the lanes' weights, in order
-        unsigned long long sum = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long y = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += y;
-        }
-        const uint32_t over = __ballot_sync(0xffffffffu, upto + sum > level);
-        if (over != 0) {
-          const int l = __ffs(over) - 1;
-          if (lane == l) found = finish(upto + sum - x);
-          found = __shfl_sync(0xffffffffu, found, l);
-        }
-        upto += __shfl_sync(0xffffffffu, sum, 31);
+    if (upto <= level && level < upto + w.a) {
+      auto pick = [&]() -> int {  // the warp in whose part the level is passed
+        int q = 0;
+        while (q < kSampleWarps - 1 && upto + sh.red[0][q] <= level) upto += sh.red[0][q++];
+        return q;
       };
-      if (heads > 0) {
-        const int v = first - head + lane;
-        look(single(v, lane < heads), [&](unsigned long long) { return v; });
-      }
-      for (int i0 = w0; i0 < w1 && found < 0; i0 += 32) {
-        const int i = i0 + lane;
-        float x[kPer];
-        unsigned long long sum = 0;
-        if (i < w1) Tr::unpack(run[i], x);
-        if (i < w1 && reaches(x, least)) {
+      const int q = pick();
+      const int a = (int)((long long)nvec * q / kSampleWarps);
+      const int n = (int)((long long)nvec * (q + 1) / kSampleWarps) - a;
+      from = a + n * warp / kSampleWarps;
+      to = a + n * (warp + 1) / kSampleWarps;
+      heads = q == 0 && warp == 0 ? head : 0;
+      tails = q == kSampleWarps - 1 && warp == kSampleWarps - 1 ? tail : 0;
+      sums();
+      if (pick() == warp) {
+        int found = -1;
+        auto look = [&](unsigned long long x, auto&& finish) {  // the lanes' weights, in order
+          unsigned long long sum = x;
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) sum += weight(x[e], first + i * kPer + e);
-        }
-        look(sum, [&](unsigned long long c) {
-          int v = first + i * kPer;
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            c += weight(x[e], first + i * kPer + e);
-            if (c <= level) ++v;
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
           }
-          return v;
-        });
+          const uint32_t over = __ballot_sync(0xffffffffu, upto + sum > level);
+          if (over != 0) {
+            const int l = __ffs(over) - 1;
+            if (lane == l) found = finish(upto + sum - x);
+            found = __shfl_sync(0xffffffffu, found, l);
+          }
+          upto += __shfl_sync(0xffffffffu, sum, 31);
+        };
+        if (heads > 0) {
+          const int v = first - head + lane;
+          look(single(v, lane < heads), [&](unsigned long long) { return v; });
+        }
+        for (int i0 = from; i0 < to && found < 0; i0 += 32) {
+          const int i = i0 + lane;
+          look(i < to ? vector_weight(i) : 0, [&](unsigned long long c) {
+            float x[kPer];
+            Tr::unpack(run[i], x);
+            int v = first + i * kPer;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+              c += weight(x[e], first + i * kPer + e);
+              if (c <= level) ++v;
+            }
+            return v;
+          });
+        }
+        if (tails > 0 && found < 0) {
+          const int v = tail0 + lane;
+          look(single(v, lane < tails), [&](unsigned long long) { return v; });
+        }
+        if (lane == 0) sh.border = found;
       }
-      if (tails > 0 && found < 0) {
-        const int v = tail0 + lane;
-        look(single(v, lane < tails), [&](unsigned long long) { return v; });
-      }
-      if (lane == 0) sh.border = found;
     }
     __syncthreads();
     SamplePeer w2 = {};
@@ -1115,35 +1202,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
         }
         if (done && want_token && u_ok) {
           const unsigned long long level = mass_part(u, sh.mass[kept - 1], false);
-          if (kept <= 128) {
-            // Each entry's mass with those of all lower indices; the lowest that passes.
-            if (tid == 0) sh.border = V;
-            __syncthreads();
-            if (tid < kept) {
-              const uint32_t mine = (uint32_t)sh.list[tid];
-              unsigned long long m = 0, last = 0;
-              for (int i = 0; i < kept; ++i) {
-                const unsigned long long upto = sh.mass[i];
-                if ((uint32_t)sh.list[i] >= mine) m += upto - last;  // (~index)
-                last = upto;
-              }
-              if (m > level) atomicMin(&sh.border, (int)~mine);
-            }
-            __syncthreads();
-            token = sh.border;
-          } else {
-            // By bisection of the index.
-            int lo = 0, hi = V - 1;
-            while (lo < hi) {
-              const int mid = lo + (hi - lo) / 2;
-              unsigned long long m = 0;
-              for (int i = tid; i < kept; i += kSampleThreads)
-                if ((int)~(uint32_t)sh.list[i] <= mid) m += sh.mass[i] - (i > 0 ? sh.mass[i - 1] : 0);
-              if (job.block_sums(0, m).mass > level) hi = mid;
-              else lo = mid + 1;
-            }
-            token = lo;
-          }
+          token = job.draw_listed(kept, level);
         }
       }
       if (n >= 0 && ctas > 1 && (share || want_kept)) {

@@ -74,7 +74,8 @@ struct AtUnit {
 
 struct AtControl {
   uint64_t full[10], empty[10];
-  uint64_t s_full[2], p_ready[2], o_full[2], q_full[2], q_empty[2];
+  uint64_t s_full[2][2];  // of a stream; units of few rows have two sets of scores in turn
+  uint64_t p_ready[2], pv_done[2], o_full[2], q_full[2], q_empty[2];
   uint64_t u_full[kAtUnits], u_empty[kAtUnits];
   uint64_t meet;  // of both warpgroups
   AtUnit unit[kAtUnits];
@@ -128,6 +129,7 @@ struct AtParams {
   float2* stats;   // [2 kAtMaxCtas, slot_rows]: (m, l)
   float* parts;    // [2 kAtMaxCtas, slot_rows, D]
   int main_ctas;
+  int join_share;  // CTAs of the join per CTA of the first kernel
 };
 struct AtMaps {
   CUtensorMap k, v;
@@ -144,7 +146,8 @@ __device__ __forceinline__ int at_token(const AtParams& a, int row) {
 }
 // Tiles of the unit of rows r0 .. and what one costs: two streams' products or one's.
 struct AtSpan {
-  int rows, lo, hi, tile0, tiles, cost;
+  int rows, lo, hi, tile0, tiles;
+  int shift;  // log2 of a tile's cost
 };
 __device__ __forceinline__ AtSpan at_unit_span(const AtParams& a, int n, int len, int r0) {
   AtSpan s;
@@ -152,7 +155,7 @@ __device__ __forceinline__ AtSpan at_unit_span(const AtParams& a, int n, int len
   at_span(a.p, n, len, at_token(a, r0), at_token(a, r0 + s.rows - 1), s.lo, s.hi);
   s.tile0 = s.lo / kAtTile;
   s.tiles = s.hi > s.lo ? (s.hi + kAtTile - 1) / kAtTile - s.tile0 : 0;
-  s.cost = s.rows > 2 * kAtFewRows ? 2 : 1;
+  s.shift = s.rows > 2 * kAtFewRows ? 1 : 0;
   return s;
 }
 // How a unit is done.  Up to kAtFewRows rows: both streams have all rows and take the
@@ -161,6 +164,11 @@ __device__ __forceinline__ bool at_in_turn(const AtUnit& u) { return u.rows <= k
 __device__ __forceinline__ bool at_few(const AtUnit& u) { return u.rows <= 2 * kAtFewRows; }
 __device__ __forceinline__ int at_first_rows(const AtUnit& u) {
   return at_in_turn(u) ? u.rows : at_few(u) ? ((u.rows + 1) / 2 + 15) / 16 * 16 : kAtTile;
+}
+
+// How many tiles the values are behind the keys: as many scores are formed ahead.
+__device__ __forceinline__ int at_lag(const AtUnit& u) {
+  return at_in_turn(u) ? 4 : at_few(u) ? 2 : 0;
 }
 
 // The head of a unit's row among all rows' heads.
@@ -176,7 +184,7 @@ __device__ __forceinline__ long long at_head_cost(const AtParams& a, int b) {
   long long cost = 0;
   for (int r0 = 0; r0 < n * a.group; r0 += kAtUnitRows) {
     const AtSpan s = at_unit_span(a, n, len, r0);
-    cost += (long long)s.tiles * s.cost;
+    cost += (long long)s.tiles << s.shift;
   }
   return cost;
 }
@@ -263,14 +271,14 @@ __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
     for (; ok && left > 0 && u.h < a.p.c.kv_heads; ++u.h) {
       for (u.r0 = 0; ok && left > 0 && u.r0 < u.n * a.group; u.r0 += kAtUnitRows) {
         const AtSpan s = at_unit_span(a, u.n, u.len, u.r0);
-        const long long c = (long long)s.tiles * s.cost;
+        const long long c = (long long)s.tiles << s.shift;
         if (off >= c) {
           off -= c;
           continue;
         }
         const long long take = min(c - off, left);
-        const int from = (int)((off + s.cost - 1) / s.cost);
-        const int to = (int)((off + take + s.cost - 1) / s.cost);
+        const int from = (int)((off + s.shift) >> s.shift);
+        const int to = (int)((off + take + s.shift) >> s.shift);
         const long long unit_end = line + c - off;  // on the line
         left -= take;
         line += take;
@@ -331,8 +339,7 @@ struct AtRing {
   }
 };
 
-// Keys then values of each tile; where the streams take the tiles in turn, the values two
-// tiles later, as the products want them.
+// Keys and values of the tiles, in the order in which the products want them.
 template <int D>
 __device__ __forceinline__ bool at_produce(const AtParams& a, const AtMaps& maps, AtControl& ctl,
                                            uint32_t base) {
@@ -379,24 +386,18 @@ __device__ __forceinline__ bool at_produce(const AtParams& a, const AtMaps& maps
       ring.step();
       ++loads;
     };
-    if (!at_in_turn(u)) {
-      int id = page_of(0);
-      for (int j = 0; ok && j < u.nt; ++j) {
-        const int next = page_of(j + 1);
-        load(&maps.k, j, id);
-        if (ok) load(&maps.v, j, id);
-        id = next;
-      }
-    } else {
-      int id = page_of(0), id1 = -1, id2 = -1;
-      for (int j = 0; ok && j < u.nt + 2; ++j) {
-        const int next = page_of(j + 1);
-        if (j >= 2) load(&maps.v, j - 2, id2);
-        if (ok && j < u.nt) load(&maps.k, j, id);
-        id2 = id1;
-        id1 = id;
-        id = next;
-      }
+    const int lag = at_lag(u);
+    int id = page_of(0), old[4] = {-1, -1, -1, -1};  // of this tile and the last four
+    for (int j = 0; ok && j < u.nt + lag; ++j) {
+      const int next = page_of(j + 1);
+      if (lag > 0 && j >= lag) load(&maps.v, j - lag, lag == 4 ? old[3] : old[1]);
+      if (ok && j < u.nt) load(&maps.k, j, id);
+      if (ok && lag == 0) load(&maps.v, j, id);
+      old[3] = old[2];
+      old[2] = old[1];
+      old[1] = old[0];
+      old[0] = id;
+      id = next;
     }
     if (!ok) break;
     walk.done(ctl);
@@ -514,15 +515,16 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     const int first = at_first_rows(u);
     return ((s == 0 || at_in_turn(u) ? first : u.rows - first) + 15) / 16 * 16;
   };
-  auto scores_few = [&](int s, int buf, int stage) {
+  auto scores_few = [&](int s, int buf, int stage, int set) {
     const uint32_t idesc = mma_idesc(128, few_cols(s), false, false);
     const uint32_t q = mma1_desc(base + S::kQ + buf * S::kFewQ, 0);
     const uint32_t k = mma1_desc(base + stage * S::kTileBytes, 0);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
-      mma1_f16(tmem + s * kAtTile, k + ((i >> 2) * (kAtTile * 128) + (i & 3) * 32) / 16,
+      mma1_f16(tmem + s * kAtTile + set * kAtFewRows,
+               k + ((i >> 2) * (kAtTile * 128) + (i & 3) * 32) / 16,
                q + ((i >> 2) * S::kFewHalf + (i & 3) * 32) / 16, idesc, i > 0, one);
-    mma1_commit(&ctl.s_full[s], one);
+    mma1_commit(&ctl.s_full[s][set], one);
   };
   auto values_few = [&](int s, int stage, int j, bool first) {
     wait(&ctl.p_ready[s], p_count[s]++);
@@ -541,6 +543,7 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
       for (int i = from; i < to; ++i)
         mma1_f16(d, v + i * 128, w + i * 128, idesc, i > from || !first, one);
     }
+    mma1_commit(&ctl.pv_done[s], one);
   };
   auto scores = [&](int s, int buf, int stage, int j) {
     const int cols = whole(j) ? kAtTile : last_step(j) * 16;
@@ -552,7 +555,7 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
       const uint32_t off = ((i >> 2) * (kAtTile * 128) + (i & 3) * 32) / 16;
       mma1_f16(tmem + s * kAtTile, q + off, k + off, idesc, i > 0, one);
     }
-    mma1_commit(&ctl.s_full[s], one);
+    mma1_commit(&ctl.s_full[s][0], one);
   };
   // Values of entries that nobody sees are set to 0 as far as the product reads them: their
   // weights are 0, but what lies there may not be finite.
@@ -591,22 +594,13 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     const int buf = q_used & 1;
     wait(&ctl.q_full[buf], q_used >> 1);
     ++q_used;
-    if (!at_in_turn(u)) {
-      const bool few = at_few(u);
+    if (!at_few(u)) {
       wait(&ctl.q_full[buf ^ 1], q_used >> 1);
       ++q_used;
-      auto score = [&](int s, int stage, int j) {
-        if (few) scores_few(s, buf ^ s, stage);
-        else scores(s, buf ^ s, stage, j);
-      };
-      auto value = [&](int s, int stage, int j) {
-        if (few) values_few(s, stage, j, j == 0);
-        else values(s, stage, j, j == 0);
-      };
       int k = ok ? take() : 0;
       if (!ok) break;
-      score(0, k, 0);
-      score(1, k, 0);
+      scores(0, buf, k, 0);
+      scores(1, buf ^ 1, k, 0);
       commit(&ctl.empty[k]);
       for (int j = 0; ok && j < u.nt; ++j) {
         if (j + 1 == u.nt) {  // the last scores are under way
@@ -616,42 +610,63 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
         const int v = take();
         if (!ok) break;
         clear(v, j);
-        value(0, v, j);
+        values(0, v, j, j == 0);
         if (!ok) break;
         if (j + 1 < u.nt) {
           k = take();
           if (!ok) break;
-          score(0, k, j + 1);
+          scores(0, buf, k, j + 1);
         } else {
           commit(&ctl.o_full[0]);
         }
-        value(1, v, j);
+        values(1, v, j, j == 0);
         if (!ok) break;
         commit(&ctl.empty[v]);
         if (j + 1 < u.nt) {
-          score(1, k, j + 1);
+          scores(1, buf ^ 1, k, j + 1);
           commit(&ctl.empty[k]);
         } else {
           commit(&ctl.o_full[1]);
         }
       }
     } else {
-      for (int j = 0; ok && j < u.nt + 2; ++j) {
-        if (j >= 2) {
+      // Each stream's next scores are formed before its last ones are weights: the softmax
+      // waits for neither product.
+      const bool turn = at_in_turn(u);
+      const int lag = at_lag(u);
+      if (!turn) {
+        wait(&ctl.q_full[buf ^ 1], q_used >> 1);
+        ++q_used;
+      }
+      for (int j = 0; ok && j < u.nt + lag; ++j) {
+        if (j >= lag) {
           const int v = take();
           if (!ok) break;
-          clear(v, j - 2);
-          values_few(j & 1, v, j - 2, j < 4);
+          clear(v, j - lag);
+          if (turn) {
+            values_few(j & 1, v, j - lag, j - lag < 2);
+          } else {
+            values_few(0, v, j - lag, j == lag);
+            if (ok) values_few(1, v, j - lag, j == lag);
+          }
           if (!ok) break;
           commit(&ctl.empty[v]);
         }
         if (j < u.nt) {
           const int k = take();
           if (!ok) break;
-          scores_few(j & 1, buf, k);
+          if (turn) {
+            scores_few(j & 1, buf, k, (j >> 1) & 1);
+          } else {
+            scores_few(0, buf, k, j & 1);
+            scores_few(1, buf ^ 1, k, j & 1);
+          }
           commit(&ctl.empty[k]);
         }
-        if (j + 1 == u.nt) commit(&ctl.q_empty[buf]);
+        if (j + 1 == u.nt) {
+          commit(&ctl.q_empty[buf]);
+          if (!turn) commit(&ctl.q_empty[buf ^ 1]);
+        }
       }
       if (!ok) break;
       commit(&ctl.o_full[0]);
@@ -674,6 +689,7 @@ __device__ __forceinline__ void at_store_row(uint16_t* out, const float (&x)[kWo
 struct AtSoft {
   int s, quarter;  // the stream; the warp's 32 lanes
   int tiles, units, meets, votes;
+  int sets[2], weights;  // scores of either set, weights of units of few rows
   bool ok;
   __device__ __forceinline__ void wait(AtControl& ctl, uint64_t* bar, int parity) {
     if (!at_wait(bar, parity & 1, &ctl.abort_flag)) ok = false;
@@ -712,7 +728,7 @@ __device__ __forceinline__ void at_unit_rows(const AtParams& a, AtControl& ctl, 
   }
   float m = -INFINITY, l = 0.0f;
   for (int j = 0; j < u.nt; ++j, ++w.tiles) {
-    w.wait(ctl, &ctl.s_full[s], w.tiles);
+    w.wait(ctl, &ctl.s_full[s][0], w.sets[0]++);
     if (!w.ok) return;
     if (!dead) {
       // Twice through the scores, 64 registers of them at a time: for the maximum, and for
@@ -869,7 +885,7 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
   const int rows = turn || s == 0 ? at_first_rows(u) : u.rows - at_first_rows(u);
   const int chunks = (rows + 15) / 16;
   const uint32_t lanes = (uint32_t)(w.quarter * 32) << 16;
-  const uint32_t scores = tmem + s * kAtTile + lanes, sums = tmem + 2 * kAtTile + lanes;
+  const uint32_t all_scores = tmem + s * kAtTile + lanes, sums = tmem + 2 * kAtTile + lanes;
   const float nan = __int_as_float(0x7fc00000);
   // This entry's line of weights: 8 rows to 16 bytes, swizzled by the entry.
   unsigned char* store = smem + S::kWeights + s * S::kFewWeights;
@@ -891,7 +907,9 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
   const float2 sc = make_float2(a.scale2, a.scale2);
   bool first = true;
   for (int j = turn ? s : 0; j < u.nt; j += turn ? 2 : 1, ++w.tiles, first = false) {
-    w.wait(ctl, &ctl.s_full[s], w.tiles);
+    const int set = (turn ? j >> 1 : j) & 1;
+    const uint32_t scores = all_scores + set * kAtFewRows;
+    w.wait(ctl, &ctl.s_full[s][set], w.sets[set]++);
     if (!w.ok) return;
     const int at = (u.tile0 + j) * kAtTile;
     if (at < lo_all || at + kAtTile > hi_all) {
@@ -940,6 +958,10 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
       if (!w.ok) return;
       raise = *(volatile int*)&ctl.raise[s][w.tiles & 1] == w.tiles;
     }
+    // The last tile's product has read the weights, and its sums are there.
+    if (!first) w.wait(ctl, &ctl.pv_done[s], w.weights - 1);
+    ++w.weights;
+    if (!w.ok) return;
     if (raise) {
 #pragma unroll 1
       for (int c = 0; c < chunks * 16; c += 16) {
@@ -975,7 +997,6 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
       w.vote(ctl);
       if (!w.ok) return;
       if (!first) {
-        // (All earlier products are done: this tile's scores came behind them.)
 #pragma unroll
         for (int q = 0; q < kChunks; ++q) {
           if (q >= chunks) break;
@@ -1117,7 +1138,10 @@ __device__ __forceinline__ bool at_softmax(const AtParams& a, AtControl& ctl, un
                                            uint32_t tmem) {
   const int warp = threadIdx.x >> 5;
   AtWalk walk;
-  AtSoft w = {(warp - kAtSoftmax) >> 2, warp & 3, 0, 0, 0, 0, true};
+  AtSoft w = {};
+  w.s = (warp - kAtSoftmax) >> 2;
+  w.quarter = warp & 3;
+  w.ok = true;
   AtUnit u;
   while (walk.next(ctl, u, w.ok)) {
     if (at_few(u)) at_unit_few<D>(a, ctl, smem, tmem, w, u, walk.slot);
@@ -1143,7 +1167,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.s_full[i][0], 1);
+      mbar_init(&ctl.s_full[i][1], 1);
+      mbar_init(&ctl.pv_done[i], 1);
       mbar_init(&ctl.p_ready[i], 4);
       mbar_init(&ctl.o_full[i], 1);
       mbar_init(&ctl.q_full[i], 1);
@@ -1192,7 +1218,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 // Joins the parts of units that lie across CTAs' borders, one warp per row; then the
 // rows that belong to no unit: of requests out of range (NaN), and those that see nothing.
 // The first CTA writes the workspace's header.
-constexpr int kAtJoinThreads = 256, kAtJoinShare = 4;  // CTAs per CTA of the first kernel
+constexpr int kAtJoinThreads = 256;
 
 template <int D>
 __device__ __forceinline__ void at_fill(const AtParams& a, long long row, float x, float lse,
@@ -1208,11 +1234,12 @@ template <int D>
 __global__ void __launch_bounds__(kAtJoinThreads)
     paged_join_kernel(const __grid_constant__ AtParams a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x / kAtJoinShare, share = blockIdx.x % kAtJoinShare;
+  const int c = blockIdx.x / a.join_share, share = blockIdx.x % a.join_share;
   const float nan = __int_as_float(0x7fc00000);
   pdl_wait();
   pdl_launch_dependents();
   const PagedParams& p = a.p;
+  const AtPart u = a.ctas[c].part[1];
   int late = 0, bad_page = 0;
   for (int i = threadIdx.x; i < a.main_ctas; i += kAtJoinThreads) {
     late |= a.ctas[i].timeout;
@@ -1261,12 +1288,10 @@ __global__ void __launch_bounds__(kAtJoinThreads)
       }
     }
   }
-  if (late || c >= a.main_ctas) return;
-  const AtPart u = a.ctas[c].part[1];
-  if (!u.used) return;
+  if (late || !u.used) return;
   const int parts = u.end - c + 1;  // CTAs c .. end have parts (but for such with none)
   for (int r = share * (kAtJoinThreads / 32) + warp; r < u.rows;
-       r += kAtJoinShare * (kAtJoinThreads / 32)) {
+       r += a.join_share * (kAtJoinThreads / 32)) {
     // 32 parts at a time, a lane the statistics of each; of further ones the sums so far are
     // rescaled.
     float m = -INFINITY, l = 0.0f, x[D / 32];

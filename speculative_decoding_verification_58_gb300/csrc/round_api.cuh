@@ -217,10 +217,12 @@ spec_status_t attn_run(const PagedParams& p, unsigned char* ws, cudaStream_t s) 
   if (!attn_map(&maps.k, p.c, p.c.k_cache, p.c.k_page, p.c.k_slot, p.c.k_head) ||
       !attn_map(&maps.v, p.c, p.c.v_cache, p.c.v_page, p.c.v_slot, p.c.v_head))
     return SPEC_ERR_CUDA;
+  // A warp of the join per row of a part, up to 16 CTAs of them.
+  a.join_share = std::min(16, (lay.slot_rows + kAtJoinThreads / 32 - 1) / (kAtJoinThreads / 32));
   if (launch(paged_attention_kernel<D>, dim3((unsigned)a.main_ctas), dim3(kAtThreads), at_smem<D>(),
              s, true, maps, a) != cudaSuccess)
     return SPEC_ERR_CUDA;
-  return launch(paged_join_kernel<D>, dim3((unsigned)(a.main_ctas * kAtJoinShare)),
+  return launch(paged_join_kernel<D>, dim3((unsigned)(a.main_ctas * a.join_share)),
                 dim3(kAtJoinThreads), 0, s, true, a) == cudaSuccess
              ? SPEC_OK
              : SPEC_ERR_CUDA;

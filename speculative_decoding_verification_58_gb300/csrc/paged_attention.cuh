@@ -88,7 +88,7 @@ struct AtControl {
   uint64_t vote[2];
   uint64_t few_done;
   long long scan[kAtThreads / 32];
-  long long start_off, start_left, start_line, total;
+  long long start_off, start_left, start_line, start_cost, total;
   int start_b;
   int abort_flag, bad_page;
   uint32_t tmem;
@@ -144,10 +144,11 @@ __device__ __forceinline__ void at_span(const PagedParams& p, int n, int len, in
 __device__ __forceinline__ int at_token(const AtParams& a, int row) {
   return (int)(((unsigned long long)(uint32_t)row * a.magic) >> a.shift);
 }
-// Tiles of the unit of rows r0 .. and what one costs: two streams' products or one's.
+// Tiles of the unit of rows r0 .. and what one costs, in parts of the time of one that only its
+// loads take (measured: 1.5 us with up to 64 rows, 1.9 with 68, 1.7 to 3 with 256).
 struct AtSpan {
   int rows, lo, hi, tile0, tiles;
-  int shift;  // log2 of a tile's cost
+  int cost;  // of a tile
 };
 __device__ __forceinline__ AtSpan at_unit_span(const AtParams& a, int n, int len, int r0) {
   AtSpan s;
@@ -155,7 +156,7 @@ __device__ __forceinline__ AtSpan at_unit_span(const AtParams& a, int n, int len
   at_span(a.p, n, len, at_token(a, r0), at_token(a, r0 + s.rows - 1), s.lo, s.hi);
   s.tile0 = s.lo / kAtTile;
   s.tiles = s.hi > s.lo ? (s.hi + kAtTile - 1) / kAtTile - s.tile0 : 0;
-  s.shift = s.rows > 2 * kAtFewRows ? 1 : 0;
+  s.cost = s.rows <= kAtFewRows ? 4 : s.rows <= 2 * kAtFewRows ? 5 : 8;
   return s;
 }
 // How a unit is done.  Up to kAtFewRows rows: both streams have all rows and take the
@@ -184,7 +185,7 @@ __device__ __forceinline__ long long at_head_cost(const AtParams& a, int b) {
   long long cost = 0;
   for (int r0 = 0; r0 < n * a.group; r0 += kAtUnitRows) {
     const AtSpan s = at_unit_span(a, n, len, r0);
-    cost += (long long)s.tiles << s.shift;
+    cost += (long long)s.tiles * s.cost;
   }
   return cost;
 }
@@ -205,6 +206,7 @@ __device__ __forceinline__ void at_share(const AtParams& a, AtControl& ctl) {
   const int b0 = min(tid * each, B), b1 = min(b0 + each, B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) mine += at_head_cost(a, b);
+  const long long head = mine;
   mine *= a.p.c.kv_heads;
   long long upto = mine;
 #pragma unroll
@@ -225,12 +227,13 @@ __device__ __forceinline__ void at_share(const AtParams& a, AtControl& ctl) {
   const long long start = at_border(total, c, G), end = at_border(total, c + 1, G);
   if (start < end && before <= start && start < before + mine) {
     for (int b = b0; b < b1; ++b) {
-      const long long x = each == 1 ? mine : at_head_cost(a, b) * a.p.c.kv_heads;
+      const long long h = each == 1 ? head : at_head_cost(a, b), x = h * a.p.c.kv_heads;
       if (start < before + x) {
         ctl.start_b = b;
         ctl.start_off = start - before;
         ctl.start_left = end - start;
         ctl.start_line = start;
+        ctl.start_cost = h;
         ctl.total = total;
         break;
       }
@@ -260,7 +263,7 @@ __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
   AtUnit u;
   u.bad = 0;
   for (int b = ctl.start_b; ok && left > 0 && b < a.p.c.B; ++b, off = 0) {
-    const long long cost = at_head_cost(a, b);
+    const long long cost = b == ctl.start_b ? ctl.start_cost : at_head_cost(a, b);
     if (cost == 0) continue;
     u.b = b;
     u.first = a.p.c.new_start[b];
@@ -271,14 +274,14 @@ __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
     for (; ok && left > 0 && u.h < a.p.c.kv_heads; ++u.h) {
       for (u.r0 = 0; ok && left > 0 && u.r0 < u.n * a.group; u.r0 += kAtUnitRows) {
         const AtSpan s = at_unit_span(a, u.n, u.len, u.r0);
-        const long long c = (long long)s.tiles << s.shift;
+        const long long c = (long long)s.tiles * s.cost;
         if (off >= c) {
           off -= c;
           continue;
         }
         const long long take = min(c - off, left);
-        const int from = (int)((off + s.shift) >> s.shift);
-        const int to = (int)((off + take + s.shift) >> s.shift);
+        const int from = ((int)off + s.cost - 1) / s.cost;
+        const int to = ((int)(off + take) + s.cost - 1) / s.cost;
         const long long unit_end = line + c - off;  // on the line
         left -= take;
         line += take;
@@ -1230,10 +1233,80 @@ __device__ __forceinline__ void at_fill(const AtParams& a, long long row, float 
     for (int i = from; i < a.p.heads; i += step) a.p.lse[row * a.p.heads + i] = lse;
 }
 
+// The rows of a unit that lies across CTAs, one warp each.
+template <int D>
+__device__ __forceinline__ void at_join(const AtParams& a, const AtPart& u, int c, int share) {
+  const PagedParams& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = u.end - c + 1;  // CTAs c .. end have parts (but for such with none)
+  for (int r = share * (kAtJoinThreads / 32) + warp; r < u.rows;
+       r += a.join_share * (kAtJoinThreads / 32)) {
+    // 32 parts at a time, a lane the statistics of each; of further ones the sums so far are
+    // rescaled.
+    float m = -INFINITY, l = 0.0f, x[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const int i = i0 + lane;
+      float2 st = make_float2(-INFINITY, 0.0f);
+      if (i < parts) {
+        // (Of a CTA without a part nothing counts; both loads go together.)
+        const int used = i == 0 ? 1 : a.ctas[c + i].part[0].used;
+        const float2 x = a.stats[(size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r];
+        if (used) st = x;
+      }
+      float top = st.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmaxf(top, m);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float fix = ex2(__fsub_rn(m, ref));
+      m = top;
+      const float w = ex2(__fsub_rn(st.x, ref));
+      // (A NaN in the statistics marks a part that read a page outside the cache.)
+      const bool counts = w != 0.0f || st.y != st.y;
+      float add = counts ? __fmul_rn(st.y, w) : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) add = __fadd_rn(add, __shfl_xor_sync(0xffffffffu, add, o));
+      l = fmaf(l, fix, add);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) x[e] = __fmul_rn(x[e], fix);
+      uint32_t some = __ballot_sync(0xffffffffu, counts);
+      while (some != 0) {
+        // Eight parts' sums at a time: their loads go together.
+        float v[8][D / 32], wk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int j = some != 0 ? __ffs(some) - 1 : -1;
+          some &= some - 1;
+          wk[k] = __shfl_sync(0xffffffffu, w, max(j, 0));
+          const float* src =
+              a.parts +
+              ((size_t)(2 * (c + i0 + j) + (i0 + j == 0 ? 1 : 0)) * a.slot_rows + r) * D;
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) v[k][e] = j >= 0 ? src[e * 32 + lane] : 0.0f;
+          if (j < 0) wk[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) x[e] = fmaf(v[k][e], wk[k], x[e]);
+      }
+    }
+    const long long head = at_head(a, u.first, u.h, u.r0 + r);
+    const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+      p.out[head * D + e * 32 + lane] =
+          (uint16_t)(pack_bf16(l == 0.0f ? 0.0f : __fmul_rn(x[e], inv), 0.0f) & 0xffff);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[head] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2f);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kAtJoinThreads)
     paged_join_kernel(const __grid_constant__ AtParams a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x / a.join_share, share = blockIdx.x % a.join_share;
   const float nan = __int_as_float(0x7fc00000);
   pdl_wait();
@@ -1267,6 +1340,7 @@ __global__ void __launch_bounds__(kAtJoinThreads)
       p.header->first_bad = INT32_MAX;
     }
   }
+  if (!late && u.used) at_join<D>(a, u, c, share);
   // Rows that nobody computed.
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
     const int first = p.c.new_start[b], last = p.c.new_start[b + 1], len = p.c.kv_len[b];
@@ -1287,67 +1361,6 @@ __global__ void __launch_bounds__(kAtJoinThreads)
         if (e == 0 && p.lse != nullptr) p.lse[head] = -INFINITY;
       }
     }
-  }
-  if (late || !u.used) return;
-  const int parts = u.end - c + 1;  // CTAs c .. end have parts (but for such with none)
-  for (int r = share * (kAtJoinThreads / 32) + warp; r < u.rows;
-       r += a.join_share * (kAtJoinThreads / 32)) {
-    // 32 parts at a time, a lane the statistics of each; of further ones the sums so far are
-    // rescaled.
-    float m = -INFINITY, l = 0.0f, x[D / 32];
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      const int i = i0 + lane;
-      float2 st = make_float2(-INFINITY, 0.0f);
-      if (i < parts && (i == 0 || a.ctas[c + i].part[0].used))
-        st = a.stats[(size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r];
-      float top = st.x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      top = fmaxf(top, m);
-      const float ref = top == -INFINITY ? 0.0f : top;
-      const float fix = ex2(__fsub_rn(m, ref));
-      m = top;
-      const float w = ex2(__fsub_rn(st.x, ref));
-      // (A NaN in the statistics marks a part that read a page outside the cache.)
-      const bool counts = w != 0.0f || st.y != st.y;
-      float add = counts ? __fmul_rn(st.y, w) : 0.0f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) add = __fadd_rn(add, __shfl_xor_sync(0xffffffffu, add, o));
-      l = fmaf(l, fix, add);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) x[e] = __fmul_rn(x[e], fix);
-      uint32_t some = __ballot_sync(0xffffffffu, counts);
-      while (some != 0) {
-        // Four parts' sums at a time: their loads go together.
-        float v[4][D / 32], wk[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int j = some != 0 ? __ffs(some) - 1 : -1;
-          some &= some - 1;
-          wk[k] = __shfl_sync(0xffffffffu, w, max(j, 0));
-          const float* src =
-              a.parts +
-              ((size_t)(2 * (c + i0 + j) + (i0 + j == 0 ? 1 : 0)) * a.slot_rows + r) * D;
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) v[k][e] = j >= 0 ? src[e * 32 + lane] : 0.0f;
-          if (j < 0) wk[k] = 0.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) x[e] = fmaf(v[k][e], wk[k], x[e]);
-      }
-    }
-    const long long head = at_head(a, u.first, u.h, u.r0 + r);
-    const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e)
-      p.out[head * D + e * 32 + lane] =
-          (uint16_t)(pack_bf16(l == 0.0f ? 0.0f : __fmul_rn(x[e], inv), 0.0f) & 0xffff);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[head] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2f);
   }
 }
 

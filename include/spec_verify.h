@@ -558,9 +558,10 @@ spec_status_t spec_clip_grad_norm(const void* const* grads, void* const* outs,
  * entries hold a NaN or (T > 0) +inf, or none above -inf, gets token -1 and a kept
  * row of NaN (which verification reports as invalid); at T = 0 a NaN is never the
  * maximum, as for spec_verify.  A uniform out of range gives token -1 alone.
- * The masses are summed as whole numbers (units of 2^-42 of the largest or finer), so
- * that a row's result does not depend on the order of its additions: the same row
- * gives the same token on every call and in every batch.
+ * K is exact: the masses that decide it are whole numbers (each right to about 2^-38
+ * of itself, in units of 2^-42 of the largest or finer), or sums in single precision
+ * where these leave no doubt, so that it does not depend on the order of additions.  A
+ * draw weighs the entries of K to 2^-20 of themselves or better, in whole numbers as well.
  */
 spec_status_t spec_sample(const void* logits, spec_dtype_t dtype, int rows, int V, int group,
                           const float* temperature, const int32_t* top_k, const float* top_p,
@@ -596,7 +597,7 @@ typedef struct {
   int kv_heads;   /* 1 to 1024 */
   int width;      /* entries of a head: 64 or 128 */
   const int32_t* page_table;  /* [B, max_pages] (device); what no request uses is not read */
-  int max_pages;              /* max_pages * page_size <= INT32_MAX */
+  int max_pages;              /* max_pages * page_size <= 2^30 */
   const int32_t* new_start;   /* [B + 1] (device), not decreasing */
   const int32_t* kv_len;      /* [B] (device): entries with the new tokens' */
   int B;
@@ -630,7 +631,7 @@ spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype
  *   causal     0 or 1: a target's pass over a chain of tokens is causal, the block
  *              of a diffusion drafter is not
  *   window     0 (none) or the number of entries a token sees; needs causal
- *   scale      finite, > 0
+ *   scale      > 0, scale log2(e) finite
  *   out        [rows, heads, width] dtype out, contiguous, 16-byte aligned
  *   lse        [rows, heads] float out, or NULL
  *   workspace  >= spec_paged_attention_workspace_bytes(rows, heads, kv_heads, width)
@@ -695,7 +696,7 @@ int spec_debug_build(void);
 spec_status_t spec_debug_checks(int32_t* failures, int32_t* first_site, int reset, void* stream);
 
 /*
- * Range-checking build: from now on the products of linear cross entropy on the
+ * Range-checking build: from now on linear cross entropy and paged attention on the
  * current device record `status` (SPEC_ERR_TIMEOUT, as if a wait had run out; SPEC_OK
  * ends it), so that what follows from a timeout can be tested without one.
  * Waits for `stream`.  A release build returns SPEC_ERR_UNSUPPORTED.

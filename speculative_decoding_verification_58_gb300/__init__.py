@@ -236,7 +236,7 @@ def spec_debug_checks(reset: bool = False, stream=None) -> tuple[int, int]:
 
 
 def spec_debug_inject(status: int, stream=None) -> None:
-    """Range-checking build: linear cross entropy records ``status`` (SPEC_ERR_TIMEOUT, or
+    """Range-checking build: linear cross entropy and paged attention record ``status`` (SPEC_ERR_TIMEOUT, or
     SPEC_OK to end it) as if a wait had run out; a release build refuses."""
     _check(lib().spec_debug_inject(status, _stream_ptr(stream)), "spec_debug_inject")
 

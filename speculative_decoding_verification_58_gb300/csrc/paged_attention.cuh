@@ -75,7 +75,7 @@ struct AtUnit {
 struct AtControl {
   uint64_t full[10], empty[10];
   uint64_t s_full[2][2];  // of a stream; units of few rows have two sets of scores in turn
-  uint64_t p_ready[2], pv_done[2], o_full[2], q_full[2], q_empty[2];
+  uint64_t p_ready[2], p_half[2], pv_done[2], o_full[2], q_full[2], q_empty[2];
   uint64_t u_full[kAtUnits], u_empty[kAtUnits];
   uint64_t meet;  // of both warpgroups
   AtUnit unit[kAtUnits];
@@ -489,7 +489,7 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
   AtWalk walk;
   AtRing<S::kStages> ring;
   const uint32_t one = mma1_elect();
-  int q_used = 0, p_count[2] = {0, 0};
+  int q_used = 0, p_count[2] = {0, 0}, half_count[2] = {0, 0};
   bool ok = true;
   AtUnit u = {};
   auto wait = [&](uint64_t* bar, int parity) {
@@ -577,18 +577,30 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
   };
+  // The first half of the weights is multiplied while the second is formed.
   auto values = [&](int s, int stage, int j, bool first) {
-    wait(&ctl.p_ready[s], p_count[s]++);
-    if (!ok) return;
     const uint32_t v = mma1_desc(base + stage * S::kTileBytes, kAtTile * 128);
     const uint32_t p = tmem + s * kAtTile, d = tmem + (2 + s) * kAtTile;
+    constexpr int kHalf = kAtTile / 32;
+    const int from = first_step(j), to = last_step(j);
+    wait(&ctl.p_half[s], half_count[s]++);
+    if (!ok) return;
     if (whole(j)) {
 #pragma unroll
-      for (int i = 0; i < kAtTile / 16; ++i)
+      for (int i = 0; i < kHalf; ++i)
         mma1_f16_ta(d, p + i * 8, v + i * 128, kPv, i > 0 || !first, one);
     } else {
-      const int from = first_step(j), to = last_step(j);
-      for (int i = from; i < to; ++i)
+      for (int i = from; i < min(to, kHalf); ++i)
+        mma1_f16_ta(d, p + i * 8, v + i * 128, kPv, i > from || !first, one);
+    }
+    wait(&ctl.p_ready[s], p_count[s]++);
+    if (!ok) return;
+    if (whole(j)) {
+#pragma unroll
+      for (int i = kHalf; i < 2 * kHalf; ++i)
+        mma1_f16_ta(d, p + i * 8, v + i * 128, kPv, 1, one);
+    } else {
+      for (int i = max(from, kHalf); i < to; ++i)
         mma1_f16_ta(d, p + i * 8, v + i * 128, kPv, i > from || !first, one);
     }
   };
@@ -802,10 +814,18 @@ __device__ __forceinline__ void at_unit_rows(const AtParams& a, AtControl& ctl, 
           x[c >> 1] = pack_bf16(e.x, e.y);
         }
         tmem_store32(scores + h / 2, x);
+        if (h == 0) {
+          tmem_wait_store();
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.p_half[s]);
+        }
       }
       const float2 t = f32x2_add(f32x2_add(add[0], add[1]), f32x2_add(add[2], add[3]));
       l = __fadd_rn(l, __fadd_rn(t.x, t.y));
       tmem_wait_store();
+    } else if (lane == 0) {
+      mbar_arrive(&ctl.p_half[s]);
     }
     tmem_fence_before();
     __syncwarp();
@@ -1174,6 +1194,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&ctl.s_full[i][1], 1);
       mbar_init(&ctl.pv_done[i], 1);
       mbar_init(&ctl.p_ready[i], 4);
+      mbar_init(&ctl.p_half[i], 4);
       mbar_init(&ctl.o_full[i], 1);
       mbar_init(&ctl.q_full[i], 1);
       mbar_init(&ctl.q_empty[i], 1);

@@ -117,7 +117,7 @@ inline spec_status_t cache_check(const spec_paged_cache_t* in, spec_dtype_t dtyp
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
   if (dtype != SPEC_BF16 || rows > SPEC_MAX_ROWS || c.B > SPEC_MAX_B || c.page_size < 8 ||
       c.page_size > 1024 || (c.page_size & (c.page_size - 1)) != 0 || c.kv_heads > 1024 ||
-      (c.width != 64 && c.width != 128) || (long long)c.max_pages * c.page_size > INT32_MAX)
+      (c.width != 64 && c.width != 128) || (long long)c.max_pages * c.page_size > (1 << 30))
     return SPEC_ERR_UNSUPPORTED;
   if (!c.k_cache || !c.v_cache || !c.page_table || !c.new_start || !c.kv_len)
     return SPEC_ERR_INVALID_ARG;
@@ -298,7 +298,7 @@ spec_status_t spec_paged_attention(const spec_paged_cache_t* cache, spec_dtype_t
   if (heads < 1 || heads % p.c.kv_heads != 0) return SPEC_ERR_INVALID_ARG;
   if (!attn_sizes_ok(rows, heads, p.c.kv_heads, p.c.width)) return SPEC_ERR_UNSUPPORTED;
   if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal) ||
-      !(scale > 0.0f && scale <= FLT_MAX))
+      !(scale > 0.0f && scale * kLog2e <= FLT_MAX))
     return SPEC_ERR_INVALID_ARG;
   const long long row = (long long)heads * p.c.width;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4))
@@ -322,7 +322,7 @@ spec_status_t spec_paged_attention(const spec_paged_cache_t* cache, spec_dtype_t
   p.q_stride = q_stride;
   p.heads = heads;
   p.causal = causal;
-  p.window = window;
+  p.window = std::min(window, 1 << 30);  // (as good as none: see max_pages)
   p.scale = scale;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;

@@ -333,12 +333,24 @@ struct SampleJob {
     for (int e = 1; e < kPer; ++e) most = fmaxf(most, x[e]);
     return most >= least;
   }
-  // Of CTA i's shared memory.
-  __device__ __forceinline__ uint32_t peek(const uint32_t* x, int i) const {
-    return ctas == 1 ? *x : dsmem_ld_u32(dsmem_map(x, i));
+  // The sum of all CTAs' words at the same place of shared memory; their loads go together.
+  __device__ __forceinline__ uint32_t sum_of(const uint32_t* x) const {
+    if (ctas == 1) return *x;
+    uint32_t v[kSampleMaxCluster], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kSampleMaxCluster; ++i) v[i] = i < ctas ? dsmem_ld_u32(dsmem_map(x, i)) : 0;
+#pragma unroll
+    for (int i = 0; i < kSampleMaxCluster; ++i) sum += v[i];
+    return sum;
   }
-  __device__ __forceinline__ unsigned long long peek(const unsigned long long* x, int i) const {
-    return ctas == 1 ? *x : dsmem_ld_u64(dsmem_map(x, i));
+  __device__ __forceinline__ unsigned long long sum_of(const unsigned long long* x) const {
+    if (ctas == 1) return *x;
+    unsigned long long v[kSampleMaxCluster], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kSampleMaxCluster; ++i) v[i] = i < ctas ? dsmem_ld_u64(dsmem_map(x, i)) : 0;
+#pragma unroll
+    for (int i = 0; i < kSampleMaxCluster; ++i) sum += v[i];
+    return sum;
   }
   // The t-th entry outside the vectors.
   __device__ __forceinline__ int edge(int t) const {
@@ -833,10 +845,7 @@ struct SampleJob {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
           const int b = kSampleFine - 1 - (tid * kEach + e);
-          n[e] = 0;
-          for (int i = 0; i < ctas; ++i)
-            n[e] += goal.by_count ? peek(&sh.hist[b], i)
-                                  : peek(&sh.fine[b], i);
+          n[e] = goal.by_count ? sum_of(&sh.hist[b]) : sum_of(&sh.fine[b]);
           mine += n[e];
         }
         unsigned long long upto = mine;
@@ -862,9 +871,7 @@ struct SampleJob {
         if (tid == 0 && sh.border >= 0) {
           w.i = sh.border;
           w.a = sh.red[1][0];
-          int c = 0;
-          for (int i = 0; i < ctas; ++i) c += (int)peek(&sh.hist[sh.border], i);
-          w.j = c;
+          w.j = (int)sum_of(&sh.hist[sh.border]);
         }
       }
       const SamplePeer* all = exchange(w);
@@ -1294,8 +1301,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
               const int b = tid * kEach + e;
-              uint32_t c = 0;
-              for (int i = 0; i < ctas; ++i) c += job.peek(&sh.hist[b], i);
+              const uint32_t c = job.sum_of(&sh.hist[b]);
               bin[e] = (float)c * ex2(__fmul_rn(-((float)b + 0.5f) * width, kLog2e));
               mine += bin[e];
               squares = fmaf(bin[e], bin[e], squares);
@@ -1374,7 +1380,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
                 c[e] = 0;
                 m[e] = 0;
                 if (b >= 0) {
-                  for (int i = 0; i < ctas; ++i) c[e] += job.peek(&sh.hist[b], i);
+                  c[e] = job.sum_of(&sh.hist[b]);
                   const uint32_t key = k0 + b;
                   m[e] = units_of({near_mass(job.s, from_order_bits(
                                                         (key << 16) | (key & 0x8000u ? 0 : 0xffffu))),
@@ -1523,7 +1529,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
       if (i >= listed) break;
       const int v = (int)~(uint32_t)sh.list[i];
       const bool mine = v >= job.first - job.head && v < job.first + nvec * kPer + job.tail;
-      if (mine) out[v] = keep[e];
+      if (mine) out[SPEC_CHECKED(v, V, kSiteSample)] = keep[e];
     }
     return;
   }

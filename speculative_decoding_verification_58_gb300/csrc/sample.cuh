@@ -80,8 +80,8 @@ __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, con
                                                          float z) {
   const FF d = two_sum(z, -s.max);
   FF x = two_prod(d.hi, s.inv.hi);
-  if (!(x.hi > -62.0f)) return 0;  // less than half a unit (or z = -inf)
   x.lo = __fmaf_rn(d.hi, s.inv.lo, __fmaf_rn(d.lo, s.inv.hi, x.lo));
+  x.hi = fmaxf(x.hi, -63.0f);  // less than half a unit (or z = -inf, and x.lo anything)
   const float nf = __fadd_rn(x.hi, 12582912.0f);  // 1.5 * 2^23: rounds to a whole number
   const int n = __float_as_int(nf) - 0x4b400000;
   const float f = __fsub_rn(x.hi, __fsub_rn(nf, 12582912.0f));  // exact, |f| <= 1/2
@@ -99,11 +99,9 @@ __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, con
   const uint32_t u3 = __umulhi(u2, u);          // units of 2^-56
   const uint32_t r = u + (u2 >> 9) + (__umulhi(u3, 715827883u) >> 16);
   const unsigned long long m = e + __umulhi((uint32_t)(e >> 8), r);  // 2^-39
-  // (hi >> 8 <= 0; with rounding it may be 0 where x is slightly above 0: z = max only.)
-  const int shift = 39 - s.unit_bits - (hi >> 8);
-  if (shift <= 0) return m << -shift;
-  if (shift > 41) return 0;
-  return (m + (1ull << (shift - 1))) >> shift;
+  // (hi >> 8 <= 0, so that the shift is 17 at least.)
+  const int shift = 62 - s.unit_bits - (hi >> 8);
+  return shift > 63 ? 0 : ((m << 23) + (1ull << ((shift - 1) & 63))) >> (shift & 63);
 }
 
 // The same in single precision, to about 2^-22 of itself, for sums that only have to tell on
@@ -280,10 +278,11 @@ __device__ __forceinline__ unsigned long long units_of(FF x) {
   return (unsigned long long)(__float2ll_rn(__fmul_rn(x.hi, up)) + __float2ll_rn(__fmul_rn(x.lo, up)));
 }
 
-// What a border is looked for by: the entries' number or their mass.
+// What a border is looked for by: a number of entries, or a share of their mass.
 struct SampleGoal {
   bool by_count;
-  unsigned long long want;
+  unsigned long long want;  // 0: the share of the mass, found in the first pass
+  float share;
 };
 
 // A CTA's part in one row.
@@ -338,18 +337,18 @@ struct SampleJob {
     if (ctas == 1) return *x;
     uint32_t v[kSampleMaxCluster], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kSampleMaxCluster; ++i) v[i] = i < ctas ? dsmem_ld_u32(dsmem_map(x, i)) : 0;
+    for (int i = 0; i < kSampleMaxCluster; ++i) v[i] = dsmem_ld_u32(dsmem_map(x, ::min(i, ctas - 1)));
 #pragma unroll
-    for (int i = 0; i < kSampleMaxCluster; ++i) sum += v[i];
+    for (int i = 0; i < kSampleMaxCluster; ++i) sum += i < ctas ? v[i] : 0;
     return sum;
   }
   __device__ __forceinline__ unsigned long long sum_of(const unsigned long long* x) const {
     if (ctas == 1) return *x;
     unsigned long long v[kSampleMaxCluster], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kSampleMaxCluster; ++i) v[i] = i < ctas ? dsmem_ld_u64(dsmem_map(x, i)) : 0;
+    for (int i = 0; i < kSampleMaxCluster; ++i) v[i] = dsmem_ld_u64(dsmem_map(x, ::min(i, ctas - 1)));
 #pragma unroll
-    for (int i = 0; i < kSampleMaxCluster; ++i) sum += v[i];
+    for (int i = 0; i < kSampleMaxCluster; ++i) sum += i < ctas ? v[i] : 0;
     return sum;
   }
   // The t-th entry outside the vectors.
@@ -816,25 +815,27 @@ struct SampleJob {
       }
       __syncthreads();
       unsigned long long count = 0, mass = 0;  // above hi
-      const float low = from_order_bits(k0 << kDrop);  // (NaN: no bound)
-      each(low == low ? low : -INFINITY, [&](const float* x, int v, int n) {
+      float low = from_order_bits(k0 << kDrop);
+      if (!(low == low)) low = -INFINITY;  // (no bound)
+      const bool all_mass = !goal.by_count && goal.want == 0;  // `count` is the mass of all
+      each(all_mass ? -INFINITY : low, [&](const float* x, int v, int n) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-          if (e >= n) continue;
           const uint32_t k = order_bits(x[e]) >> kDrop;
-          if (k < k0 || entry_rank(x[e], v + e) < from) continue;
-          const unsigned long long m = goal.by_count ? 0 : entry_mass(s, sh.table, x[e]);
-          if (k > k1) {
-            ++count;
-            mass += m;
-          } else {
-            const int b = (int)((k - k0) >> shift);
-            atomicAdd(&sh.hist[b], 1u);
-            if (m != 0) atomicAdd(&sh.fine[b], m);
+          const bool counts = (e < n) & (entry_rank(x[e], v + e) >= from);
+          if (goal.by_count) {
+            count += counts & (k > k1) ? 1 : 0;
+          } else if (all_mass || k >= k0) {
+            const unsigned long long m = counts ? entry_mass(s, sh.table, x[e]) : 0;
+            if (all_mass) count += m;
+            mass += k > k1 ? m : 0;
+            if ((m != 0) & (k >= k0) & (k <= k1)) atomicAdd(&sh.fine[(k - k0) >> shift], m);
           }
+          if (counts & (k >= k0) & (k <= k1)) atomicAdd(&sh.hist[(k - k0) >> shift], 1u);
         }
       });
       const CountMass above = cluster_sums(count, mass);
+      if (all_mass) goal.want = mass_part(goal.share, above.count, true);
       // From the top bin down: thread t has two bins, and what is above them.
       const unsigned long long start = goal.by_count ? above.count : above.mass;
       SamplePeer w = {};
@@ -890,7 +891,7 @@ struct SampleJob {
         __syncthreads();
         if (tid == 0) sh.count = 0;
         __syncthreads();
-        each(low == low ? low : -INFINITY, [&](const float* x, int v, int n) {
+        each(low, [&](const float* x, int v, int n) {
 #pragma unroll
           for (int e = 0; e < kPer; ++e) {
             if (e >= n) continue;
@@ -1271,7 +1272,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
     }
     if (!done) {
       const uint32_t top_bits = order_bits(most);
-      if (cut_k) limit = job.border_rank({true, (unsigned long long)st.top_k}, 0, 0, top_bits);
+      if (cut_k) limit = job.border_rank({true, (unsigned long long)st.top_k, 0.0f}, 0, 0, top_bits);
       if (cut_p) {
         // The border is among the entries whose mass is at least their share of what may be
         // left out; where about, a histogram of the distances from the maximum shows.
@@ -1462,17 +1463,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
           lo = order_bits(z_lo);
           hi = order_bits(fminf(z_hi, most));
         }
-        if (found == 0) {
-          unsigned long long m = 0;
-          const float z = limit > 0 ? from_order_bits((uint32_t)(limit >> 32)) : -INFINITY;
-          job.each(z, [&](const float* x, int v, int k) {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e)
-              if (e < k && entry_rank(x[e], v + e) >= limit) m += entry_mass(job.s, sh.table, x[e]);
-          });
-          const unsigned long long total = job.cluster_sums(0, m).mass;
-          found = job.border_rank({false, mass_part(st.top_p, total, true)}, limit, lo, hi);
-        }
+        if (found == 0) found = job.border_rank({false, 0, st.top_p}, limit, lo, hi);
         limit = found > limit ? found : limit;
       }
       limit = min_rank > limit ? min_rank : limit;

@@ -112,10 +112,8 @@ struct AtPart {
 };
 struct AtCta {
   AtPart part[2];
-  int timeout, bad_page;
-  int pad[14];
 };
-static_assert(sizeof(AtCta) == 128, "one line per CTA");
+constexpr int kAtLate = 1, kAtBadPage = 2;  // what a CTA has met: a timeout, a page outside the cache
 
 struct AtParams {
   PagedParams p;
@@ -126,6 +124,7 @@ struct AtParams {
   int slot_rows;   // rows of a part
   float scale2;    // scale log2 e
   AtCta* ctas;     // [kAtMaxCtas]
+  int* met;        // [kAtMaxCtas]
   float2* stats;   // [2 kAtMaxCtas, slot_rows]: (m, l)
   float* parts;    // [2 kAtMaxCtas, slot_rows, D]
   int main_ctas;
@@ -1233,8 +1232,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __syncthreads();
   tmem_fence_after();
   if (threadIdx.x == 0) {
-    a.ctas[blockIdx.x].timeout = ctl.abort_flag;
-    a.ctas[blockIdx.x].bad_page = ctl.bad_page;
+    a.met[blockIdx.x] = (ctl.abort_flag ? kAtLate : 0) | (ctl.bad_page ? kAtBadPage : 0);
   }
   if (warp == kAtIssuer) tmem1_free(tmem, 512);
 }
@@ -1334,17 +1332,15 @@ __global__ void __launch_bounds__(kAtJoinThreads)
   pdl_launch_dependents();
   const PagedParams& p = a.p;
   const AtPart u = a.ctas[c].part[1];
-  int late = 0, bad_page = 0;
-  for (int i = threadIdx.x; i < a.main_ctas; i += kAtJoinThreads) {
-    late |= a.ctas[i].timeout;
-    bad_page |= a.ctas[i].bad_page;
-  }
+  int met = 0;
+  for (int i = threadIdx.x; i < a.main_ctas; i += kAtJoinThreads) met |= a.met[i];
+  int late = met & kAtLate;
 #ifdef SPEC_DEBUG
   late |= g_debug_inject == SPEC_ERR_TIMEOUT;
 #endif
   late = __syncthreads_or(late);
-  bad_page = __syncthreads_or(bad_page);
   if (blockIdx.x == 0) {
+    const int bad_page = __syncthreads_or(met & kAtBadPage);
     int bad = 0;
     for (int b = threadIdx.x; b < p.c.B; b += kAtJoinThreads)
       bad += !request_ok(p, p.c.new_start[b], p.c.new_start[b + 1], p.c.kv_len[b]);

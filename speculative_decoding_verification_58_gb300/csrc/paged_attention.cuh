@@ -14,14 +14,26 @@
 //
 // In a CTA: a warp that loads pages by TMA into a ring of tiles, one that issues the
 // products, one that loads queries, one that works out the units, and two
-// warpgroups of softmax, a row per thread.  Each warpgroup has a stream of its own, with
-// scores and sums in tensor memory: in a unit of more than 128 rows, a half of the
-// rows each, over the same tiles; in a smaller one the same rows, the even tiles
-// and the odd ones, joined at the end.  One stream's softmax so runs under the other's
-// products.  The weights exp(s - m) go back to tensor memory as bfloat16 (relative 2^-8: the
-// products take both operands in one type) over the scores they come from, and are
-// the product's first operand there.  The running maximum is only raised when a score
-// passes it by more than 2^8, which leaves the sums' scaling out of almost every tile.
+// warpgroups of softmax.  Each warpgroup has a stream of its own, with scores and sums in
+// tensor memory, so that one stream's softmax runs under the other's products.
+//   more than 128 rows: each stream has 128 of them, a thread has a row.  The weights
+//     exp(s - m) go back to tensor memory over the scores they come from, and are the
+//     product's first operand there; a half of them is multiplied while the other is formed.
+//   up to 128 rows: the tiles are transposed, S^T = K Q^T and O^T += V^T P^T: a thread
+//     has an entry and all rows.  Up to 64 rows both streams have all of them and take
+//     the tiles in turn, else each has a part of the rows and all tiles.
+// The weights are rounded to bfloat16 (relative 2^-8: the products take both operands in one
+// type).  The running maximum is only raised when a score passes it by more than 2^8,
+// which leaves the sums' scaling out of almost every tile.
+//
+// Measured: 64 single tokens over up to 16384 entries (3.1 GB of keys and values) 475 to 496 us,
+// 6.3 to 6.6 TB/s: memory.  32 requests of up to 17 tokens over up to 8192 entries, pages
+// of 16: 186 us, 4.4 TB/s (pages of 64: 160 us; a page of 16 slots is 2 KB a copy, and the
+// copies of a tile take the loading as long as memory does).  Two chunks of 4096 tokens
+// behind 8192: 903 to 928 us, 1.17 to 1.2 PFLOP/s (51 % of the tensor cores' cycles): a
+// stream's softmax takes 1.1 us of a tile, the other's products 0.65.  One token over 8000
+// entries 23 us: 4.5 until the first page is on its way, 8 for three or four tiles and the
+// part's store, 5 for the join, and their launches.
 #pragma once
 
 #include "paged.cuh"
@@ -31,6 +43,7 @@
 namespace specv {
 
 constexpr int kAtThreads = 384;
+// Roles by warp; the softmax's warpgroups are the second and third.
 constexpr int kAtProducer = 0, kAtIssuer = 1, kAtQueries = 2, kAtPlanner = 3, kAtSoftmax = 4;
 constexpr int kAtTile = 128;      // entries per tile, rows per stream
 constexpr int kAtUnitRows = 256;  // rows per unit
@@ -355,6 +368,8 @@ __device__ __forceinline__ bool at_produce(const AtParams& a, const AtMaps& maps
   int loads = 0;
   bool ok = true;
   AtUnit u;
+  // The previous kernel's stores (the append) before this one's asynchronous reads.
+  asm volatile("fence.proxy.async;" ::: "memory");
   while (walk.next(ctl, u, ok)) {
     const int32_t* table = a.p.c.page_table + (size_t)u.b * a.p.c.max_pages;
     bool bad = false;

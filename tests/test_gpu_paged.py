@@ -230,6 +230,39 @@ def test_many_requests_of_mixed_lengths():
     b.run(False)
 
 
+def test_more_requests_than_threads():
+    g = torch.Generator().manual_seed(5)
+    for B in (385, 1500):
+        n = torch.randint(0, 6, (B,), generator=g).tolist()
+        t = torch.randint(0, 200, (B,), generator=g).tolist()
+        b = Batch([(x, max(x, y)) for x, y in zip(n, t)], Hk=1, G=2, D=64, P=16)
+        out, lse = sv.spec_paged_attention(b.q, *b.arrays(), need_lse=True)
+        b.check(out, lse, only=set(range(0, B, 7)) | {B - 1})
+        again = sv.spec_paged_attention(b.q, *b.arrays())
+        assert torch.equal(out, again)
+
+
+def test_units_of_all_kinds_in_turn():
+    """Small and large units next to each other in one CTA: their queries and weights take the
+    same shared memory."""
+    sizes = []
+    for i in range(40):
+        sizes += [(1, 3 + i), (100, 140), (20, 30), (1, 1), (40, 41), (70, 200 + i), (2, 600)]
+    for D in (64, 128):
+        b = Batch(sizes, Hk=2, G=4, D=D, P=64)
+        out, lse = sv.spec_paged_attention(b.q, *b.arrays(), need_lse=True)
+        b.check(out, lse, only=set(range(0, len(sizes), 5)) | {1, 2, 3, 4})
+
+
+def test_shared_pages():
+    """Requests with a common prefix name the same pages."""
+    b = Batch([(3, 200), (5, 210), (1, 140)], P=32)
+    for i in (1, 2):
+        b.table[i, :4] = b.table[0, :4]
+    b.run(True)
+    b.run(False)
+
+
 def test_long_context():
     b = Batch([(1, 100003), (17, 65537)], Hk=2, G=4, P=64)
     b.run(True)

@@ -574,14 +574,6 @@ __device__ __forceinline__ float og_exp_down(float x) {
   return __fmul_rn(ex2(-y), fmaf(rest, -kLn2f, 1.0f));
 }
 
-__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
-  return v;
-}
-
 // A window at a shared address; kShift: `shift` bytes into the blocks there.
 template <typename TIn, bool kShift>
 __device__ __forceinline__ OgWin og_smem(uint32_t addr, int shift) {

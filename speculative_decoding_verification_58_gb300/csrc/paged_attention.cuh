@@ -30,7 +30,7 @@
 // 6.3 to 6.6 TB/s: memory.  32 requests of up to 17 tokens over up to 8192 entries, pages
 // of 16: 186 us, 4.4 TB/s (pages of 64: 160 us; a page of 16 slots is 2 KB a copy, and the
 // copies of a tile take the loading as long as memory does).  Two chunks of 4096 tokens
-// behind 8192: 903 to 928 us, 1.17 to 1.2 PFLOP/s (51 % of the tensor cores' cycles): a
+// behind 8192: 955 us, 1.13 PFLOP/s (half of the tensor cores' cycles): a
 // stream's softmax takes 1.1 us of a tile, the other's products 0.65.  One token over 8000
 // entries 23 us: 4.5 until the first page is on its way, 8 for three or four tiles and the
 // part's store, 5 for the join, and their launches.
@@ -85,6 +85,15 @@ struct AtUnit {
   int bad;         // a page outside the cache
 };
 
+// The tiles of a unit, and which of their entries, that some of its rows see and others do not
+// and whose values are not finite.  (The rows of a unit end, and under a window start, within
+// 256 entries: in three tiles each.)
+struct AtOdd {
+  int tiles;
+  int tile[6];
+  uint32_t entries[6][kAtTile / 32];
+};
+
 struct AtControl {
   uint64_t full[10], empty[10];
   uint64_t s_full[2][2];  // of a stream; units of few rows have two sets of scores in turn
@@ -92,6 +101,7 @@ struct AtControl {
   uint64_t u_full[kAtUnits], u_empty[kAtUnits];
   uint64_t meet;  // of both warpgroups
   AtUnit unit[kAtUnits];
+  AtOdd odd[kAtUnits];
   // Few rows, per stream and row: the maximum in use, negated (inf: none yet), and what scores
   // take for it; what the sums are multiplied by.
   __align__(16) float above[2][kAtFewRows];  // (read four at a time)
@@ -104,6 +114,7 @@ struct AtControl {
   long long start_off, start_left, start_line, start_cost, total;
   int start_b;
   int abort_flag, bad_page;
+  uint32_t found_odd[kAtTile / 32];
   uint32_t tmem;
 };
 
@@ -266,6 +277,7 @@ __device__ __forceinline__ bool at_plan(const AtParams& a, AtControl& ctl) {
     if (round > 0 && !at_wait(&ctl.u_empty[slot], (round - 1) & 1, &ctl.abort_flag)) ok = false;
     if (!ok) return;
     ctl.unit[slot] = u;
+    ctl.odd[slot].tiles = 0;
     mbar_arrive(&ctl.u_full[slot]);
     if (++slot == kAtUnits) {
       slot = 0;
@@ -493,6 +505,74 @@ __device__ __forceinline__ bool at_load_queries(const AtParams& a, AtControl& ct
   return ok;
 }
 
+// Two bfloat16, those that are infinite or NaN as 0.
+__device__ __forceinline__ uint32_t at_finite(uint32_t x) {
+  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+  return x;
+}
+
+// 0 x + y of two bfloat16.
+__device__ __forceinline__ uint32_t at_zero_times(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(y));
+  return r;
+}
+
+// Values of a tile's entries from .. to - 1, which only some rows of the unit see: the others'
+// weights for them are 0, and where one is not finite the product would be NaN.  Those are set
+// to 0, and the rows that see them add them at the end.  A function of its own:
+// two chunks of 4096 tokens take 1005 us with it inlined, 955 so, 912 if nothing is looked at.
+template <int D>
+__device__ __noinline__ void at_sift(AtControl& ctl, int slot, uint32_t v, int tile, int from,
+                                     int to) {
+  const int lane = threadIdx.x & 31;
+  from = max(from - tile * kAtTile, 0);
+  to = min(to - tile * kAtTile, kAtTile);
+  if (from >= to) return;
+  const int chunks = (to - from) * (D / 8);
+  auto chunk = [&](int i) {
+    const int row = from + i / (D / 8), e = i % (D / 8);
+    return v + (e >> 3) * (kAtTile * 128) + row * 128 + (((e ^ row) & 7) << 4);
+  };
+  // (0 times them, added up, is NaN where one is.)
+  uint32_t sum = 0;
+  for (int first = lane; first < chunks; first += 32 * 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = ld_shared16(chunk(min(first + 32 * i, chunks - 1)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      sum = at_zero_times(
+          x[i].x, at_zero_times(x[i].y, at_zero_times(x[i].z, at_zero_times(x[i].w, sum))));
+  }
+  if (!__any_sync(0xffffffffu, (sum & 0x7fff7fffu) != 0)) return;
+  for (int i = lane; i < chunks; i += 32) {
+    const uint4 x = ld_shared16(chunk(i));
+    const uint4 y = make_uint4(at_finite(x.x), at_finite(x.y), at_finite(x.z), at_finite(x.w));
+    if (((x.x ^ y.x) | (x.y ^ y.y) | (x.z ^ y.z) | (x.w ^ y.w)) != 0) {
+      const int row = from + i / (D / 8);
+      st_shared16(chunk(i), y);
+      atomicOr(&ctl.found_odd[row >> 5], 1u << (row & 31));
+    }
+  }
+  __syncwarp();
+  if (lane == 0) {
+    AtOdd& odd = ctl.odd[slot];
+    const int n = odd.tiles;
+    odd.tile[n] = tile;
+#pragma unroll
+    for (int i = 0; i < kAtTile / 32; ++i) {
+      odd.entries[n][i] = ctl.found_odd[i];
+      ctl.found_odd[i] = 0;
+    }
+    odd.tiles = n + 1;
+    __threadfence_block();
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
 // The products: S = Q K^T and O += P V, of the streams in turn.
 template <int D>
 __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint32_t base,
@@ -618,8 +698,19 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
         mma1_f16_ta(d, p + i * 8, v + i * 128, kPv, i > from || !first, one);
     }
   };
+  int lo_all = 0, hi_all = 0;  // entries that all rows of the unit see
+  auto sift = [&](int stage, int j) {
+    const int tile = u.tile0 + j;
+    if (tile * kAtTile < lo_all)
+      at_sift<D>(ctl, walk.slot, base + stage * S::kTileBytes, tile, u.lo, lo_all);
+    if ((tile + 1) * kAtTile > hi_all)
+      at_sift<D>(ctl, walk.slot, base + stage * S::kTileBytes, tile, hi_all, u.hi);
+  };
   auto commit = [&](uint64_t* bar) { mma1_commit(bar, one); };
   while (ok && walk.next(ctl, u, ok)) {
+    int unused;
+    at_span(a.p, u.n, u.len, 0, at_token(a, u.r0), unused, hi_all);
+    at_span(a.p, u.n, u.len, at_token(a, u.r0 + u.rows - 1), 0, lo_all, unused);
     const int buf = q_used & 1;
     wait(&ctl.q_full[buf], q_used >> 1);
     ++q_used;
@@ -639,6 +730,7 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
         const int v = take();
         if (!ok) break;
         clear(v, j);
+        sift(v, j);
         values(0, v, j, j == 0);
         if (!ok) break;
         if (j + 1 < u.nt) {
@@ -672,6 +764,7 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
           const int v = take();
           if (!ok) break;
           clear(v, j - lag);
+          sift(v, j - lag);
           if (turn) {
             values_few(j & 1, v, j - lag, j - lag < 2);
           } else {
@@ -704,6 +797,40 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
     walk.done(ctl);
   }
   return ok;
+}
+
+// The values that were set to 0 join a row's results of dimensions e0 .. e1 - 1, which this
+// thread has written.  (The row's weights for them are above 0: a sum that one enters is it.)
+template <int D>
+__device__ __noinline__ void at_join_odd(const AtParams& a, const AtControl& ctl, int slot, int r,
+                                         int e0, int e1) {
+  const AtUnit& u = ctl.unit[slot];
+  const AtOdd& odd = ctl.odd[slot];
+  const spec_paged_cache_t& c = a.p.c;
+  int lo, hi;
+  const int t = at_token(a, u.r0 + r);
+  at_span(a.p, u.n, u.len, t, t, lo, hi);
+  uint16_t* out = a.p.out + at_head(a, u.first, u.h, u.r0 + r) * D;
+  float* part = a.parts + ((size_t)u.slot * a.slot_rows + r) * D;
+  for (int i = 0; i < odd.tiles; ++i)
+    for (int w = 0; w < kAtTile / 32; ++w)
+      for (uint32_t bits = odd.entries[i][w]; bits != 0; bits &= bits - 1) {
+        const int at = odd.tile[i] * kAtTile + w * 32 + __ffs(bits) - 1;
+        if (at < lo || at >= hi) continue;
+        const int page = c.page_table[(size_t)u.b * c.max_pages + (at >> a.page_bits)];
+        const uint16_t* x = static_cast<const uint16_t*>(c.v_cache) + page * c.v_page +
+                            (at & (c.page_size - 1)) * c.v_slot + u.h * c.v_head;
+        for (int e = e0; e < e1; ++e) {
+          if ((x[e] & 0x7f80) != 0x7f80) continue;
+          const float v = __uint_as_float((uint32_t)x[e] << 16);
+          if (u.slot >= 0) {
+            part[e] += v;
+          } else {
+            const float y = __uint_as_float((uint32_t)out[e] << 16);
+            out[e] = (uint16_t)(pack_bf16(y + v, 0.0f) & 0xffff);
+          }
+        }
+      }
 }
 
 // 32 results of a row, scaled.
@@ -875,6 +1002,8 @@ __device__ __forceinline__ void at_unit_rows(const AtParams& a, AtControl& ctl, 
         }
       }
     }
+    if (live && !bad && *(volatile int*)&ctl.odd[slot].tiles > 0)
+      at_join_odd<D>(a, ctl, slot, r, 0, D);
     if (live) {
       if (!whole) a.stats[slot_row] = make_float2(m, l);
       else if (a.p.lse != nullptr)
@@ -1162,6 +1291,10 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
         a.parts[((size_t)u.slot * a.slot_rows + r0 - u.r0 + r) * D + row] = y;
     }
   }
+  if (row < D && !bad && *(volatile int*)&ctl.odd[slot].tiles > 0)
+    for (int c = turn ? s * 16 : 0; c < rows; c += turn ? 32 : 16)
+      for (int r = c; r < min(c + 16, rows); ++r)
+        at_join_odd<D>(a, ctl, slot, r0 - u.r0 + r, row, row + 1);
   tmem_fence_before();
   // Neither stream's next products may write sums that the other still reads, nor queries
   // what is in the weights' place.
@@ -1224,6 +1357,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       ctl.raise[i][0] = ctl.raise[i][1] = 0;
     }
     ctl.abort_flag = ctl.bad_page = 0;
+    for (int i = 0; i < kAtTile / 32; ++i) ctl.found_odd[i] = 0;
     fence_mbar_init();
   }
   if (warp == kAtIssuer) tmem1_alloc(&ctl.tmem, 512);

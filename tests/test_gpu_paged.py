@@ -200,6 +200,64 @@ def test_what_lies_past_the_entries_is_not_used(fill):
             assert torch.equal(b2.run(True)[0], out)
 
 
+@pytest.mark.parametrize("odd", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 1), (True, 3), (True, 40), (True, 200),
+                                           (False, 0)])
+@pytest.mark.parametrize("D,G,P", [(128, 4, 16), (64, 2, 64), (128, 1, 256)])
+def test_values_that_some_rows_do_not_see(D, G, P, causal, window, odd):
+    """A value that is not finite is met by its dimension's results of the rows that see it, and
+    by nothing else: the other results are those of a 0 in its place."""
+    sizes = [(6, 300), (6, 6), (1, 77), (20, 400), (31, 31), (100, 300), (300, 520), (2, 130)]
+    b = Batch(sizes, Hk=2, G=G, D=D, P=P, seed=11)
+    spots = []  # request, entry, head, dimension
+    for i, (n, t) in enumerate(sizes):
+        for j, x in enumerate({t - 1, t - n, t - n // 2 - 1, max(0, t - n - 20), t // 3}):
+            spots.append((i, x, j % 2, (7 * j + 13 * i) % D))
+    v = b.v.clone()
+
+    def put(what):
+        b.v.copy_(v)
+        for i, x, h, d in spots:
+            b.v[b.table[i, x // P].long(), x % P, h, d] = what
+
+    put(0.0)
+    want, lse = b.run(causal, window)
+    want = want.clone()
+    for i, x, h, d in spots:
+        n, t = sizes[i]
+        for k in range(n):
+            at = t - n + k
+            if not causal or (x <= at and (window == 0 or x > at - window)):
+                want[b.starts[i] + k, h * G:(h + 1) * G, d] += odd
+    put(odd)
+    out, l2 = sv.spec_paged_attention(b.q, *b.arrays(), causal=causal, window=window, need_lse=True)
+    assert torch.equal(lse, l2)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
+
+
+@pytest.mark.parametrize("odd", [math.nan, math.inf])
+@pytest.mark.parametrize("window", [0, 3, 150])
+def test_keys_that_some_rows_do_not_see(window, odd):
+    sizes = [(6, 300), (20, 400), (100, 300), (300, 520)]
+    b = Batch(sizes, Hk=2, G=4, seed=12)
+    want, lse = b.run(True, window)
+    k = b.k.clone()
+    for i, (n, t) in enumerate(sizes):
+        x = t - n // 2 - 1
+        b.k[b.table[i, x // b.P].long(), x % b.P] = odd
+    out, l2 = sv.spec_paged_attention(b.q, *b.arrays(), causal=True, window=window, need_lse=True)
+    for i, (n, t) in enumerate(sizes):
+        at = torch.arange(t - n, t, device=DEV)
+        x = t - n // 2 - 1
+        rows = b.starts[i] + torch.nonzero((at >= x) & ((at - window < x) if window else True))[:, 0]
+        if math.isnan(odd):
+            assert bool(torch.isnan(out[rows]).all()) and bool(torch.isnan(l2[rows]).all())
+        out[rows], l2[rows] = want[rows], lse[rows]
+    b.k.copy_(k)
+    b.check(out, l2, True, window)
+
+
 @pytest.mark.parametrize("sharp", [0.01, 8.0, 64.0])
 def test_flat_and_sharp_scores(sharp):
     b = Batch([(1, 2000), (17, 700), (150, 150)], sharp=sharp)

@@ -85,6 +85,7 @@ struct MassScale {
   FF inv;  // log2(e) / T
   int unit_bits;
   float floor;
+  float near;  // what the sums in single precision are next to
 };
 __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, const MassTable& t,
                                                          float z) {
@@ -114,10 +115,10 @@ __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, con
   return shift > 63 ? 0 : ((m << 23) + (1ull << ((shift - 1) & 63))) >> (shift & 63);
 }
 
-// The same in single precision, to about 2^-22 of itself, for sums that only have to tell on
-// which side of a border they are.  (What is below `floor` has no mass.)
+// exp((z - near) / T) in single precision, to about 2^-21 of itself, for sums that only have
+// to tell on which side of a border they are.  (What is below `floor` has no mass.)
 __device__ __forceinline__ float near_mass(const MassScale& s, float z) {
-  const float d = __fsub_rn(fmaxf(z, s.floor), s.max);
+  const float d = __fsub_rn(fmaxf(z, s.floor), s.near);
   return ex2(__fmaf_rn(d, s.inv.hi, __fmul_rn(d, s.inv.lo)));
 }
 // In whole units of 2^-32 (the largest entry's 2^32 - 1 then), for the draw.
@@ -125,12 +126,19 @@ __device__ __forceinline__ uint32_t draw_mass(const MassScale& s, float z) {
   return __float2uint_rn(__fmul_rn(ex2(__fmul_rn(__fsub_rn(z, s.max), s.inv.hi)), 4294967296.0f));
 }
 // A scale next to `max`; false where the temperature is too high for `floor` to leave out
-// entries of -inf.
+// entries of -inf.  `near` is the next multiple of a power of two up to T ln 2: a difference
+// from the maximum itself is off by the same for all entries of a binade, whose last bits the
+// maximum's go beyond (by 2^-21 around 10; sums next to it moved borders by up to 10^-7
+// of the mass), one from a round number by as much up as down.
 __device__ __forceinline__ bool mass_scale(MassScale& s, float max, FF inv, int unit_bits) {
   s.max = max;
   s.inv = inv;
   s.unit_bits = unit_bits;
   s.floor = __fsub_rn(max, __fdiv_rn(200.0f, inv.hi));
+  const float step =
+      __uint_as_float(__float_as_uint(__fdiv_rn(1.0f, inv.hi)) & 0x7f800000u);
+  const float steps = __fdiv_rn(max, step);
+  s.near = fabsf(steps) < 8388608.0f ? __fmul_rn(ceilf(steps), step) : max;
   return s.floor >= -FLT_MAX;
 }
 
@@ -1184,14 +1192,15 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   }
   bad |= !(most >= -FLT_MAX);
   scaled &= mass_scale(job.s, most, sh.inv, p.unit_bits);
-  // The row's mass next to its largest entry's, in units of 2^-kNearBits; 0: not known.
+  // The row's mass next to `near`, in units of 2^-kNearBits; 0: not known.
   unsigned long long about = 0;
   if (share && !bad) {
     SamplePeer w = {};
     if (tid == 0) {
       double x = (double)sum.hi + (double)sum.lo;
-      if (s0.max != most)
-        x *= exp2(((double)s0.max - (double)most) * ((double)sh.inv.hi + (double)sh.inv.lo));
+      if (s0.near != job.s.near)
+        x *= exp2(((double)s0.near - (double)job.s.near) *
+                  ((double)sh.inv.hi + (double)sh.inv.lo));
       x *= 1099511627776.0;
       w.a = x > 0.0 && x < 4611686018427387904.0 ? (unsigned long long)x : 0;
       w.i = !(x < 4611686018427387904.0) || !scaled;
@@ -1291,7 +1300,8 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
         // left out; where about, a histogram of the distances from the maximum shows.
         uint32_t lo = (uint32_t)(limit >> 32), hi = top_bits;
         unsigned long long found = 0;
-        const float mass = (float)about * exp2f(-(float)kNearBits);
+        const float mass = (float)about * exp2f(-(float)kNearBits) *
+                           ex2(__fmul_rn(__fsub_rn(job.s.near, most), job.s.inv.hi));
         const float range = logf((float)V / ((1.0f - st.top_p) * mass)) + 0.001f;
         const float per = __fmul_rn(__fmul_rn(job.s.inv.hi, kLn2f), (float)kSampleBins / range);
         if (about != 0 && range > 0.0f && per > 0.0f && per <= FLT_MAX) {

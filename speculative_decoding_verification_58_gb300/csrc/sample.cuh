@@ -1192,8 +1192,13 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   }
   bad |= !(most >= -FLT_MAX);
   scaled &= mass_scale(job.s, most, sh.inv, p.unit_bits);
+  // The sums to come are next to what the first pass's were where it can be, so that an entry
+  // has the same mass in all of them and what a large one is off by is in common.
+  if (share && ctas == 1 && __fmul_rn(__fsub_rn(most, s0.near), sh.inv.hi) < 8.0f)
+    job.s.near = s0.near;
   // The row's mass next to `near`, in units of 2^-kNearBits; 0: not known.
   unsigned long long about = 0;
+  bool apart = false;
   if (share && !bad) {
     SamplePeer w = {};
     if (tid == 0) {
@@ -1203,13 +1208,14 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
                   ((double)sh.inv.hi + (double)sh.inv.lo));
       x *= 1099511627776.0;
       w.a = x > 0.0 && x < 4611686018427387904.0 ? (unsigned long long)x : 0;
-      w.i = !(x < 4611686018427387904.0) || !scaled;
+      w.i = !(x < 4611686018427387904.0) || !scaled ? 1 : s0.near != job.s.near ? 2 : 0;
     }
     all = job.exchange(w);
     bool known = true;
     for (int i = 0; i < ctas; ++i) {
       about += all[i].a;
-      known = known && all[i].i == 0;
+      known = known && all[i].i != 1;
+      apart |= all[i].i == 2;
     }
     if (!known) about = 0;
   }
@@ -1223,8 +1229,9 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   // Sums in single precision on both sides: what they are off by in common (the exponential's
   // mean error is -5e-8) does not matter, and what is left of it is a few parts in 10^9 of
   // the mass (thousands of entries, 10^-7 each).  Unless the border is some six times as far,
-  // the exact sums decide.
-  const unsigned long long want = mass_part(st.top_p, about, true), doubt = about >> 25;
+  // the exact sums decide.  (Of sums next to different numbers an entry's share is off by up to
+  // 2^-22 of itself: 2^-21 of the mass.)
+  const unsigned long long want = mass_part(st.top_p, about, true), doubt = about >> (apart ? 21 : 25);
   auto border_of = [&](int n, unsigned long long above) -> int {  // in the sorted list, or -1
     if (n <= 0 || want <= above) return -1;
     const int i = first_reaching(sh.mass, n, want - above);

@@ -338,3 +338,24 @@ def test_past_32_bit_offsets():
     assert torch.equal(tokens.long(), at)
     sv.spec_truncate(z, T, top_k=k, kept=z)
     assert torch.equal((z[-64:] > -math.inf).sum(1), torch.full((64,), 3, device=DEV))
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_borders_of_many_flat_float_rows(seed):
+    """Where the mass reaches top_p, against sums in 64 bits: entries of 10^-6 of the mass, and
+    maxima whose last bits the other entries do not have."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    B, n, V = 16, 17, 151936
+    z = torch.randn((B, n, V), generator=g, device="cuda")
+    z -= 1.1 * torch.log(torch.arange(1, V + 1, device="cuda", dtype=torch.float32))
+    T = 0.8 + 0.5 * torch.rand(B, generator=g, device="cuda")
+    p = torch.where(torch.arange(B, device="cuda") % 2 == 0, 0.95, 0.99)
+    kept = sv.spec_truncate(z, T, top_p=p) != -math.inf
+    for b in range(B):
+        zs, order = torch.sort(z[b], dim=1, descending=True, stable=True)
+        m = torch.exp((zs.double() - zs[:, :1].double()) / T[b].double())
+        upto = torch.cumsum(m, 1)
+        less = upto - m - p[b].double() * upto[:, -1:]
+        want = torch.zeros_like(kept[b]).scatter_(1, order, less < 0)
+        unclear = torch.zeros_like(want).scatter_(1, order, less.abs() < 1e-11 * upto[:, -1:])
+        assert bool(((kept[b] == want) | unclear).all())

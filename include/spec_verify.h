@@ -559,9 +559,10 @@ spec_status_t spec_clip_grad_norm(const void* const* grads, void* const* outs,
  * row of NaN (which verification reports as invalid); at T = 0 a NaN is never the
  * maximum, as for spec_verify.  A uniform out of range gives token -1 alone.
  * K is exact: the masses that decide it are whole numbers (each right to about 2^-38
- * of itself, in units of 2^-42 of the largest or finer), or sums in single precision
- * where these leave no doubt, so that it does not depend on the order of additions.  A
- * draw weighs the entries of K to 2^-20 of themselves or better, in whole numbers as well.
+ * of itself, in units of 2^-42 of the largest or finer; temperatures up to 2^100), or sums in
+ * single precision where these leave no doubt, so that it does not depend on the order of
+ * additions.  A draw from more of a row than the entries that the kernel lists weighs
+ * them by the same masses.
  */
 spec_status_t spec_sample(const void* logits, spec_dtype_t dtype, int rows, int V, int group,
                           const float* temperature, const int32_t* top_k, const float* top_p,

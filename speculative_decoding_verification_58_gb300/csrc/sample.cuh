@@ -11,12 +11,15 @@
 // units of 2^-42 of the largest (2^-45 for V up to 2^18), formed to about 2^-37 of itself,
 // and sums of masses are 64-bit integers: exact, and the same in any order of additions.
 // Sums in single precision stand in for them only where they are far enough from the border
-// (see `doubt`), and weigh the entries of a draw from all over a row, where a relative
-// error of 10^-7 moves one token in millions of draws.
+// (see `doubt`).  A draw is a border too, and weighs its entries alike: by masses that are
+// quicker to form and right to 2^-28 where the level is further than what sums of those may be
+// off by from both sums next to it, by the exact ones else.  (Weights from the exponential
+// unit alone, 10^-7 off, draw another token in one of some hundred rows: every border between
+// two of 10^5 entries may be on the wrong side of the level.)
 //
 // Measured on rows of 151936 (2048 of them, us; reading them once takes 92 in bfloat16 and
 // 184 in float): greedy 124 and 216, top_k = 50 218 and 294, top_k = 400 343 and 384, no
-// truncation 299 and 423, top_p = 0.95 alone on rows with Zipf's tail 1255 and 1235; one
+// truncation 640 and 740 (with exact masses alone 1000 and 1040), top_p = 0.95 alone on rows with Zipf's tail 1255 and 1235; one
 // row, top_k = 50: 13.  Greedy and top-k rows are bound by memory and by the latencies of the
 // list's steps (two CTAs an SM; four of 256 threads: 200, but rows that take several
 // passes then do not stay in L2: top_p 1743), the others by instruction issue.
@@ -86,6 +89,11 @@ struct MassScale {
   int unit_bits;
   float floor;
   float near;  // what the sums in single precision are next to
+  // For quick_mass: x = max log2(e) / T is start / 32 (less the bits of its rounding constant)
+  // and `rest`; entries below `low` have less than half a unit.
+  float rest, low;
+  int start;
+  bool quick;
 };
 __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, const MassTable& t,
                                                          float z) {
@@ -121,10 +129,45 @@ __device__ __forceinline__ float near_mass(const MassScale& s, float z) {
   const float d = __fsub_rn(fmaxf(z, s.floor), s.near);
   return ex2(__fmaf_rn(d, s.inv.hi, __fmul_rn(d, s.inv.lo)));
 }
-// In whole units of 2^-32 (the largest entry's 2^32 - 1 then), for the draw.
-__device__ __forceinline__ uint32_t draw_mass(const MassScale& s, float z) {
-  return __float2uint_rn(__fmul_rn(ex2(__fmul_rn(__fsub_rn(z, s.max), s.inv.hi)), 4294967296.0f));
+// The same mass as entry_mass, but for 2^-28 of itself and two units, in a third of its
+// instructions: sums of it tell on which side of a border they are unless they are next to it
+// (`quick_doubt`).  x = (z - max) log2(e) / T is k / 32 + r, |r| < 2^-5; 2^r = 1 + q by four
+// terms of its series.  Roundings of r: 2^-31 each of z's part and the maximum's, of their
+// product with inv.lo and of `rest`, 2^-30 of their sum, times ln 2; q: 2^-30 of its sum, 2^-31
+// of ln 2; 2^(k / 32) in units of 2^-30 and its product with 1 + q: half a unit each; what the
+// series leaves out 2^-34: 4.4 2^-30 in all.  (Measured: 2^-28.3 at most.)
+constexpr float kQuickRound = 393216.0f;  // 1.5 2^18: rounds to 1 / 32
+struct QuickTable {
+  int e[32];
+};
+constexpr QuickTable quick_table() {
+  QuickTable t = {};
+  for (int j = 0; j < 32; ++j)
+    t.e[j] = (int)((mass_table().e[8 * j] + 256) >> 9);
+  return t;
 }
+__device__ const QuickTable g_quick_table = quick_table();
+
+__device__ __forceinline__ unsigned long long quick_mass(const MassScale& s, const int* table, float z) {
+  constexpr float kOne = 4294967296.0f;  // (q in units of 2^-32)
+  const float x = fmaxf(z, s.low);
+  const float t = __fmaf_rn(x, s.inv.hi, kQuickRound);
+  const float r = __fadd_rn(__fmaf_rn(x, s.inv.hi, -__fsub_rn(t, kQuickRound)),
+                            __fmaf_rn(x, s.inv.lo, -s.rest));
+  const int k = __float_as_int(t) - s.start;
+  const int e = table[k & 31];
+  const float h = __fmaf_rn(r, __fmaf_rn(r, 0.00961812910762847716f * kOne, 0.0555041086648215800f * kOne),
+                            0.240226506959100712f * kOne);
+  const int q = __float2int_rn(__fmaf_rn(r, kLn2f * kOne, __fmul_rn(__fmul_rn(r, r), h)));
+  const long long m = (long long)e * q + (((long long)e << 32) | 0x80000000u);
+  // (k is 1 at most, -57 * 32 at least.)
+  return ((m >> 32) << 15) >> (45 - s.unit_bits - (k >> 5));
+}
+// How far a sum of quick masses may be from the exact ones': of n entries, `total` in all.
+__device__ __forceinline__ unsigned long long quick_doubt(unsigned long long total, int n) {
+  return (total >> 26) + 2ull * n;
+}
+
 // A scale next to `max`; false where the temperature is too high for `floor` to leave out
 // entries of -inf.  `near` is the next multiple of a power of two up to T ln 2: a difference
 // from the maximum itself is off by the same for all entries of a binade, whose last bits the
@@ -139,6 +182,13 @@ __device__ __forceinline__ bool mass_scale(MassScale& s, float max, FF inv, int 
       __uint_as_float(__float_as_uint(__fdiv_rn(1.0f, inv.hi)) & 0x7f800000u);
   const float steps = __fdiv_rn(max, step);
   s.near = fabsf(steps) < 8388608.0f ? __fmul_rn(ceilf(steps), step) : max;
+  FF x = two_prod(max, inv.hi);
+  x.lo = __fmaf_rn(max, inv.lo, x.lo);
+  const float k = rintf(__fmul_rn(x.hi, 32.0f));
+  s.rest = __fadd_rn(__fsub_rn(x.hi, __fmul_rn(k, 0.03125f)), x.lo);  // (the difference is exact)
+  s.low = __fsub_rn(max, __fdiv_rn(56.0f, inv.hi));
+  s.quick = fabsf(x.hi) <= 16384.0f && inv.hi >= 0x1p-80f && s.low >= -FLT_MAX;
+  s.start = __float_as_int(kQuickRound) + (s.quick ? (int)k : 0);
   return s.floor >= -FLT_MAX;
 }
 
@@ -249,6 +299,7 @@ struct SampleShared {
     unsigned long long fine[kSampleFine];
   };
   MassTable table;
+  QuickTable quick;
   unsigned long long sums[256];  // of a draw from the list
   SamplePeer peer[2][kSampleMaxCluster];
   unsigned long long red[2][kSampleWarps];
@@ -701,13 +752,14 @@ struct SampleJob {
   }
 
   // The first index, ascending, whose weight with all lower ones' exceeds `level(total)`; -1
-  // if none does.  Weights of the warps' runs first; the warp in whose run the level is passed
+  // if none does, or if the level is not further than `doubt(total)` from both that sum and
+  // the one before.  Weights of the warps' runs first; the warp in whose run the level is passed
   // goes through it again.
   // Then the CTA in whose run the level is passed goes through that warp's run again, shared
   // out among its warps, and one of these through its share (one warp through all of the
   // run, a load after the other, took 17 us of a row of 151936).
-  template <typename W, typename L>
-  __device__ __forceinline__ int locate(float least, W&& weight, L&& level_of) {
+  template <typename W, typename L, typename D>
+  __device__ __forceinline__ int locate(float least, W&& weight, L&& level_of, D&& doubt_of) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tail0 = first + nvec * kPer;
     auto single = [&](int v, bool here) -> unsigned long long {
@@ -750,7 +802,7 @@ struct SampleJob {
       if (i < rank) upto += all[i].a;
       total += all[i].a;
     }
-    const unsigned long long level = level_of(total);
+    const unsigned long long level = level_of(total), doubt = doubt_of(total);
     if (upto <= level && level < upto + w.a) {
       auto pick = [&]() -> int {  // the warp in whose part the level is passed
         int q = 0;
@@ -777,32 +829,41 @@ struct SampleJob {
           const uint32_t over = __ballot_sync(0xffffffffu, upto + sum > level);
           if (over != 0) {
             const int l = __ffs(over) - 1;
-            if (lane == l) found = finish(upto + sum - x);
+            if (lane == l) found = finish(upto + sum - x, upto + sum);
             found = __shfl_sync(0xffffffffu, found, l);
           }
           upto += __shfl_sync(0xffffffffu, sum, 31);
         };
+        // (The sums before an entry and with it.)
+        auto sure = [&](int v, unsigned long long less, unsigned long long sum) {
+          return level - less >= doubt && sum - level > doubt ? v : -2;
+        };
         if (heads > 0) {
           const int v = first - head + lane;
-          look(single(v, lane < heads), [&](unsigned long long) { return v; });
+          look(single(v, lane < heads),
+               [&](unsigned long long less, unsigned long long sum) { return sure(v, less, sum); });
         }
-        for (int i0 = from; i0 < to && found < 0; i0 += 32) {
+        for (int i0 = from; i0 < to && found == -1; i0 += 32) {
           const int i = i0 + lane;
-          look(i < to ? vector_weight(i) : 0, [&](unsigned long long c) {
+          look(i < to ? vector_weight(i) : 0, [&](unsigned long long less, unsigned long long) {
             float x[kPer];
             Tr::unpack(run[i], x);
             int v = first + i * kPer;
+            unsigned long long sum = less;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-              c += weight(x[e], first + i * kPer + e);
-              if (c <= level) ++v;
+              if (sum > level) break;
+              less = sum;
+              sum += weight(x[e], first + i * kPer + e);
+              v = first + i * kPer + e;
             }
-            return v;
+            return sure(v, less, sum);
           });
         }
-        if (tails > 0 && found < 0) {
+        if (tails > 0 && found == -1) {
           const int v = tail0 + lane;
-          look(single(v, lane < tails), [&](unsigned long long) { return v; });
+          look(single(v, lane < tails),
+               [&](unsigned long long less, unsigned long long sum) { return sure(v, less, sum); });
         }
         if (lane == 0) sh.border = found;
       }
@@ -948,7 +1009,7 @@ struct SampleJob {
             z, [&](float y, int at) -> unsigned long long {
               return order_bits(y) >> kDrop == b0 && entry_rank(y, at) >= from ? 1 : 0;
             },
-            [&](unsigned long long) { return nth - 1; });
+            [&](unsigned long long) { return nth - 1; }, [](unsigned long long) { return 0ull; });
         return entry_rank(z, v);
       }
       lo = b0 << kDrop;
@@ -969,6 +1030,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   if (ctas > 1) cluster_arrive();  // (waited for before the first word to another CTA)
   if (tid == 0) sh.count = 0;
   for (int i = tid; i < 256; i += kSampleThreads) sh.table.e[i] = g_mass_table.e[i];
+  if (tid < 32) sh.quick.e[tid] = g_quick_table.e[tid];
   pdl_wait();
   pdl_launch_dependents();
   SampleJob<TIn> job = {sh, p};
@@ -1471,7 +1533,8 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
                                                 [&](float y, int) -> unsigned long long {
                                                   return order_bits(y) >> 16 == key ? 1 : 0;
                                                 },
-                                                [&](unsigned long long) { return nth - 1; }));
+                                                [&](unsigned long long) { return nth - 1; },
+                                                [](unsigned long long) { return 0ull; }));
             }
           } else {
           // What is above those bins, and their entries one by one.
@@ -1511,13 +1574,26 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
         // (z itself decides but for the entries equal to the last one kept.)
         const float z_least = limit > 0 ? from_order_bits((uint32_t)(limit >> 32)) : -INFINITY;
         const uint32_t last = ~(uint32_t)limit;
-        token = job.locate(
-            z_least,
-            [&](float z, int v) -> unsigned long long {
-              const uint32_t m = draw_mass(job.s, z);
-              return (z > z_least) | ((z == z_least) & ((uint32_t)v <= last)) ? m : 0;
-            },
-            [&](unsigned long long total) { return mass_part(u, total, false); });
+        auto drawn = [&](float z, int v) -> bool {
+          return (z > z_least) | ((z == z_least) & ((uint32_t)v <= last));
+        };
+        auto level = [&](unsigned long long total) { return mass_part(u, total, false); };
+        // Quick masses tell the token, but for one draw in some hundred over a flat row.
+        if (job.s.quick)
+          token = job.locate(
+              z_least,
+              [&](float z, int v) -> unsigned long long {
+                const unsigned long long m = quick_mass(job.s, sh.quick.e, z);
+                return drawn(z, v) ? m : 0;
+              },
+              level, [&](unsigned long long total) { return quick_doubt(total, V); });
+        if (token < 0)
+          token = job.locate(
+              z_least,
+              [&](float z, int v) -> unsigned long long {
+                return drawn(z, v) ? entry_mass(job.s, sh.table, z) : 0;
+              },
+              level, [](unsigned long long) { return 0ull; });
       }
     }
     if (!u_ok) token = -1;

@@ -1346,6 +1346,8 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
           limit = sh.list[kept - 1];
         }
         if (done && want_token && u_ok) {
+          // (The draw takes the same masses wherever it looks, in whichever of the calls a row is.)
+          if (share) job.list_masses(kept, false);
           const unsigned long long level = mass_part(u, sh.mass[kept - 1], false);
           token = job.draw_listed(kept, level);
         }

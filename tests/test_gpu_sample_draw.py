@@ -138,3 +138,42 @@ def test_largest_vocabulary_peaked():
     after = float(w[V // 3 + 1:].sum() / w.sum())
     u = 1.0 - 2 * after * torch.rand(64, generator=gen(9), device=DEV)
     check_row(z, 1.0, u.clamp(max=1.0 - 2.0 ** -24), 16, most_unclear=1.0)
+
+
+def steps(V, dt, seed):
+    """A thousand entries of a few values, the rest far below: what top-p keeps of such a row is
+    among its largest thousand."""
+    g = gen(seed)
+    z = torch.full((V,), -12.0, device=DEV)
+    at = torch.randperm(V, generator=g, device=DEV)[:1000]
+    values = torch.tensor([5.0, 4.3, 4.1, 2.7], device=DEV)
+    z[at] = values[torch.randint(0, 4, (1000,), generator=g, device=DEV)]
+    z[at[0]] = 5.6
+    return z.to(DT[dt])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,T,p", [("steps", 0.7, 0.9), ("steps", 1.3, 0.9), ("zipf", 0.7, 0.5),
+                                      ("zipf", 0.5, 0.8)])
+def test_uniforms_at_borders_of_listed_entries(kind, T, p, dt):
+    z = steps(FULL, dt, 8) if kind == "steps" else zipf(1, FULL, 3)[0].to(DT[dt])
+    u = border_uniforms(z, T, 1024, 5, p=p)
+    check_row(z, T, u, 512, p=p)
+    check_row(z, T, u[:48], 3, p=p)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["steps", "zipf", "gauss"])
+@pytest.mark.parametrize("p", [0.5, 0.9, 1.0])
+def test_a_row_draws_the_same_in_every_batch(p, kind, dt):
+    V = 50021
+    z = steps(V, dt, 8) if kind == "steps" else (
+        zipf(1, V, 3)[0] if kind == "zipf" else torch.randn(V, generator=gen(4), device=DEV)).to(DT[dt])
+    u = border_uniforms(z, 0.8, 512, 5, p=p)
+    want = None
+    for rows in (512, 150, 37, 1):
+        tok = [sv.spec_sample(z.expand(v.numel(), -1).contiguous(), per_row(0.8, v.numel()), v.contiguous(),
+                              **settings(v.numel(), p=p)) for v in u[:512 if rows > 1 else 40].split(rows)]
+        tok = torch.cat(tok)
+        want = tok if want is None else want
+        assert torch.equal(tok, want[:tok.numel()])

@@ -559,10 +559,10 @@ spec_status_t spec_clip_grad_norm(const void* const* grads, void* const* outs,
  * row of NaN (which verification reports as invalid); at T = 0 a NaN is never the
  * maximum, as for spec_verify.  A uniform out of range gives token -1 alone.
  * K is exact: the masses that decide it are whole numbers (each right to about 2^-38
- * of itself, in units of 2^-42 of the largest or finer; temperatures up to 2^100), or sums in
- * single precision where these leave no doubt, so that it does not depend on the order of
- * additions.  A draw weighs the entries of K by these masses as well: neither K nor the token
- * depends on the other rows of the call.
+ * of itself, in units of 2^-42 of the largest or finer; temperatures up to 2^100), or sums of
+ * less exact ones where the border is further from them than they may be off by.  A draw
+ * weighs the entries of K by these masses as well.  So neither K nor the token depends on the
+ * order of additions or on the other rows of the call.
  */
 spec_status_t spec_sample(const void* logits, spec_dtype_t dtype, int rows, int V, int group,
                           const float* temperature, const int32_t* top_k, const float* top_p,

@@ -10,12 +10,12 @@
 // So where a border is decided every entry's mass exp((z - max) / T) is a whole number of
 // units of 2^-42 of the largest (2^-45 for V up to 2^18), formed to about 2^-37 of itself,
 // and sums of masses are 64-bit integers: exact, and the same in any order of additions.
-// Sums in single precision stand in for them only where they are far enough from the border
-// (see `doubt`).  A draw is a border too, and weighs its entries alike: by masses that are
-// quicker to form and right to 2^-28 where the level is further than what sums of those may be
-// off by from both sums next to it, by the exact ones else.  (Weights from the exponential
-// unit alone, 10^-7 off, draw another token in one of some hundred rows: every border between
-// two of 10^5 entries may be on the wrong side of the level.)
+// Masses that are less exact, but quicker to form, stand in for them only where the border is
+// further away than their sums may be off by (quick_mass, 2^-28 of themselves; near_mass, 2^-16,
+// of what is far below it).  A draw is a border too, and weighs its entries alike.  (Weights from
+// the exponential unit alone, 10^-7 off, draw another token in one of some hundred rows: every
+// border between two of 10^5 entries may be on the wrong side of the level.  And errors of that
+// size do not average out where thousands of entries are equal, as plateaus of bfloat16 rows.)
 //
 // Measured on rows of 151936 (2048 of them, us; reading them once takes 92 in bfloat16 and
 // 184 in float): greedy 124 and 216, top_k = 50 218 and 294, top_k = 400 343 and 384, no
@@ -87,8 +87,7 @@ struct MassScale {
   float max;
   FF inv;  // log2(e) / T
   int unit_bits;
-  float floor;
-  float near;  // what the sums in single precision are next to
+  float floor;  // of near_mass
   // For quick_mass: x = max log2(e) / T is start / 32 (less the bits of its rounding constant)
   // and `rest`; entries below `low` have less than half a unit.
   float rest, low;
@@ -123,11 +122,11 @@ __device__ __forceinline__ unsigned long long entry_mass(const MassScale& s, con
   return shift > 63 ? 0 : ((m << 23) + (1ull << ((shift - 1) & 63))) >> (shift & 63);
 }
 
-// exp((z - near) / T) in single precision, to about 2^-21 of itself, for sums that only have
-// to tell on which side of a border they are.  (What is below `floor` has no mass.)
+// exp((z - max) / T) in single precision for z <= max, to 2^-16 of itself: |x| <= 64 has three
+// roundings of 2^-24 of itself, times ln 2, and the exponential is right to 2^-22.  (What is
+// below `floor` counts as 2^-64.)
 __device__ __forceinline__ float near_mass(const MassScale& s, float z) {
-  const float d = __fsub_rn(fmaxf(z, s.floor), s.near);
-  return ex2(__fmaf_rn(d, s.inv.hi, __fmul_rn(d, s.inv.lo)));
+  return ex2(__fmul_rn(__fsub_rn(fmaxf(z, s.floor), s.max), s.inv.hi));
 }
 // The same mass as entry_mass, but for 2^-28 of itself and two units, in a third of its
 // instructions: sums of it tell on which side of a border they are unless they are next to it
@@ -165,23 +164,16 @@ __device__ __forceinline__ unsigned long long quick_mass(const MassScale& s, con
 }
 // How far a sum of quick masses may be from the exact ones': of n entries, `total` in all.
 __device__ __forceinline__ unsigned long long quick_doubt(unsigned long long total, int n) {
-  return (total >> 26) + 2ull * n;
+  return (total >> 27) + 2ull * n;
 }
 
-// A scale next to `max`; false where the temperature is too high for `floor` to leave out
-// entries of -inf.  `near` is the next multiple of a power of two up to T ln 2: a difference
-// from the maximum itself is off by the same for all entries of a binade, whose last bits the
-// maximum's go beyond (by 2^-21 around 10; sums next to it moved borders by up to 10^-7
-// of the mass), one from a round number by as much up as down.
+// Masses next to the largest entry's; false where the temperature is too high for `floor` to
+// leave out entries of -inf.
 __device__ __forceinline__ bool mass_scale(MassScale& s, float max, FF inv, int unit_bits) {
   s.max = max;
   s.inv = inv;
   s.unit_bits = unit_bits;
-  s.floor = __fsub_rn(max, __fdiv_rn(200.0f, inv.hi));
-  const float step =
-      __uint_as_float(__float_as_uint(__fdiv_rn(1.0f, inv.hi)) & 0x7f800000u);
-  const float steps = __fdiv_rn(max, step);
-  s.near = fabsf(steps) < 8388608.0f ? __fmul_rn(ceilf(steps), step) : max;
+  s.floor = __fsub_rn(max, __fdiv_rn(64.0f, inv.hi));
   FF x = two_prod(max, inv.hi);
   x.lo = __fmaf_rn(max, inv.lo, x.lo);
   const float k = rintf(__fmul_rn(x.hi, 32.0f));
@@ -263,11 +255,13 @@ __device__ __forceinline__ RowSettings row_settings(const SampleParams& p, int r
 //     below, as a rule; what is not below the bound goes to a list in shared memory.  The
 //     list, sorted, has all of K: no mass of any other entry is needed.  (If it has less than
 //     top_k, or does not fit, the entries are counted as for a larger top_k.)
-//   top_p alone: the same pass, which lists about the largest thousand and sums the row's mass
-//     in single precision.  If the border is not in the list, a histogram of the distances
-//     from the maximum shows where about it is, a third pass sums what is above that
-//     place and counts or lists the entries there; where that leaves a doubt, exact
-//     masses above the place and in fine bins of the entries' bits decide.
+//   top_p alone: the same pass, which lists about the largest thousand and sums the others'
+//     masses in single precision.  The list's exact masses decide where the border is in it,
+//     whatever the others' may be within the error of their sum.  If it is not, a histogram
+//     of the distances from the maximum shows where about it is, a third pass sums quick
+//     masses, of all entries and of those above that place, and counts or lists the entries
+//     there; where that leaves a doubt, exact masses above the place and in fine bins of
+//     the entries' bits decide.
 //   Larger top_k: fine bins of the bits over all entries, counted, finer and finer until a bin's
 //     entries fit the list or are all equal.
 // Passes after the first find the row in L2.  (Histograms of every row's whole range by bits,
@@ -331,6 +325,15 @@ __device__ __forceinline__ unsigned long long dsmem_ld_u64(uint32_t a) {
   return v;
 }
 
+// A 64-bit sum in shared memory by its halves: the hardware adds 32 bits there, and thousands of
+// equal entries add to one place (as one 64-bit addition: rows of 2 ms).
+__device__ __forceinline__ void add_u64(unsigned long long* sum, unsigned long long x) {
+  uint32_t* half = reinterpret_cast<uint32_t*>(sum);
+  const uint32_t lo = (uint32_t)x, old = atomicAdd(half, lo);
+  const uint32_t hi = (uint32_t)(x >> 32) + (old + lo < old ? 1 : 0);
+  if (hi != 0) atomicAdd(half + 1, hi);
+}
+
 // The first of n ascending sums that is at least `want`, n if none.
 __device__ __forceinline__ int first_reaching(const unsigned long long* sums, int n,
                                               unsigned long long want) {
@@ -341,13 +344,6 @@ __device__ __forceinline__ int first_reaching(const unsigned long long* sums, in
     else lo = mid + 1;
   }
   return lo;
-}
-
-// A sum of near masses in units of 2^-kNearBits.
-constexpr int kNearBits = 40;
-__device__ __forceinline__ unsigned long long units_of(FF x) {
-  const float up = 1099511627776.0f;
-  return (unsigned long long)(__float2ll_rn(__fmul_rn(x.hi, up)) + __float2ll_rn(__fmul_rn(x.lo, up)));
 }
 
 // What a border is looked for by: a number of entries, or a share of their mass.
@@ -665,9 +661,8 @@ struct SampleJob {
     for (int e = 0; e < kE; ++e) sh.list[at + e] = x[e];
     __syncthreads();
   }
-  // In sh.mass the masses of the sorted list's entries, summed up; `near`: those in single
-  // precision, in units of 2^-kNearBits.
-  __device__ __forceinline__ void list_masses(int n, bool near) {
+  // In sh.mass the masses of the sorted list's entries, summed up.
+  __device__ __forceinline__ void list_masses(int n) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kEach = kSampleList / kSampleThreads;
     unsigned long long m[kEach], mine = 0;
@@ -675,7 +670,7 @@ struct SampleJob {
     for (int e = 0; e < kEach; ++e) {
       const int i = threadIdx.x * kEach + e;
       const float z = i < n ? from_order_bits((uint32_t)(sh.list[i] >> 32)) : -INFINITY;
-      m[e] = near ? units_of({near_mass(s, z), 0.0f}) : entry_mass(s, sh.table, z);
+      m[e] = entry_mass(s, sh.table, z);
       mine += m[e];
     }
     unsigned long long upto = mine;
@@ -877,6 +872,12 @@ struct SampleJob {
     return found;
   }
 
+  // The value of a key.  (The bits that bfloat16 does not have are ones in a negative number's
+  // order.)
+  static __device__ __forceinline__ float key_value(uint32_t k) {
+    return from_order_bits(sizeof(TIn) == 4 ? k : (k << 16) | (k & 0x8000u ? 0u : 0xffffu));
+  }
+
   // The largest rank from which on the entries of rank `from` and more reach the goal (all of
   // them together do).  lo .. hi: order bits between which it is thought to be; taken to be
   // anywhere if it is not.
@@ -900,6 +901,7 @@ struct SampleJob {
       float low = from_order_bits(k0 << kDrop);
       if (!(low == low)) low = -INFINITY;  // (no bound)
       const bool all_mass = !goal.by_count && goal.want == 0;  // `count` is the mass of all
+      const bool equal = kDrop && shift == 0;  // a bin's entries are
       each(all_mass ? -INFINITY : low, [&](const float* x, int v, int n) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
@@ -911,7 +913,7 @@ struct SampleJob {
             const unsigned long long m = counts ? entry_mass(s, sh.table, x[e]) : 0;
             if (all_mass) count += m;
             mass += k > k1 ? m : 0;
-            if ((m != 0) & (k >= k0) & (k <= k1)) atomicAdd(&sh.fine[(k - k0) >> shift], m);
+            if (!equal && (m != 0) & (k >= k0) & (k <= k1)) add_u64(&sh.fine[(k - k0) >> shift], m);
           }
           if (counts & (k >= k0) & (k <= k1)) atomicAdd(&sh.hist[(k - k0) >> shift], 1u);
         }
@@ -928,7 +930,12 @@ struct SampleJob {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
           const int b = kSampleFine - 1 - (tid * kEach + e);
-          n[e] = goal.by_count ? sum_of(&sh.hist[b]) : sum_of(&sh.fine[b]);
+          if (goal.by_count || equal) {
+            n[e] = sum_of(&sh.hist[b]);
+            if (!goal.by_count && n[e] != 0) n[e] *= entry_mass(s, sh.table, key_value(k0 + b));
+          } else {
+            n[e] = sum_of(&sh.fine[b]);
+          }
           mine += n[e];
         }
         unsigned long long upto = mine;
@@ -989,7 +996,7 @@ struct SampleJob {
           if (goal.by_count) {
             i = (int)(goal.want - before) - 1;
           } else {
-            list_masses(n, false);
+            list_masses(n);
             i = first_reaching(sh.mass, n, goal.want - before);
           }
           w2.a = sh.list[::min(i, n - 1)];
@@ -998,8 +1005,7 @@ struct SampleJob {
       }
       if (shift == 0) {
         // All equal: the lowest indices, as many as are wanted.
-        // (The bits that bfloat16 does not have are ones in a negative number's order.)
-        const float z = from_order_bits((b0 << kDrop) | (kDrop && !(b0 & 0x8000u) ? 0xffffu : 0u));
+        const float z = key_value(b0);
         unsigned long long nth = goal.want - before;
         if (!goal.by_count) {
           const unsigned long long m = entry_mass(s, sh.table, z);
@@ -1091,8 +1097,8 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
     if (tid == 64 && st.min_p > 0.0f) sh.min_off = (double)st.T * log((double)st.min_p);
   }
 
-  // First pass: the list, the largest, and with `share` the row's mass in single precision,
-  // next to the largest of the sample.
+  // First pass: the list, the largest, and with `share` the mass of what is not listed in single
+  // precision, next to the largest of the sample (which none of it is above).
   bool bad = !st.ok, overflow = false;
   float top = -INFINITY;  // the largest entry of the vectors
   const float edge = tid < edges ? Tr::to_float(job.row[SPEC_CHECKED(job.edge(tid), V, kSiteSample)])
@@ -1105,6 +1111,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   bool scaled = true;
   if (!listing) load(0);
   FF sum = {0.0f, 0.0f};
+  float listed_sum = 0.0f;  // about
   if (listing) {
     float half[2 * kSampleBatch], most = -INFINITY;
 #pragma unroll
@@ -1137,12 +1144,14 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
       __syncthreads();
       for (int w = 0; w < kSampleWarps; ++w) most = fmaxf(most, sh.mine[w].x);
       scaled = mass_scale(s0, most >= -FLT_MAX && most <= FLT_MAX ? most : 0.0f, sh.inv, p.unit_bits);
-      if (tid < edges) sum.hi = near_mass(s0, edge);
     }
   }
   // (An entry of -inf has no mass, and is -inf in the result too.)
   float least = fmaxf(from_order_bits(least_bits << 16), -FLT_MAX);
-  if (listing && edge >= least) job.append(edge, job.edge(tid));
+  if (listing && tid < edges) {
+    if (edge >= least) job.append(edge, job.edge(tid));
+    if (share) (edge >= least ? listed_sum : sum.hi) = near_mass(s0, edge);
+  }
   for (int i0 = 0; i0 < nvec; i0 += kStep) {
     uint4 v[kSampleBatch];
 #pragma unroll
@@ -1170,12 +1179,16 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
       if (listing && most >= least) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
-          if (x[e] >= least) job.append(x[e], job.first + i * kPer + e);
+          if (x[e] >= least) {
+            job.append(x[e], job.first + i * kPer + e);
+            if (share) listed_sum = __fadd_rn(listed_sum, near_mass(s0, x[e]));
+          }
       }
       if (share) {
         float part[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) part[e & 1] = __fadd_rn(part[e & 1], near_mass(s0, x[e]));
+        for (int e = 0; e < kPer; ++e)
+          part[e & 1] = __fadd_rn(part[e & 1], near_mass(s0, x[e] >= least ? -INFINITY : x[e]));
         sum = ff_add_f(sum, __fadd_rn(part[0], part[1]));
       }
     }
@@ -1216,10 +1229,15 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
     float m = top;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (share) sum = warp_sum_ff(sum);
+    if (share) {
+      sum = warp_sum_ff(sum);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) listed_sum += __shfl_xor_sync(0xffffffffu, listed_sum, o);
+    }
     __syncthreads();
     if (lane == 0) {
       sh.mine[warp].x = m;
+      sh.mine[warp].y = listed_sum;
       sh.mine[warp].a = best;
       sh.mine[warp].b = ((unsigned long long)__float_as_uint(sum.lo) << 32) | __float_as_uint(sum.hi);
     }
@@ -1231,8 +1249,10 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
         const SamplePeer q = sh.mine[w];
         word.x = fmaxf(word.x, q.x);
         word.a = q.a > word.a ? q.a : word.a;
-        if (share)
+        if (share) {
+          if (w > 0) listed_sum += q.y;
           all = ff_add(all, {__uint_as_float((uint32_t)q.b), __uint_as_float((uint32_t)(q.b >> 32))});
+        }
       }
       sum = all;
       word.b = least_bits;
@@ -1254,32 +1274,34 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   }
   bad |= !(most >= -FLT_MAX);
   scaled &= mass_scale(job.s, most, sh.inv, p.unit_bits);
-  // The sums to come are next to what the first pass's were where it can be, so that an entry
-  // has the same mass in all of them and what a large one is off by is in common.
-  if (share && ctas == 1 && __fmul_rn(__fsub_rn(most, s0.near), sh.inv.hi) < 8.0f)
-    job.s.near = s0.near;
-  // The row's mass next to `near`, in units of 2^-kNearBits; 0: not known.
-  unsigned long long about = 0;
-  bool apart = false;
+  // The mass of what is not listed, between `rest_lo` and `rest_hi` units; about that of the
+  // row, next to the largest entry's (0: not known).
+  unsigned long long rest_lo = 0, rest_hi = 0;
+  float about = 0.0f;
+  bool known = false;
   if (share && !bad) {
     SamplePeer w = {};
     if (tid == 0) {
-      double x = (double)sum.hi + (double)sum.lo;
-      if (s0.near != job.s.near)
-        x *= exp2(((double)s0.near - (double)job.s.near) *
-                  ((double)sh.inv.hi + (double)sh.inv.lo));
-      x *= 1099511627776.0;
-      w.a = x > 0.0 && x < 4611686018427387904.0 ? (unsigned long long)x : 0;
-      w.i = !(x < 4611686018427387904.0) || !scaled ? 1 : s0.near != job.s.near ? 2 : 0;
+      const double shift = exp2(((double)s0.max - (double)most) *
+                                    ((double)sh.inv.hi + (double)sh.inv.lo) + (double)p.unit_bits);
+      const double rest = ((double)sum.hi + (double)sum.lo) * shift;
+      const bool fits = rest < 9.2e18 && scaled;
+      w.a = fits ? (unsigned long long)rest : 0;
+      w.i = fits;
+      w.x = (float)((rest + (double)listed_sum * shift) * exp2(-(double)p.unit_bits));
     }
     all = job.exchange(w);
-    bool known = true;
+    known = true;
+    unsigned long long rest = 0;
     for (int i = 0; i < ctas; ++i) {
-      about += all[i].a;
-      known = known && all[i].i != 1;
-      apart |= all[i].i == 2;
+      rest += all[i].a;
+      about += all[i].x;
+      known = known && all[i].i != 0;
     }
-    if (!known) about = 0;
+    // (near_mass is off by 2^-16 of itself; V: whole units, what is below `floor`, and sums.)
+    rest_lo = rest - min(rest, (rest >> 15) + V);
+    rest_hi = rest + (rest >> 15) + V;
+    if (!known || !(about <= FLT_MAX)) about = 0.0f;
   }
 
   int token = -1;
@@ -1288,20 +1310,6 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
   float u = want_token ? p.uniforms[r] : 0.0f;
   const bool u_ok = u >= 0.0f && u < 1.0f;
   if (!u_ok) u = 0.0f;
-  // Sums in single precision on both sides: what they are off by in common (the exponential's
-  // mean error is -5e-8) does not matter, and what is left of it is a few parts in 10^9 of
-  // the mass (thousands of entries, 10^-7 each).  Unless the border is some six times as far,
-  // the exact sums decide.  (Of sums next to different numbers an entry's share is off by up to
-  // 2^-22 of itself: 2^-21 of the mass.)
-  const unsigned long long want = mass_part(st.top_p, about, true), doubt = about >> (apart ? 21 : 25);
-  auto border_of = [&](int n, unsigned long long above) -> int {  // in the sorted list, or -1
-    if (n <= 0 || want <= above) return -1;
-    const int i = first_reaching(sh.mass, n, want - above);
-    if (i >= n) return -1;
-    const unsigned long long upto = above + sh.mass[i];
-    const unsigned long long less = above + (i > 0 ? sh.mass[i - 1] : 0);
-    return upto - want > doubt && want - less > doubt ? i : -1;
-  };
   if (bad) {
   } else if (greedy) {
     token = (int)~(uint32_t)limit;
@@ -1312,21 +1320,30 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
     if (st.min_p > 0.0f)
       min_rank = (unsigned long long)order_bits(__double2float_ru((double)most + sh.min_off)) << 32;
     bool done = false;
-    if (listing && !overflow && (few || about != 0)) {
-      if ((few && sh.count > kSampleLong) || ctas > 1) job.cut_list(least_bits);
+    if (listing && !overflow && (few || known)) {
+      if (few && (sh.count > kSampleLong || ctas > 1)) job.cut_list(least_bits);
       const int n = job.gather();
       bool enough = true;  // of a share's mass, to hold the border
+      unsigned long long want_lo = 0, want_hi = 0;
       if (n >= 0 && rank == 0 && share) {
         unsigned long long m = 0;
         for (int i = tid; i < n; i += kSampleThreads)
-          m += units_of({near_mass(job.s, from_order_bits((uint32_t)(sh.list[i] >> 32))), 0.0f});
-        enough = job.block_sums(0, m).mass >= want;
+          m += entry_mass(job.s, sh.table, from_order_bits((uint32_t)(sh.list[i] >> 32)));
+        m = job.block_sums(0, m).mass;
+        want_lo = mass_part(st.top_p, m + rest_lo, true);
+        want_hi = mass_part(st.top_p, m + rest_hi, true);
+        enough = m >= want_hi;
       }
       if (few && n < min(st.top_k, V) && !(n >= 0 && least_bits == 0)) enough = false;
       if (n >= 0 && rank == 0 && enough) {
         job.sort(n);
-        job.list_masses(n, share);
-        int kept = few ? min(n, st.top_k) : border_of(n, 0) + 1;
+        job.list_masses(n);
+        int kept = min(n, st.top_k);
+        if (share) {
+          // (The CTAs' lists have all entries from the largest of their bounds on.)
+          const int i = first_reaching(sh.mass, n, want_lo);
+          kept = i < n && sh.mass[i] >= want_hi && (uint32_t)(sh.list[i] >> 48) >= least_bits ? i + 1 : 0;
+        }
         if (few && cut_p) {
           const unsigned long long part = mass_part(st.top_p, sh.mass[kept - 1], true);
           kept = min(first_reaching(sh.mass, kept, part) + 1, kept);
@@ -1346,8 +1363,6 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
           limit = sh.list[kept - 1];
         }
         if (done && want_token && u_ok) {
-          // (The draw takes the same masses wherever it looks, in whichever of the calls a row is.)
-          if (share) job.list_masses(kept, false);
           const unsigned long long level = mass_part(u, sh.mass[kept - 1], false);
           token = job.draw_listed(kept, level);
         }
@@ -1371,11 +1386,9 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
         // left out; where about, a histogram of the distances from the maximum shows.
         uint32_t lo = (uint32_t)(limit >> 32), hi = top_bits;
         unsigned long long found = 0;
-        const float mass = (float)about * exp2f(-(float)kNearBits) *
-                           ex2(__fmul_rn(__fsub_rn(job.s.near, most), job.s.inv.hi));
-        const float range = logf((float)V / ((1.0f - st.top_p) * mass)) + 0.001f;
+        const float range = logf((float)V / ((1.0f - st.top_p) * about)) + 0.001f;
         const float per = __fmul_rn(__fmul_rn(job.s.inv.hi, kLn2f), (float)kSampleBins / range);
-        if (about != 0 && range > 0.0f && per > 0.0f && per <= FLT_MAX) {
+        if (about > 0.0f && range > 0.0f && per > 0.0f && per <= FLT_MAX) {
           __syncthreads();
           for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.hist[i] = 0;
           __syncthreads();
@@ -1434,7 +1447,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
             // A bin's entries are off its middle by up to half a width, all alike at worst: four
             // standard deviations of that.
             const float slack = 1.2f * width * sqrtf(squares);
-            const float goal = st.top_p * mass;
+            const float goal = st.top_p * about;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
               const float upper = below + bin[e];
@@ -1456,23 +1469,25 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
           // bfloat16: the entries between are counted by their bits, of which there are few (a
           // flat row may have thousands of the same).
           const uint32_t k0 = order_bits(z_lo) >> 16, k1 = order_bits(fminf(z_hi, most)) >> 16;
-          if (sizeof(TIn) == 2 && k1 - k0 < (uint32_t)kSampleFine) {
+          if (!job.s.quick) {
+          } else if (sizeof(TIn) == 2 && k1 - k0 < (uint32_t)kSampleFine) {
             __syncthreads();
             for (int i = tid; i < kSampleFine; i += kSampleThreads) sh.hist[i] = 0;
             __syncthreads();
-            sum = {0.0f, 0.0f};
-            job.each(z_lo, [&](const float* x, int v, int k) {
-              float part = 0.0f;
+            unsigned long long all_mass = 0, mass = 0;  // (above the keys)
+            job.each(-INFINITY, [&](const float* x, int v, int k) {
 #pragma unroll
               for (int e = 0; e < kPer; ++e) {
                 const uint32_t key = order_bits(x[e]) >> 16;
-                const float m = near_mass(job.s, x[e]);
-                part = __fadd_rn(part, (e < k) & (key > k1) ? m : 0.0f);
+                const unsigned long long m = quick_mass(job.s, sh.quick.e, x[e]);
+                all_mass += e < k ? m : 0;
+                mass += (e < k) & (key > k1) ? m : 0;
                 if ((e < k) & (key >= k0) & (key <= k1)) atomicAdd(&sh.hist[key - k0], 1u);
               }
-              sum = ff_add_f(sum, part);
             });
-            const unsigned long long above = job.cluster_sums(0, units_of(sum)).mass;
+            const CountMass sums = job.cluster_sums(all_mass, mass);
+            const unsigned long long above = sums.mass, doubt = quick_doubt(sums.count, V);
+            const unsigned long long want = mass_part(st.top_p, sums.count, true);
             // Thread t has two keys, from the top down.
             SamplePeer w2 = {};
             if (rank == 0) {
@@ -1487,9 +1502,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
                 if (b >= 0) {
                   c[e] = job.sum_of(&sh.hist[b]);
                   const uint32_t key = k0 + b;
-                  m[e] = units_of({near_mass(job.s, from_order_bits(
-                                                        (key << 16) | (key & 0x8000u ? 0 : 0xffffu))),
-                                   0.0f});
+                  m[e] = entry_mass(job.s, sh.table, job.key_value(key));
                 }
                 mine += c[e] * m[e];
               }
@@ -1527,7 +1540,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
             const unsigned long long nth = got[0].a;
             if (bin >= 0) {
               const uint32_t key = k0 + bin;
-              const float z = from_order_bits((key << 16) | (key & 0x8000u ? 0 : 0xffffu));
+              const float z = job.key_value(key);
               // The lowest indices of those equal to the last.
               found = whole ? (unsigned long long)order_bits(z) << 32
                             : entry_rank(z, job.locate(
@@ -1543,25 +1556,29 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
           __syncthreads();
           if (tid == 0) sh.count = 0;
           __syncthreads();
-          sum = {0.0f, 0.0f};
-          job.each(z_lo, [&](const float* x, int v, int k) {
-            float part = 0.0f;
+          unsigned long long all_mass = 0, mass = 0;  // (above the bins)
+          job.each(-INFINITY, [&](const float* x, int v, int k) {
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-              const float m = near_mass(job.s, x[e]);
-              part = __fadd_rn(part, (e < k) & (x[e] > z_hi) ? m : 0.0f);
+              const unsigned long long m = quick_mass(job.s, sh.quick.e, x[e]);
+              all_mass += e < k ? m : 0;
+              mass += (e < k) & (x[e] > z_hi) ? m : 0;
               if ((e < k) & (x[e] >= z_lo) & (x[e] <= z_hi)) job.append(x[e], v + e);
             }
-            sum = ff_add_f(sum, part);
           });
-          const unsigned long long above = job.cluster_sums(0, units_of(sum)).mass;
+          const CountMass sums = job.cluster_sums(all_mass, mass);
+          const unsigned long long above = sums.mass, doubt = quick_doubt(sums.count, V);
+          const unsigned long long want = mass_part(st.top_p, sums.count, true);
           const int n = job.gather();
           SamplePeer w2 = {};
           if (rank == 0 && n > 0) {
             job.sort(n);
-            job.list_masses(n, true);
-            const int i = border_of(n, above);
-            if (i >= 0) w2.a = sh.list[i];
+            job.list_masses(n);
+            const int i = want > above ? first_reaching(sh.mass, n, want - above) : n;
+            if (i < n) {
+              const unsigned long long less = above + (i > 0 ? sh.mass[i - 1] : 0);
+              if (above + sh.mass[i] - want > doubt && want - less > doubt) w2.a = sh.list[i];
+            }
           }
           found = job.exchange(w2)[0].a;
           }

@@ -109,7 +109,7 @@ struct AtControl {
   float fix[2][kAtFewRows];
   int raise[2][2];
   uint64_t vote[2];
-  uint64_t few_done;
+  uint64_t few_done[2];  // of units of few rows, in turn
   long long scan[kAtThreads / 32];
   long long start_off, start_left, start_line, start_cost, total;
   int start_b;
@@ -454,19 +454,22 @@ __device__ __forceinline__ bool at_load_queries(const AtParams& a, AtControl& ct
     if (l >= 0 && !at_wait(&ctl.q_empty[l & 1], (l >> 1) & 1, &ctl.abort_flag)) ok = false;
     ok = __all_sync(0xffffffffu, ok);
   };
-  int done = 0;
-  auto few_over = [&](int f) {  // the first f units of few rows are (their phases in order)
-    for (; ok && done < f; ++done) {
-      if (!at_wait(&ctl.few_done, done & 1, &ctl.abort_flag)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-    }
+  // The f-th unit of few rows is over.  (A barrier each for odd and even ones: a phase is told from
+  // the one before the last by nothing, and both of the last two units may end before either
+  // is waited for, if the next one is planned late.  Unit f + 2 only starts behind this wait.)
+  auto few_over = [&](int f) {
+    if (ok && f >= 0 && !at_wait(&ctl.few_done[f & 1], (f >> 1) & 1, &ctl.abort_flag)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
   };
   while (walk.next(ctl, u, ok)) {
     // Buffers and weights of units of few rows lie over the others' buffers.
     const bool few = at_few(u);
-    if (few) few_over(few_units++ - 1);
+    if (few) few_over(few_units++ - 2);
     if (few != was_few) {
-      if (was_few) few_over(few_units);
+      if (was_few) {
+        few_over(few_units - 2);
+        few_over(few_units - 1);
+      }
       if (ok) empty(used - 1);
     }
     was_few = few;
@@ -844,7 +847,7 @@ __device__ __forceinline__ void at_store_row(uint16_t* out, const float (&x)[kWo
 // A softmax warp: which lanes of tensor memory it has, and how often it has waited for what.
 struct AtSoft {
   int s, quarter;  // the stream; the warp's 32 lanes
-  int tiles, units, meets, votes;
+  int tiles, units, few_units, meets, votes;
   int sets[2], weights;  // scores of either set, weights of units of few rows
   bool ok;
   __device__ __forceinline__ void wait(AtControl& ctl, uint64_t* bar, int parity) {
@@ -1300,7 +1303,8 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
   // what is in the weights' place.
   if (turn) w.meet(ctl);
   else w.vote(ctl);
-  if (w.ok && w.quarter == 0 && lane == 0) mbar_arrive(&ctl.few_done);
+  if (w.ok && w.quarter == 0 && lane == 0) mbar_arrive(&ctl.few_done[w.few_units & 1]);
+  ++w.few_units;
 }
 
 template <int D>
@@ -1351,8 +1355,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&ctl.u_empty[i], kAtReaders);
     }
     mbar_init(&ctl.meet, 8);
-    mbar_init(&ctl.few_done, 2);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.few_done[i], 2);
       mbar_init(&ctl.vote[i], 4);
       ctl.raise[i][0] = ctl.raise[i][1] = 0;
     }

@@ -645,8 +645,9 @@ spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype
  * pages hold past kv_len is not used, whatever it is, nor is an entry that the token
  * does not see.  A key that is not finite makes the rows that see it what the formula
  * gives, and a value that is not finite their results of its dimension (infinite or NaN).
- * A request whose rows or kv_len are out of range gets NaN rows as far as they lie in 0 .. rows - 1, and so do rows that
- * read a page outside the cache; both record SPEC_ERR_BAD_INPUT, readable with
+ * A request whose rows or kv_len are out of range gets NaN rows as far as they lie in
+ * 0 .. rows - 1, and so does a row that sees an entry of a page outside the cache (the request's
+ * other rows do not); both record SPEC_ERR_BAD_INPUT, readable with
  * spec_verify_device_status() on `workspace`.  A device-side wait that runs out records
  * SPEC_ERR_TIMEOUT and leaves NaN.
  */

@@ -82,7 +82,7 @@ struct AtUnit {
   int lo, hi;      // entries that some row sees
   int tile0, nt;   // tiles done here
   int slot;        // where the part goes, -1: the result itself
-  int bad;         // a page outside the cache
+  int bad;         // some row sees a page outside the cache
 };
 
 // The tiles of a unit, and which of their entries, that some of its rows see and others do not
@@ -385,14 +385,15 @@ __device__ __forceinline__ bool at_produce(const AtParams& a, const AtMaps& maps
   while (walk.next(ctl, u, ok)) {
     const int32_t* table = a.p.c.page_table + (size_t)u.b * a.p.c.max_pages;
     bool bad = false;
-    // This lane's page of a tile: its number, -1 for one not to be loaded.
+    // This lane's page of a tile: its number, -1 for one not to be loaded.  (In the place of one
+    // outside the cache the first is: rows that do not see it go on as if it were any.)
     auto page_of = [&](int j) -> int {
       const int pos = (u.tile0 + j) * kAtTile + piece * box;
       if (j >= u.nt || !mine || pos >= u.hi || pos + box <= u.lo) return -1;
       const int id = table[pos >> a.page_bits];
       if (id >= 0 && id < a.p.c.num_pages) return id;
       bad = true;
-      return -1;
+      return 0;
     };
     auto load = [&](const CUtensorMap* map, int j, int id) {
       if (ring.round > 0 &&
@@ -802,6 +803,20 @@ __device__ __forceinline__ bool at_issue(const AtParams& a, AtControl& ctl, uint
   return ok;
 }
 
+// Whether a row sees a page outside the cache among the unit's tiles done here.
+__device__ __noinline__ bool at_row_bad(const AtParams& a, const AtControl& ctl, int slot, int r) {
+  const AtUnit& u = ctl.unit[slot];  // (not a copy: a caller's registers)
+  const int t = at_token(a, u.r0 + r);
+  int lo, hi;
+  at_span(a.p, u.n, u.len, t, t, lo, hi);
+  lo = max(lo, u.tile0 * kAtTile);
+  hi = min(hi, (u.tile0 + u.nt) * kAtTile);
+  const int32_t* table = a.p.c.page_table + (size_t)u.b * a.p.c.max_pages;
+  for (int i = lo >> a.page_bits; lo < hi && i <= (hi - 1) >> a.page_bits; ++i)
+    if (table[i] < 0 || table[i] >= a.p.c.num_pages) return true;
+  return false;
+}
+
 // The values that were set to 0 join a row's results of dimensions e0 .. e1 - 1, which this
 // thread has written.  (The row's weights for them are above 0: a sum that one enters is it.)
 template <int D>
@@ -978,7 +993,7 @@ __device__ __forceinline__ void at_unit_rows(const AtParams& a, AtControl& ctl, 
   if (!w.ok) return;
   w.wait(ctl, &ctl.o_full[s], w.units++);
   if (!w.ok) return;
-  const bool bad = *(volatile int*)&ctl.unit[slot].bad;
+  const bool bad = *(volatile int*)&ctl.unit[slot].bad && live && at_row_bad(a, ctl, slot, r);
   if (bad) l = nan;
   if (!dead) {
     const bool whole = u.slot < 0;
@@ -1257,9 +1272,10 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
           __fadd_rn(__fadd_rn(f[0], f[kAtFewRows]), __fadd_rn(f[2 * kAtFewRows], f[3 * kAtFewRows]));
       all = fmaf(l1, w1, all);
     }
-    if (bad) all = nan;
+    const bool bad_row = bad && at_row_bad(a, ctl, slot, r0 - u.r0 + row);
+    if (bad_row) all = nan;
     const float inv = whole ? (all == 0.0f ? 0.0f : __fdividef(1.0f, all)) : 1.0f;
-    ctl.fix[s][row] = bad ? nan : __fmul_rn(turn && s == 1 ? w1 : w0, inv);
+    ctl.fix[s][row] = bad_row ? nan : __fmul_rn(turn && s == 1 ? w1 : w0, inv);
     if (!turn || s == 0) {
       if (!whole)
         a.stats[(size_t)u.slot * a.slot_rows + r0 - u.r0 + row] = make_float2(top, all);
@@ -1294,10 +1310,11 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
         a.parts[((size_t)u.slot * a.slot_rows + r0 - u.r0 + r) * D + row] = y;
     }
   }
-  if (row < D && !bad && *(volatile int*)&ctl.odd[slot].tiles > 0)
+  if (row < D && *(volatile int*)&ctl.odd[slot].tiles > 0)
     for (int c = turn ? s * 16 : 0; c < rows; c += turn ? 32 : 16)
       for (int r = c; r < min(c + 16, rows); ++r)
-        at_join_odd<D>(a, ctl, slot, r0 - u.r0 + r, row, row + 1);
+        if (ctl.fix[turn ? 0 : s][r] == ctl.fix[turn ? 0 : s][r])  // (else it is NaN already)
+          at_join_odd<D>(a, ctl, slot, r0 - u.r0 + r, row, row + 1);
   tmem_fence_before();
   // Neither stream's next products may write sums that the other still reads, nor queries
   // what is in the weights' place.

@@ -640,8 +640,8 @@ spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype
  *              that may overlap; needs no initialisation
  *
  * Scores, softmax and sums are in single precision; the weights exp(s_j - max) are
- * rounded to bfloat16 for the product with the values.  A token that sees no
- * entry gets out 0 and lse -inf.  Rows of no request keep their values.  What the
+ * rounded to bfloat16 for the product with the values.  A token that sees no entry, or
+ * none whose score is above -inf, gets out 0 and lse -inf.  Rows of no request keep their values.  What the
  * pages hold past kv_len is not used, whatever it is, nor is an entry that the token
  * does not see.  A key that is not finite makes the rows that see it what the formula
  * gives, and a value that is not finite their results of its dimension (infinite or NaN).

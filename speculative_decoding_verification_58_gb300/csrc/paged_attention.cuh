@@ -1260,13 +1260,14 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
     const float m0 = -ctl.above[turn ? 0 : s][row], m1 = turn ? -ctl.above[1][row] : -INFINITY;
     const float top = fmaxf(m0, m1), ref = top == -INFINITY ? 0.0f : top;
     const float w0 = ex2(__fsub_rn(m0, ref)), w1 = ex2(__fsub_rn(m1, ref));
+    // (A weight of 0 is no reason to leave a stream out: its sums may hold what is not finite.)
     float all = 0.0f;
-    if (w0 != 0.0f) {
+    if (m0 != -INFINITY) {
       const float* f = found[turn ? 0 : s] + row;
       all = __fadd_rn(__fadd_rn(f[0], f[kAtFewRows]), __fadd_rn(f[2 * kAtFewRows], f[3 * kAtFewRows]));
       all = __fmul_rn(all, w0);
     }
-    if (w1 != 0.0f) {
+    if (m1 != -INFINITY) {
       const float* f = found[1] + row;
       const float l1 =
           __fadd_rn(__fadd_rn(f[0], f[kAtFewRows]), __fadd_rn(f[2 * kAtFewRows], f[3 * kAtFewRows]));
@@ -1275,7 +1276,9 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
     const bool bad_row = bad && at_row_bad(a, ctl, slot, r0 - u.r0 + row);
     if (bad_row) all = nan;
     const float inv = whole ? (all == 0.0f ? 0.0f : __fdividef(1.0f, all)) : 1.0f;
-    ctl.fix[s][row] = bad_row ? nan : __fmul_rn(turn && s == 1 ? w1 : w0, inv);
+    // (Below 0: a stream in which the row has seen nothing, and whose sums may be anything.)
+    const bool mine = (turn && s == 1 ? m1 : m0) != -INFINITY;
+    ctl.fix[s][row] = bad_row ? nan : mine ? __fmul_rn(turn && s == 1 ? w1 : w0, inv) : -1.0f;
     if (!turn || s == 0) {
       if (!whole)
         a.stats[(size_t)u.slot * a.slot_rows + r0 - u.r0 + row] = make_float2(top, all);
@@ -1299,10 +1302,9 @@ __device__ __forceinline__ void at_unit_few(const AtParams& a, AtControl& ctl,
     for (int e = 0; e < 16; ++e) {
       const int r = c + e;
       if (r >= rows) break;
-      const float w0 = ctl.fix[turn ? 0 : s][r], w1 = turn ? ctl.fix[1][r] : 0.0f;
-      // (A stream without tiles left nothing in tensor memory.)
-      const float y = __fadd_rn(w0 == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o0[e]), w0),
-                                w1 == 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o1[e]), w1));
+      const float w0 = ctl.fix[turn ? 0 : s][r], w1 = turn ? ctl.fix[1][r] : -1.0f;
+      const float y = __fadd_rn(w0 < 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o0[e]), w0),
+                                w1 < 0.0f ? 0.0f : __fmul_rn(__uint_as_float(o1[e]), w1));
       if (whole)
         a.p.out[at_head(a, u.first, u.h, r0 + r) * D + row] =
             (uint16_t)(pack_bf16(y, 0.0f) & 0xffff);
@@ -1452,8 +1454,9 @@ __device__ __forceinline__ void at_join(const AtParams& a, const AtPart& u, int 
       const float fix = ex2(__fsub_rn(m, ref));
       m = top;
       const float w = ex2(__fsub_rn(st.x, ref));
-      // (A NaN in the statistics marks a part that read a page outside the cache.)
-      const bool counts = w != 0.0f || st.y != st.y;
+      // (Parts of weight 0 as well: their sums may hold what is not finite.  A NaN in the
+      // statistics marks one in which the row sees a page outside the cache.)
+      const bool counts = st.x != -INFINITY || st.y != st.y;
       float add = counts ? __fmul_rn(st.y, w) : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) add = __fadd_rn(add, __shfl_xor_sync(0xffffffffu, add, o));

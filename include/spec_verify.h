@@ -637,7 +637,8 @@ spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype
  *   lse        [rows, heads] float out, or NULL
  *   workspace  >= spec_paged_attention_workspace_bytes(rows, heads, kv_heads, width)
  *              bytes (0 for unsupported sizes), 256-byte aligned; not shared by calls
- *              that may overlap; needs no initialisation
+ *              that may overlap; needs no initialisation.  Refused
+ *              (SPEC_ERR_INVALID_ARG) where it shares memory with another argument
  *
  * Scores, softmax and sums are in single precision; the weights exp(s_j - max) are
  * rounded to bfloat16 for the product with the values.  A token that sees no entry, or

@@ -316,6 +316,10 @@ spec_status_t spec_paged_attention(const spec_paged_cache_t* cache, spec_dtype_t
       return SPEC_ERR_INVALID_ARG;
   if (overlap(out, no, lse, nl)) return SPEC_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < nw) return SPEC_ERR_WORKSPACE;
+  if (overlap(workspace, nw, q, nq) || overlap(workspace, nw, out, no) ||
+      overlap(workspace, nw, lse, nl) || overlap(workspace, nw, p.c.k_cache, nk) ||
+      overlap(workspace, nw, p.c.v_cache, nv) || meets_tables(p.c, workspace, nw))
+    return SPEC_ERR_INVALID_ARG;
   NvtxRange r("spec_paged_attention");
   DeviceOf on_device(workspace);
   if (!on_device.ok()) return SPEC_ERR_CUDA;

@@ -1,0 +1,25 @@
+"""Further refusals of the paged cache's and sampling's calls, before any CUDA call (no GPU needed)."""
+
+import ctypes
+
+import pytest
+
+import speculative_decoding_verification_58_gb300 as sv
+from test_round_abi import A, BAD, WSP, cache, lib  # noqa: F401 (a fixture)
+
+
+def attend(lib, q=6 * A, rows=5, H=4, out=7 * A, lse=8 * A, w=9 * A, n=1 << 40, window=0, **kw):
+    c = cache(**kw)
+    return lib.spec_paged_attention(ctypes.byref(c), 1, q, rows, H, 256, 1, window, 0.1, out, lse, w, n,
+                                    None)
+
+
+def test_a_workspace_inside_another_argument(lib):
+    size = int(lib.spec_paged_attention_workspace_bytes(5, 4, 2, 64))
+    assert size % 256 == 0
+    # What an argument's last byte is in, and what ends behind its first.
+    for at, n in ((6 * A, 5 * 4 * 64 * 2), (7 * A, 5 * 4 * 64 * 2), (8 * A, 5 * 4 * 4), (3 * A, 3 * 4 * 4),
+                  (4 * A, 16), (5 * A, 12), (A, 10 * 16 * 2 * 64 * 2), (2 * A, 10 * 16 * 2 * 64 * 2)):
+        for w in (at, (at + n - 1) // 256 * 256, at - size + 256):
+            assert attend(lib, w=w) == BAD, (hex(at), hex(w))
+    assert attend(lib, w=7 * A, n=size - 1) == WSP

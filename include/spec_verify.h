@@ -587,6 +587,8 @@ spec_status_t spec_truncate(const void* logits, spec_dtype_t dtype, int rows, in
  * packed batch (its L_b drafts and the token before them, say: the rows of
  * spec_verify_packed), and its last entries: token t is entry
  * kv_len[b] - (number of new tokens) + t.
+ * All buffers are device memory (append: a k_cache that is not, attention: a workspace
+ * that is not, is SPEC_ERR_INVALID_ARG).
  */
 typedef struct {
   void* k_cache;  /* [num_pages, page_size, kv_heads, width], 16-byte aligned, entries of a */

@@ -270,6 +270,7 @@ spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype
   NvtxRange r("spec_kv_append");
   DeviceOf on_device(p.c.k_cache);
   if (!on_device.ok()) return SPEC_ERR_CUDA;
+  if (!on_device.device()) return SPEC_ERR_INVALID_ARG;
   p.rows = rows;
   p.k_new = static_cast<const uint16_t*>(k_new);
   p.v_new = static_cast<const uint16_t*>(v_new);
@@ -323,6 +324,7 @@ spec_status_t spec_paged_attention(const spec_paged_cache_t* cache, spec_dtype_t
   NvtxRange r("spec_paged_attention");
   DeviceOf on_device(workspace);
   if (!on_device.ok()) return SPEC_ERR_CUDA;
+  if (!on_device.device()) return SPEC_ERR_INVALID_ARG;
   p.rows = rows;
   p.q = static_cast<const uint16_t*>(q);
   p.q_stride = q_stride;

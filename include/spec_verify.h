@@ -614,7 +614,10 @@ typedef struct {
  * A request whose rows lie outside 0 .. rows - 1, whose kv_len is less than its
  * number of new tokens or more than max_pages * page_size, and a token whose page
  * lies outside the cache are left out (spec_paged_attention on the same arrays
- * reports them).  Other entries of the cache keep their values.
+ * reports them).  Other entries of the cache keep their values.  k_cache and v_cache
+ * are two caches (one in both places is SPEC_ERR_INVALID_ARG; attention may read one as
+ * both); two tokens of one entry (requests that share the page they append to) leave
+ * either's, in parts.
  */
 spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype,
                              const void* k_new, const void* v_new, int rows, long long k_stride,

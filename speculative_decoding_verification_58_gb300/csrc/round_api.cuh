@@ -267,6 +267,10 @@ spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype
     if (overlap(o.first, o.second, k_new, kn) || overlap(o.first, o.second, v_new, vn) ||
         meets_tables(p.c, o.first, o.second))
       return SPEC_ERR_INVALID_ARG;
+  // One cache in both places.  (Interleaved ones share a range, but no entry.)
+  const uintptr_t ka = reinterpret_cast<uintptr_t>(p.c.k_cache);
+  const uintptr_t va = reinterpret_cast<uintptr_t>(p.c.v_cache);
+  if ((ka > va ? ka - va : va - ka) < (uintptr_t)p.c.width * 2) return SPEC_ERR_INVALID_ARG;
   NvtxRange r("spec_kv_append");
   DeviceOf on_device(p.c.k_cache);
   if (!on_device.ok()) return SPEC_ERR_CUDA;

@@ -23,3 +23,14 @@ def test_a_workspace_inside_another_argument(lib):
         for w in (at, (at + n - 1) // 256 * 256, at - size + 256):
             assert attend(lib, w=w) == BAD, (hex(at), hex(w))
     assert attend(lib, w=7 * A, n=size - 1) == WSP
+
+
+def test_one_cache_as_keys_and_values(lib):
+    def append(**kw):
+        c = cache(**kw)
+        return lib.spec_kv_append(ctypes.byref(c), 1, 6 * A, 7 * A, 5, 128, 128, None)
+
+    assert append(v_cache=A) == BAD and append(v_cache=A + 64) == BAD and append(k_cache=2 * A + 112) == BAD
+    # Keys and values side by side in a page.
+    side = dict(v_cache=A + 2 * 64, k_page=4096, v_page=4096, k_slot=256, v_slot=256, k_head=128, v_head=128)
+    assert append(**side) != BAD

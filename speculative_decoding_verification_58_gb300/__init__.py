@@ -1107,7 +1107,9 @@ class PagedCache:
             ws = _need_workspace(workspace, "workspace", max(n, 256), dev, stream)
             self.out, self.lse, self.workspace = out, lse, ws
             self._attend = lib().spec_paged_attention
-            self._attend_args = (c, dt, q.data_ptr(), rows, H, q.stride(0), int(causal), int(window),
+            # (A C int: of a larger number it would get the lower bits.)
+            window = max(-1, min(int(window), 2 ** 31 - 1))
+            self._attend_args = (c, dt, q.data_ptr(), rows, H, q.stride(0), int(causal), window,
                                  D ** -0.5 if scale is None else float(scale), out.data_ptr(),
                                  None if lse is None else lse.data_ptr(), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), st)

@@ -34,3 +34,18 @@ def test_one_cache_as_keys_and_values(lib):
     # Keys and values side by side in a page.
     side = dict(v_cache=A + 2 * 64, k_page=4096, v_page=4096, k_slot=256, v_slot=256, k_head=128, v_head=128)
     assert append(**side) != BAD
+
+
+def test_windows_wider_than_a_c_int(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(sv, "_need_cuda", lambda t, name: None)
+    monkeypatch.setattr(sv, "_stream_on", lambda stream, device: 0)
+    i32 = torch.int32
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    arrays = (k, k.clone(), torch.zeros(1, 3, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(1, dtype=i32))
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    for window, want in ((0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                         (2 ** 32, 2 ** 31 - 1), (2 ** 32 + 7, 2 ** 31 - 1), (-1, -1), (-2 ** 32, -1)):
+        bound = sv.PagedCache(*arrays, q=q, window=window)
+        assert sv.lib().spec_paged_attention.argtypes[7] is ctypes.c_int
+        assert ctypes.c_int(bound._attend_args[7]).value == want

@@ -691,7 +691,9 @@ def _alloc_on(stream, device):
         return contextlib.nullcontext()
     cuda = _torch().cuda
     if not hasattr(stream, "cuda_stream"):
-        stream = cuda.ExternalStream(int(stream), device=device)
+        # (An external stream of handle 0 would be a new one.)
+        stream = cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            cuda.default_stream(device)
     return cuda.stream(stream)
 
 

@@ -962,7 +962,6 @@ class Sampler:
         if kept is not None:
             _need(kept, "kept", logits.dtype, shape + (V,), dev)
         self._keep = (logits, temperature, uniforms, top_k, top_p, min_p)
-        self._stream = stream
         self.tokens, self.kept = tokens if uniforms is not None else None, kept
         self._head = (logits.data_ptr(), dt, B * n, V, n, temperature.data_ptr(),
                       *(None if t is None else t.data_ptr() for t in (top_k, top_p, min_p)))
@@ -988,7 +987,8 @@ class Sampler:
         """Enqueue the truncation; returns the truncated logits."""
         if self._truncate_args is None:
             logits = self._keep[0]
-            with _alloc_on(self._stream, logits.device):
+            # (On the stream that the object is bound to, whichever is current by now.)
+            with _alloc_on(self._st, logits.device):
                 self.kept = _torch().empty_like(logits)
             self._truncate_args = self._head + (self.kept.data_ptr(), self._st)
         _check(self._truncate(*self._truncate_args), "spec_truncate")

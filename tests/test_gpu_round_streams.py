@@ -25,3 +25,21 @@ def test_handles_of_streams():
                 assert torch.cuda.current_stream(dev).cuda_stream == want
     with sv._alloc_on(side.cuda_stream, dev):
         assert torch.cuda.current_stream(dev).cuda_stream == side.cuda_stream
+
+
+def test_a_sampler_used_under_another_stream():
+    z = torch.randn((3, 2, 5000), device="cuda")
+    T = torch.full((3,), 0.7, device="cuda")
+    k = torch.full((3,), 40, dtype=torch.int32, device="cuda")
+    want = sv.spec_truncate(z, T, top_k=k)
+    sampler = sv.Sampler(z, T, top_k=k)  # bound to the default stream
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        kept = sampler.truncate()
+    torch.cuda.current_stream().synchronize()
+    assert torch.equal(kept, want)
+    # Its memory belongs to the stream it is written on.
+    segments = [s for s in torch.cuda.memory_snapshot()
+                if s["address"] <= kept.data_ptr() < s["address"] + s["total_size"]]
+    assert [s["stream"] for s in segments] == [0]

@@ -1,5 +1,6 @@
 """Further refusals of the paged cache's and sampling's calls, before any CUDA call (no GPU needed)."""
 
+import contextlib
 import ctypes
 
 import pytest
@@ -49,3 +50,21 @@ def test_windows_wider_than_a_c_int(monkeypatch):
         bound = sv.PagedCache(*arrays, q=q, window=window)
         assert sv.lib().spec_paged_attention.argtypes[7] is ctypes.c_int
         assert ctypes.c_int(bound._attend_args[7]).value == want
+
+
+def test_the_first_truncation_allocates_on_its_own_stream(monkeypatch):
+    torch = pytest.importorskip("torch")
+    streams = []
+
+    def alloc_on(stream, device):
+        streams.append(stream)
+        return contextlib.nullcontext()
+
+    monkeypatch.setattr(sv, "_need_cuda", lambda t, name: None)
+    monkeypatch.setattr(sv, "_stream_on", lambda stream, device: 77)  # the current one when it is made
+    monkeypatch.setattr(sv, "_alloc_on", alloc_on)
+    sampler = sv.Sampler(torch.zeros(2, 3, 50), torch.ones(2))
+    monkeypatch.setattr(sv, "_stream_on", lambda stream, device: 99)
+    sampler._truncate = lambda *args: 0 if args[-1] == 77 else 1
+    assert sampler.truncate().shape == (2, 3, 50)
+    assert streams == [77]

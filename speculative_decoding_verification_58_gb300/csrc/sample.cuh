@@ -1024,6 +1024,20 @@ struct SampleJob {
   }
 };
 
+// The draw by exact masses, for all threads.  A function of its own, with a copy of the job: its
+// code within the kernel costs the other paths registers (2048 rows, top_k = 50: 240 us, 227 so).
+template <typename TIn>
+__device__ __noinline__ int exact_draw(SampleJob<TIn> job, float least, uint32_t last, float u) {
+  return job.locate(
+      least,
+      [&](float z, int v) -> unsigned long long {
+        return (z > least) | ((z == least) & ((uint32_t)v <= last)) ? entry_mass(job.s, job.sh.table, z)
+                                                                    : 0;
+      },
+      [&](unsigned long long total) { return mass_part(u, total, false); },
+      [](unsigned long long) { return 0ull; });
+}
+
 template <typename TIn>
 __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
     sample_kernel(const __grid_constant__ SampleParams p) {
@@ -1606,13 +1620,7 @@ __global__ void __launch_bounds__(kSampleThreads, kSamplePerSm)
                 return drawn(z, v) ? m : 0;
               },
               level, [&](unsigned long long total) { return quick_doubt(total, V); });
-        if (token < 0)
-          token = job.locate(
-              z_least,
-              [&](float z, int v) -> unsigned long long {
-                return drawn(z, v) ? entry_mass(job.s, sh.table, z) : 0;
-              },
-              level, [](unsigned long long) { return 0ull; });
+        if (token < 0) token = exact_draw<TIn>(job, z_least, last, u);  // (the last exchange)
       }
     }
     if (!u_ok) token = -1;

@@ -603,13 +603,14 @@ typedef struct {
   int max_pages;              /* max_pages * page_size <= 2^30 */
   const int32_t* new_start;   /* [B + 1] (device), not decreasing */
   const int32_t* kv_len;      /* [B] (device): entries with the new tokens' */
-  int B;
+  int B;                      /* 1 to SPEC_MAX_B */
 } spec_paged_cache_t;
 
 /*
  * Write the new tokens' keys and values into the cache.
  *   k_new, v_new  [rows, kv_heads, width] dtype, 16-byte aligned, rows k_stride and
  *                 v_stride entries apart (multiples of 8), heads `width` apart
+ *   rows          below 1: SPEC_ERR_INVALID_ARG; above SPEC_MAX_ROWS: SPEC_ERR_UNSUPPORTED
  *   dtype         SPEC_BF16; SPEC_F32 is SPEC_ERR_UNSUPPORTED
  * A request whose rows lie outside 0 .. rows - 1, whose kv_len is less than its
  * number of new tokens or more than max_pages * page_size, and a token whose page
@@ -632,6 +633,7 @@ spec_status_t spec_kv_append(const spec_paged_cache_t* cache, spec_dtype_t dtype
  *
  *   q          [rows, heads, width] dtype, 16-byte aligned, rows q_stride entries
  *              apart (a multiple of 8), heads `width` apart
+ *   rows       as for spec_kv_append
  *   dtype      SPEC_BF16; SPEC_F32 is SPEC_ERR_UNSUPPORTED
  *   heads      a multiple of kv_heads, at most 1024
  *   causal     0 or 1: a target's pass over a chain of tokens is causal, the block

@@ -28,11 +28,11 @@
 //
 // Measured: 64 single tokens over up to 16384 entries (3.1 GB of keys and values) 475 to 496 us,
 // 6.3 to 6.6 TB/s: memory.  32 requests of up to 17 tokens over up to 8192 entries, pages
-// of 16: 186 us, 4.4 TB/s (pages of 64: 160 us; a page of 16 slots is 2 KB a copy, and the
+// of 16: 189 us, 4.3 TB/s (pages of 64: 160 us; a page of 16 slots is 2 KB a copy, and the
 // copies of a tile take the loading as long as memory does).  Two chunks of 4096 tokens
-// behind 8192: 955 us, 1.13 PFLOP/s (half of the tensor cores' cycles): a
+// behind 8192: 958 us, 1.13 PFLOP/s (half of the tensor cores' cycles): a
 // stream's softmax takes 1.1 us of a tile, the other's products 0.65.  One token over 8000
-// entries 23 us: 4.5 until the first page is on its way, 8 for three or four tiles and the
+// entries 24 us: 4.5 until the first page is on its way, 8 for three or four tiles and the
 // part's store, 5 for the join, and their launches.
 #pragma once
 

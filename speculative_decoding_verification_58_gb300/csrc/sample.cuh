@@ -18,11 +18,12 @@
 // size do not average out where thousands of entries are equal, as plateaus of bfloat16 rows.)
 //
 // Measured on rows of 151936 (2048 of them, us; reading them once takes 92 in bfloat16 and
-// 184 in float): greedy 124 and 216, top_k = 50 218 and 294, top_k = 400 343 and 384, no
-// truncation 640 and 740 (with exact masses alone 1000 and 1040), top_p = 0.95 alone on rows with Zipf's tail 1255 and 1235; one
-// row, top_k = 50: 13.  Greedy and top-k rows are bound by memory and by the latencies of the
-// list's steps (two CTAs an SM; four of 256 threads: 200, but rows that take several
-// passes then do not stay in L2: top_p 1743), the others by instruction issue.
+// 184 in float): greedy 119 and 215, top_k = 50 227 and 294, top_k = 400 353 and 394, no
+// truncation 590 to 670 and 735 (a draw by exact masses alone: 1000 and 1040), top_p = 0.95 alone
+// on rows with Zipf's tail 1760 and 1660; one row, top_k = 50: 17.  Greedy and top-k rows are
+// bound by memory and by the latencies of the list's steps (two CTAs an SM; four of 256
+// threads: 200, but the rows no longer stay in L2, and those that take several passes
+// take longer), the others by instruction issue.
 #pragma once
 
 #include "common.cuh"
